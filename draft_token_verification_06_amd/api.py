@@ -331,6 +331,96 @@ def verify_tree(target, draft, node_tokens, parent, *, mode="stochastic", seed=0
     return res
 
 
+def _rows_i32(t, B, cols, name):
+    """Row stride of an int32 device tensor (B, >= cols) with unit column stride."""
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != B or t.shape[1] < cols \
+            or (t.shape[1] > 1 and t.stride(1) != 1) or (B > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: expected an int32 device tensor of shape ({B}, >={cols}) with unit column stride")
+    return t.stride(0) if B > 1 else t.shape[1]
+
+
+def _seq_stride(t, name):
+    """Sequence stride of (B, R, V) logits whose sequences do not overlap (0 = dense)."""
+    B, R, V = t.shape
+    if R == 1 and t.dim() == 3 and t.stride(1) != V:
+        t = t.as_strided(t.shape, (t.stride(0), V, t.stride(2)))  # one row: its row stride says nothing
+    stride = _logits(t, R, name)
+    if B > 1 and stride < R * V:
+        raise ValueError(f"{name}: sequences overlap")
+    return stride if B > 1 else 0
+
+
+def adjust_logits(logits, *, tokens=None, parent=None, history=None, history_len=None, prompt_len=None,
+                  repetition=None, presence=None, frequency=None, bias_tokens=None, bias_values=None,
+                  allowed=None, row_count=None, out=None):
+    """Penalties, biases and grammar masks on logits rows: sv_adjust_logits.
+
+    logits (B, R, V) as verify_window / verify_tree take them.  Row i of a
+    window follows tokens[:, :i]; with parent (a host sequence of R entries)
+    row v follows the tokens of its path.  history (B, cap) int32 with
+    history_len and prompt_len (B,) int32; repetition, presence, frequency (B,)
+    float32; bias_tokens / bias_values (B, n) int32 / float32; allowed int32
+    (B, R, ceil(V / 32)) bit masks (rows or sequences may be expanded);
+    row_count (B,) int32.  Returns out (a new tensor when None; out=logits
+    works in place)."""
+    if logits.dim() != 3:
+        raise ValueError(f"logits: expected shape (B, R, V), got {tuple(logits.shape)}")
+    B, R, V = logits.shape
+    stride = _seq_stride(logits, "logits")
+    dev = logits.device
+    par = None
+    if parent is not None:
+        if len(parent) != R:
+            raise ValueError("parent must have one entry per row")
+        par = (ctypes.c_int32 * R)(*parent)
+    tokens_stride = history_stride = cap = n_bias = mask_seq = mask_row = 0
+    if tokens is not None:
+        tokens_stride = _rows_i32(tokens, B, R if parent is not None else R - 1, "tokens")
+    if history is not None:
+        history_stride = _rows_i32(history, B, 0, "history")
+        cap = history.shape[1]
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len need a history")
+    for name, t, dtype in (("history_len", history_len, torch.int32), ("prompt_len", prompt_len, torch.int32),
+                           ("row_count", row_count, torch.int32), ("repetition", repetition, torch.float32),
+                           ("presence", presence, torch.float32), ("frequency", frequency, torch.float32)):
+        _optional(t, dtype, B, name)
+    if tokens is None and R > 1 and not (repetition is None and presence is None and frequency is None):
+        raise ValueError("penalties on more than one row need the rows' tokens")
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values go together")
+    if bias_tokens is not None:
+        n_bias = bias_tokens.shape[-1]
+        _i32(bias_tokens, (B, n_bias), "bias_tokens")
+        if bias_values.dtype != torch.float32 or not bias_values.is_cuda or not bias_values.is_contiguous() \
+                or tuple(bias_values.shape) != (B, n_bias):
+            raise ValueError(f"bias_values: expected a contiguous float32 device tensor of shape ({B}, {n_bias})")
+    if allowed is not None:
+        W = (V + 31) // 32
+        if allowed.dtype != torch.int32 or not allowed.is_cuda or tuple(allowed.shape) != (B, R, W) \
+                or (W > 1 and allowed.stride(2) != 1):
+            raise ValueError(f"allowed: expected an int32 device tensor of shape ({B}, {R}, {W}) with unit word stride")
+        mask_seq, mask_row = allowed.stride(0), allowed.stride(1)
+    _same_device(dev, tokens=tokens, history=history, history_len=history_len, prompt_len=prompt_len,
+                 repetition=repetition, presence=presence, frequency=frequency, bias_tokens=bias_tokens,
+                 bias_values=bias_values, allowed=allowed, row_count=row_count)
+    if out is None:
+        out = torch.empty(B, R, V, dtype=logits.dtype, device=dev)
+        out_stride = 0
+    else:
+        if out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape:
+            raise ValueError("out must match logits in dtype, device and shape")
+        out_stride = _seq_stride(out, "out")
+    with torch.cuda.device(dev):
+        _check(lib().sv_adjust_logits(
+            _ptr(logits), stride, _ptr(out), out_stride, _DTYPE_CODE[logits.dtype],
+            _ptr(tokens), tokens_stride, par, _ptr(row_count), B, R, V,
+            _ptr(history), history_stride, cap, _ptr(history_len), _ptr(prompt_len),
+            _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), n_bias,
+            _ptr(allowed), mask_seq, mask_row, _stream(dev)))
+    return out
+
+
 def rollback(buf_tokens, buf_len, stage, verified, verified_len, *, len_offset=0):
     """Per-stage buffer rollback: sv_rollback (in place on buf_tokens/buf_len).
     Row s of `verified` must hold at least verified_len[s] + len_offset tokens

@@ -1,0 +1,261 @@
+// Logits adjustment (gfx950): penalties for repeated tokens, biases and
+// grammar masks on the rows a verification call reads.
+//
+// Row r of a sequence follows the sequence's history and the row's path (the
+// drafts before it, or the tree nodes down to it), so with n the occurrences
+// of token t in history[prompt_len ..) and on the path, and seen(t) when t is
+// anywhere in the history or on the path:
+//   y = x(t);  seen: y = y > 0 ? y / repetition : y * repetition
+//   n > 0:     y = y - frequency * n - presence
+//   y += bias(t);  not allowed: y = -inf
+// in float32, rounded once to the storage type.  Elements nothing applies to
+// keep their bits.
+//
+// Bound: HBM (each row read once and written once).  A workgroup owns kChunk
+// consecutive tokens of one sequence and every thread one 16-byte vector of
+// them, over all rows: the history is counted once per chunk into LDS, each
+// thread takes its vector's counts and biases into registers, and the row
+// loop needs no barrier.  Path tokens are bit sets over the tree's nodes
+// restricted to the chunk, nearly always empty, so a row costs its load, its
+// mask byte and its store.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sv_device.h"
+#include "sv_launch.h"
+#include "sv_plan.h"
+
+namespace sv {
+
+// Row starts are aligned to the element only (an odd vocabulary): vectors are
+// moved with element alignment, which global memory instructions allow.
+typedef unsigned int u32x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
+
+// Storage type of a float value, as bits.
+template <int DT> __device__ __forceinline__ uint32_t enc(float x);
+template <> __device__ __forceinline__ uint32_t enc<DT_F32>(float x) { return __float_as_uint(x); }
+template <> __device__ __forceinline__ uint32_t enc<DT_BF16>(float x) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+}
+template <> __device__ __forceinline__ uint32_t enc<DT_F16>(float x) {
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+}
+
+template <int DT> __device__ __forceinline__ uint4 load_elems(const char *p, int valid) {
+  constexpr int kEPV = Elt<DT>::kEPV;
+  if (valid >= kEPV) {
+    const u32x4_e2_t v = *as_global<u32x4_e2_t>(static_cast<const void *>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < kEPV; ++k)
+    if (k < valid) {
+      if (DT == DT_F32) w[k] = Elt<DT>::raw(p, k);
+      else w[k / 2] |= Elt<DT>::raw(p, k) << (16 * (k & 1));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT> __device__ __forceinline__ void store_elems(char *p, uint4 v, int valid) {
+  constexpr int kEPV = Elt<DT>::kEPV;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (valid >= kEPV) {
+    *reinterpret_cast<SV_GLOBAL u32x4_e2_t *>(reinterpret_cast<uintptr_t>(p)) = u32x4_e2_t{v.x, v.y, v.z, v.w};
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kEPV; ++k)
+    if (k < valid) {
+      if (DT == DT_F32) reinterpret_cast<uint32_t *>(p)[k] = w[k];
+      else reinterpret_cast<uint16_t *>(p)[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+    }
+}
+
+// -inf in the elements whose bit of m is clear.
+template <int DT> __device__ __forceinline__ uint4 mask_elems(uint4 v, uint32_t m) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (DT == DT_F32) {
+      w[i] = (m >> i) & 1 ? w[i] : Elt<DT>::kNegInfPair;
+    } else {
+      const uint32_t keep = ((m >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((m >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
+      w[i] = (w[i] & keep) | (Elt<DT>::kNegInfPair & ~keep);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr uint32_t kSeenInPrompt = 0x80000000u;
+
+template <int DT>
+__global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) {
+  using E = Elt<DT>;
+  constexpr int kEPV = E::kEPV;
+  constexpr int kChunk = kAdjustThreads * kEPV;
+  constexpr uint32_t kFull = (1u << kEPV) - 1;
+  constexpr int kWords = kTreeMaxNodes / 64;
+  __shared__ uint32_t s_count[kChunk];  // occurrences past the prompt; kSeenInPrompt
+  __shared__ uint16_t s_bias[kChunk];   // 1 + index of the last bias entry that names the token
+  __shared__ int32_t s_node[kTreeMaxNodes];
+  __shared__ uint64_t s_in[kWords];               // nodes whose token lies in the chunk
+  __shared__ uint64_t s_path[kTreeMaxNodes][kWords];  // those on each row's path
+
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / A.chunks;
+  const int base = (blockIdx.x - b * A.chunks) * kChunk;
+  const int rows = A.row_count ? min(max(A.row_count[b], 0), A.R) : A.R;
+  if (rows == 0) return;  // the same for the whole workgroup
+  const bool counted = A.repetition || A.presence || A.frequency;
+  const bool history = counted && A.history;
+  const bool biased = A.n_bias > 0;
+  const bool paths = counted && A.tokens && A.R > 1;
+  const int words = (A.R + 63) / 64;
+
+  if (history)
+    for (int i = tid; i < kChunk; i += kAdjustThreads) s_count[i] = 0;
+  if (biased)
+    for (int i = tid; i < kChunk / 2; i += kAdjustThreads) reinterpret_cast<uint32_t *>(s_bias)[i] = 0;
+  if (paths) {
+    static_assert(kAdjustThreads >= kTreeMaxNodes, "one thread per node");
+    if (tid < words * 64) {
+      // row v's own node: the draft before row v, or the tree node's token
+      int t = -1;
+      if (tid >= 1 && tid < A.R) t = A.tokens[b * A.tokens_stride + (A.tree ? tid : tid - 1)];
+      const bool in = t >= base && t < A.V && t - base < kChunk;
+      s_node[tid] = t;
+      const uint64_t bits = __ballot(in);
+      if ((tid & 63) == 0) s_in[tid >> 6] = bits;
+    }
+  }
+  __syncthreads();
+  if (history) {
+    const int len = A.history_len ? min(max(A.history_len[b], 0), A.history_cap) : A.history_cap;
+    const int prompt = A.prompt_len ? min(max(A.prompt_len[b], 0), len) : 0;
+    const int32_t *h = A.history + b * A.history_stride;
+    for (int i = tid; i < len; i += kAdjustThreads) {
+      const int t = h[i];
+      if (t >= base && t < A.V && t - base < kChunk) {
+        if (i < prompt) atomicOr(&s_count[t - base], kSeenInPrompt);
+        else atomicAdd(&s_count[t - base], 1u);
+      }
+    }
+  }
+  if (biased) {
+    // the last entry that names a token counts: the largest index wins, in any order
+    const int32_t *bt = A.bias_tokens + static_cast<int64_t>(b) * A.n_bias;
+    for (int j = tid; j < A.n_bias; j += kAdjustThreads) {
+      const int t = bt[j];
+      if (t >= base && t < A.V && t - base < kChunk) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(s_bias) + ((t - base) >> 1);
+        const int sh = 16 * ((t - base) & 1);
+        uint32_t old = *w;
+        while (((old >> sh) & 0xFFFFu) < static_cast<uint32_t>(j + 1)) {
+          const uint32_t was = atomicCAS(w, old, (old & ~(0xFFFFu << sh)) | (static_cast<uint32_t>(j + 1) << sh));
+          if (was == old) break;
+          old = was;
+        }
+      }
+    }
+  }
+  if (paths && tid < A.R) {
+    uint64_t bits[kWords] = {};
+    for (int v = tid; v > 0; v = A.tree ? A.parent[v] : v - 1) {
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+        if (w < words && w == (v >> 6)) bits[w] |= s_in[w] & (1ull << (v & 63));
+    }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+      if (w < words) s_path[tid][w] = bits[w];
+  }
+  __syncthreads();
+
+  const int t0 = base + tid * kEPV;  // this thread's first token
+  const int valid = min(kEPV, A.V - t0);
+  if (valid <= 0) return;
+  uint32_t count[kEPV];
+  float bias[kEPV];
+  bool touched = false;
+#pragma unroll
+  for (int k = 0; k < kEPV; ++k) {
+    count[k] = history ? s_count[tid * kEPV + k] : 0u;
+    bias[k] = 0.0f;
+    touched |= count[k] != 0;
+  }
+  if (biased) {
+#pragma unroll
+    for (int k = 0; k < kEPV; ++k) {
+      const int j = s_bias[tid * kEPV + k];
+      if (j > 0) {
+        bias[k] = A.bias_values[static_cast<int64_t>(b) * A.n_bias + j - 1];
+        touched = true;
+      }
+    }
+  }
+  const float rho = A.repetition ? A.repetition[b] : 1.0f;
+  const float pres = A.presence ? A.presence[b] : 0.0f;
+  const float freq = A.frequency ? A.frequency[b] : 0.0f;
+
+  const int64_t row_bytes = static_cast<int64_t>(A.V) * E::kBytes;
+  const char *in = A.in + b * A.in_stride_bytes + static_cast<int64_t>(t0) * E::kBytes;
+  char *out = A.out + b * A.out_stride_bytes + static_cast<int64_t>(t0) * E::kBytes;
+  const uint8_t *allowed =
+      A.allowed ? reinterpret_cast<const uint8_t *>(A.allowed + b * A.allowed_seq_stride) + t0 / 8 : nullptr;
+  const int nibble = t0 & 7;  // float32 vectors: half a byte of the mask
+  for (int r = 0; r < rows; ++r, in += row_bytes, out += row_bytes) {
+    uint32_t m = kFull;
+    if (allowed) m = (allowed[r * A.allowed_row_stride * 4] >> nibble) & kFull;
+    uint32_t on_path[kEPV] = {};
+    bool apply = touched;
+    if (paths) {
+      for (int w = 0; w < words; ++w)
+        for (uint64_t bits = s_path[r][w]; bits; bits &= bits - 1) {
+          const int d = s_node[w * 64 + __builtin_ctzll(bits)] - t0;
+#pragma unroll
+          for (int k = 0; k < kEPV; ++k) on_path[k] += d == k;
+          apply |= d >= 0 && d < kEPV;
+        }
+    }
+    if (A.in_place && !apply && m == kFull) continue;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (m != 0) x = load_elems<DT>(in, valid);
+    if (apply && m != 0) {
+      float y[kEPV];
+      E::vec(x, y);
+#pragma unroll
+      for (int k = 0; k < kEPV; ++k) {
+        const uint32_t n = (count[k] & ~kSeenInPrompt) + on_path[k];
+        if (count[k] != 0 || n != 0) y[k] = y[k] > 0.0f ? y[k] / rho : y[k] * rho;
+        if (n != 0) y[k] = y[k] - freq * static_cast<float>(n) - pres;
+        if (bias[k] != 0.0f) y[k] += bias[k];
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = DT == DT_F32 ? enc<DT>(y[i % kEPV]) : enc<DT>(y[2 * i % kEPV]) | (enc<DT>(y[(2 * i + 1) % kEPV]) << 16);
+      x = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (m != kFull) x = mask_elems<DT>(x, m);
+    store_elems<DT>(out, x, valid);
+  }
+}
+
+int adjust_chunks(int dtype, int V) {
+  const int chunk = kAdjustThreads * (dtype == DT_F32 ? 4 : 8);
+  return (V + chunk - 1) / chunk;
+}
+
+void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st) {
+  A.chunks = adjust_chunks(dtype, A.V);
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(B) * A.chunks));
+  if (dtype == DT_F32)
+    hipLaunchKernelGGL(k_adjust_logits<DT_F32>, grid, dim3(kAdjustThreads), 0, st, A);
+  else if (dtype == DT_BF16)
+    hipLaunchKernelGGL(k_adjust_logits<DT_BF16>, grid, dim3(kAdjustThreads), 0, st, A);
+  else
+    hipLaunchKernelGGL(k_adjust_logits<DT_F16>, grid, dim3(kAdjustThreads), 0, st, A);
+}
+
+}  // namespace sv

@@ -544,4 +544,77 @@ int sv_verify_window_lmhead(const void *hidden_target, const void *unembed_targe
   return launch_status();
 }
 
+int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t out_seq_stride, int dtype,
+                     const int32_t *tokens, int64_t tokens_stride, const int32_t *parent_host,
+                     const int32_t *row_count, int32_t B, int32_t R, int32_t V,
+                     const int32_t *history, int64_t history_stride, int32_t history_cap,
+                     const int32_t *history_len, const int32_t *prompt_len,
+                     const float *repetition, const float *presence, const float *frequency,
+                     const int32_t *bias_tokens, const float *bias_values, int32_t n_bias,
+                     const uint32_t *allowed, int64_t allowed_seq_stride, int64_t allowed_row_stride,
+                     hipStream_t stream) {
+  const int eb = elem_bytes(dtype);
+  if (eb == 0) return SV_EDTYPE;
+  if (B < 1 || R < 1 || V < 1 || V > kMaxVocab) return SV_EINVAL;
+  if (!logits || !out || !aligned(logits, eb) || !aligned(out, eb)) return SV_EINVAL;
+  AdjustArgs A{};
+  if (parent_host) {
+    TreeMeta meta;
+    const int tst = build_tree(parent_host, R, &meta);
+    if (tst != SV_OK) return tst;
+    std::memcpy(A.parent, meta.parent, sizeof(A.parent));
+    A.tree = 1;
+  } else if (R > SV_MAX_GAMMA + 1) {
+    return SV_EINVAL;
+  }
+  const int64_t seq_elems = static_cast<int64_t>(R) * V;
+  if (seq_stride == 0) seq_stride = seq_elems;
+  if (out_seq_stride == 0) out_seq_stride = seq_elems;
+  if (seq_stride < seq_elems || out_seq_stride < seq_elems) return SV_EINVAL;
+  const bool counted = repetition || presence || frequency;
+  if (counted && R > 1 && !tokens) return SV_EINVAL;
+  const int64_t row_tokens = parent_host ? R : R - 1;
+  if (tokens && tokens_stride == 0) tokens_stride = row_tokens;
+  if (tokens && B > 1 && tokens_stride < row_tokens) return SV_EINVAL;
+  if (history_cap < 0 || (history_cap > 0 && !history)) return SV_EINVAL;
+  if (history && history_stride == 0) history_stride = history_cap;
+  if (history && B > 1 && history_stride < history_cap) return SV_EINVAL;
+  if (n_bias < 0 || n_bias > SV_ADJUST_MAX_BIAS || (n_bias > 0 && (!bias_tokens || !bias_values))) return SV_EINVAL;
+  if (allowed && (!aligned(allowed, 4) || allowed_seq_stride < 0 || allowed_row_stride < 0)) return SV_EINVAL;
+  if (!grid_fits(static_cast<int64_t>(B) * adjust_chunks(dtype, V), kAdjustThreads)) return SV_EINVAL;
+  A.in = static_cast<const char *>(logits);
+  A.in_stride_bytes = seq_stride * eb;
+  A.out = static_cast<char *>(out);
+  A.out_stride_bytes = out_seq_stride * eb;
+  // In place (the same rows), or the two spans are disjoint.
+  A.in_place = A.in == A.out && (B == 1 || seq_stride == out_seq_stride);
+  if (!A.in_place) {
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(logits), o0 = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t i1 = i0 + ((B - 1) * seq_stride + seq_elems) * eb;
+    const uintptr_t o1 = o0 + ((B - 1) * out_seq_stride + seq_elems) * eb;
+    if (i0 < o1 && o0 < i1) return SV_EINVAL;
+  }
+  A.tokens = tokens;
+  A.tokens_stride = tokens_stride;
+  A.row_count = row_count;
+  A.R = R;
+  A.V = V;
+  A.history = history_cap > 0 ? history : nullptr;
+  A.history_stride = history_stride;
+  A.history_len = history_len;
+  A.prompt_len = prompt_len;
+  A.history_cap = history_cap;
+  A.n_bias = n_bias;
+  A.repetition = repetition;
+  A.presence = presence;
+  A.frequency = frequency;
+  A.bias_tokens = bias_tokens;
+  A.bias_values = bias_values;
+  A.allowed = allowed;
+  A.allowed_seq_stride = allowed_seq_stride;
+  A.allowed_row_stride = allowed_row_stride;
+  launch_adjust_logits(dtype, A, B, stream);
+  return launch_status();
+}
+
 }  // extern "C"

@@ -94,6 +94,35 @@ struct LmDecideArgs {
   int32_t *arrive;               // arrival counters of the draw, zeroed here
 };
 
+// Logits adjustment.  Row r of a sequence follows tokens[0 .. r - 1] (window)
+// or carries node r of the tree given by parent.
+struct AdjustArgs {
+  const char *in;
+  int64_t in_stride_bytes;
+  char *out;
+  int64_t out_stride_bytes;
+  const int32_t *tokens;  // [B] rows of tokens_stride
+  int64_t tokens_stride;
+  const int32_t *row_count;
+  int32_t R, V;
+  const int32_t *history;
+  int64_t history_stride;
+  const int32_t *history_len, *prompt_len;
+  int32_t history_cap, n_bias;
+  const float *repetition, *presence, *frequency;
+  const int32_t *bias_tokens;
+  const float *bias_values;
+  const uint32_t *allowed;
+  int64_t allowed_seq_stride, allowed_row_stride;  // words
+  int32_t chunks;   // token chunks per row (set by the launcher)
+  int32_t in_place; // out is in: only what changes is touched
+  int32_t tree;
+  int16_t parent[kTreeMaxNodes];
+};
+constexpr int kAdjustThreads = 256;
+int adjust_chunks(int dtype, int V);
+void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st);
+
 // Launches the GEMMs of two problems (target rows, draft rows) as one grid.
 void launch_lm_gemm(LmGemmArgs A0, LmGemmArgs A1, hipStream_t st);
 int64_t lm_gemm_blocks(int64_t M, int V);

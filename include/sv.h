@@ -82,6 +82,7 @@ typedef enum { SV_TREE_GREEDY = 0, SV_TREE_STOCHASTIC = 1, SV_TREE_MULTI_CANDIDA
 #define SV_MAX_GAMMA 64
 #define SV_TREE_MAX_NODES 256
 #define SV_LMHEAD_K_STEP 64
+#define SV_ADJUST_MAX_BIAS 65535
 #define SV_LMHEAD_MAX_HIDDEN 65536
 #define SV_TREE_MAX_DEPTH 64
 /* Device scratch of sv_verify_window_noalloc, per GPU (8 MiB). */
@@ -309,6 +310,53 @@ int sv_verify_window_lmhead(const void *hidden_target, const void *unembed_targe
                             int32_t *n_accepted, int32_t *out_tokens,
                             float *p_draft, float *q_draft,
                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Logits adjustment: penalties for repeated tokens, biases and grammar masks
+ * on the rows of a window or tree, before they are verified (or before a draft
+ * is drawn from them).
+ *   logits, out [B][R][V], `dtype`; rows of one sequence contiguous, sequences
+ *               seq_stride / out_seq_stride ELEMENTS apart (0 = dense).  out is
+ *               logits itself (same stride: in place) or does not overlap it.
+ *   tokens      [B] rows of tokens_stride (0 = dense) int32, the drafts.
+ *   parent_host NULL: a window; row i follows tokens[b][0 .. i-1] (R - 1 are
+ *               read), so target rows (R = gamma + 1) and draft rows
+ *               (R = gamma) take the same array.  R <= SV_MAX_GAMMA + 1.
+ *               Else HOST [R], a tree as in sv_verify_tree: row v follows the
+ *               tokens tokens[b][v] of the nodes from the root's child to v
+ *               (entry 0 is ignored).
+ *   row_count   [B] or NULL (= R): rows of each sequence to adjust (clamped to
+ *               [0, R]); the others of `out` are left as they were.
+ *   history     [B] rows of history_stride (0 = history_cap) int32: the tokens
+ *               so far, history_len[b] of them (NULL = history_cap; clamped to
+ *               [0, history_cap]), the first prompt_len[b] the prompt (NULL =
+ *               0).  NULL with history_cap 0: no history.
+ *   repetition, presence, frequency [B] float or NULL (= 1, 0, 0).
+ *   bias_tokens, bias_values [B][n_bias]: added to those tokens' logits.  Of
+ *               several entries that name one token the last counts.
+ *               n_bias <= SV_ADJUST_MAX_BIAS.
+ *   allowed     NULL, or bit masks: token t of row r is allowed when bit
+ *               t % 32 of word allowed[b * allowed_seq_stride +
+ *               r * allowed_row_stride + t / 32] is set (strides in 32-bit
+ *               words; 0 shares a mask between sequences or rows).
+ * With n the occurrences of t in the history after the prompt and on the
+ * row's path, and t seen when it is anywhere in the history or on the path:
+ *   seen:  x = x > 0 ? x / repetition : x * repetition   (repetition > 0)
+ *   n > 0: x = x - frequency * n - presence
+ *   bias;  then x = -inf when t is not allowed
+ * in float32, rounded once to dtype.  Tokens outside [0, V) anywhere are
+ * skipped.  A disallowed logit is -inf whatever it was (NaN included); a row
+ * that allows nothing becomes all -inf (a greedy argmax of 0).  Logits that
+ * nothing applies to keep their bits; in place they are neither read nor
+ * written.  tokens may be NULL when R = 1 or no penalty is given. */
+int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t out_seq_stride, int dtype,
+                     const int32_t *tokens, int64_t tokens_stride, const int32_t *parent_host,
+                     const int32_t *row_count, int32_t B, int32_t R, int32_t V,
+                     const int32_t *history, int64_t history_stride, int32_t history_cap,
+                     const int32_t *history_len, const int32_t *prompt_len,
+                     const float *repetition, const float *presence, const float *frequency,
+                     const int32_t *bias_tokens, const float *bias_values, int32_t n_bias,
+                     const uint32_t *allowed, int64_t allowed_seq_stride, int64_t allowed_row_stride,
+                     hipStream_t stream);
 
 #ifdef __cplusplus
 }

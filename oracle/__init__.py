@@ -42,6 +42,7 @@ from .verify import (
     rollback,
     hierarchy_three_stage,
 )
+from .operators import row_paths, adjust_logits, lmhead_quant, attention
 
 __all__ = [
     "philox4x64_10",
@@ -61,4 +62,8 @@ __all__ = [
     "verify_window_lmhead",
     "rollback",
     "hierarchy_three_stage",
+    "row_paths",
+    "adjust_logits",
+    "lmhead_quant",
+    "attention",
 ]
