@@ -421,6 +421,49 @@ def adjust_logits(logits, *, tokens=None, parent=None, history=None, history_len
     return out
 
 
+def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32, out=None):
+    """Logits from hidden states on 4-bit weights with group scales:
+    sv_lmhead_quant.  hidden (..., K) bf16 or fp16; weights (V, K / 2) uint8,
+    scales (V, K / group) of hidden's dtype, zeros (V, K / group) uint8 or None.
+    Returns (..., V) logits of out_dtype (float32 or hidden's dtype), or fills
+    out."""
+    if hidden.dtype not in (torch.bfloat16, torch.float16) or not hidden.is_cuda or hidden.dim() < 1:
+        raise ValueError("hidden: expected a bf16 or fp16 device tensor")
+    dev, K = hidden.device, hidden.shape[-1]
+    lead = hidden.shape[:-1]
+    if weights.dtype != torch.uint8 or not weights.is_cuda or not weights.is_contiguous() or weights.dim() != 2 \
+            or 2 * weights.shape[1] != K:
+        raise ValueError(f"weights: expected a contiguous uint8 device tensor of shape (V, {K // 2})")
+    V = weights.shape[0]
+    if scales.dtype != hidden.dtype or not scales.is_cuda or not scales.is_contiguous() or scales.dim() != 2 \
+            or scales.shape[0] != V or scales.shape[1] < 1 or K % scales.shape[1]:
+        raise ValueError(f"scales: expected a contiguous {hidden.dtype} device tensor of shape ({V}, {K} / group)")
+    if zeros is not None and (zeros.dtype != torch.uint8 or not zeros.is_cuda or not zeros.is_contiguous()
+                              or zeros.shape != scales.shape):
+        raise ValueError(f"zeros: expected a contiguous uint8 device tensor of shape {tuple(scales.shape)}")
+    if out is None:
+        if out_dtype not in (torch.float32, hidden.dtype):
+            raise ValueError(f"out_dtype: expected float32 or {hidden.dtype}")
+        out = torch.empty(*lead, V, dtype=out_dtype, device=dev)
+    elif out.dtype not in (torch.float32, hidden.dtype) or tuple(out.shape) != (*lead, V) or not out.is_contiguous():
+        raise ValueError(f"out: expected a contiguous float32 or {hidden.dtype} device tensor of shape {(*lead, V)}")
+    _same_device(dev, weights=weights, scales=scales, zeros=zeros, out=out)
+    M = out.numel() // V if V else 0
+    if M == 0:
+        return out
+    try:
+        rows = hidden.view(M, K)
+    except RuntimeError:
+        raise ValueError("hidden: rows must be one stride apart") from None
+    if rows.stride(1) != 1 or (M > 1 and rows.stride(0) < K):
+        raise ValueError("hidden: rows must be contiguous and not overlap")
+    with torch.cuda.device(dev):
+        _check(lib().sv_lmhead_quant(
+            _ptr(rows), rows.stride(0) if M > 1 else 0, _DTYPE_CODE[hidden.dtype], _ptr(weights), _ptr(scales), _ptr(zeros),
+            M, K, V, K // scales.shape[1], _ptr(out), 0, _DTYPE_CODE[out.dtype], _stream(dev)))
+    return out
+
+
 def rollback(buf_tokens, buf_len, stage, verified, verified_len, *, len_offset=0):
     """Per-stage buffer rollback: sv_rollback (in place on buf_tokens/buf_len).
     Row s of `verified` must hold at least verified_len[s] + len_offset tokens

@@ -617,4 +617,40 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
   return launch_status();
 }
 
+int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
+                    const uint8_t *weights, const void *scales, const uint8_t *zeros,
+                    int32_t M, int32_t K, int32_t V, int32_t group,
+                    void *out, int64_t out_row_stride, int out_dtype, hipStream_t stream) {
+  if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
+  if (out_dtype != SV_DT_F32 && out_dtype != dtype) return SV_EDTYPE;
+  if (M < 1 || V < 1 || V > kMaxVocab) return SV_EINVAL;
+  if (group != 32 && group != 64 && group != 128) return SV_EINVAL;
+  if (K < SV_LMHEAD_K_STEP || K > SV_LMHEAD_MAX_HIDDEN || K % SV_LMHEAD_K_STEP != 0 || K % group != 0) return SV_EINVAL;
+  if (!hidden || !weights || !scales || !out) return SV_EINVAL;
+  if (hidden_row_stride == 0) hidden_row_stride = K;
+  if (out_row_stride == 0) out_row_stride = V;
+  if (M > 1 && (hidden_row_stride < K || hidden_row_stride % 8 != 0 || out_row_stride < V)) return SV_EINVAL;
+  if (!aligned(hidden, 16) || !aligned(weights, 16) || !aligned(scales, 2) || !aligned(out, elem_bytes(out_dtype)))
+    return SV_EINVAL;
+  // grid (column tiles, row tiles), both bounded by the smallest tile
+  if (!grid_fits((static_cast<int64_t>(V) + kLmQuantMinCols - 1) / kLmQuantMinCols, kLmQuantThreads) ||
+      (static_cast<int64_t>(M) + kLmQuantMinRows - 1) / kLmQuantMinRows > kMaxGridY)
+    return SV_EINVAL;
+  LmQuantArgs A{};
+  A.h = static_cast<const uint16_t *>(hidden);
+  A.lda = hidden_row_stride;
+  A.w = weights;
+  A.scales = static_cast<const uint16_t *>(scales);
+  A.zeros = zeros;
+  A.M = M;
+  A.V = V;
+  A.K = K;
+  A.group = group;
+  A.out = out;
+  A.out_stride = out_row_stride;
+  A.out_f32 = out_dtype == SV_DT_F32;
+  launch_lm_quant(dtype, A, stream);
+  return launch_status();
+}
+
 }  // extern "C"

@@ -123,6 +123,23 @@ constexpr int kAdjustThreads = 256;
 int adjust_chunks(int dtype, int V);
 void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st);
 
+// LM head on 4-bit weights: rows of h (stride lda elements) against w [V][K / 2]
+// with scales [V][K / group] of h's type and zeros [V][K / group] or null (8).
+struct LmQuantArgs {
+  const uint16_t *h;
+  int64_t lda;
+  const uint8_t *w;
+  const uint16_t *scales;
+  const uint8_t *zeros;
+  int32_t M, V, K, group;
+  void *out;  // [M] rows of out_stride, float32 or h's type
+  int64_t out_stride;
+  int32_t out_f32;
+};
+constexpr int kLmQuantThreads = 256;
+constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 64;  // of a workgroup's tile
+void launch_lm_quant(int dtype, const LmQuantArgs &A, hipStream_t st);
+
 // Launches the GEMMs of two problems (target rows, draft rows) as one grid.
 void launch_lm_gemm(LmGemmArgs A0, LmGemmArgs A1, hipStream_t st);
 int64_t lm_gemm_blocks(int64_t M, int V);

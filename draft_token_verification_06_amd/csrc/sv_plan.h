@@ -73,6 +73,7 @@ constexpr int kLmGemmThreads = 512;
 // count, so a launch of `blocks` workgroups of `threads` along one dimension
 // must stay within it; the entry points reject calls whose grids would not.
 constexpr int64_t kMaxGridItems = 0xFFFFFFFFll;
+constexpr int64_t kMaxGridY = 65535;
 inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks >= 1 && blocks <= kMaxGridItems / threads; }
 
 struct RowPlan {

@@ -358,6 +358,28 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
                      const uint32_t *allowed, int64_t allowed_seq_stride, int64_t allowed_row_stride,
                      hipStream_t stream);
 
+/* LM head on 4-bit weights with group scales: rows of logits for the verify
+ * calls (or for drafting) from hidden states and a quantised unembedding.
+ *   logits[m][v] = sum_k hidden[m][k] * scales[v][k / group]
+ *                                     * (q[v][k] - zeros[v][k / group])
+ *   hidden  [M] rows of hidden_row_stride elements (0 = K), `dtype` SV_DT_BF16
+ *           or SV_DT_F16; 16-byte aligned, the stride a multiple of 8.
+ *   weights [V][K / 2] bytes: q[v][k] in 0..15, even k in the low half of byte
+ *           k / 2; 16-byte aligned.
+ *   scales  [V][K / group], of hidden's type.
+ *   zeros   [V][K / group] bytes, at most 15, or NULL (= 8).
+ *   group   32, 64 or 128; K a multiple of group and of SV_LMHEAD_K_STEP, at
+ *           most SV_LMHEAD_MAX_HIDDEN.
+ *   out     [M] rows of out_row_stride elements (0 = V), SV_DT_F32 or hidden's
+ *           type, not overlapping the inputs.  Dense rows of M = B * (gamma + 1)
+ *           are the target_logits of sv_verify_window.
+ * Weights enter the products exactly; sums are held in float32 and rounded
+ * once.  M <= 1,048,560. */
+int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
+                    const uint8_t *weights, const void *scales, const uint8_t *zeros,
+                    int32_t M, int32_t K, int32_t V, int32_t group,
+                    void *out, int64_t out_row_stride, int out_dtype, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,144 @@
+"""4-bit LM head on the GPU against the float64 definition.
+
+Tolerance, element by element: a logit is a float32 sum of K products and as
+many terms of the groups' correction, in K / G partial sums of G + G terms that
+are scaled and added.  Every term passes through at most n = 2 G + K / G + 4
+roundings of 2^-24 of a partial sum, and the terms' sizes (|h| s (16 + q) and
+|h| s (16 + z), together at most 62 / 24 of the oracle's |h| s (24 + |q - z|))
+bound the partial sums; then half a step of the output type.  Those bounds
+assume that every rounding is at its worst; as independent ones they give
+2^-24 sqrt(n) 30 / 4.6, below 1e-5 of the logits' norm for the sizes here."""
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_06_amd as sv
+import oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+HALF_STEP = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+def make(M, K, V, G, dtype, zeros, seed, strided=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    h = torch.randn(M, K + (24 if strided else 0), generator=g, device=DEV)
+    h[:, K // 3] *= 10
+    h = h.to(DT[dtype])[:, :K]
+    w = torch.randint(0, 256, (V, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = ((0.5 + torch.rand(V, K // G, generator=g, device=DEV)) * 0.02).to(DT[dtype])
+    z = torch.randint(0, 16, (V, K // G), generator=g, device=DEV, dtype=torch.uint8) if zeros else None
+    return h, w, s, z
+
+
+def check(got, h, w, s, z, G):
+    want, size = oracle.lmhead_quant(h.double().cpu().numpy(), w.cpu().numpy(), s.double().cpu().numpy(),
+                                     None if z is None else z.cpu().numpy())
+    g = got.double().cpu().numpy().reshape(want.shape)
+    n = 2 * G + h.shape[-1] // G + 4
+    tol = n * 2.0 ** -24 * (62 / 24) * size + HALF_STEP[got.dtype] * np.abs(want) * (1 + 2.0 ** -7) + 2.0 ** -25
+    err = np.abs(g - want)
+    assert (err <= tol).all(), float((err / tol).max())
+    if got.dtype == torch.float32:
+        assert np.linalg.norm(g - want) <= 1e-5 * np.linalg.norm(want)
+
+
+CASES = [
+    # M, K, V, G, dtype, zeros, out
+    (1, 64, 1, 32, "bf16", False, "f32"),
+    (1, 64, 17, 64, "f16", True, "f32"),
+    (2, 128, 63, 128, "bf16", True, "f32"),
+    (3, 192, 65, 64, "bf16", True, "same"),
+    (16, 320, 257, 32, "f16", True, "f32"),
+    (17, 512, 130, 128, "bf16", False, "same"),
+    (32, 64, 100, 64, "bf16", False, "f32"),
+    (33, 448, 1001, 64, "f16", False, "same"),
+    (64, 2048, 515, 128, "bf16", True, "f32"),
+    (65, 1088, 300, 32, "bf16", True, "f32"),
+    (130, 256, 129, 128, "f16", True, "f32"),
+    (256, 1280, 200, 64, "bf16", False, "f32"),
+    (1, 8192, 999, 128, "bf16", True, "f32"),
+    (5, 4096, 50257, 128, "bf16", True, "f32"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_against_definition(case):
+    print("lmhead_quant", case, flush=True)
+    M, K, V, G, dtype, zeros, out = case
+    h, w, s, z = make(M, K, V, G, dtype, zeros, 3 * M + K)
+    got = sv.lmhead_quant(h, w, s, z, out_dtype=torch.float32 if out == "f32" else DT[dtype])
+    torch.cuda.synchronize()
+    check(got, h, w, s, z, G)
+
+
+def test_strided_rows_and_given_out():
+    """Hidden rows with a stride (the last positions of a longer batch), into a
+    given output that nothing outside the rows changes."""
+    h, w, s, z = make(7, 256, 333, 64, "bf16", True, 5, strided=True)
+    whole = torch.full((9, 333), -5.0, device=DEV)
+    sv.lmhead_quant(h, w, s, z, out=whole[1:8])
+    torch.cuda.synchronize()
+    check(whole[1:8], h, w, s, z, 64)
+    assert (whole[0] == -5).all() and (whole[8] == -5).all()
+    seq = torch.randn(3, 6, 256, device=DEV).to(torch.bfloat16)
+    got = sv.lmhead_quant(seq[:, -1], w, s, z)
+    check(got, seq[:, -1], w, s, z, 64)
+    got = sv.lmhead_quant(seq, w, s, z)
+    assert got.shape == (3, 6, 333)
+    check(got, seq.reshape(18, 256), w, s, z, 64)
+    assert sv.lmhead_quant(seq[:0], w, s, z).shape == (0, 6, 333)
+
+
+def test_rows_do_not_depend_on_the_batch():
+    """Each row's logits are the same bits alone and in any batch of the same
+    tile height (the sums run in a fixed order)."""
+    h, w, s, z = make(16, 512, 700, 32, "bf16", True, 9)
+    whole = sv.lmhead_quant(h, w, s, z)
+    for m in (0, 7, 15):
+        assert torch.equal(sv.lmhead_quant(h[m:m + 1], w, s, z)[0], whole[m])
+    assert torch.equal(whole, sv.lmhead_quant(h, w, s, z))
+
+
+def test_large_means_and_infinite_scales():
+    """Hidden values far from zero mean (the correction cancels most of the
+    sum), and an infinite scale that stays in its own column."""
+    h, w, s, z = make(4, 1024, 96, 128, "bf16", True, 2)
+    h = (h.float() + 100).to(torch.bfloat16)
+    got = sv.lmhead_quant(h, w, s, z)
+    want, size = oracle.lmhead_quant(h.double().cpu().numpy(), w.cpu().numpy(), s.double().cpu().numpy(), z.cpu().numpy())
+    tol = (2 * 128 + 12) * 2.0 ** -24 * (62 / 24) * size
+    assert (np.abs(got.double().cpu().numpy() - want) <= tol).all()
+    s = s.clone()
+    s[5, 3] = float("inf")
+    again = sv.lmhead_quant(h, w, s, z)
+    keep = [v for v in range(96) if v != 5]
+    assert torch.equal(again[:, keep], got[:, keep]) and not torch.isfinite(again[:, 5]).any()
+
+
+def test_window_from_quantised_hidden_states():
+    """The logits feed sv_verify_window: (B, gamma + 1, V) in one call."""
+    B, g, V = 3, 4, 5000
+    h, w, s, z = make(B * (g + 1), 256, V, 64, "bf16", True, 4)
+    t = sv.lmhead_quant(h.view(B, g + 1, 256), w, s, z)
+    toks = t[:, :g].argmax(-1).to(torch.int32).contiguous()
+    r = sv.verify_greedy(t, toks)
+    assert r.n_accepted.tolist() == [g] * B
+    assert torch.equal(r.out_tokens[:, g], t[:, g].argmax(-1).to(torch.int32))
+
+
+def test_binding_refuses_on_device():
+    h, w, s, z = make(4, 256, 40, 64, "bf16", True, 1)
+    bad = [(h.float(), w, s, z), (h, w.int(), s, z), (h, w[:, :64], s, z), (h, w, s.half(), z), (h, w, s[:30], z),
+           (h, w, s, z.int()), (h, w, s, z[:, :2]), (h[:, ::2], w[:, :64].contiguous(), s, z), (h[:1].expand(4, 256), w, s, z),
+           (h, w.cpu(), s, z), (h, w, s[:, :3].contiguous(), None)]
+    for a in bad:
+        with pytest.raises(ValueError):
+            sv.lmhead_quant(*a)
+    with pytest.raises(ValueError):
+        sv.lmhead_quant(h, w, s, z, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        sv.lmhead_quant(h, w, s, z, out=torch.empty(4, 41, device=DEV))
+    with pytest.raises(sv.SvError):
+        sv.lmhead_quant(h, w, s[:, :1].contiguous(), None)   # group 256
