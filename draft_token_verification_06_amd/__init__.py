@@ -19,6 +19,9 @@ from .api import (  # noqa: F401
     tree_max_depth,
     rollback,
     adjust_logits,
+    attention,
+    attention_workspace,
+    AttentionResult,
     lmhead_quant,
     probe_read,
     SV_OP_WINDOW,
@@ -30,5 +33,5 @@ from .api import (  # noqa: F401
 __all__ = [
     "SvError", "WindowResult", "TreeResult", "workspace_size", "workspace",
     "verify_window", "verify_window_noalloc", "verify_window_lmhead", "verify_greedy", "verify_tree", "tree_max_depth", "rollback",
-    "adjust_logits", "lmhead_quant", "probe_read",
+    "adjust_logits", "attention", "attention_workspace", "AttentionResult", "lmhead_quant", "probe_read",
 ]

@@ -464,6 +464,105 @@ def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32
     return out
 
 
+@dataclass
+class AttentionResult:
+    out: torch.Tensor
+    lse: Optional[torch.Tensor] = None
+
+
+def attention_workspace(B, R, Hq, Hkv, D, P, max_ctx, device):
+    """A workspace for attention calls of these sizes."""
+    nbytes = int(lib().sv_attention_workspace(B, R, Hq, Hkv, D, P, max_ctx))
+    if nbytes == 0:
+        raise ValueError("invalid sizes for an attention workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _heads(t, dtype, shape, name):
+    """Token stride of (..., tokens, H, D) keys, values or queries with dense heads."""
+    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected a {dtype} device tensor of shape {shape}")
+    H, D = shape[-2:]
+    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(-3) if shape[-3] > 1 else 0
+
+
+def attention(q, k_cache, v_cache, ctx_len, *, prefix_k=None, prefix_v=None, parent=None, row_count=None,
+              scale=None, max_ctx=None, return_lse=False, out=None, ws=None):
+    """Attention of a window's or tree's rows over a shared prefix, the cached
+    context and the rows' ancestors: sv_attention.
+
+    q (B, R, Hq, D); k_cache, v_cache (B, cap, Hkv, D) with ctx_len[b]
+    committed tokens followed by the step's R rows; prefix_k, prefix_v (P, Hkv,
+    D) or None.  parent (a host sequence) makes the rows a tree.  scale defaults
+    to D ** -0.5, max_ctx (an upper bound of ctx_len) to cap - R.  out: an
+    AttentionResult to fill."""
+    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q: expected a bf16 or fp16 device tensor of shape (B, R, Hq, D)")
+    B, R, Hq, D = q.shape
+    dev = q.device
+    q_stride = _heads(q, q.dtype, (B, R, Hq, D), "q")
+    if R == 1:
+        q_stride = q.stride(0) if B > 1 else 0
+    elif B > 1 and q.stride(0) != R * q_stride:
+        raise ValueError("q: rows must be one stride apart")
+    if k_cache.dim() != 4 or k_cache.shape[0] != B or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache: expected shape ({B}, cap, Hkv, {D}), got {tuple(k_cache.shape)}")
+    cap, Hkv = k_cache.shape[1], k_cache.shape[2]
+    tok_stride = _heads(k_cache, q.dtype, (B, cap, Hkv, D), "k_cache")
+    _heads(v_cache, q.dtype, (B, cap, Hkv, D), "v_cache")
+    if v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same strides")
+    seq_stride = k_cache.stride(0) if B > 1 else 0
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError("the query heads must be a multiple of the kv heads")
+    if (B > 1 and seq_stride == 0) or (cap > 1 and tok_stride < Hkv * D) or ((B > 1 or R > 1) and q_stride < Hq * D):
+        raise ValueError("tokens, rows or sequences overlap")
+    P = prefix_stride = 0
+    if (prefix_k is None) != (prefix_v is None):
+        raise ValueError("prefix_k and prefix_v go together")
+    if prefix_k is not None:
+        P = prefix_k.shape[0]
+        prefix_stride = _heads(prefix_k, q.dtype, (P, Hkv, D), "prefix_k")
+        _heads(prefix_v, q.dtype, (P, Hkv, D), "prefix_v")
+        if prefix_k.stride() != prefix_v.stride() or (P > 1 and prefix_stride < Hkv * D):
+            raise ValueError("prefix_k and prefix_v must have the same strides, tokens not overlapping")
+    _optional(ctx_len, torch.int32, B, "ctx_len")
+    _optional(row_count, torch.int32, B, "row_count")
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, prefix_k=prefix_k, prefix_v=prefix_v, ctx_len=ctx_len,
+                 row_count=row_count)
+    par = None
+    if parent is not None:
+        if len(parent) != R:
+            raise ValueError("parent must have one entry per row")
+        par = (ctypes.c_int32 * R)(*parent)
+    if max_ctx is None:
+        max_ctx = cap - R
+    if scale is None:
+        scale = D ** -0.5
+    if ws is None:
+        ws = attention_workspace(B, R, Hq, Hkv, D, P, max_ctx, dev)
+        ws_bytes = ws.numel()
+    else:
+        ws_bytes = _ws_bytes(ws, dev)
+    if out is None:
+        out = AttentionResult(torch.empty(B, R, Hq, D, dtype=q.dtype, device=dev),
+                              torch.empty(B, R, Hq, dtype=torch.float32, device=dev) if return_lse else None)
+    else:
+        if out.out is None:
+            raise ValueError("out is a required output")
+        _out_tensor(out.out, q.dtype, (B, R, Hq, D), dev, "out")
+        _out_tensor(out.lse, torch.float32, (B, R, Hq), dev, "lse")
+    with torch.cuda.device(dev):
+        _check(lib().sv_attention(
+            _ptr(q), q_stride, _DTYPE_CODE[q.dtype], _ptr(k_cache), _ptr(v_cache), seq_stride, tok_stride, cap,
+            _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None, prefix_stride, P,
+            _ptr(ctx_len), _ptr(row_count), par, B, R, Hq, Hkv, D, max_ctx, scale,
+            _ptr(out.out), _ptr(out.lse), _ptr(ws), ws_bytes, _stream(dev)))
+    return out
+
+
 def rollback(buf_tokens, buf_len, stage, verified, verified_len, *, len_offset=0):
     """Per-stage buffer rollback: sv_rollback (in place on buf_tokens/buf_len).
     Row s of `verified` must hold at least verified_len[s] + len_offset tokens

@@ -654,3 +654,93 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
 }
 
 }  // extern "C"
+
+namespace {
+
+bool attention_sizes_ok(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
+  if (B < 1 || R < 1 || R > SV_TREE_MAX_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > SV_ATTENTION_MAX_HEADS) return false;
+  if (D != 64 && D != 128) return false;
+  if (P < 0 || P > SV_ATTENTION_MAX_KEYS || max_ctx < 0 || max_ctx > SV_ATTENTION_MAX_KEYS) return false;
+  if (static_cast<int64_t>(B) * R > (int64_t{1} << 30) / Hq) return false;
+  const AttendPlan L = plan_attention(B, R, Hq, Hkv, D, P, max_ctx);
+  return grid_fits(L.prefix_items + L.own_blocks, kAttendThreads) &&
+         grid_fits((static_cast<int64_t>(B) * R * Hq + 3) / 4, 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sv_attention_workspace(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
+  if (!attention_sizes_ok(B, R, Hq, Hkv, D, P, max_ctx)) return 0;
+  return plan_attention(B, R, Hq, Hkv, D, P, max_ctx).total;
+}
+
+int sv_attention(const void *q, int64_t q_row_stride, int dtype,
+                 const void *k_cache, const void *v_cache, int64_t cache_seq_stride, int64_t cache_tok_stride, int32_t cap,
+                 const void *prefix_k, const void *prefix_v, int64_t prefix_tok_stride, int32_t P,
+                 const int32_t *ctx_len, const int32_t *row_count, const int32_t *parent_host,
+                 int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_ctx, float scale,
+                 void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
+  if (!attention_sizes_ok(B, R, Hq, Hkv, D, P, max_ctx)) return SV_EINVAL;
+  AttendArgs A{};
+  if (parent_host) {
+    TreeMeta meta;
+    const int tst = build_tree(parent_host, R, &meta);
+    if (tst != SV_OK) return tst;
+    std::memcpy(A.parent, meta.parent, sizeof(A.parent));
+    A.tree = 1;
+  } else if (R > SV_MAX_GAMMA + 1) {
+    return SV_EINVAL;
+  }
+  if (!q || !k_cache || !v_cache || !ctx_len || !out || (P > 0 && (!prefix_k || !prefix_v))) return SV_EINVAL;
+  if (cap < 1 || static_cast<int64_t>(max_ctx) + R > cap) return SV_EINVAL;
+  if (!(scale == scale) || scale - scale != 0.0f) return SV_EINVAL;
+  const int64_t q_elems = static_cast<int64_t>(Hq) * D, kv_elems = static_cast<int64_t>(Hkv) * D;
+  if (q_row_stride == 0) q_row_stride = q_elems;
+  if (cache_tok_stride == 0) cache_tok_stride = kv_elems;
+  if (cache_seq_stride == 0) cache_seq_stride = cache_tok_stride * cap;
+  if (prefix_tok_stride == 0) prefix_tok_stride = kv_elems;
+  if (q_row_stride < q_elems || cache_tok_stride < kv_elems || cache_seq_stride < 0 || prefix_tok_stride < kv_elems) return SV_EINVAL;
+  if (q_row_stride % 8 || cache_tok_stride % 8 || cache_seq_stride % 8 || prefix_tok_stride % 8) return SV_EINVAL;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
+    return SV_EINVAL;
+  if (P > 0 && (!aligned(prefix_k, 16) || !aligned(prefix_v, 16))) return SV_EINVAL;
+  const AttendPlan L = plan_attention(B, R, Hq, Hkv, D, P, max_ctx);
+  const int ws = check_workspace(workspace, workspace_bytes, L.total);
+  if (ws != SV_OK) return ws;
+  A.q = static_cast<const uint16_t *>(q);
+  A.q_row_stride = q_row_stride;
+  A.k = static_cast<const uint16_t *>(k_cache);
+  A.v = static_cast<const uint16_t *>(v_cache);
+  A.seq_stride = cache_seq_stride;
+  A.tok_stride = cache_tok_stride;
+  A.prefix_k = static_cast<const uint16_t *>(prefix_k);
+  A.prefix_v = static_cast<const uint16_t *>(prefix_v);
+  A.prefix_tok_stride = prefix_tok_stride;
+  A.ctx_len = ctx_len;
+  A.row_count = row_count;
+  A.B = B;
+  A.R = R;
+  A.Hq = Hq;
+  A.Hkv = Hkv;
+  A.n = Hq / Hkv;
+  A.P = P;
+  A.max_ctx = max_ctx;
+  A.prefix_parts = L.prefix_parts;
+  A.prefix_chunk = L.prefix_chunk;
+  A.prefix_items = static_cast<int32_t>(L.prefix_items);
+  A.own_parts = L.own_parts;
+  A.own_chunk = L.own_chunk;
+  A.own_tiles = L.own_tiles;
+  A.scale_log2 = scale * 1.4426950408889634f;
+  A.part_o = static_cast<float *>(workspace);
+  A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + L.ml_off);
+  A.out = static_cast<uint16_t *>(out);
+  A.lse = lse;
+  launch_attend(dtype, D, A, L, stream);
+  return launch_status();
+}
+
+}  // extern "C"

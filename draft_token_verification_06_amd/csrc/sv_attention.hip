@@ -1,0 +1,448 @@
+// Attention of a step's rows (gfx950): the rows of a window or tree over the
+// batch's shared prefix, their sequence's cached context and their own
+// ancestors.
+//
+// The keys of a row are split among work items: the prefix into ranges that
+// all rows of a kv head share (so its keys and values are read once per tile
+// of rows of the whole batch, not once per sequence), and each sequence's
+// cache, the step's own keys at its end, into ranges of chunk_own keys.  An
+// item runs one pass over its range with a running maximum and sum and leaves
+// an unnormalised float32 output with (maximum, sum); k_attend_combine joins
+// the items of a row in a fixed order.
+//
+// Matrix layout (v_mfma_f32_32x32x16): scores are formed transposed, S^T = K
+// Q^T, so that a lane holds 16 keys of one row (column l % 32; keys 8 (r / 4) +
+// 4 (l / 32) + r % 4): maxima and sums stay in the lane up to one exchange with
+// lane l ^ 32, and the exponentials are already the operand of O^T = V^T P^T,
+// whose k order may be any as long as both operands share it.  V^T is read
+// from row-major LDS by the transposing LDS read (each 16 lanes take a 4 x 16
+// block and get its columns).
+//
+// Rows of a group of query heads that share a kv head are stacked into one
+// tile.  A workgroup's four waves split the tile's rows (WQ = 4: 128 rows, for
+// the prefix of a batch) or the keys of a tile (WQ = 1: 32 rows, for the few
+// rows of one sequence, where cache bandwidth is the bound).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sv_device.h"
+#include "sv_launch.h"
+#include "sv_plan.h"
+
+namespace sv {
+
+typedef __bf16 at_bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 at_f16x8_t __attribute__((ext_vector_type(8)));
+typedef float at_f32x16_t __attribute__((ext_vector_type(16)));
+typedef short at_i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) at_i16x4_t *lds_i16x4_t;
+
+constexpr int kAtThreads = kAttendThreads;
+
+template <int DT> struct AtElt;
+template <> struct AtElt<DT_BF16> {
+  static constexpr uint32_t kExp = 0x7F80u;  // exponent of infinities and NaN
+  __device__ static __forceinline__ at_f32x16_t mma(uint4 a, uint4 b, at_f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8_t, a), __builtin_bit_cast(at_bf16x8_t, b), c, 0, 0, 0);
+  }
+  // Two exponentials in [0, 1] to the storage type, rounded to nearest.
+  __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, v2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+  }
+  __device__ static __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
+};
+template <> struct AtElt<DT_F16> {
+  static constexpr uint32_t kExp = 0x7C00u;
+  __device__ static __forceinline__ at_f32x16_t mma(uint4 a, uint4 b, at_f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(at_f16x8_t, a), __builtin_bit_cast(at_f16x8_t, b), c, 0, 0, 0);
+  }
+  __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
+    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, v2{static_cast<_Float16>(lo), static_cast<_Float16>(hi)});
+  }
+  __device__ static __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x)); }
+};
+
+// What one work item computes: rows [row0, row0 + rows) of a stack of rows
+// (stack row i is query row base_row + i / n, head kvh n + i % n) over keys
+// [k0, k1) at k / v; keys from `draft` on are the step's own and follow the
+// ancestor sets (s_anc), the others are seen by every row.
+struct Item {
+  const uint16_t *k, *v;
+  int64_t tok_stride;
+  int64_t base_row;  // query row (b * R + r) of stack row 0
+  int row0, rows;
+  int kvh;
+  int k0, k1, draft;
+  int part;
+};
+
+__device__ __forceinline__ float swap_half(float x) { return __shfl_xor(x, 32); }
+
+template <int D> constexpr int at_lds_row() { return D + 8; }  // elements; 16 bytes of padding spread the banks
+template <int D, int WQ> constexpr int at_tile_keys() { return WQ == 1 ? 128 : 64; }
+template <int D, int WQ> constexpr size_t at_tile_bytes() {
+  const size_t kv = 2 * static_cast<size_t>(at_tile_keys<D, WQ>()) * at_lds_row<D>() * 2;
+  const size_t merge = WQ == 1 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
+  return kv > merge ? kv : merge;
+}
+
+template <int DT, int D, int WQ>
+__device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it, char *lds, const uint32_t (*s_anc)[8],
+                                            float2 (*s_ml)[32]) {
+  using T = AtElt<DT>;
+  constexpr int WK = 4 / WQ;
+  constexpr int KT = at_tile_keys<D, WQ>();
+  constexpr int SB = KT / (32 * WK);      // 32-key blocks per wave and tile
+  constexpr int kRow = at_lds_row<D>();
+  constexpr int kChunks = D / 8;          // 16-byte pieces per row
+  constexpr int kLoads = KT * kChunks / kAtThreads;
+  uint16_t *s_k = reinterpret_cast<uint16_t *>(lds);
+  uint16_t *s_v = s_k + KT * kRow;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wq = wave % WQ, wk = wave / WQ;
+  const int q32 = lane & 31, half = lane >> 5;
+
+  // this lane's row, its query fragments: d = 16 s + 8 half ..
+  const int i = it.row0 + wq * 32 + q32;
+  const int ic = min(i, it.rows - 1);
+  const int64_t qrow = it.base_row + ic / A.n;
+  const int head = it.kvh * A.n + ic % A.n;
+  uint4 qf[D / 16];
+  {
+    const uint16_t *p = A.q + qrow * A.q_row_stride + head * D + half * 8;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) qf[s] = load_vec(p + s * 16);
+  }
+  const int r = static_cast<int>(qrow % A.R);
+
+  at_f32x16_t o[D / 32];
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[t][e] = 0.0f;
+  float m = kNegInf, l = 0.0f;  // l: this half's keys only
+
+  uint4 rk[kLoads], rv[kLoads];
+  const int piece = tid % kChunks, first = tid / kChunks;
+  constexpr int kRowsPerPass = kAtThreads / kChunks;
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int64_t key = min(t0 + first + j * kRowsPerPass, it.k1 - 1);
+      rk[j] = load_vec(it.k + key * it.tok_stride + piece * 8);
+      rv[j] = load_vec(it.v + key * it.tok_stride + piece * 8);
+    }
+  };
+  load(it.k0);
+  for (int t0 = it.k0; t0 < it.k1; t0 += KT) {
+    // Keys past the range get zero values: their exponentials are zero, but
+    // zero times what a cache holds behind its end need not be.
+    bool odd = false;  // a value of the step's own keys is infinite or NaN
+    const bool masked = t0 + KT > it.draft;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int row = first + j * kRowsPerPass;
+      uint4 v = rv[j];
+      if (t0 + row >= it.k1) v = make_uint4(0, 0, 0, 0);
+      if (masked) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          odd |= (w[k] & T::kExp) == T::kExp || ((w[k] >> 16) & T::kExp) == T::kExp;
+      }
+      *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 8) = rk[j];
+      *reinterpret_cast<uint4 *>(s_v + row * kRow + piece * 8) = v;
+    }
+    bool slow = false;
+    if (masked) slow = __syncthreads_or(odd);
+    else __syncthreads();
+    if (t0 + KT < it.k1) load(t0 + KT);
+#pragma unroll
+    for (int sb = 0; sb < SB; ++sb) {
+      const int kb = (wk * SB + sb) * 32;  // this block's first key in the tile
+      if (t0 + kb >= it.k1) continue;
+      at_f32x16_t s;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+        s = T::mma(*reinterpret_cast<const uint4 *>(s_k + (kb + q32) * kRow + d * 16 + half * 8), qf[d], s);
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = s[e] * A.scale_log2;
+      if (t0 + kb + 32 > it.draft || t0 + kb + 32 > it.k1) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = t0 + kb + 8 * (e >> 2) + 4 * half + (e & 3);
+          const int own = key - it.draft;
+          const bool ok = key < it.k1 && (own < 0 || ((s_anc[r][(own & 255) >> 5] >> (own & 31)) & 1));
+          x[e] = ok ? x[e] : kNegInf;
+        }
+      }
+      float top = x[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+      top = fmaxf(top, swap_half(top));
+      const float mn = fmaxf(m, top);
+      const float mu = mn == kNegInf ? 0.0f : mn;
+      const float alpha = exp2_fast(m - mu);
+      m = mn;
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = exp2_fast(x[e] - mu);
+        sum += x[e];
+      }
+      l = l * alpha + sum;
+#pragma unroll
+      for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[t][e] *= alpha;
+      if (!slow) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const uint4 p = make_uint4(T::pack(x[8 * ks], x[8 * ks + 1]), T::pack(x[8 * ks + 2], x[8 * ks + 3]),
+                                     T::pack(x[8 * ks + 4], x[8 * ks + 5]), T::pack(x[8 * ks + 6], x[8 * ks + 7]));
+          // lane l: block of 4 keys x 16 values; its address is row (l % 16) / 4, values 4 (l % 4)
+          const uint16_t *base = s_v + (kb + ks * 16 + 4 * half + ((lane & 15) >> 2)) * kRow + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+#pragma unroll
+          for (int t = 0; t < D / 32; ++t) {
+            const at_i16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32));
+            const at_i16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32 + 8 * kRow));
+            const uint2 u0 = __builtin_bit_cast(uint2, a0), u1 = __builtin_bit_cast(uint2, a1);
+            o[t] = T::mma(make_uint4(u0.x, u0.y, u1.x, u1.y), p, o[t]);
+          }
+        }
+      } else {
+        // Some own key holds an infinity or NaN, which must reach only the
+        // rows that see it: one key at a time, skipping zero exponentials.
+        for (int e = 0; e < 16; ++e) {
+          const float mine = x[0], other = swap_half(mine);
+#pragma unroll
+          for (int z = 0; z < 15; ++z) x[z] = x[z + 1];
+          for (int hh = 0; hh < 2; ++hh) {
+            const float p = hh == half ? mine : other;
+            const uint16_t *vrow = s_v + (kb + 8 * (e >> 2) + 4 * hh + (e & 3)) * kRow + 4 * half;
+            if (p != 0.0f) {
+#pragma unroll
+              for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int f = 0; f < 16; ++f)
+                  o[t][f] += p * Elt<DT>::dec(vrow[t * 32 + 8 * (f >> 2) + (f & 3)]);
+            }
+          }
+        }
+      }
+    }
+  }
+  l += swap_half(l);
+
+  const int64_t rows_all = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  if (WQ == 4) {
+    if (i < it.rows) {
+      const int64_t at = it.part * rows_all + qrow * A.Hq + head;
+      float *po = A.part_o + at * D;
+#pragma unroll
+      for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          *reinterpret_cast<float4 *>(po + t * 32 + 8 * f + 4 * half) =
+              make_float4(o[t][4 * f], o[t][4 * f + 1], o[t][4 * f + 2], o[t][4 * f + 3]);
+      if (half == 0) A.part_ml[at] = make_float2(m, l);
+    }
+    return;
+  }
+  // The waves hold the same rows over different keys: joined in wave order.
+  float *s_o = reinterpret_cast<float *>(lds);
+  if (half == 0) s_ml[wave][q32] = make_float2(m, l);
+  __syncthreads();  // also: every wave is done with the tiles
+  float M = kNegInf;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][q32].x);
+  const float f = m == kNegInf ? 0.0f : exp2_fast(m - M);
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<float4 *>(s_o + (wave * 32 + q32) * (D + 4) + t * 32 + 8 * g + 4 * half) =
+          make_float4(o[t][4 * g] * f, o[t][4 * g + 1] * f, o[t][4 * g + 2] * f, o[t][4 * g + 3] * f);
+  __syncthreads();
+  for (int z = tid; z < 32 * (D / 4); z += kAtThreads) {
+    const int q = z / (D / 4), c = z % (D / 4);
+    const int qi = it.row0 + q;
+    if (qi >= it.rows) continue;
+    float4 a = *reinterpret_cast<const float4 *>(s_o + q * (D + 4) + c * 4);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      const float4 b = *reinterpret_cast<const float4 *>(s_o + (w * 32 + q) * (D + 4) + c * 4);
+      a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    }
+    const int64_t at = it.part * rows_all + (it.base_row + qi / A.n) * A.Hq + it.kvh * A.n + qi % A.n;
+    *reinterpret_cast<float4 *>(A.part_o + at * D + c * 4) = a;
+    if (c == 0) {
+      float Mq = kNegInf, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) Mq = fmaxf(Mq, s_ml[w][q].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (s_ml[w][q].x != kNegInf) L += s_ml[w][q].y * exp2_fast(s_ml[w][q].x - Mq);
+      A.part_ml[at] = make_float2(Mq, L);
+    }
+  }
+}
+
+__device__ __forceinline__ bool bad_len(const AttendArgs &A, int len) { return len < 0 || len > A.max_ctx; }
+__device__ __forceinline__ int live_rows(const AttendArgs &A, int b) {
+  return A.row_count ? min(max(A.row_count[b], 0), A.R) : A.R;
+}
+
+template <int DT, int D, int WQP, int WQO>
+__global__ void __launch_bounds__(kAtThreads) k_attend(AttendArgs A) {
+  constexpr size_t kBytes = at_tile_bytes<D, WQP>() > at_tile_bytes<D, WQO>() ? at_tile_bytes<D, WQP>() : at_tile_bytes<D, WQO>();
+  __shared__ uint4 s_tile[kBytes / sizeof(uint4)];
+  __shared__ uint32_t s_anc[kTreeMaxNodes][8];
+  __shared__ float2 s_ml[4][32];
+  char *lds = reinterpret_cast<char *>(s_tile);
+  Item it{};
+  int id = blockIdx.x;
+  if (id < A.prefix_items) {
+    // row tiles of one (kv head, range) are Hkv * parts apart: a multiple of 8
+    // of those keeps them on one XCD
+    const int pairs = A.Hkv * A.prefix_parts;
+    const int pair = id % pairs;
+    it.kvh = pair % A.Hkv;
+    it.part = pair / A.Hkv;
+    it.row0 = id / pairs * (32 * WQP);
+    it.rows = A.B * A.R * A.n;
+    it.base_row = 0;
+    it.k = A.prefix_k + it.kvh * D;
+    it.v = A.prefix_v + it.kvh * D;
+    it.tok_stride = A.prefix_tok_stride;
+    it.k0 = it.part * A.prefix_chunk;
+    it.k1 = min(it.k0 + A.prefix_chunk, A.P);
+    it.draft = it.k1 + (1 << 30);
+    if (A.P - it.k0 <= 0) return;
+    attend_item<DT, D, WQP>(A, it, lds, s_anc, s_ml);
+    return;
+  }
+  id -= A.prefix_items;
+  // row tiles of the same keys are 8 blocks apart (one XCD), then the next keys
+  const int tiles = A.own_tiles;
+  const int octet = id / (8 * tiles), within = id % (8 * tiles);
+  int key_item = octet * 8 + within % 8;
+  const int tile = within / 8;
+  if (key_item >= A.B * A.Hkv * A.own_parts) return;
+  it.kvh = key_item % A.Hkv;
+  key_item /= A.Hkv;
+  const int split = key_item % A.own_parts;
+  const int b = key_item / A.own_parts;
+  const int len = A.ctx_len[b];
+  const int live = live_rows(A, b);
+  if (bad_len(A, len) || live == 0) return;
+  it.k0 = split * A.own_chunk;
+  it.k1 = min(it.k0 + A.own_chunk, len + live);
+  it.draft = len;
+  it.row0 = tile * (32 * WQO);
+  it.rows = live * A.n;
+  if (it.k0 >= it.k1 || it.row0 >= it.rows) return;
+  it.part = A.prefix_parts + split;
+  it.base_row = static_cast<int64_t>(b) * A.R;
+  it.k = A.k + b * A.seq_stride + it.kvh * D;
+  it.v = A.v + b * A.seq_stride + it.kvh * D;
+  it.tok_stride = A.tok_stride;
+  if (it.k1 > len) {
+    // ancestor sets of the rows, one row per thread
+    for (int v = threadIdx.x; v < A.R; v += kAtThreads) {
+      uint32_t w[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) w[x] = 0;
+      if (A.tree) {
+        for (int u = v; u >= 0; u = A.parent[u])
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] |= x == (u >> 5) ? 1u << (u & 31) : 0u;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int n = v + 1 - 32 * x;
+          w[x] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s_anc[v][x] = w[x];
+    }
+  }
+  // (the first barrier of the pass orders these writes)
+  attend_item<DT, D, WQO>(A, it, lds, s_anc, s_ml);
+}
+
+// One wave per (row, head): the row's items in order, weighted by their
+// maxima; a sequence whose length is out of range gets NaN.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) k_attend_combine(AttendArgs A) {
+  constexpr int E = D / 64;
+  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= rows) return;
+  const int64_t br = row / A.Hq;
+  const int b = static_cast<int>(br / A.R), r = static_cast<int>(br % A.R);
+  const int live = live_rows(A, b);
+  if (r >= live) return;
+  const int len = A.ctx_len[b];
+  float acc[E] = {};
+  float M = kNegInf, L = 0.0f;
+  if (bad_len(A, len)) {
+    M = L = __builtin_nanf("");
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = L;
+  } else {
+    const int parts = A.prefix_parts + (len + live + A.own_chunk - 1) / A.own_chunk;
+    for (int p = 0; p < parts; ++p) M = fmaxf(M, A.part_ml[p * rows + row].x);
+    for (int p = 0; p < parts; ++p) {
+      const float2 ml = A.part_ml[p * rows + row];
+      const float f = ml.x == kNegInf ? 0.0f : exp2_fast(ml.x - M);
+      L += f * ml.y;
+      const float *po = A.part_o + (p * rows + row) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += f * po[e];
+    }
+  }
+  uint16_t *out = A.out + row * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = AtElt<DT>::bits(acc[e] / L);
+  if (A.lse && lane == 0) A.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+}
+
+namespace {
+
+template <int DT, int D>
+void launch_type(const AttendArgs &A, const AttendPlan &P, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks));
+  if (P.prefix_wide && P.own_wide)
+    hipLaunchKernelGGL((k_attend<DT, D, 4, 4>), grid, dim3(kAtThreads), 0, st, A);
+  else if (P.prefix_wide)
+    hipLaunchKernelGGL((k_attend<DT, D, 4, 1>), grid, dim3(kAtThreads), 0, st, A);
+  else if (P.own_wide)
+    hipLaunchKernelGGL((k_attend<DT, D, 1, 4>), grid, dim3(kAtThreads), 0, st, A);
+  else
+    hipLaunchKernelGGL((k_attend<DT, D, 1, 1>), grid, dim3(kAtThreads), 0, st, A);
+  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  hipLaunchKernelGGL((k_attend_combine<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, A);
+}
+
+}  // namespace
+
+void launch_attend(int dtype, int D, const AttendArgs &A, const AttendPlan &P, hipStream_t st) {
+  if (dtype == DT_BF16) {
+    if (D == 64) launch_type<DT_BF16, 64>(A, P, st);
+    else launch_type<DT_BF16, 128>(A, P, st);
+  } else {
+    if (D == 64) launch_type<DT_F16, 64>(A, P, st);
+    else launch_type<DT_F16, 128>(A, P, st);
+  }
+}
+
+}  // namespace sv

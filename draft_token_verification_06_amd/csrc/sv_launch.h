@@ -140,6 +140,29 @@ constexpr int kLmQuantThreads = 256;
 constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 64;  // of a workgroup's tile
 void launch_lm_quant(int dtype, const LmQuantArgs &A, hipStream_t st);
 
+// Attention of a step's rows.  Strides in elements; heads are D apart.
+struct AttendArgs {
+  const uint16_t *q;
+  int64_t q_row_stride;
+  const uint16_t *k, *v;  // [B] caches of cap tokens
+  int64_t seq_stride, tok_stride;
+  const uint16_t *prefix_k, *prefix_v;
+  int64_t prefix_tok_stride;
+  const int32_t *ctx_len, *row_count;
+  int32_t B, R, Hq, Hkv, n;  // n = Hq / Hkv
+  int32_t P, max_ctx;
+  int32_t prefix_parts, prefix_chunk, prefix_items;
+  int32_t own_parts, own_chunk, own_tiles;
+  float scale_log2;  // score scale times log2(e)
+  float *part_o;     // [parts][B R Hq][D] unnormalised outputs
+  float2 *part_ml;   // [parts][B R Hq] (maximum, sum)
+  uint16_t *out;     // [B][R][Hq][D]
+  float *lse;        // [B][R][Hq] or null
+  int32_t tree;
+  int16_t parent[kTreeMaxNodes];
+};
+void launch_attend(int dtype, int D, const AttendArgs &A, const AttendPlan &P, hipStream_t st);
+
 // Launches the GEMMs of two problems (target rows, draft rows) as one grid.
 void launch_lm_gemm(LmGemmArgs A0, LmGemmArgs A1, hipStream_t st);
 int64_t lm_gemm_blocks(int64_t M, int V);

@@ -161,4 +161,50 @@ inline LmLayout make_lm_layout(int64_t B, int32_t gamma, int32_t V) {
   return L;
 }
 
+// Work items of an attention call.  Stacked rows (query rows times the heads of
+// a group) come in tiles of 32 (four waves share the keys) or 128 (four waves
+// share the rows); keys are split into ranges until the items fill the chip.
+constexpr int kAttendThreads = 256;
+constexpr int kAttendWideRows = 64;        // more stacked rows than this: tiles of 128
+constexpr int64_t kAttendItems = 1024;     // items wanted per launch (2 workgroups on each of 256 CUs, twice)
+constexpr int kAttendMinKeys = 256;        // keys per range at least
+struct AttendPlan {
+  int prefix_wide, own_wide;
+  int prefix_parts, prefix_chunk, own_parts, own_chunk, own_tiles;
+  int64_t prefix_items, own_blocks;
+  size_t ml_off, total;
+};
+
+inline void split_keys(int64_t keys, int64_t items_per_range, int *parts, int *chunk) {
+  int64_t want = (kAttendItems + items_per_range - 1) / items_per_range;
+  const int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys;
+  if (want > most) want = most;
+  if (want < 1) want = 1;
+  int64_t c = (keys + want - 1) / want;
+  c = (c + 127) / 128 * 128;
+  *chunk = static_cast<int>(c);
+  *parts = static_cast<int>((keys + c - 1) / c);
+}
+
+inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx) {
+  AttendPlan L{};
+  const int64_t n = Hq / Hkv;
+  const int64_t all = B * R * n, own = R * n;
+  L.prefix_wide = all > kAttendWideRows;
+  L.own_wide = own > kAttendWideRows;
+  L.prefix_chunk = 1;
+  if (P > 0) {
+    const int64_t tiles = (all + (L.prefix_wide ? 127 : 31)) / (L.prefix_wide ? 128 : 32);
+    split_keys(P, tiles * Hkv, &L.prefix_parts, &L.prefix_chunk);
+    L.prefix_items = tiles * Hkv * L.prefix_parts;
+  }
+  L.own_tiles = static_cast<int>((own + (L.own_wide ? 127 : 31)) / (L.own_wide ? 128 : 32));
+  split_keys(max_ctx + R, B * Hkv * L.own_tiles, &L.own_parts, &L.own_chunk);
+  L.own_blocks = (B * Hkv * L.own_parts + 7) / 8 * 8 * L.own_tiles;
+  const size_t slots = static_cast<size_t>(L.prefix_parts + L.own_parts) * static_cast<size_t>(B * R * Hq);
+  L.ml_off = align256(slots * static_cast<size_t>(D) * sizeof(float));
+  L.total = align256(L.ml_off + slots * 2 * sizeof(float));
+  return L;
+}
+
 }  // namespace sv

@@ -83,6 +83,8 @@ typedef enum { SV_TREE_GREEDY = 0, SV_TREE_STOCHASTIC = 1, SV_TREE_MULTI_CANDIDA
 #define SV_TREE_MAX_NODES 256
 #define SV_LMHEAD_K_STEP 64
 #define SV_ADJUST_MAX_BIAS 65535
+#define SV_ATTENTION_MAX_HEADS 1024
+#define SV_ATTENTION_MAX_KEYS (1 << 24)
 #define SV_LMHEAD_MAX_HIDDEN 65536
 #define SV_TREE_MAX_DEPTH 64
 /* Device scratch of sv_verify_window_noalloc, per GPU (8 MiB). */
@@ -379,6 +381,43 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                     const uint8_t *weights, const void *scales, const uint8_t *zeros,
                     int32_t M, int32_t K, int32_t V, int32_t group,
                     void *out, int64_t out_row_stride, int out_dtype, hipStream_t stream);
+
+/* Attention of a step's rows: every row of a window or tree over the prefix
+ * the whole batch shares, its sequence's cached context and its own ancestors
+ * (what produces the hidden states the rows' logits come from).
+ *   q        [B][R] rows of q_row_stride elements (0 = Hq * D), each Hq heads
+ *            of D; `dtype` SV_DT_BF16 or SV_DT_F16.  D is 64 or 128.  Query
+ *            head h reads kv head h / (Hq / Hkv).
+ *   k_cache, v_cache  [B] caches cache_seq_stride elements apart (0 = dense),
+ *            of cap tokens cache_tok_stride elements apart (0 = Hkv * D), each
+ *            Hkv heads of D.  The first ctx_len[b] tokens are committed; the R
+ *            rows' own keys and values follow them.
+ *   prefix_k, prefix_v  P tokens prefix_tok_stride elements apart (0 = Hkv *
+ *            D), seen by every row of every sequence; P = 0: none.
+ *   ctx_len  [B] int32 in [0, max_ctx]; max_ctx + R <= cap.  max_ctx only
+ *            bounds the lengths (the work follows the lengths themselves).  A
+ *            sequence whose length is outside gets rows of NaN, and nothing of
+ *            its cache is read.
+ *   row_count  [B] or NULL (= R): rows of each sequence to compute (clamped
+ *            to [0, R]); the others of out and lse are left as they were, and
+ *            their keys and values are not used.
+ *   parent_host  NULL: a window, row i sees rows 0..i (R <= SV_MAX_GAMMA + 1);
+ *            else HOST [R], a tree as in sv_verify_tree: a node sees its
+ *            ancestors and itself.
+ *   out      [B][R][Hq][D], dense; lse [B][R][Hq] float or NULL: the logarithm
+ *            of the row's sum of exp(scale * q.k).
+ * Scores, softmax statistics and sums are float32; the exponentials enter the
+ * second product in dtype.  Keys and values past a sequence's rows do not
+ * matter, whatever they hold, nor do those of nodes a row does not see.
+ * Strides are multiples of 8 elements, tensors 16-byte aligned; workspace of
+ * sv_attention_workspace bytes (0: sizes outside the rules). */
+size_t sv_attention_workspace(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx);
+int sv_attention(const void *q, int64_t q_row_stride, int dtype,
+                 const void *k_cache, const void *v_cache, int64_t cache_seq_stride, int64_t cache_tok_stride, int32_t cap,
+                 const void *prefix_k, const void *prefix_v, int64_t prefix_tok_stride, int32_t P,
+                 const int32_t *ctx_len, const int32_t *row_count, const int32_t *parent_host,
+                 int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_ctx, float scale,
+                 void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
