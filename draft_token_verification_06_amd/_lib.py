@@ -32,17 +32,22 @@ _SIGNATURES = {
     "sv_rollback": (_c.c_int, [_P, _P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I32, _P]),
     "sv_verify_window_lmhead": (_c.c_int, [_P, _P, _I32, _P, _P, _I32, _P, _P, _I32, _I32, _I32,
                                            _U64, _U64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "sv_probe_blocks": (_I32, [_SZ]),
+    "sv_probe_read": (_c.c_int, [_P, _SZ, _P, _P]),
+}
+
+# include/sv_step.h
+_STEP_SIGNATURES = {
     "sv_adjust_logits": (_c.c_int, [_P, _I64, _P, _I64, _c.c_int, _P, _I64, _P, _P, _I32, _I32, _I32,
                                     _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _P]),
     "sv_lmhead_quant": (_c.c_int, [_P, _I64, _c.c_int, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _c.c_int, _P]),
     "sv_attention_workspace": (_SZ, [_I32] * 7),
     "sv_attention": (_c.c_int, [_P, _I64, _c.c_int, _P, _P, _I64, _I64, _I32, _P, _P, _I64, _I32, _P, _P, _P,
                                 _I32, _I32, _I32, _I32, _I32, _I32, _c.c_float, _P, _P, _P, _SZ, _P]),
-    "sv_probe_blocks": (_I32, [_SZ]),
-    "sv_probe_read": (_c.c_int, [_P, _SZ, _P, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
+STEP_EXPORTED = tuple(_STEP_SIGNATURES)
 
 _lib = None
 
@@ -69,7 +74,7 @@ def lib():
     import torch  # noqa: F401  -- torch's HIP runtime must be the one the library binds to
 
     handle = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in _SIGNATURES.items():
+    for name, (res, args) in (*_SIGNATURES.items(), *_STEP_SIGNATURES.items()):
         fn = getattr(handle, name)
         fn.restype = res
         fn.argtypes = args

@@ -331,23 +331,56 @@ def verify_tree(target, draft, node_tokens, parent, *, mode="stochastic", seed=0
     return res
 
 
-def _rows_i32(t, B, cols, name):
+# Checks of the operators below.  They run before every launch, small calls
+# are bound by them, so each is one test of what it names.
+def _vec(t, dtype, B, dev, name):
+    """Address of a contiguous (B,) device tensor, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != dev or t.shape != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape ({B},) on {dev}")
+    return t.data_ptr()
+
+
+def _rows_i32(t, B, cols, dev, name):
     """Row stride of an int32 device tensor (B, >= cols) with unit column stride."""
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != B or t.shape[1] < cols \
-            or (t.shape[1] > 1 and t.stride(1) != 1) or (B > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name}: expected an int32 device tensor of shape ({B}, >={cols}) with unit column stride")
-    return t.stride(0) if B > 1 else t.shape[1]
+    if t.dtype != torch.int32 or t.device != dev or t.dim() != 2:
+        raise ValueError(f"{name}: expected an int32 tensor of shape ({B}, >={cols}) on {dev}")
+    n, width = t.shape
+    row, col = t.stride()
+    if n != B or width < cols or (width > 1 and col != 1) or (B > 1 and row < width):
+        raise ValueError(f"{name}: expected shape ({B}, >={cols}) with unit column stride, rows not overlapping")
+    return row if B > 1 else width
 
 
 def _seq_stride(t, name):
-    """Sequence stride of (B, R, V) logits whose sequences do not overlap (0 = dense)."""
+    """Sequence stride of (B, R, V) logits whose rows are dense and whose sequences do not overlap (0 = dense)."""
     B, R, V = t.shape
-    if R == 1 and t.dim() == 3 and t.stride(1) != V:
-        t = t.as_strided(t.shape, (t.stride(0), V, t.stride(2)))  # one row: its row stride says nothing
-    stride = _logits(t, R, name)
-    if B > 1 and stride < R * V:
+    seq, row, col = t.stride()
+    if (V > 1 and col != 1) or (R > 1 and row != V):
+        raise ValueError(f"{name}: rows of one sequence must be contiguous")
+    if B > 1 and seq < R * V:
         raise ValueError(f"{name}: sequences overlap")
-    return stride if B > 1 else 0
+    return seq if B > 1 else 0
+
+
+def _parents(parent, R):
+    if parent is None:
+        return None
+    if len(parent) != R:
+        raise ValueError("parent must have one entry per row")
+    return (ctypes.c_int32 * R)(*parent)
+
+
+def _launch(dev, fn, *args):
+    """Calls fn on dev's current stream with dev current."""
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, torch.cuda.current_stream(dev.index).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev.index).cuda_stream)
+    if status != 0:
+        raise SvError(status)
 
 
 def adjust_logits(logits, *, tokens=None, parent=None, history=None, history_len=None, prompt_len=None,
@@ -363,61 +396,54 @@ def adjust_logits(logits, *, tokens=None, parent=None, history=None, history_len
     (B, R, ceil(V / 32)) bit masks (rows or sequences may be expanded);
     row_count (B,) int32.  Returns out (a new tensor when None; out=logits
     works in place)."""
-    if logits.dim() != 3:
-        raise ValueError(f"logits: expected shape (B, R, V), got {tuple(logits.shape)}")
+    dtype, dev = logits.dtype, logits.device
+    if logits.dim() != 3 or dtype not in _DTYPE_CODE or dev.type != "cuda":
+        raise ValueError("logits: expected a float32, bfloat16 or float16 device tensor of shape (B, R, V)")
     B, R, V = logits.shape
     stride = _seq_stride(logits, "logits")
-    dev = logits.device
-    par = None
-    if parent is not None:
-        if len(parent) != R:
-            raise ValueError("parent must have one entry per row")
-        par = (ctypes.c_int32 * R)(*parent)
+    par = _parents(parent, R)
+    tokens_ptr = history_ptr = bias_ptr = values_ptr = allowed_ptr = None
     tokens_stride = history_stride = cap = n_bias = mask_seq = mask_row = 0
     if tokens is not None:
-        tokens_stride = _rows_i32(tokens, B, R if parent is not None else R - 1, "tokens")
+        tokens_stride = _rows_i32(tokens, B, R if parent is not None else R - 1, dev, "tokens")
+        tokens_ptr = tokens.data_ptr()
+    elif R > 1 and not (repetition is None and presence is None and frequency is None):
+        raise ValueError("penalties on more than one row need the rows' tokens")
     if history is not None:
-        history_stride = _rows_i32(history, B, 0, "history")
+        history_stride = _rows_i32(history, B, 0, dev, "history")
         cap = history.shape[1]
+        history_ptr = history.data_ptr()
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len need a history")
-    for name, t, dtype in (("history_len", history_len, torch.int32), ("prompt_len", prompt_len, torch.int32),
-                           ("row_count", row_count, torch.int32), ("repetition", repetition, torch.float32),
-                           ("presence", presence, torch.float32), ("frequency", frequency, torch.float32)):
-        _optional(t, dtype, B, name)
-    if tokens is None and R > 1 and not (repetition is None and presence is None and frequency is None):
-        raise ValueError("penalties on more than one row need the rows' tokens")
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values go together")
     if bias_tokens is not None:
         n_bias = bias_tokens.shape[-1]
-        _i32(bias_tokens, (B, n_bias), "bias_tokens")
-        if bias_values.dtype != torch.float32 or not bias_values.is_cuda or not bias_values.is_contiguous() \
-                or tuple(bias_values.shape) != (B, n_bias):
-            raise ValueError(f"bias_values: expected a contiguous float32 device tensor of shape ({B}, {n_bias})")
+        for t, want, name in ((bias_tokens, torch.int32, "bias_tokens"), (bias_values, torch.float32, "bias_values")):
+            if t.dtype != want or t.device != dev or t.shape != (B, n_bias) or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous {want} tensor of shape ({B}, {n_bias}) on {dev}")
+        bias_ptr, values_ptr = bias_tokens.data_ptr(), bias_values.data_ptr()
     if allowed is not None:
         W = (V + 31) // 32
-        if allowed.dtype != torch.int32 or not allowed.is_cuda or tuple(allowed.shape) != (B, R, W) \
+        if allowed.dtype != torch.int32 or allowed.device != dev or allowed.shape != (B, R, W) \
                 or (W > 1 and allowed.stride(2) != 1):
-            raise ValueError(f"allowed: expected an int32 device tensor of shape ({B}, {R}, {W}) with unit word stride")
+            raise ValueError(f"allowed: expected an int32 tensor of shape ({B}, {R}, {W}) with unit word stride on {dev}")
         mask_seq, mask_row = allowed.stride(0), allowed.stride(1)
-    _same_device(dev, tokens=tokens, history=history, history_len=history_len, prompt_len=prompt_len,
-                 repetition=repetition, presence=presence, frequency=frequency, bias_tokens=bias_tokens,
-                 bias_values=bias_values, allowed=allowed, row_count=row_count)
+        allowed_ptr = allowed.data_ptr()
+    args = (_vec(history_len, torch.int32, B, dev, "history_len"), _vec(prompt_len, torch.int32, B, dev, "prompt_len"),
+            _vec(repetition, torch.float32, B, dev, "repetition"), _vec(presence, torch.float32, B, dev, "presence"),
+            _vec(frequency, torch.float32, B, dev, "frequency"))
+    rows_ptr = _vec(row_count, torch.int32, B, dev, "row_count")
+    out_stride = 0
     if out is None:
-        out = torch.empty(B, R, V, dtype=logits.dtype, device=dev)
-        out_stride = 0
+        out = torch.empty((B, R, V), dtype=dtype, device=dev)
     else:
-        if out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape:
+        if out.dtype != dtype or out.device != dev or out.shape != logits.shape:
             raise ValueError("out must match logits in dtype, device and shape")
         out_stride = _seq_stride(out, "out")
-    with torch.cuda.device(dev):
-        _check(lib().sv_adjust_logits(
-            _ptr(logits), stride, _ptr(out), out_stride, _DTYPE_CODE[logits.dtype],
-            _ptr(tokens), tokens_stride, par, _ptr(row_count), B, R, V,
-            _ptr(history), history_stride, cap, _ptr(history_len), _ptr(prompt_len),
-            _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), n_bias,
-            _ptr(allowed), mask_seq, mask_row, _stream(dev)))
+    _launch(dev, lib().sv_adjust_logits, logits.data_ptr(), stride, out.data_ptr(), out_stride, _DTYPE_CODE[dtype],
+            tokens_ptr, tokens_stride, par, rows_ptr, B, R, V, history_ptr, history_stride, cap, *args,
+            bias_ptr, values_ptr, n_bias, allowed_ptr, mask_seq, mask_row)
     return out
 
 
@@ -427,40 +453,39 @@ def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32
     scales (V, K / group) of hidden's dtype, zeros (V, K / group) uint8 or None.
     Returns (..., V) logits of out_dtype (float32 or hidden's dtype), or fills
     out."""
-    if hidden.dtype not in (torch.bfloat16, torch.float16) or not hidden.is_cuda or hidden.dim() < 1:
+    dtype, dev = hidden.dtype, hidden.device
+    if (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda" or hidden.dim() < 1:
         raise ValueError("hidden: expected a bf16 or fp16 device tensor")
-    dev, K = hidden.device, hidden.shape[-1]
-    lead = hidden.shape[:-1]
-    if weights.dtype != torch.uint8 or not weights.is_cuda or not weights.is_contiguous() or weights.dim() != 2 \
-            or 2 * weights.shape[1] != K:
-        raise ValueError(f"weights: expected a contiguous uint8 device tensor of shape (V, {K // 2})")
+    K, lead = hidden.shape[-1], hidden.shape[:-1]
+    if weights.dtype != torch.uint8 or weights.device != dev or weights.dim() != 2 or 2 * weights.shape[1] != K \
+            or not weights.is_contiguous():
+        raise ValueError(f"weights: expected a contiguous uint8 tensor of shape (V, {K // 2}) on {dev}")
     V = weights.shape[0]
-    if scales.dtype != hidden.dtype or not scales.is_cuda or not scales.is_contiguous() or scales.dim() != 2 \
-            or scales.shape[0] != V or scales.shape[1] < 1 or K % scales.shape[1]:
-        raise ValueError(f"scales: expected a contiguous {hidden.dtype} device tensor of shape ({V}, {K} / group)")
-    if zeros is not None and (zeros.dtype != torch.uint8 or not zeros.is_cuda or not zeros.is_contiguous()
-                              or zeros.shape != scales.shape):
-        raise ValueError(f"zeros: expected a contiguous uint8 device tensor of shape {tuple(scales.shape)}")
+    if scales.dtype != dtype or scales.device != dev or scales.dim() != 2 or scales.shape[0] != V \
+            or scales.shape[1] < 1 or K % scales.shape[1] or not scales.is_contiguous():
+        raise ValueError(f"scales: expected a contiguous {dtype} tensor of shape ({V}, {K} / group) on {dev}")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.device != dev or zeros.shape != scales.shape
+                              or not zeros.is_contiguous()):
+        raise ValueError(f"zeros: expected a contiguous uint8 tensor of shape {tuple(scales.shape)} on {dev}")
     if out is None:
-        if out_dtype not in (torch.float32, hidden.dtype):
-            raise ValueError(f"out_dtype: expected float32 or {hidden.dtype}")
-        out = torch.empty(*lead, V, dtype=out_dtype, device=dev)
-    elif out.dtype not in (torch.float32, hidden.dtype) or tuple(out.shape) != (*lead, V) or not out.is_contiguous():
-        raise ValueError(f"out: expected a contiguous float32 or {hidden.dtype} device tensor of shape {(*lead, V)}")
-    _same_device(dev, weights=weights, scales=scales, zeros=zeros, out=out)
+        if out_dtype != torch.float32 and out_dtype != dtype:
+            raise ValueError(f"out_dtype: expected float32 or {dtype}")
+        out = torch.empty((*lead, V), dtype=out_dtype, device=dev)
+    elif (out.dtype != torch.float32 and out.dtype != dtype) or out.device != dev or out.shape != (*lead, V) \
+            or not out.is_contiguous():
+        raise ValueError(f"out: expected a contiguous float32 or {dtype} tensor of shape {(*lead, V)} on {dev}")
     M = out.numel() // V if V else 0
     if M == 0:
         return out
     try:
-        rows = hidden.view(M, K)
+        rows = hidden if hidden.dim() == 2 else hidden.view(M, K)
     except RuntimeError:
         raise ValueError("hidden: rows must be one stride apart") from None
     if rows.stride(1) != 1 or (M > 1 and rows.stride(0) < K):
         raise ValueError("hidden: rows must be contiguous and not overlap")
-    with torch.cuda.device(dev):
-        _check(lib().sv_lmhead_quant(
-            _ptr(rows), rows.stride(0) if M > 1 else 0, _DTYPE_CODE[hidden.dtype], _ptr(weights), _ptr(scales), _ptr(zeros),
-            M, K, V, K // scales.shape[1], _ptr(out), 0, _DTYPE_CODE[out.dtype], _stream(dev)))
+    _launch(dev, lib().sv_lmhead_quant, rows.data_ptr(), rows.stride(0) if M > 1 else 0, _DTYPE_CODE[dtype],
+            weights.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+            M, K, V, K // scales.shape[1], out.data_ptr(), 0, _DTYPE_CODE[out.dtype])
     return out
 
 
@@ -478,14 +503,18 @@ def attention_workspace(B, R, Hq, Hkv, D, P, max_ctx, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _heads(t, dtype, shape, name):
-    """Token stride of (..., tokens, H, D) keys, values or queries with dense heads."""
-    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected a {dtype} device tensor of shape {shape}")
-    H, D = shape[-2:]
-    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(-3) if shape[-3] > 1 else 0
+def _keys_values(k, v, dtype, dev, H, D, name):
+    """Strides of a pair of (..., tokens, H, D) tensors with dense heads."""
+    if k.dtype != dtype or v.dtype != dtype or k.device != dev or v.device != dev or k.shape != v.shape:
+        raise ValueError(f"{name}: expected two {dtype} tensors of one shape on {dev}")
+    if k.shape[-2:] != (H, D):
+        raise ValueError(f"{name}: expected heads of shape ({H}, {D}), got {tuple(k.shape[-2:])}")
+    st = k.stride()
+    if v.stride() != st:
+        raise ValueError(f"{name}: keys and values must have the same strides")
+    if st[-1] != 1 or (H > 1 and st[-2] != D) or (k.shape[-3] > 1 and st[-3] < H * D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, tokens not overlapping")
+    return st
 
 
 def attention(q, k_cache, v_cache, ctx_len, *, prefix_k=None, prefix_v=None, parent=None, row_count=None,
@@ -498,45 +527,42 @@ def attention(q, k_cache, v_cache, ctx_len, *, prefix_k=None, prefix_v=None, par
     D) or None.  parent (a host sequence) makes the rows a tree.  scale defaults
     to D ** -0.5, max_ctx (an upper bound of ctx_len) to cap - R.  out: an
     AttentionResult to fill."""
-    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float16):
+    dtype, dev = q.dtype, q.device
+    if q.dim() != 4 or (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda":
         raise ValueError("q: expected a bf16 or fp16 device tensor of shape (B, R, Hq, D)")
     B, R, Hq, D = q.shape
-    dev = q.device
-    q_stride = _heads(q, q.dtype, (B, R, Hq, D), "q")
-    if R == 1:
-        q_stride = q.stride(0) if B > 1 else 0
-    elif B > 1 and q.stride(0) != R * q_stride:
-        raise ValueError("q: rows must be one stride apart")
-    if k_cache.dim() != 4 or k_cache.shape[0] != B or k_cache.shape[3] != D:
+    qs = q.stride()
+    if qs[3] != 1 or (Hq > 1 and qs[2] != D):
+        raise ValueError("q: the heads of a row must be contiguous")
+    q_stride = qs[1] if R > 1 else qs[0] if B > 1 else 0
+    if (B > 1 and R > 1 and qs[0] != R * q_stride) or (B * R > 1 and q_stride < Hq * D):
+        raise ValueError("q: rows must be one stride apart and not overlap")
+    if k_cache.dim() != 4 or k_cache.shape[0] != B:
         raise ValueError(f"k_cache: expected shape ({B}, cap, Hkv, {D}), got {tuple(k_cache.shape)}")
     cap, Hkv = k_cache.shape[1], k_cache.shape[2]
-    tok_stride = _heads(k_cache, q.dtype, (B, cap, Hkv, D), "k_cache")
-    _heads(v_cache, q.dtype, (B, cap, Hkv, D), "v_cache")
-    if v_cache.stride() != k_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same strides")
-    seq_stride = k_cache.stride(0) if B > 1 else 0
+    st = _keys_values(k_cache, v_cache, dtype, dev, Hkv, D, "k_cache and v_cache")
     if Hkv < 1 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the kv heads")
-    if (B > 1 and seq_stride == 0) or (cap > 1 and tok_stride < Hkv * D) or ((B > 1 or R > 1) and q_stride < Hq * D):
-        raise ValueError("tokens, rows or sequences overlap")
+    seq_stride, tok_stride = st[0] if B > 1 else 0, st[1] if cap > 1 else 0
+    if B > 1 and seq_stride <= 0:
+        raise ValueError("k_cache and v_cache: sequences overlap")
     P = prefix_stride = 0
+    pk = pv = None
     if (prefix_k is None) != (prefix_v is None):
         raise ValueError("prefix_k and prefix_v go together")
     if prefix_k is not None:
+        if prefix_k.dim() != 3:
+            raise ValueError(f"prefix_k: expected shape (P, {Hkv}, {D}), got {tuple(prefix_k.shape)}")
         P = prefix_k.shape[0]
-        prefix_stride = _heads(prefix_k, q.dtype, (P, Hkv, D), "prefix_k")
-        _heads(prefix_v, q.dtype, (P, Hkv, D), "prefix_v")
-        if prefix_k.stride() != prefix_v.stride() or (P > 1 and prefix_stride < Hkv * D):
-            raise ValueError("prefix_k and prefix_v must have the same strides, tokens not overlapping")
-    _optional(ctx_len, torch.int32, B, "ctx_len")
-    _optional(row_count, torch.int32, B, "row_count")
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, prefix_k=prefix_k, prefix_v=prefix_v, ctx_len=ctx_len,
-                 row_count=row_count)
-    par = None
-    if parent is not None:
-        if len(parent) != R:
-            raise ValueError("parent must have one entry per row")
-        par = (ctypes.c_int32 * R)(*parent)
+        prefix_st = _keys_values(prefix_k, prefix_v, dtype, dev, Hkv, D, "prefix_k and prefix_v")
+        if P > 0:
+            prefix_stride = prefix_st[0] if P > 1 else 0
+            pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
+    if ctx_len is None:
+        raise ValueError("ctx_len is required")
+    len_ptr = _vec(ctx_len, torch.int32, B, dev, "ctx_len")
+    rows_ptr = _vec(row_count, torch.int32, B, dev, "row_count")
+    par = _parents(parent, R)
     if max_ctx is None:
         max_ctx = cap - R
     if scale is None:
@@ -547,19 +573,16 @@ def attention(q, k_cache, v_cache, ctx_len, *, prefix_k=None, prefix_v=None, par
     else:
         ws_bytes = _ws_bytes(ws, dev)
     if out is None:
-        out = AttentionResult(torch.empty(B, R, Hq, D, dtype=q.dtype, device=dev),
-                              torch.empty(B, R, Hq, dtype=torch.float32, device=dev) if return_lse else None)
+        out = AttentionResult(torch.empty((B, R, Hq, D), dtype=dtype, device=dev),
+                              torch.empty((B, R, Hq), dtype=torch.float32, device=dev) if return_lse else None)
     else:
         if out.out is None:
             raise ValueError("out is a required output")
-        _out_tensor(out.out, q.dtype, (B, R, Hq, D), dev, "out")
+        _out_tensor(out.out, dtype, (B, R, Hq, D), dev, "out")
         _out_tensor(out.lse, torch.float32, (B, R, Hq), dev, "lse")
-    with torch.cuda.device(dev):
-        _check(lib().sv_attention(
-            _ptr(q), q_stride, _DTYPE_CODE[q.dtype], _ptr(k_cache), _ptr(v_cache), seq_stride, tok_stride, cap,
-            _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None, prefix_stride, P,
-            _ptr(ctx_len), _ptr(row_count), par, B, R, Hq, Hkv, D, max_ctx, scale,
-            _ptr(out.out), _ptr(out.lse), _ptr(ws), ws_bytes, _stream(dev)))
+    _launch(dev, lib().sv_attention, q.data_ptr(), q_stride, _DTYPE_CODE[dtype], k_cache.data_ptr(), v_cache.data_ptr(),
+            seq_stride, tok_stride, cap, pk, pv, prefix_stride, P, len_ptr, rows_ptr, par, B, R, Hq, Hkv, D, max_ctx, scale,
+            out.out.data_ptr(), None if out.lse is None else out.lse.data_ptr(), ws.data_ptr(), ws_bytes)
     return out
 
 

@@ -21,6 +21,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "sv_device.h"
 #include "sv_launch.h"
 #include "sv_plan.h"
@@ -87,6 +89,7 @@ template <int DT> __device__ __forceinline__ uint4 mask_elems(uint4 v, uint32_t 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+constexpr int64_t kAdjustItems = 2048;  // workgroups wanted per launch (8 of 256 threads on each of 256 CUs)
 constexpr uint32_t kSeenInPrompt = 0x80000000u;
 
 template <int DT>
@@ -103,10 +106,13 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
   __shared__ uint64_t s_path[kTreeMaxNodes][kWords];  // those on each row's path
 
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / A.chunks;
-  const int base = (blockIdx.x - b * A.chunks) * kChunk;
-  const int rows = A.row_count ? min(max(A.row_count[b], 0), A.R) : A.R;
-  if (rows == 0) return;  // the same for the whole workgroup
+  const int group = blockIdx.x % A.row_groups;
+  const int item = blockIdx.x / A.row_groups;
+  const int b = item / A.chunks;
+  const int base = (item - b * A.chunks) * kChunk;
+  const int live = A.row_count ? min(max(A.row_count[b], 0), A.R) : A.R;
+  const int row0 = group * A.group_rows, rows = min(row0 + A.group_rows, live);
+  if (row0 >= rows) return;  // the same for the whole workgroup
   const bool counted = A.repetition || A.presence || A.frequency;
   const bool history = counted && A.history;
   const bool biased = A.n_bias > 0;
@@ -134,12 +140,18 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
     const int len = A.history_len ? min(max(A.history_len[b], 0), A.history_cap) : A.history_cap;
     const int prompt = A.prompt_len ? min(max(A.prompt_len[b], 0), len) : 0;
     const int32_t *h = A.history + b * A.history_stride;
-    for (int i = tid; i < len; i += kAdjustThreads) {
-      const int t = h[i];
-      if (t >= base && t < A.V && t - base < kChunk) {
-        if (i < prompt) atomicOr(&s_count[t - base], kSeenInPrompt);
-        else atomicAdd(&s_count[t - base], 1u);
-      }
+    // kBatch loads in flight per thread: a long history costs few round trips
+    constexpr int kBatch = 8;
+    for (int i0 = tid; i0 < len; i0 += kBatch * kAdjustThreads) {
+      int t[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) t[j] = i0 + j * kAdjustThreads < len ? h[i0 + j * kAdjustThreads] : -1;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (t[j] >= base && t[j] < A.V && t[j] - base < kChunk) {
+          if (i0 + j * kAdjustThreads < prompt) atomicOr(&s_count[t[j] - base], kSeenInPrompt);
+          else atomicAdd(&s_count[t[j] - base], 1u);
+        }
     }
   }
   if (biased) {
@@ -204,41 +216,63 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
   const uint8_t *allowed =
       A.allowed ? reinterpret_cast<const uint8_t *>(A.allowed + b * A.allowed_seq_stride) + t0 / 8 : nullptr;
   const int nibble = t0 & 7;  // float32 vectors: half a byte of the mask
-  for (int r = 0; r < rows; ++r, in += row_bytes, out += row_bytes) {
-    uint32_t m = kFull;
-    if (allowed) m = (allowed[r * A.allowed_row_stride * 4] >> nibble) & kFull;
-    uint32_t on_path[kEPV] = {};
-    bool apply = touched;
-    if (paths) {
-      for (int w = 0; w < words; ++w)
-        for (uint64_t bits = s_path[r][w]; bits; bits &= bits - 1) {
-          const int d = s_node[w * 64 + __builtin_ctzll(bits)] - t0;
+  // kAhead rows at a time: their mask bytes, then their vectors, in flight together.
+  constexpr int kAhead = 4;
+  for (int r0 = row0; r0 < rows; r0 += kAhead) {
+    uint32_t m[kAhead];
+    uint4 x[kAhead];
+    bool near[kAhead];  // some token of the row's path lies in the chunk (the same for the workgroup)
 #pragma unroll
-          for (int k = 0; k < kEPV; ++k) on_path[k] += d == k;
-          apply |= d >= 0 && d < kEPV;
-        }
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = min(r0 + u, rows - 1);
+      m[u] = kFull;
+      if (allowed) m[u] = (allowed[r * A.allowed_row_stride * 4] >> nibble) & kFull;
     }
-    if (A.in_place && !apply && m == kFull) continue;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (m != 0) x = load_elems<DT>(in, valid);
-    if (apply && m != 0) {
-      float y[kEPV];
-      E::vec(x, y);
 #pragma unroll
-      for (int k = 0; k < kEPV; ++k) {
-        const uint32_t n = (count[k] & ~kSeenInPrompt) + on_path[k];
-        if (count[k] != 0 || n != 0) y[k] = y[k] > 0.0f ? y[k] / rho : y[k] * rho;
-        if (n != 0) y[k] = y[k] - freq * static_cast<float>(n) - pres;
-        if (bias[k] != 0.0f) y[k] += bias[k];
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = min(r0 + u, rows - 1);
+      near[u] = false;
+      if (paths)
+        for (int w = 0; w < words; ++w) near[u] |= s_path[r][w] != 0;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (m[u] != 0 && !(A.in_place && !touched && !near[u] && m[u] == kFull)) x[u] = load_elems<DT>(in + r * row_bytes, valid);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = r0 + u;
+      if (r >= rows) break;
+      uint32_t on_path[kEPV] = {};
+      bool apply = touched;
+      if (near[u]) {
+        for (int w = 0; w < words; ++w)
+          for (uint64_t bits = s_path[r][w]; bits; bits &= bits - 1) {
+            const int d = s_node[w * 64 + __builtin_ctzll(bits)] - t0;
+#pragma unroll
+            for (int k = 0; k < kEPV; ++k) on_path[k] += d == k;
+            apply |= d >= 0 && d < kEPV;
+          }
       }
-      uint32_t w[4];
+      if (A.in_place && !apply && m[u] == kFull) continue;
+      uint4 v = x[u];
+      if (apply && m[u] != 0) {
+        float y[kEPV];
+        E::vec(v, y);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = DT == DT_F32 ? enc<DT>(y[i % kEPV]) : enc<DT>(y[2 * i % kEPV]) | (enc<DT>(y[(2 * i + 1) % kEPV]) << 16);
-      x = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < kEPV; ++k) {
+          const uint32_t n = (count[k] & ~kSeenInPrompt) + on_path[k];
+          if (count[k] != 0 || n != 0) y[k] = y[k] > 0.0f ? y[k] / rho : y[k] * rho;
+          if (n != 0) y[k] = y[k] - freq * static_cast<float>(n) - pres;
+          if (bias[k] != 0.0f) y[k] += bias[k];
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = DT == DT_F32 ? enc<DT>(y[i % kEPV]) : enc<DT>(y[2 * i % kEPV]) | (enc<DT>(y[(2 * i + 1) % kEPV]) << 16);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (m[u] != kFull) v = mask_elems<DT>(v, m[u]);
+      store_elems<DT>(out + r * row_bytes, v, valid);
     }
-    if (m != kFull) x = mask_elems<DT>(x, m);
-    store_elems<DT>(out, x, valid);
   }
 }
 
@@ -249,7 +283,14 @@ int adjust_chunks(int dtype, int V) {
 
 void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st) {
   A.chunks = adjust_chunks(dtype, A.V);
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(B) * A.chunks));
+  // Few sequences and many rows (a tree): rows go to several workgroups, each
+  // of which counts the history again.  Four at least stay together, which is
+  // what a thread keeps in flight.
+  const int64_t items = static_cast<int64_t>(B) * A.chunks;
+  const int64_t want = std::min<int64_t>((kAdjustItems + items - 1) / items, (A.R + 3) / 4);
+  A.group_rows = static_cast<int32_t>((A.R + want - 1) / want);
+  A.row_groups = (A.R + A.group_rows - 1) / A.group_rows;
+  const dim3 grid(static_cast<unsigned>(items * A.row_groups));
   if (dtype == DT_F32)
     hipLaunchKernelGGL(k_adjust_logits<DT_F32>, grid, dim3(kAdjustThreads), 0, st, A);
   else if (dtype == DT_BF16)

@@ -8,6 +8,7 @@
 #include "sv.h"
 #include "sv_launch.h"
 #include "sv_plan.h"
+#include "sv_step.h"
 
 using namespace sv;
 

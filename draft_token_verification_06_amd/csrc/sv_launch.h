@@ -114,7 +114,8 @@ struct AdjustArgs {
   const float *bias_values;
   const uint32_t *allowed;
   int64_t allowed_seq_stride, allowed_row_stride;  // words
-  int32_t chunks;   // token chunks per row (set by the launcher)
+  int32_t chunks;   // token chunks per row; rows split into groups of group_rows (set by the launcher)
+  int32_t row_groups, group_rows;
   int32_t in_place; // out is in: only what changes is touched
   int32_t tree;
   int16_t parent[kTreeMaxNodes];
