@@ -43,10 +43,12 @@ template <> __device__ __forceinline__ uint32_t enc<DT_F16>(float x) {
   return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
 }
 
-template <int DT> __device__ __forceinline__ uint4 load_elems(const char *p, int valid) {
+// kStream: with the nontemporal hint (rows that pass through once).
+template <int DT, bool kStream> __device__ __forceinline__ uint4 load_elems(const char *p, int valid) {
   constexpr int kEPV = Elt<DT>::kEPV;
   if (valid >= kEPV) {
-    const u32x4_e2_t v = *as_global<u32x4_e2_t>(static_cast<const void *>(p));
+    const SV_GLOBAL u32x4_e2_t *g = as_global<u32x4_e2_t>(static_cast<const void *>(p));
+    const u32x4_e2_t v = kStream ? __builtin_nontemporal_load(g) : *g;
     return make_uint4(v.x, v.y, v.z, v.w);
   }
   uint32_t w[4] = {0, 0, 0, 0};
@@ -59,11 +61,14 @@ template <int DT> __device__ __forceinline__ uint4 load_elems(const char *p, int
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int DT> __device__ __forceinline__ void store_elems(char *p, uint4 v, int valid) {
+template <int DT, bool kStream> __device__ __forceinline__ void store_elems(char *p, uint4 v, int valid) {
   constexpr int kEPV = Elt<DT>::kEPV;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   if (valid >= kEPV) {
-    *reinterpret_cast<SV_GLOBAL u32x4_e2_t *>(reinterpret_cast<uintptr_t>(p)) = u32x4_e2_t{v.x, v.y, v.z, v.w};
+    SV_GLOBAL u32x4_e2_t *g = reinterpret_cast<SV_GLOBAL u32x4_e2_t *>(reinterpret_cast<uintptr_t>(p));
+    const u32x4_e2_t x = {v.x, v.y, v.z, v.w};
+    if (kStream) __builtin_nontemporal_store(x, g);
+    else *g = x;
     return;
   }
 #pragma unroll
@@ -92,16 +97,21 @@ template <int DT> __device__ __forceinline__ uint4 mask_elems(uint4 v, uint32_t 
 constexpr int64_t kAdjustItems = 2048;  // workgroups wanted per launch (8 of 256 threads on each of 256 CUs)
 constexpr uint32_t kSeenInPrompt = 0x80000000u;
 
-template <int DT>
+// kMode: rows copied to another place, cached or streamed, or changed in place.
+enum : int { ADJ_COPY = 0, ADJ_STREAM = 1, ADJ_IN_PLACE = 2 };
+
+template <int DT, int kMode>
 __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) {
   using E = Elt<DT>;
   constexpr int kEPV = E::kEPV;
+  constexpr bool kStream = kMode == ADJ_STREAM, kInPlace = kMode == ADJ_IN_PLACE;
   constexpr int kChunk = kAdjustThreads * kEPV;
   constexpr uint32_t kFull = (1u << kEPV) - 1;
   constexpr int kWords = kTreeMaxNodes / 64;
   __shared__ uint32_t s_count[kChunk];  // occurrences past the prompt; kSeenInPrompt
   __shared__ uint16_t s_bias[kChunk];   // 1 + index of the last bias entry that names the token
   __shared__ int32_t s_node[kTreeMaxNodes];
+  __shared__ int16_t s_parent[kTreeMaxNodes];
   __shared__ uint64_t s_in[kWords];               // nodes whose token lies in the chunk
   __shared__ uint64_t s_path[kTreeMaxNodes][kWords];  // those on each row's path
 
@@ -119,6 +129,44 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
   const bool paths = counted && A.tokens && A.R > 1;
   const int words = (A.R + 63) / 64;
 
+  const int t0 = base + tid * kEPV;  // this thread's first token
+  const int valid = min(kEPV, A.V - t0);
+  const int64_t row_bytes = static_cast<int64_t>(A.V) * E::kBytes;
+  const char *in = A.in + b * A.in_stride_bytes + static_cast<int64_t>(t0) * E::kBytes;
+  char *out = A.out + b * A.out_stride_bytes + static_cast<int64_t>(t0) * E::kBytes;
+  const uint8_t *allowed =
+      A.allowed ? reinterpret_cast<const uint8_t *>(A.allowed + b * A.allowed_seq_stride) + t0 / 8 : nullptr;
+  const int nibble = t0 & 7;  // float32 vectors: half a byte of the mask
+  // kAhead rows at a time: their mask bytes, then their vectors, in flight
+  // together (from a disallowed vector nothing is read).  Rows copied
+  // elsewhere are all read, so the first ones set out before the counting.
+  constexpr int kAhead = 4;
+  struct Rows {
+    uint32_t m[kAhead];
+    uint4 x[kAhead];
+  };
+  auto fetch = [&](int r0, Rows &f, auto wanted) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = min(r0 + u, rows - 1);
+      f.m[u] = kFull;
+      if (allowed) f.m[u] = (allowed[r * A.allowed_row_stride * 4] >> nibble) & kFull;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = min(r0 + u, rows - 1);
+      f.x[u] = make_uint4(0, 0, 0, 0);
+      if (f.m[u] != 0 && wanted(r, f.m[u])) f.x[u] = load_elems<DT, kStream>(in + r * row_bytes, valid);
+    }
+  };
+  const auto every = [](int, uint32_t) { return true; };
+  Rows next;
+  if (!kInPlace && valid > 0) fetch(row0, next, every);
+
+  const float rho = A.repetition ? A.repetition[b] : 1.0f;
+  const float pres = A.presence ? A.presence[b] : 0.0f;
+  const float freq = A.frequency ? A.frequency[b] : 0.0f;
+
   if (history)
     for (int i = tid; i < kChunk; i += kAdjustThreads) s_count[i] = 0;
   if (biased)
@@ -131,6 +179,9 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
       if (tid >= 1 && tid < A.R) t = A.tokens[b * A.tokens_stride + (A.tree ? tid : tid - 1)];
       const bool in = t >= base && t < A.V && t - base < kChunk;
       s_node[tid] = t;
+      // the walks below read parents from LDS: a step through the argument
+      // block would cost a trip to memory each
+      s_parent[tid] = A.tree ? A.parent[tid] : static_cast<int16_t>(tid - 1);
       const uint64_t bits = __ballot(in);
       if ((tid & 63) == 0) s_in[tid >> 6] = bits;
     }
@@ -173,7 +224,7 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
   }
   if (paths && tid < A.R) {
     uint64_t bits[kWords] = {};
-    for (int v = tid; v > 0; v = A.tree ? A.parent[v] : v - 1) {
+    for (int v = tid; v > 0; v = s_parent[v]) {
 #pragma unroll
       for (int w = 0; w < kWords; ++w)
         if (w < words && w == (v >> 6)) bits[w] |= s_in[w] & (1ull << (v & 63));
@@ -184,8 +235,6 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
   }
   __syncthreads();
 
-  const int t0 = base + tid * kEPV;  // this thread's first token
-  const int valid = min(kEPV, A.V - t0);
   if (valid <= 0) return;
   uint32_t count[kEPV];
   float bias[kEPV];
@@ -206,36 +255,19 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
       }
     }
   }
-  const float rho = A.repetition ? A.repetition[b] : 1.0f;
-  const float pres = A.presence ? A.presence[b] : 0.0f;
-  const float freq = A.frequency ? A.frequency[b] : 0.0f;
-
-  const int64_t row_bytes = static_cast<int64_t>(A.V) * E::kBytes;
-  const char *in = A.in + b * A.in_stride_bytes + static_cast<int64_t>(t0) * E::kBytes;
-  char *out = A.out + b * A.out_stride_bytes + static_cast<int64_t>(t0) * E::kBytes;
-  const uint8_t *allowed =
-      A.allowed ? reinterpret_cast<const uint8_t *>(A.allowed + b * A.allowed_seq_stride) + t0 / 8 : nullptr;
-  const int nibble = t0 & 7;  // float32 vectors: half a byte of the mask
-  // kAhead rows at a time: their mask bytes, then their vectors, in flight together.
-  constexpr int kAhead = 4;
+  auto near = [&](int r) {  // some token of the row's path lies in the chunk (the same for the workgroup)
+    bool any = false;
+    if (paths)
+      for (int w = 0; w < words; ++w) any |= s_path[r][w] != 0;
+    return any;
+  };
   for (int r0 = row0; r0 < rows; r0 += kAhead) {
-    uint32_t m[kAhead];
-    uint4 x[kAhead];
-    bool near[kAhead];  // some token of the row's path lies in the chunk (the same for the workgroup)
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int r = min(r0 + u, rows - 1);
-      m[u] = kFull;
-      if (allowed) m[u] = (allowed[r * A.allowed_row_stride * 4] >> nibble) & kFull;
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int r = min(r0 + u, rows - 1);
-      near[u] = false;
-      if (paths)
-        for (int w = 0; w < words; ++w) near[u] |= s_path[r][w] != 0;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (m[u] != 0 && !(A.in_place && !touched && !near[u] && m[u] == kFull)) x[u] = load_elems<DT>(in + r * row_bytes, valid);
+    Rows now;
+    if (kInPlace) {
+      fetch(r0, now, [&](int r, uint32_t m) { return touched || m != kFull || near(r); });
+    } else {
+      now = next;
+      if (r0 + kAhead < rows) fetch(r0 + kAhead, next, every);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -243,7 +275,7 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
       if (r >= rows) break;
       uint32_t on_path[kEPV] = {};
       bool apply = touched;
-      if (near[u]) {
+      if (near(r)) {
         for (int w = 0; w < words; ++w)
           for (uint64_t bits = s_path[r][w]; bits; bits &= bits - 1) {
             const int d = s_node[w * 64 + __builtin_ctzll(bits)] - t0;
@@ -252,9 +284,9 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
             apply |= d >= 0 && d < kEPV;
           }
       }
-      if (A.in_place && !apply && m[u] == kFull) continue;
-      uint4 v = x[u];
-      if (apply && m[u] != 0) {
+      if (kInPlace && !apply && now.m[u] == kFull) continue;
+      uint4 v = now.x[u];
+      if (apply && now.m[u] != 0) {
         float y[kEPV];
         E::vec(v, y);
 #pragma unroll
@@ -270,8 +302,8 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
           w[i] = DT == DT_F32 ? enc<DT>(y[i % kEPV]) : enc<DT>(y[2 * i % kEPV]) | (enc<DT>(y[(2 * i + 1) % kEPV]) << 16);
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (m[u] != kFull) v = mask_elems<DT>(v, m[u]);
-      store_elems<DT>(out + r * row_bytes, v, valid);
+      if (now.m[u] != kFull) v = mask_elems<DT>(v, now.m[u]);
+      store_elems<DT, kStream>(out + r * row_bytes, v, valid);
     }
   }
 }
@@ -280,6 +312,22 @@ int adjust_chunks(int dtype, int V) {
   const int chunk = kAdjustThreads * (dtype == DT_F32 ? 4 : 8);
   return (V + chunk - 1) / chunk;
 }
+
+namespace {
+
+constexpr int64_t kAdjustStreamBytes = 256ll << 20;
+
+template <int kMode>
+void launch_type(int dtype, const AdjustArgs &A, dim3 grid, hipStream_t st) {
+  if (dtype == DT_F32)
+    hipLaunchKernelGGL((k_adjust_logits<DT_F32, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
+  else if (dtype == DT_BF16)
+    hipLaunchKernelGGL((k_adjust_logits<DT_BF16, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
+  else
+    hipLaunchKernelGGL((k_adjust_logits<DT_F16, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
+}
+
+}  // namespace
 
 void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st) {
   A.chunks = adjust_chunks(dtype, A.V);
@@ -291,12 +339,16 @@ void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st) {
   A.group_rows = static_cast<int32_t>((A.R + want - 1) / want);
   A.row_groups = (A.R + A.group_rows - 1) / A.group_rows;
   const dim3 grid(static_cast<unsigned>(items * A.row_groups));
-  if (dtype == DT_F32)
-    hipLaunchKernelGGL(k_adjust_logits<DT_F32>, grid, dim3(kAdjustThreads), 0, st, A);
-  else if (dtype == DT_BF16)
-    hipLaunchKernelGGL(k_adjust_logits<DT_BF16>, grid, dim3(kAdjustThreads), 0, st, A);
+  // Rows that do not fit the Infinity Cache between this call and the next
+  // pass through it with the nontemporal hint; smaller ones are left there for
+  // the verification that reads them.
+  const int64_t bytes = 2 * static_cast<int64_t>(B) * A.R * A.V * (dtype == DT_F32 ? 4 : 2);
+  if (A.in_place)
+    launch_type<ADJ_IN_PLACE>(dtype, A, grid, st);
+  else if (bytes > kAdjustStreamBytes)
+    launch_type<ADJ_STREAM>(dtype, A, grid, st);
   else
-    hipLaunchKernelGGL(k_adjust_logits<DT_F16>, grid, dim3(kAdjustThreads), 0, st, A);
+    launch_type<ADJ_COPY>(dtype, A, grid, st);
 }
 
 }  // namespace sv
