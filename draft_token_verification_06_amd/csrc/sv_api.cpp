@@ -633,9 +633,10 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
   if (M > 1 && (hidden_row_stride < K || hidden_row_stride % 8 != 0 || out_row_stride < V)) return SV_EINVAL;
   if (!aligned(hidden, 16) || !aligned(weights, 16) || !aligned(scales, 2) || !aligned(out, elem_bytes(out_dtype)))
     return SV_EINVAL;
-  // grid (column tiles, row tiles), both bounded by the smallest tile
-  if (!grid_fits((static_cast<int64_t>(V) + kLmQuantMinCols - 1) / kLmQuantMinCols, kLmQuantThreads) ||
-      (static_cast<int64_t>(M) + kLmQuantMinRows - 1) / kLmQuantMinRows > kMaxGridY)
+  // one workgroup per column and row tile (column tiles in eights), counted with the smallest tile
+  if (!grid_fits(((static_cast<int64_t>(V) + kLmQuantMinCols - 1) / kLmQuantMinCols + 7) / 8 * 8 *
+                     ((static_cast<int64_t>(M) + kLmQuantMinRows - 1) / kLmQuantMinRows),
+                 kLmQuantThreads))
     return SV_EINVAL;
   LmQuantArgs A{};
   A.h = static_cast<const uint16_t *>(hidden);

@@ -136,6 +136,7 @@ struct LmQuantArgs {
   void *out;  // [M] rows of out_stride, float32 or h's type
   int64_t out_stride;
   int32_t out_f32;
+  int32_t row_blocks;  // set by the launcher
 };
 constexpr int kLmQuantThreads = 256;
 constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 64;  // of a workgroup's tile

@@ -12,12 +12,12 @@
 //
 // v_mfma_f32_16x16x32: lane l supplies A[l % 16][8 (l / 16) + j] and the same
 // of B's column l % 16; accumulator register r of lane l is
-// C[4 (l / 16) + r][l % 16].  A lane loads 16 bytes (32 values) of one weight
-// row, four lanes 64 contiguous bytes; a 4 x 4 exchange of dwords between
-// those four lanes (two lane-swap instructions per pair) gives every lane the
-// 8 values of each 32-value step, in the rows' own layout.  Within 8 values
-// the order is 0 4 1 5 2 6 3 7 (the nibble pairs of a dword), and the hidden
-// rows are stored to LDS in that order.
+// C[4 (l / 16) + r][l % 16].  Weight rows are loaded 128 bytes at a time (8
+// lanes a row: whole cache lines; 16 rows of 64 bytes ran a third slower), and
+// pass through a piece of LDS of their wave's own to the lanes that multiply
+// them.  Within 8 values the order is 0 4 1 5 2 6 3 7 (the nibble pairs of a
+// dword), and the hidden rows are stored to LDS in that order, with the sums of
+// their groups.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,10 +29,11 @@ namespace sv {
 
 typedef __bf16 q_bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 q_f16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 q_bf16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 q_f16x2_t __attribute__((ext_vector_type(2)));
 typedef float q_f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kQStep = 128;               // K values per step: 16 bytes of weights per lane
-constexpr int kQRow = kQStep + 8;         // LDS row of a step: 16 bytes of padding spread the banks
 constexpr int kQThreads = kLmQuantThreads;
 constexpr int kQWaves = kQThreads / 64;
 
@@ -40,6 +41,10 @@ template <int DT> struct QuantElt;
 template <> struct QuantElt<DT_BF16> {
   static constexpr uint32_t kOne = 0x41804180u, kMask = 0x00780078u;  // 16.0 twice; the nibble's mantissa bits
   static constexpr int kShift = 3;
+  // c + the two values of a, in float32
+  __device__ static __forceinline__ float sum2(uint32_t a, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(q_bf16x2_t, a), __builtin_bit_cast(q_bf16x2_t, 0x3F803F80u), c, false);
+  }
   __device__ static __forceinline__ q_f32x4_t mma(uint4 a, uint4 b, q_f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(q_bf16x8_t, a), __builtin_bit_cast(q_bf16x8_t, b), c, 0, 0, 0);
   }
@@ -47,38 +52,52 @@ template <> struct QuantElt<DT_BF16> {
 template <> struct QuantElt<DT_F16> {
   static constexpr uint32_t kOne = 0x4C004C00u, kMask = 0x03C003C0u;
   static constexpr int kShift = 6;
+  __device__ static __forceinline__ float sum2(uint32_t a, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(q_f16x2_t, a), __builtin_bit_cast(q_f16x2_t, 0x3C003C00u), c, false);
+  }
   __device__ static __forceinline__ q_f32x4_t mma(uint4 a, uint4 b, q_f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(q_f16x8_t, a), __builtin_bit_cast(q_f16x8_t, b), c, 0, 0, 0);
   }
 };
 
-// The 8 values 16 + q of a dword of nibbles, in the order 0 4 1 5 2 6 3 7.
-template <int DT> __device__ __forceinline__ uint4 unpack8(uint32_t w) {
-  using Q = QuantElt<DT>;
+// The 8 values 16 + q of a dword of nibbles, in the order 0 4 1 5 2 6 3 7.  The
+// two constants come in registers, one of them scalar: only then do AND and OR
+// become one instruction.
+template <int DT> __device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t mask, uint32_t one) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int sh = Q::kShift - 4 * i;
-    o[i] = ((sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh >= 0 ? 0 : -sh)) & Q::kMask) | Q::kOne;
+    const int sh = QuantElt<DT>::kShift - 4 * i;
+    o[i] = ((sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh >= 0 ? 0 : -sh)) & mask) | one;
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Rows of 16 lanes hold 16-byte blocks b0..b3 of 64 bytes; afterwards register
-// s of the row g holds dword g of block s.
-__device__ __forceinline__ void exchange4(uint32_t (&r)[4]) {
+// Rows of 16 lanes (quads) hold the 16-byte blocks b0..b3 of a step, 32 values
+// each.  One MFMA multiplies one register of all four, so dwords are exchanged
+// between the quads until a register holds values of one group only: not at
+// all for groups of 128, between the halves of the wave for 64, and a full 4 x
+// 4 exchange for 32.  step_at() is where register s of a quad then lies.
+template <int kGroup> __device__ __forceinline__ void exchange(uint32_t (&r)[4]) {
+  if (kGroup <= 64)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const auto p = __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false);
-    r[i] = p[0];
-    r[i + 2] = p[1];
-  }
+    for (int i = 0; i < 2; ++i) {
+      const auto p = __builtin_amdgcn_permlane32_swap(r[i], r[i + 2], false, false);
+      r[i] = p[0];
+      r[i + 2] = p[1];
+    }
+  if (kGroup <= 32)
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const auto p = __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false);
-    r[i] = p[0];
-    r[i + 1] = p[1];
-  }
+    for (int i = 0; i < 4; i += 2) {
+      const auto p = __builtin_amdgcn_permlane16_swap(r[i], r[i + 1], false, false);
+      r[i] = p[0];
+      r[i + 1] = p[1];
+    }
+}
+template <int kGroup> __device__ __forceinline__ int step_at(int s, int quad) {
+  if (kGroup == 32) return s * 32 + quad * 8;
+  if (kGroup == 64) return ((s & 2) + (quad & 1)) * 32 + ((quad & 2) + (s & 1)) * 8;
+  return quad * 32 + s * 8;
 }
 
 // A workgroup barrier that orders LDS only: global loads stay in flight.
@@ -95,87 +114,110 @@ template <int DT> __device__ __forceinline__ void store_logit(const LmQuantArgs 
 }
 
 // MT x NT tiles of 16 x 16 per wave; the waves of a workgroup lie side by
-// side along V.  kGroup: values per scale.
-template <int DT, int MT, int NT, int kGroup, int PF>
-__global__ void __launch_bounds__(kQThreads) k_lm_quant(LmQuantArgs A) {
+// side along V and share the hidden rows, scales and zero points of kChunk
+// values of K in LDS.  kGroup: values per scale.  Weights go from memory to
+// registers a chunk ahead and stay in flight across the barriers.
+template <int DT, int MT, int NT, int kGroup, int kChunk>
+__global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(LmQuantArgs A) {
   using E = Elt<DT>;
   using Q = QuantElt<DT>;
-  constexpr int kRows = 16 * MT;
-  constexpr int kG = kQStep / kGroup;              // groups per step
-  constexpr int kSub = kGroup / 32;                // MFMA steps per group
-  constexpr int kLoads = kRows * (kQStep / 8) / kQThreads;  // 16-byte loads of a step's hidden rows per thread
-  __shared__ uint16_t s_a[2][kRows * kQRow];
-  __shared__ float s_sum[2][kG][kRows];  // sums of the hidden values per group
+  constexpr int kRows = 16 * MT, kCols = 16 * NT * kQWaves;
+  constexpr int kSteps = kChunk / kQStep;
+  constexpr int kG = kQStep / kGroup, kGC = kChunk / kGroup;  // groups per step and chunk
+  constexpr int kSub = kGroup / 32;                           // MFMAs per group and tile
+  constexpr int kARow = kChunk + 8;                           // 16 bytes of padding spread the banks
+  constexpr int kPieces = kChunk / 8;                         // 16-byte pieces per row of a chunk
+  constexpr int kRowsPerPass = kQThreads / kPieces;
+  constexpr int kLoads = kRows / kRowsPerPass;
+  constexpr int kScales = (kGC * kCols + kQThreads - 1) / kQThreads;
+  static_assert(kRows % kRowsPerPass == 0, "whole passes");
+  __shared__ uint16_t s_a[kRows * kARow];
+  __shared__ uint4 s_w[kQWaves][NT][128];  // a step's weights on their way to the lanes that multiply them
+  __shared__ float s_sum[kGC][kRows];    // sums of the hidden values per group
+  __shared__ float2 s_scale[kGC][kCols];  // scale, -(16 + zero)
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c16 = lane & 15, quad = lane >> 4;
-  const int row0 = blockIdx.y * kRows;
-  const int col0 = (blockIdx.x * kQWaves + wave) * (16 * NT);
-  const int steps = (A.K + kQStep - 1) / kQStep;
-  const int groups = A.K / kGroup;
+  // column tiles round the XCDs, the row blocks of one column tile on one XCD
+  const int ct = blockIdx.x / (8 * A.row_blocks) * 8 + blockIdx.x % 8;
+  const int row0 = blockIdx.x / 8 % A.row_blocks * kRows;
+  const int col0 = ct * kCols;
+  if (col0 >= A.V) return;
+  const int chunks = (A.K + kChunk - 1) / kChunk;
+  const int groups = A.K / kGroup, blocks = A.K / 32;
 
-  // hidden rows of a step: thread -> row (tid / 16) + 16 j, 16-byte piece tid % 16
   uint4 ra[kLoads];
-  const int piece = tid & 15;
-  const uint16_t *hrow[kLoads];
-  bool live[kLoads];
-#pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int r = row0 + (tid >> 4) + 16 * j;
-    live[j] = r < A.M;
-    hrow[j] = A.h + (live[j] ? r : 0) * A.lda + piece * 8;
-  }
-  auto load_a = [&](int step) {
-    const bool in = step * kQStep + piece * 8 < A.K;
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-      ra[j] = in && live[j] ? load_vec(hrow[j] + step * kQStep) : make_uint4(0, 0, 0, 0);
-  };
-  auto store_a = [&](int buf) {
+  const int piece = tid % kPieces, first = tid / kPieces;
+  auto load_a = [&](int chunk) {
+    const bool in = chunk * kChunk + piece * 8 < A.K;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      float x[8];
-      E::vec(ra[j], x);
-      float s = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+      const int r = row0 + first + j * kRowsPerPass;
+      ra[j] = make_uint4(0, 0, 0, 0);
+      if (in && r < A.M) ra[j] = load_vec(A.h + r * A.lda + chunk * kChunk + piece * 8);
+    }
+  };
+  auto store_a = [&]() {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int r = first + j * kRowsPerPass;
+      if (row0 + r >= A.M) continue;  // these rows were zeroed once
+      float s = Q::sum2(ra[j].x, Q::sum2(ra[j].y, Q::sum2(ra[j].z, Q::sum2(ra[j].w, 0.0f))));
       s += dpp_f32<0xB1>(s);
       s += dpp_f32<0x4E>(s);
       if (kGroup >= 64) s += dpp_f32<0x141>(s);   // the other half of 8 lanes
       if (kGroup >= 128) s += dpp_f32<0x140>(s);  // the other half of 16 lanes
-      const int r = (tid >> 4) + 16 * j;
-      if (piece % (kGroup / 8) == 0) s_sum[buf][piece / (kGroup / 8)][r] = s;
+      if (piece % (kGroup / 8) == 0) s_sum[piece / (kGroup / 8)][r] = s;
       const uint4 v = ra[j];
       const uint4 p = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
                                  __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
-      *reinterpret_cast<uint4 *>(&s_a[buf][r * kQRow + piece * 8]) = p;
+      *reinterpret_cast<uint4 *>(&s_a[r * kARow + piece * 8]) = p;
     }
   };
-
-  // weight rows of this lane's columns (past V: the last row, never stored)
-  const uint8_t *wrow[NT];
-  const uint16_t *srow[NT];
-  const uint8_t *zrow[NT];
-  uint4 rw[PF][NT];
-  uint32_t rs[PF][NT][kG], rz[PF][NT][kG];
+  uint32_t rs[kScales], rz[kScales];
+  auto load_scales = [&](int chunk) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t v = min(col0 + t * 16 + c16, A.V - 1);
-    wrow[t] = A.w + v * (A.K / 2);
-    srow[t] = A.scales + v * groups;
-    zrow[t] = A.zeros ? A.zeros + v * groups : nullptr;
-  }
-  auto load_w = [&](int slot, int step) {
-    // blocks and groups past the end meet zero hidden values: any in-bounds data will do
-    const int block = min(step * 4 + quad, A.K / 32 - 1);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      rw[slot][t] = load_vec(wrow[t] + block * 16);
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        const int at = min(step * kG + g, groups - 1);
-        rs[slot][t][g] = E::raw(srow[t], at);
-        rz[slot][t][g] = A.zeros ? as_global<uint8_t>(zrow[t])[at] : 8u;
-      }
+    for (int j = 0; j < kScales; ++j) {
+      const int x = tid + j * kQThreads;
+      const int64_t v = min(col0 + x / kGC, A.V - 1);
+      const int g = min(chunk * kGC + x % kGC, groups - 1);
+      rs[j] = E::raw(A.scales, v * groups + g);
+      rz[j] = A.zeros ? as_global<uint8_t>(A.zeros)[v * groups + g] : 8u;
     }
   };
+  auto store_scales = [&]() {
+#pragma unroll
+    for (int j = 0; j < kScales; ++j) {
+      const int x = tid + j * kQThreads;
+      if (x < kGC * kCols) s_scale[x % kGC][x / kGC] = make_float2(E::dec(rs[j]), -16.0f - static_cast<float>(rz[j]));
+    }
+  };
+  // Weights arrive two steps at a time: one load takes 8 rows of 128 bytes (a
+  // cache line each), two loads the 16 rows of a tile.  Rows past V: the last
+  // row, never stored.  Where K ends inside the two steps, blocks past it meet
+  // zero hidden values, and the row's last block stands in for them.
+  const uint8_t *wtile = A.w + col0 * static_cast<int64_t>(A.K / 2);
+  const int last = (A.K - 1) / (2 * kQStep);
+  uint32_t woff[NT][2], wtail[NT][2];
+  uint4 rw[kSteps][NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = i * 8 + (lane >> 3), block = (lane & 7) ^ (n >> 1);
+      woff[t][i] = static_cast<uint32_t>(min(wave * NT * 16 + t * 16 + n, A.V - 1 - col0)) * (A.K / 2) + block * 16;
+      wtail[t][i] = woff[t][i] - max(last * 8 + block - (blocks - 1), 0) * 16;
+    }
+  auto load_w = [&](int slot, int pair) {
+    const int at = min(pair, last);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        rw[slot + i][t] = load_stream(reinterpret_cast<const uint4 *>(wtile + at * 128 + (at == last ? wtail[t][i] : woff[t][i])));
+  };
+  uint32_t mask, one;
+  asm("s_mov_b32 %0, %1" : "=s"(mask) : "i"(Q::kMask));
+  asm("v_mov_b32 %0, %1" : "=v"(one) : "i"(Q::kOne));
 
   q_f32x4_t acc[MT][NT];
 #pragma unroll
@@ -184,54 +226,57 @@ __global__ void __launch_bounds__(kQThreads) k_lm_quant(LmQuantArgs A) {
     for (int t = 0; t < NT; ++t) acc[m][t] = q_f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   load_a(0);
+  load_scales(0);
 #pragma unroll
-  for (int u = 0; u < PF; ++u) load_w(u, min(u, steps - 1));
-  store_a(0);
-  load_a(min(1, steps - 1));
-  lds_barrier();
-  for (int i0 = 0; i0 < steps; i0 += PF) {
+  for (int u = 0; u < kSteps; u += 2) load_w(u, u / 2);
+  for (int r = A.M - row0 + wave; r < kRows; r += kQWaves) {
+    for (int x = lane; x < kPieces; x += 64) *reinterpret_cast<uint4 *>(&s_a[r * kARow + x * 8]) = make_uint4(0, 0, 0, 0);
+    if (lane < kGC) s_sum[lane][r] = 0.0f;
+  }
+  for (int c = 0; c < chunks; ++c) {
+    if (c > 0) lds_barrier();  // every wave is done with the previous chunk
+    store_a();
+    store_scales();
+    load_a(min(c + 1, chunks - 1));
+    load_scales(min(c + 1, chunks - 1));
+    lds_barrier();
 #pragma unroll
-    for (int u = 0; u < PF; ++u) {
-      const int i = i0 + u;
-      if (i >= steps) break;
-      const int buf = i & 1;
-      // Stage the next step while this one multiplies: the buffer it goes to
-      // was last read before the barrier that ended the previous step.
-      store_a(buf ^ 1);
-      load_a(min(i + 2, steps - 1));
+    for (int u = 0; u < kSteps; ++u) {
       uint32_t w[NT][4];
-      float sc[NT][kG], zp[NT][kG];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        w[t][0] = rw[u][t].x;
-        w[t][1] = rw[u][t].y;
-        w[t][2] = rw[u][t].z;
-        w[t][3] = rw[u][t].w;
-        exchange4(w[t]);
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          sc[t][g] = E::dec(rs[u][t][g]);
-          zp[t][g] = -16.0f - static_cast<float>(rz[u][t][g]);
+        if (u % 2 == 0) {
+          s_w[wave][t][lane] = rw[u][t];
+          s_w[wave][t][64 + lane] = rw[u + 1][t];
         }
+        const uint4 x = s_w[wave][t][c16 * 8 + ((u % 2 * 4 + quad) ^ (c16 >> 1))];
+        w[t][0] = x.x;
+        w[t][1] = x.y;
+        w[t][2] = x.z;
+        w[t][3] = x.w;
+        exchange<kGroup>(w[t]);
       }
-      load_w(u, min(i + PF, steps - 1));
+      if (u % 2 == 0) load_w(u, ((c + 1) * kSteps + u) / 2);  // past the end: the last steps again, unused
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         q_f32x4_t part[MT][NT];
+        float2 sc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sc[t] = s_scale[u * kG + g][(wave * NT + t) * 16 + c16];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const float4 hs = *reinterpret_cast<const float4 *>(&s_sum[buf][g][m * 16 + quad * 4]);
+          const float4 hs = *reinterpret_cast<const float4 *>(&s_sum[u * kG + g][m * 16 + quad * 4]);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) part[m][t] = q_f32x4_t{zp[t][g] * hs.x, zp[t][g] * hs.y, zp[t][g] * hs.z, zp[t][g] * hs.w};
+          for (int t = 0; t < NT; ++t) part[m][t] = q_f32x4_t{sc[t].y * hs.x, sc[t].y * hs.y, sc[t].y * hs.z, sc[t].y * hs.w};
         }
 #pragma unroll
         for (int s = g * kSub; s < (g + 1) * kSub; ++s) {
           uint4 b[NT];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) b[t] = unpack8<DT>(w[t][s]);
+          for (int t = 0; t < NT; ++t) b[t] = unpack8<DT>(w[t][s], mask, one);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(&s_a[buf][(m * 16 + c16) * kQRow + s * 32 + quad * 8]);
+            const uint4 a = *reinterpret_cast<const uint4 *>(&s_a[(m * 16 + c16) * kARow + u * kQStep + step_at<kGroup>(s, quad)]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) part[m][t] = Q::mma(a, b[t], part[m][t]);
           }
@@ -241,14 +286,15 @@ __global__ void __launch_bounds__(kQThreads) k_lm_quant(LmQuantArgs A) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][t][e] = __builtin_fmaf(sc[t][g], part[m][t][e], acc[m][t][e]);
+            for (int e = 0; e < 4; ++e) acc[m][t][e] = __builtin_fmaf(sc[t].x, part[m][t][e], acc[m][t][e]);
+        // one group's partial sums at a time: interleaving several would spill
+        if (MT * NT > 2) __builtin_amdgcn_sched_barrier(0);
       }
-      lds_barrier();
     }
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int v = col0 + t * 16 + c16;
+    const int v = col0 + (wave * NT + t) * 16 + c16;
     if (v >= A.V) continue;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -262,25 +308,33 @@ __global__ void __launch_bounds__(kQThreads) k_lm_quant(LmQuantArgs A) {
 
 namespace {
 
-template <int DT, int MT, int NT, int PF>
-void launch_tiles(const LmQuantArgs &A, hipStream_t st) {
-  const dim3 grid((A.V + 16 * NT * kQWaves - 1) / (16 * NT * kQWaves), (A.M + 16 * MT - 1) / (16 * MT));
+template <int DT, int MT, int NT, int kChunk>
+void launch_tiles(LmQuantArgs A, hipStream_t st) {
+  const int cols = 16 * NT * kQWaves;
+  A.row_blocks = (A.M + 16 * MT - 1) / (16 * MT);
+  const dim3 grid(static_cast<unsigned>((A.V + cols - 1) / cols + 7) / 8 * 8 * A.row_blocks);
   if (A.group == 32)
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 32, PF>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 32, kChunk>), grid, dim3(kQThreads), 0, st, A);
   else if (A.group == 64)
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, PF>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, kChunk>), grid, dim3(kQThreads), 0, st, A);
   else
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, PF>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, kChunk>), grid, dim3(kQThreads), 0, st, A);
 }
 
+// Tiles by rows: the fewest 16-row tiles that hold them, as weights are
+// unpacked once per row block; past 64 rows in blocks of 64 or 80, whichever
+// pads less.
 template <int DT>
 void launch_type(const LmQuantArgs &A, hipStream_t st) {
-  if (A.M <= 16)
-    launch_tiles<DT, 1, 1, 4>(A, st);
-  else if (A.M <= 32)
-    launch_tiles<DT, 2, 1, 4>(A, st);
+  const int64_t M = A.M;
+  if (M <= 16)
+    launch_tiles<DT, 1, 2, 256>(A, st);
+  else if (M <= 32)
+    launch_tiles<DT, 2, 2, 256>(A, st);
+  else if ((M + 63) / 64 * 64 <= (M + 79) / 80 * 80)
+    launch_tiles<DT, 4, 2, 256>(A, st);
   else
-    launch_tiles<DT, 4, 2, 2>(A, st);
+    launch_tiles<DT, 5, 2, 256>(A, st);
 }
 
 }  // namespace
