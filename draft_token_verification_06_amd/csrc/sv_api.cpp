@@ -2,6 +2,8 @@
 // carving and kernel dispatch.  No allocation, no synchronisation; every
 // launch goes to the caller's stream.
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -736,7 +738,9 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
   A.own_parts = L.own_parts;
   A.own_chunk = L.own_chunk;
   A.own_tiles = L.own_tiles;
-  A.scale_log2 = scale * 1.4426950408889634f;
+  // never zero: masked products are -inf, and 0 * -inf is no number
+  A.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  A.negate = scale < 0.0f;
   A.part_o = static_cast<float *>(workspace);
   A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + L.ml_off);
   A.out = static_cast<uint16_t *>(out);

@@ -78,7 +78,11 @@ struct Item {
   int part;
 };
 
-__device__ __forceinline__ float swap_half(float x) { return __shfl_xor(x, 32); }
+// The values of lanes l and l ^ 32 (in either order): one lane-swap instruction.
+__device__ __forceinline__ float2 both_halves(float x) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return make_float2(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
 
 template <int D> constexpr int at_lds_row() { return D + 8; }  // elements; 16 bytes of padding spread the banks
 template <int D, int WQ> constexpr int at_tile_keys() { return WQ == 1 ? 128 : 64; }
@@ -86,6 +90,22 @@ template <int D, int WQ> constexpr size_t at_tile_bytes() {
   const size_t kv = 2 * static_cast<size_t>(at_tile_keys<D, WQ>()) * at_lds_row<D>() * 2;
   const size_t merge = WQ == 1 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
   return kv > merge ? kv : merge;
+}
+
+// a (values d .. d + 3 of a row with ancestor set anc) plus the infinities and
+// NaN among the row's own keys' values.
+template <int DT> __device__ float4 add_odd(const Item &it, const uint32_t *anc, int d, float4 a) {
+  for (int key = max(it.k0, it.draft); key < it.k1; ++key) {
+    const int own = key - it.draft;
+    if (!((anc[own >> 5] >> (own & 31)) & 1)) continue;
+    const uint2 w = *reinterpret_cast<const uint2 *>(it.v + key * it.tok_stride + d);
+    const uint32_t b[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+    float *x = &a.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((b[k] & AtElt<DT>::kExp) == AtElt<DT>::kExp) x[k] += Elt<DT>::dec(b[k]);
+  }
+  return a;
 }
 
 template <int DT, int D, int WQ>
@@ -113,7 +133,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   {
     const uint16_t *p = A.q + qrow * A.q_row_stride + head * D + half * 8;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) qf[s] = load_vec(p + s * 16);
+    for (int s = 0; s < D / 16; ++s) {
+      qf[s] = load_vec(p + s * 16);
+      // a negative scale acts on the queries' signs, so that larger products are larger scores
+      if (A.negate) qf[s] = make_uint4(qf[s].x ^ 0x80008000u, qf[s].y ^ 0x80008000u, qf[s].z ^ 0x80008000u, qf[s].w ^ 0x80008000u);
+    }
   }
   const int r = static_cast<int>(qrow % A.R);
 
@@ -135,11 +159,13 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
       rv[j] = load_vec(it.v + key * it.tok_stride + piece * 8);
     }
   };
+  bool odd = false;
   load(it.k0);
   for (int t0 = it.k0; t0 < it.k1; t0 += KT) {
     // Keys past the range get zero values: their exponentials are zero, but
     // zero times what a cache holds behind its end need not be.
-    bool odd = false;  // a value of the step's own keys is infinite or NaN
+    // Infinities and NaN among the step's own values, which must reach only the
+    // rows that see them, are left out here and added at the end.
     const bool masked = t0 + KT > it.draft;
     __syncthreads();
 #pragma unroll
@@ -147,98 +173,92 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
       const int row = first + j * kRowsPerPass;
       uint4 v = rv[j];
       if (t0 + row >= it.k1) v = make_uint4(0, 0, 0, 0);
-      if (masked) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      if (masked && t0 + row >= it.draft && t0 + row < it.k1) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          odd |= (w[k] & T::kExp) == T::kExp || ((w[k] >> 16) & T::kExp) == T::kExp;
+        for (int k = 0; k < 4; ++k) {
+          if ((w[k] & T::kExp) == T::kExp) w[k] &= 0xFFFF0000u, odd = true;
+          if (((w[k] >> 16) & T::kExp) == T::kExp) w[k] &= 0xFFFFu, odd = true;
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
       }
       *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 8) = rk[j];
       *reinterpret_cast<uint4 *>(s_v + row * kRow + piece * 8) = v;
     }
-    bool slow = false;
-    if (masked) slow = __syncthreads_or(odd);
-    else __syncthreads();
+    __syncthreads();
     if (t0 + KT < it.k1) load(t0 + KT);
+    if (t0 + wk * SB * 32 >= it.k1) continue;  // nothing of this tile for this wave
+    // raw products of the wave's blocks of 32 keys
+    at_f32x16_t s[SB];
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb) {
-      const int kb = (wk * SB + sb) * 32;  // this block's first key in the tile
-      if (t0 + kb >= it.k1) continue;
-      at_f32x16_t s;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+      for (int e = 0; e < 16; ++e) s[sb][e] = 0.0f;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
-        s = T::mma(*reinterpret_cast<const uint4 *>(s_k + (kb + q32) * kRow + d * 16 + half * 8), qf[d], s);
-      float x[16];
+        s[sb] = T::mma(*reinterpret_cast<const uint4 *>(s_k + ((wk * SB + sb) * 32 + q32) * kRow + d * 16 + half * 8), qf[d], s[sb]);
+    }
+    if (masked || t0 + KT > it.k1) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = s[e] * A.scale_log2;
-      if (t0 + kb + 32 > it.draft || t0 + kb + 32 > it.k1) {
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int key = t0 + kb + 8 * (e >> 2) + 4 * half + (e & 3);
+          const int key = t0 + (wk * SB + sb) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
           const int own = key - it.draft;
           const bool ok = key < it.k1 && (own < 0 || ((s_anc[r][(own & 255) >> 5] >> (own & 31)) & 1));
-          x[e] = ok ? x[e] : kNegInf;
+          s[sb][e] = ok ? s[sb][e] : kNegInf;
         }
-      }
-      float top = x[0];
+    }
+    float top = kNegInf;
 #pragma unroll
-      for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-      top = fmaxf(top, swap_half(top));
-      const float mn = fmaxf(m, top);
-      const float mu = mn == kNegInf ? 0.0f : mn;
-      const float alpha = exp2_fast(m - mu);
-      m = mn;
-      float sum = 0.0f;
+    for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = exp2_fast(x[e] - mu);
-        sum += x[e];
-      }
-      l = l * alpha + sum;
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[sb][e]);
+    const float2 tops = both_halves(top);
+    const float mn = fmaxf(m, fmaxf(tops.x, tops.y));
+    // Outputs are rescaled only when some row's maximum rose: 1 is exact.
+    if (__any(mn > m)) {
+      const float alpha = m == kNegInf ? 0.0f : exp2_fast((m - mn) * A.scale_log2);
+      l *= alpha;
 #pragma unroll
       for (int t = 0; t < D / 32; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[t][e] *= alpha;
-      if (!slow) {
+      m = mn;
+    }
+    const float mu = m == kNegInf ? 0.0f : m * A.scale_log2;
+    float sum = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const uint4 p = make_uint4(T::pack(x[8 * ks], x[8 * ks + 1]), T::pack(x[8 * ks + 2], x[8 * ks + 3]),
-                                     T::pack(x[8 * ks + 4], x[8 * ks + 5]), T::pack(x[8 * ks + 6], x[8 * ks + 7]));
-          // lane l: block of 4 keys x 16 values; its address is row (l % 16) / 4, values 4 (l % 4)
-          const uint16_t *base = s_v + (kb + ks * 16 + 4 * half + ((lane & 15) >> 2)) * kRow + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-          for (int t = 0; t < D / 32; ++t) {
-            const at_i16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32));
-            const at_i16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32 + 8 * kRow));
-            const uint2 u0 = __builtin_bit_cast(uint2, a0), u1 = __builtin_bit_cast(uint2, a1);
-            o[t] = T::mma(make_uint4(u0.x, u0.y, u1.x, u1.y), p, o[t]);
-          }
-        }
-      } else {
-        // Some own key holds an infinity or NaN, which must reach only the
-        // rows that see it: one key at a time, skipping zero exponentials.
-        for (int e = 0; e < 16; ++e) {
-          const float mine = x[0], other = swap_half(mine);
+      for (int e = 0; e < 16; ++e) {
+        s[sb][e] = exp2_fast(__builtin_fmaf(s[sb][e], A.scale_log2, -mu));
+        sum += s[sb][e];
+      }
+    l += sum;
 #pragma unroll
-          for (int z = 0; z < 15; ++z) x[z] = x[z + 1];
-          for (int hh = 0; hh < 2; ++hh) {
-            const float p = hh == half ? mine : other;
-            const uint16_t *vrow = s_v + (kb + 8 * (e >> 2) + 4 * hh + (e & 3)) * kRow + 4 * half;
-            if (p != 0.0f) {
+    for (int sb = 0; sb < SB; ++sb) {
+      const int kb = (wk * SB + sb) * 32;  // this block's first key in the tile
 #pragma unroll
-              for (int t = 0; t < D / 32; ++t)
+      for (int ks = 0; ks < 2; ++ks) {
+        const uint4 p = make_uint4(T::pack(s[sb][8 * ks], s[sb][8 * ks + 1]), T::pack(s[sb][8 * ks + 2], s[sb][8 * ks + 3]),
+                                   T::pack(s[sb][8 * ks + 4], s[sb][8 * ks + 5]), T::pack(s[sb][8 * ks + 6], s[sb][8 * ks + 7]));
+        // lane l: block of 4 keys x 16 values; its address is row (l % 16) / 4, values 4 (l % 4)
+        const uint16_t *base = s_v + (kb + ks * 16 + 4 * half + ((lane & 15) >> 2)) * kRow + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
 #pragma unroll
-                for (int f = 0; f < 16; ++f)
-                  o[t][f] += p * Elt<DT>::dec(vrow[t * 32 + 8 * (f >> 2) + (f & 3)]);
-            }
-          }
+        for (int t = 0; t < D / 32; ++t) {
+          const at_i16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32));
+          const at_i16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32 + 8 * kRow));
+          const uint2 u0 = __builtin_bit_cast(uint2, a0), u1 = __builtin_bit_cast(uint2, a1);
+          o[t] = T::mma(make_uint4(u0.x, u0.y, u1.x, u1.y), p, o[t]);
         }
       }
     }
   }
-  l += swap_half(l);
+  // (also: every wave is done with the tiles)
+  const bool any_odd = it.k1 > it.draft ? __syncthreads_or(odd) : (__syncthreads(), false);
+  const float2 ls = both_halves(l);
+  l = ls.x + ls.y;
 
   const int64_t rows_all = static_cast<int64_t>(A.B) * A.R * A.Hq;
   if (WQ == 4) {
@@ -248,9 +268,12 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
 #pragma unroll
       for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          *reinterpret_cast<float4 *>(po + t * 32 + 8 * f + 4 * half) =
-              make_float4(o[t][4 * f], o[t][4 * f + 1], o[t][4 * f + 2], o[t][4 * f + 3]);
+        for (int f = 0; f < 4; ++f) {
+          float4 a = make_float4(o[t][4 * f], o[t][4 * f + 1], o[t][4 * f + 2], o[t][4 * f + 3]);
+          const int d = t * 32 + 8 * f + 4 * half;
+          if (any_odd) a = add_odd<DT>(it, s_anc[r], d, a);
+          *reinterpret_cast<float4 *>(po + d) = a;
+        }
       if (half == 0) A.part_ml[at] = make_float2(m, l);
     }
     return;
@@ -258,11 +281,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   // The waves hold the same rows over different keys: joined in wave order.
   float *s_o = reinterpret_cast<float *>(lds);
   if (half == 0) s_ml[wave][q32] = make_float2(m, l);
-  __syncthreads();  // also: every wave is done with the tiles
+  __syncthreads();
   float M = kNegInf;
 #pragma unroll
   for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][q32].x);
-  const float f = m == kNegInf ? 0.0f : exp2_fast(m - M);
+  const float f = m == kNegInf ? 0.0f : exp2_fast((m - M) * A.scale_log2);
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
@@ -280,6 +303,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
       const float4 b = *reinterpret_cast<const float4 *>(s_o + (w * 32 + q) * (D + 4) + c * 4);
       a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
     }
+    if (any_odd) a = add_odd<DT>(it, s_anc[qi / A.n], c * 4, a);
     const int64_t at = it.part * rows_all + (it.base_row + qi / A.n) * A.Hq + it.kvh * A.n + qi % A.n;
     *reinterpret_cast<float4 *>(A.part_o + at * D + c * 4) = a;
     if (c == 0) {
@@ -288,7 +312,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
       for (int w = 0; w < 4; ++w) Mq = fmaxf(Mq, s_ml[w][q].x);
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        if (s_ml[w][q].x != kNegInf) L += s_ml[w][q].y * exp2_fast(s_ml[w][q].x - Mq);
+        if (s_ml[w][q].x != kNegInf) L += s_ml[w][q].y * exp2_fast((s_ml[w][q].x - Mq) * A.scale_log2);
       A.part_ml[at] = make_float2(Mq, L);
     }
   }
@@ -300,10 +324,11 @@ __device__ __forceinline__ int live_rows(const AttendArgs &A, int b) {
 }
 
 template <int DT, int D, int WQP, int WQO>
-__global__ void __launch_bounds__(kAtThreads) k_attend(AttendArgs A) {
+__global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
   constexpr size_t kBytes = at_tile_bytes<D, WQP>() > at_tile_bytes<D, WQO>() ? at_tile_bytes<D, WQP>() : at_tile_bytes<D, WQO>();
   __shared__ uint4 s_tile[kBytes / sizeof(uint4)];
   __shared__ uint32_t s_anc[kTreeMaxNodes][8];
+  __shared__ int16_t s_parent[kTreeMaxNodes];
   __shared__ float2 s_ml[4][32];
   char *lds = reinterpret_cast<char *>(s_tile);
   Item it{};
@@ -354,13 +379,18 @@ __global__ void __launch_bounds__(kAtThreads) k_attend(AttendArgs A) {
   it.v = A.v + b * A.seq_stride + it.kvh * D;
   it.tok_stride = A.tok_stride;
   if (it.k1 > len) {
-    // ancestor sets of the rows, one row per thread
+    // ancestor sets of the rows, one row per thread; parents go to LDS first,
+    // as a walk through the argument block would cost a trip to memory a step
+    if (A.tree) {
+      for (int v = threadIdx.x; v < A.R; v += kAtThreads) s_parent[v] = A.parent[v];
+      __syncthreads();
+    }
     for (int v = threadIdx.x; v < A.R; v += kAtThreads) {
       uint32_t w[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) w[x] = 0;
       if (A.tree) {
-        for (int u = v; u >= 0; u = A.parent[u])
+        for (int u = v; u >= 0; u = s_parent[u])
 #pragma unroll
           for (int x = 0; x < 8; ++x) w[x] |= x == (u >> 5) ? 1u << (u & 31) : 0u;
       } else {
@@ -403,7 +433,7 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendArgs A) {
     for (int p = 0; p < parts; ++p) M = fmaxf(M, A.part_ml[p * rows + row].x);
     for (int p = 0; p < parts; ++p) {
       const float2 ml = A.part_ml[p * rows + row];
-      const float f = ml.x == kNegInf ? 0.0f : exp2_fast(ml.x - M);
+      const float f = ml.x == kNegInf ? 0.0f : exp2_fast((ml.x - M) * A.scale_log2);
       L += f * ml.y;
       const float *po = A.part_o + (p * rows + row) * D + lane * E;
 #pragma unroll
@@ -413,7 +443,7 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendArgs A) {
   uint16_t *out = A.out + row * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = AtElt<DT>::bits(acc[e] / L);
-  if (A.lse && lane == 0) A.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+  if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L)) * 0.6931471805599453f;
 }
 
 namespace {

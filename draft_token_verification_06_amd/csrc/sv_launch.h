@@ -155,9 +155,10 @@ struct AttendArgs {
   int32_t P, max_ctx;
   int32_t prefix_parts, prefix_chunk, prefix_items;
   int32_t own_parts, own_chunk, own_tiles;
-  float scale_log2;  // score scale times log2(e)
+  float scale_log2;  // magnitude of the score scale, times log2(e)
+  int32_t negate;    // the scale is negative
   float *part_o;     // [parts][B R Hq][D] unnormalised outputs
-  float2 *part_ml;   // [parts][B R Hq] (maximum, sum)
+  float2 *part_ml;   // [parts][B R Hq] (largest product, sum)
   uint16_t *out;     // [B][R][Hq][D]
   float *lse;        // [B][R][Hq] or null
   int32_t tree;

@@ -166,8 +166,9 @@ inline LmLayout make_lm_layout(int64_t B, int32_t gamma, int32_t V) {
 // share the rows); keys are split into ranges until the items fill the chip.
 constexpr int kAttendThreads = 256;
 constexpr int kAttendWideRows = 64;        // more stacked rows than this: tiles of 128
-constexpr int64_t kAttendItems = 1024;     // items wanted per launch (2 workgroups on each of 256 CUs, twice)
-constexpr int kAttendMinKeys = 256;        // keys per range at least
+constexpr int64_t kAttendSlots = 512;      // workgroups that run at once: 2 on each of 256 CUs
+constexpr int kAttendMinKeys = 128;        // keys per range at least (a tile)
+constexpr int kAttendItemKeys = 192;       // an item's own cost (start, join), in keys
 struct AttendPlan {
   int prefix_wide, own_wide;
   int prefix_parts, prefix_chunk, own_parts, own_chunk, own_tiles;
@@ -175,15 +176,28 @@ struct AttendPlan {
   size_t ml_off, total;
 };
 
-inline void split_keys(int64_t keys, int64_t items_per_range, int *parts, int *chunk) {
-  int64_t want = (kAttendItems + items_per_range - 1) / items_per_range;
-  const int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys;
-  if (want > most) want = most;
-  if (want < 1) want = 1;
-  int64_t c = (keys + want - 1) / want;
-  c = (c + 127) / 128 * 128;
-  *chunk = static_cast<int>(c);
-  *parts = static_cast<int>((keys + c - 1) / c);
+// Ranges of `keys` keys for `items` items each: the number that ends first when
+// rounds of kAttendSlots items take turns.  balance: lengths differ, so items
+// are kept at 512 keys where there are enough for four rounds.
+inline void split_keys(int64_t keys, int64_t items, bool balance, int *parts, int *chunk) {
+  int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys;
+  if (most > 256) most = 256;
+  int64_t best = -1;
+  auto chunk_of = [&](int64_t p) { return ((keys + p - 1) / p + 127) / 128 * 128; };
+  for (int64_t p = 1; p <= most; ++p) {
+    const int64_t rounds = (items * p + kAttendSlots - 1) / kAttendSlots;
+    const int64_t cost = rounds * (chunk_of(p) + kAttendItemKeys);
+    if (best < 0 || cost < best) {
+      best = cost;
+      *chunk = static_cast<int>(chunk_of(p));
+    }
+  }
+  if (balance) {
+    int64_t p = (4 * kAttendSlots + items - 1) / items;
+    if (p > (keys + 511) / 512) p = (keys + 511) / 512;
+    if (chunk_of(p) < *chunk) *chunk = static_cast<int>(chunk_of(p));
+  }
+  *parts = static_cast<int>((keys + *chunk - 1) / *chunk);
 }
 
 inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx) {
@@ -195,11 +209,11 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
   L.prefix_chunk = 1;
   if (P > 0) {
     const int64_t tiles = (all + (L.prefix_wide ? 127 : 31)) / (L.prefix_wide ? 128 : 32);
-    split_keys(P, tiles * Hkv, &L.prefix_parts, &L.prefix_chunk);
+    split_keys(P, tiles * Hkv, false, &L.prefix_parts, &L.prefix_chunk);
     L.prefix_items = tiles * Hkv * L.prefix_parts;
   }
   L.own_tiles = static_cast<int>((own + (L.own_wide ? 127 : 31)) / (L.own_wide ? 128 : 32));
-  split_keys(max_ctx + R, B * Hkv * L.own_tiles, &L.own_parts, &L.own_chunk);
+  split_keys(max_ctx + R, B * Hkv * L.own_tiles, true, &L.own_parts, &L.own_chunk);
   L.own_blocks = (B * Hkv * L.own_parts + 7) / 8 * 8 * L.own_tiles;
   const size_t slots = static_cast<size_t>(L.prefix_parts + L.own_parts) * static_cast<size_t>(B * R * Hq);
   L.ml_off = align256(slots * static_cast<size_t>(D) * sizeof(float));
