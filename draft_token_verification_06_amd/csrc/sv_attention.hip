@@ -20,8 +20,8 @@
 //
 // Rows of a group of query heads that share a kv head are stacked into one
 // tile.  A workgroup's four waves split the tile's rows (WQ = 4: 128 rows, for
-// the prefix of a batch) or the keys of a tile (WQ = 1: 32 rows, for the few
-// rows of one sequence, where cache bandwidth is the bound).
+// the prefix of a batch), the keys of a tile (WQ = 1: 32 rows, for the few rows
+// of one sequence, where cache bandwidth is the bound), or both (WQ = 2: 64).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -88,7 +88,7 @@ template <int D> constexpr int at_lds_row() { return D + 8; }  // elements; 16 b
 template <int D, int WQ> constexpr int at_tile_keys() { return WQ == 1 ? 128 : 64; }
 template <int D, int WQ> constexpr size_t at_tile_bytes() {
   const size_t kv = 2 * static_cast<size_t>(at_tile_keys<D, WQ>()) * at_lds_row<D>() * 2;
-  const size_t merge = WQ == 1 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
+  const size_t merge = WQ < 4 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
   return kv > merge ? kv : merge;
 }
 
@@ -110,7 +110,7 @@ template <int DT> __device__ float4 add_odd(const Item &it, const uint32_t *anc,
 
 template <int DT, int D, int WQ>
 __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it, char *lds, const uint32_t (*s_anc)[8],
-                                            float2 (*s_ml)[32]) {
+                                            float2 *s_ml) {
   using T = AtElt<DT>;
   constexpr int WK = 4 / WQ;
   constexpr int KT = at_tile_keys<D, WQ>();
@@ -278,29 +278,31 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
     }
     return;
   }
-  // The waves hold the same rows over different keys: joined in wave order.
+  // WK waves hold the same rows over different keys: joined in wave order.
+  constexpr int kRows = 32 * WQ;
   float *s_o = reinterpret_cast<float *>(lds);
-  if (half == 0) s_ml[wave][q32] = make_float2(m, l);
+  const int row = wq * 32 + q32;
+  if (half == 0) s_ml[wk * kRows + row] = make_float2(m, l);
   __syncthreads();
   float M = kNegInf;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][q32].x);
+  for (int w = 0; w < WK; ++w) M = fmaxf(M, s_ml[w * kRows + row].x);
   const float f = m == kNegInf ? 0.0f : exp2_fast((m - M) * A.scale_log2);
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      *reinterpret_cast<float4 *>(s_o + (wave * 32 + q32) * (D + 4) + t * 32 + 8 * g + 4 * half) =
+      *reinterpret_cast<float4 *>(s_o + (wk * kRows + row) * (D + 4) + t * 32 + 8 * g + 4 * half) =
           make_float4(o[t][4 * g] * f, o[t][4 * g + 1] * f, o[t][4 * g + 2] * f, o[t][4 * g + 3] * f);
   __syncthreads();
-  for (int z = tid; z < 32 * (D / 4); z += kAtThreads) {
+  for (int z = tid; z < kRows * (D / 4); z += kAtThreads) {
     const int q = z / (D / 4), c = z % (D / 4);
     const int qi = it.row0 + q;
     if (qi >= it.rows) continue;
     float4 a = *reinterpret_cast<const float4 *>(s_o + q * (D + 4) + c * 4);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      const float4 b = *reinterpret_cast<const float4 *>(s_o + (w * 32 + q) * (D + 4) + c * 4);
+    for (int w = 1; w < WK; ++w) {
+      const float4 b = *reinterpret_cast<const float4 *>(s_o + (w * kRows + q) * (D + 4) + c * 4);
       a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
     }
     if (any_odd) a = add_odd<DT>(it, s_anc[qi / A.n], c * 4, a);
@@ -309,10 +311,12 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
     if (c == 0) {
       float Mq = kNegInf, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) Mq = fmaxf(Mq, s_ml[w][q].x);
+      for (int w = 0; w < WK; ++w) Mq = fmaxf(Mq, s_ml[w * kRows + q].x);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (s_ml[w][q].x != kNegInf) L += s_ml[w][q].y * exp2_fast((s_ml[w][q].x - Mq) * A.scale_log2);
+      for (int w = 0; w < WK; ++w) {
+        const float2 v = s_ml[w * kRows + q];
+        if (v.x != kNegInf) L += v.y * exp2_fast((v.x - Mq) * A.scale_log2);
+      }
       A.part_ml[at] = make_float2(Mq, L);
     }
   }
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
   __shared__ uint4 s_tile[kBytes / sizeof(uint4)];
   __shared__ uint32_t s_anc[kTreeMaxNodes][8];
   __shared__ int16_t s_parent[kTreeMaxNodes];
-  __shared__ float2 s_ml[4][32];
+  __shared__ float2 s_ml[128];  // [waves on the same rows][rows]
   char *lds = reinterpret_cast<char *>(s_tile);
   Item it{};
   int id = blockIdx.x;
@@ -448,17 +452,23 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendArgs A) {
 
 namespace {
 
+template <int DT, int D, int WQP>
+void launch_own(const AttendArgs &A, const AttendPlan &P, dim3 grid, hipStream_t st) {
+  if (P.own_waves == 4)
+    hipLaunchKernelGGL((k_attend<DT, D, WQP, 4>), grid, dim3(kAtThreads), 0, st, A);
+  else if (P.own_waves == 2)
+    hipLaunchKernelGGL((k_attend<DT, D, WQP, 2>), grid, dim3(kAtThreads), 0, st, A);
+  else
+    hipLaunchKernelGGL((k_attend<DT, D, WQP, 1>), grid, dim3(kAtThreads), 0, st, A);
+}
+
 template <int DT, int D>
 void launch_type(const AttendArgs &A, const AttendPlan &P, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks));
-  if (P.prefix_wide && P.own_wide)
-    hipLaunchKernelGGL((k_attend<DT, D, 4, 4>), grid, dim3(kAtThreads), 0, st, A);
-  else if (P.prefix_wide)
-    hipLaunchKernelGGL((k_attend<DT, D, 4, 1>), grid, dim3(kAtThreads), 0, st, A);
-  else if (P.own_wide)
-    hipLaunchKernelGGL((k_attend<DT, D, 1, 4>), grid, dim3(kAtThreads), 0, st, A);
+  if (P.prefix_waves == 4)
+    launch_own<DT, D, 4>(A, P, grid, st);
   else
-    hipLaunchKernelGGL((k_attend<DT, D, 1, 1>), grid, dim3(kAtThreads), 0, st, A);
+    launch_own<DT, D, 1>(A, P, grid, st);
   const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
   hipLaunchKernelGGL((k_attend_combine<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, A);
 }

@@ -162,58 +162,63 @@ inline LmLayout make_lm_layout(int64_t B, int32_t gamma, int32_t V) {
 }
 
 // Work items of an attention call.  Stacked rows (query rows times the heads of
-// a group) come in tiles of 32 (four waves share the keys) or 128 (four waves
-// share the rows); keys are split into ranges until the items fill the chip.
+// a group) come in tiles of 32, 64 or 128, on 1, 2 or 4 of a workgroup's waves
+// (the others share a tile's keys); keys are split into ranges until the items
+// fill the chip.
 constexpr int kAttendThreads = 256;
 constexpr int kAttendWideRows = 64;        // more stacked rows than this: tiles of 128
 constexpr int64_t kAttendSlots = 512;      // workgroups that run at once: 2 on each of 256 CUs
 constexpr int kAttendMinKeys = 128;        // keys per range at least (a tile)
-constexpr int kAttendItemKeys = 192;       // an item's own cost (start, join), in keys
 struct AttendPlan {
-  int prefix_wide, own_wide;
+  int prefix_waves, own_waves;  // waves along the rows
   int prefix_parts, prefix_chunk, own_parts, own_chunk, own_tiles;
   int64_t prefix_items, own_blocks;
   size_t ml_off, total;
 };
 
-// Ranges of `keys` keys for `items` items each: the number that ends first when
-// rounds of kAttendSlots items take turns.  balance: lengths differ, so items
-// are kept at 512 keys where there are enough for four rounds.
-inline void split_keys(int64_t keys, int64_t items, bool balance, int *parts, int *chunk) {
-  int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys;
-  if (most > 256) most = 256;
-  int64_t best = -1;
+// Ranges of `keys` keys for `items` items of `rows` rows each: the number that
+// ends first when rounds of kAttendSlots items take turns.  An item costs its
+// keys, a tile's start and end, and its partial output, written and read
+// again: two keys' bytes per row.  Where the launch has work for many rounds
+// already (many), ranges of about `most_keys` keep the items few and even.
+inline void split_keys(int64_t keys, int64_t items, int64_t rows, bool many, int64_t most_keys, int *parts, int *chunk) {
   auto chunk_of = [&](int64_t p) { return ((keys + p - 1) / p + 127) / 128 * 128; };
-  for (int64_t p = 1; p <= most; ++p) {
-    const int64_t rounds = (items * p + kAttendSlots - 1) / kAttendSlots;
-    const int64_t cost = rounds * (chunk_of(p) + kAttendItemKeys);
-    if (best < 0 || cost < best) {
-      best = cost;
-      *chunk = static_cast<int>(chunk_of(p));
+  int64_t c = chunk_of((keys + most_keys - 1) / most_keys);
+  if (!many) {
+    int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys;
+    if (most > 256) most = 256;
+    int64_t best = -1;
+    for (int64_t p = 1; p <= most; ++p) {
+      const int64_t rounds = (items * p + kAttendSlots - 1) / kAttendSlots;
+      const int64_t cost = rounds * (chunk_of(p) + kAttendMinKeys + 2 * rows);
+      if (best < 0 || cost < best) {
+        best = cost;
+        c = chunk_of(p);
+      }
     }
   }
-  if (balance) {
-    int64_t p = (4 * kAttendSlots + items - 1) / items;
-    if (p > (keys + 511) / 512) p = (keys + 511) / 512;
-    if (chunk_of(p) < *chunk) *chunk = static_cast<int>(chunk_of(p));
-  }
-  *parts = static_cast<int>((keys + *chunk - 1) / *chunk);
+  *chunk = static_cast<int>(c);
+  *parts = static_cast<int>((keys + c - 1) / c);
 }
 
 inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx) {
   AttendPlan L{};
   const int64_t n = Hq / Hkv;
   const int64_t all = B * R * n, own = R * n;
-  L.prefix_wide = all > kAttendWideRows;
-  L.own_wide = own > kAttendWideRows;
+  L.prefix_waves = all > kAttendWideRows ? 4 : 1;
+  L.own_waves = own > kAttendWideRows ? 4 : own > 32 ? 2 : 1;
+  const int64_t prefix_rows = 32 * L.prefix_waves, own_rows = 32 * L.own_waves;
+  const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
+  L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
+  const int64_t own_keys = max_ctx + R, own_items = B * Hkv * L.own_tiles;
+  const bool own_many = own_items * ((own_keys + 511) / 512) >= 4 * kAttendSlots;
+  split_keys(own_keys, own_items, own < own_rows ? own : own_rows, own_many, 512, &L.own_parts, &L.own_chunk);
   L.prefix_chunk = 1;
   if (P > 0) {
-    const int64_t tiles = (all + (L.prefix_wide ? 127 : 31)) / (L.prefix_wide ? 128 : 32);
-    split_keys(P, tiles * Hkv, false, &L.prefix_parts, &L.prefix_chunk);
+    const bool many = own_many || tiles * Hkv * ((P + 1023) / 1024) >= 4 * kAttendSlots;
+    split_keys(P, tiles * Hkv, all < prefix_rows ? all : prefix_rows, many, 1024, &L.prefix_parts, &L.prefix_chunk);
     L.prefix_items = tiles * Hkv * L.prefix_parts;
   }
-  L.own_tiles = static_cast<int>((own + (L.own_wide ? 127 : 31)) / (L.own_wide ? 128 : 32));
-  split_keys(max_ctx + R, B * Hkv * L.own_tiles, true, &L.own_parts, &L.own_chunk);
   L.own_blocks = (B * Hkv * L.own_parts + 7) / 8 * 8 * L.own_tiles;
   const size_t slots = static_cast<size_t>(L.prefix_parts + L.own_parts) * static_cast<size_t>(B * R * Hq);
   L.ml_off = align256(slots * static_cast<size_t>(D) * sizeof(float));
