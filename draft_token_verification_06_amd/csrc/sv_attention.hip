@@ -149,15 +149,24 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   float m = kNegInf, l = 0.0f;  // l: this half's keys only
 
   uint4 rk[kLoads], rv[kLoads];
-  const int piece = tid % kChunks, first = tid / kChunks;
-  constexpr int kRowsPerPass = kAtThreads / kChunks;
+  // WQ = 1: every wave fills its own 32 keys of the tile and reads only those,
+  // so the waves run apart until the end; else the workgroup fills the tile.
+  constexpr bool kApart = WQ == 1;
+  constexpr int kRowsPerPass = (kApart ? 64 : kAtThreads) / kChunks;
+  const int piece = tid % kChunks, first = kApart ? wave * 32 + lane / kChunks : tid / kChunks;
   auto load = [&](int t0) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const int64_t key = min(t0 + first + j * kRowsPerPass, it.k1 - 1);
-      rk[j] = load_vec(it.k + key * it.tok_stride + piece * 8);
-      rv[j] = load_vec(it.v + key * it.tok_stride + piece * 8);
+      const uint16_t *pk = it.k + key * it.tok_stride + piece * 8, *pv = it.v + key * it.tok_stride + piece * 8;
+      // one sequence's cache is read once: streamed
+      rk[j] = kApart ? load_stream(reinterpret_cast<const uint4 *>(pk)) : load_vec(pk);
+      rv[j] = kApart ? load_stream(reinterpret_cast<const uint4 *>(pv)) : load_vec(pv);
     }
+  };
+  auto tile_barrier = [&]() {
+    if (kApart) __builtin_amdgcn_wave_barrier();
+    else __syncthreads();
   };
   bool odd = false;
   load(it.k0);
@@ -167,7 +176,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
     // Infinities and NaN among the step's own values, which must reach only the
     // rows that see them, are left out here and added at the end.
     const bool masked = t0 + KT > it.draft;
-    __syncthreads();
+    tile_barrier();
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const int row = first + j * kRowsPerPass;
@@ -185,7 +194,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
       *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 8) = rk[j];
       *reinterpret_cast<uint4 *>(s_v + row * kRow + piece * 8) = v;
     }
-    __syncthreads();
+    tile_barrier();
     if (t0 + KT < it.k1) load(t0 + KT);
     if (t0 + wk * SB * 32 >= it.k1) continue;  // nothing of this tile for this wave
     // raw products of the wave's blocks of 32 keys
@@ -282,23 +291,24 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   constexpr int kRows = 32 * WQ;
   float *s_o = reinterpret_cast<float *>(lds);
   const int row = wq * 32 + q32;
+  const int live = min(kRows, it.rows - it.row0);
   if (half == 0) s_ml[wk * kRows + row] = make_float2(m, l);
   __syncthreads();
   float M = kNegInf;
 #pragma unroll
   for (int w = 0; w < WK; ++w) M = fmaxf(M, s_ml[w * kRows + row].x);
   const float f = m == kNegInf ? 0.0f : exp2_fast((m - M) * A.scale_log2);
+  if (row < live)
 #pragma unroll
-  for (int t = 0; t < D / 32; ++t)
+    for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      *reinterpret_cast<float4 *>(s_o + (wk * kRows + row) * (D + 4) + t * 32 + 8 * g + 4 * half) =
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4 *>(s_o + (wk * kRows + row) * (D + 4) + t * 32 + 8 * g + 4 * half) =
           make_float4(o[t][4 * g] * f, o[t][4 * g + 1] * f, o[t][4 * g + 2] * f, o[t][4 * g + 3] * f);
   __syncthreads();
-  for (int z = tid; z < kRows * (D / 4); z += kAtThreads) {
+  for (int z = tid; z < live * (D / 4); z += kAtThreads) {
     const int q = z / (D / 4), c = z % (D / 4);
     const int qi = it.row0 + q;
-    if (qi >= it.rows) continue;
     float4 a = *reinterpret_cast<const float4 *>(s_o + q * (D + 4) + c * 4);
 #pragma unroll
     for (int w = 1; w < WK; ++w) {
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
       for (int x = 0; x < 8; ++x) s_anc[v][x] = w[x];
     }
   }
-  // (the first barrier of the pass orders these writes)
+  __syncthreads();
   attend_item<DT, D, WQO>(A, it, lds, s_anc, s_ml);
 }
 
