@@ -368,16 +368,18 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
     return;
   }
   id -= A.prefix_items;
-  // row tiles of the same keys are 8 blocks apart (one XCD), then the next keys
-  const int tiles = A.own_tiles;
-  const int octet = id / (8 * tiles), within = id % (8 * tiles);
-  int key_item = octet * 8 + within % 8;
-  const int tile = within / 8;
-  if (key_item >= A.B * A.Hkv * A.own_parts) return;
-  it.kvh = key_item % A.Hkv;
-  key_item /= A.Hkv;
-  const int split = key_item % A.own_parts;
-  const int b = key_item / A.own_parts;
+  // All heads and row tiles of a range of one sequence's tokens follow each
+  // other on one XCD (8 blocks apart): together they read whole tokens.  With
+  // a head per XCD instead, every XCD reads the same eighth of the memory
+  // channels.
+  const int per = A.Hkv * A.own_tiles;
+  const int j = id / 8;
+  const int range = j / per * 8 + id % 8;
+  if (range >= A.B * A.own_parts) return;
+  const int tile = j % per % A.own_tiles;
+  it.kvh = j % per / A.own_tiles;
+  const int split = range / A.B;  // every sequence's first range, then the second ..: full ones go first
+  const int b = range % A.B;
   const int len = A.ctx_len[b];
   const int live = live_rows(A, b);
   if (bad_len(A, len) || live == 0) return;

@@ -327,8 +327,10 @@ void launch_tiles(LmQuantArgs A, hipStream_t st) {
 template <int DT>
 void launch_type(const LmQuantArgs &A, hipStream_t st) {
   const int64_t M = A.M;
-  if (M <= 16)
-    launch_tiles<DT, 1, 2, 256>(A, st);
+  if (M <= 16 && A.V < 512 * 128)
+    launch_tiles<DT, 1, 1, 512>(A, st);  // 64 columns: 128 would leave CUs idle (V = 32000: 11 us, 13 with 128)
+  else if (M <= 16)
+    launch_tiles<DT, 1, 2, 256>(A, st);  // (V = 128256, M = 8: 58 us, 65 with 64 columns)
   else if (M <= 32)
     launch_tiles<DT, 2, 2, 256>(A, st);
   else if ((M + 63) / 64 * 64 <= (M + 79) / 80 * 80)

@@ -211,15 +211,15 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
   const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
   L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
   const int64_t own_keys = max_ctx + R, own_items = B * Hkv * L.own_tiles;
-  const bool own_many = own_items * ((own_keys + 511) / 512) >= 4 * kAttendSlots;
-  split_keys(own_keys, own_items, own < own_rows ? own : own_rows, own_many, 512, &L.own_parts, &L.own_chunk);
+  const bool own_many = own_items * ((own_keys + 1023) / 1024) >= 4 * kAttendSlots;
+  split_keys(own_keys, own_items, own < own_rows ? own : own_rows, own_many, 1024, &L.own_parts, &L.own_chunk);
   L.prefix_chunk = 1;
   if (P > 0) {
     const bool many = own_many || tiles * Hkv * ((P + 1023) / 1024) >= 4 * kAttendSlots;
     split_keys(P, tiles * Hkv, all < prefix_rows ? all : prefix_rows, many, 1024, &L.prefix_parts, &L.prefix_chunk);
     L.prefix_items = tiles * Hkv * L.prefix_parts;
   }
-  L.own_blocks = (B * Hkv * L.own_parts + 7) / 8 * 8 * L.own_tiles;
+  L.own_blocks = (B * L.own_parts + 7) / 8 * 8 * Hkv * L.own_tiles;
   const size_t slots = static_cast<size_t>(L.prefix_parts + L.own_parts) * static_cast<size_t>(B * R * Hq);
   L.ml_off = align256(slots * static_cast<size_t>(D) * sizeof(float));
   L.total = align256(L.ml_off + slots * 2 * sizeof(float));
