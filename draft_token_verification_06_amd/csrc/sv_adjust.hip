@@ -100,8 +100,10 @@ constexpr uint32_t kSeenInPrompt = 0x80000000u;
 // kMode: rows copied to another place, cached or streamed, or changed in place.
 enum : int { ADJ_COPY = 0, ADJ_STREAM = 1, ADJ_IN_PLACE = 2 };
 
-template <int DT, int kMode>
-__global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) {
+// tree: nothing for a window, or the TreeParents.
+template <int DT, int kMode, class... Tree>
+__global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A, Tree... tree) {
+  constexpr bool kTree = sizeof...(Tree) > 0;
   using E = Elt<DT>;
   constexpr int kEPV = E::kEPV;
   constexpr bool kStream = kMode == ADJ_STREAM, kInPlace = kMode == ADJ_IN_PLACE;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
   __shared__ uint32_t s_count[kChunk];  // occurrences past the prompt; kSeenInPrompt
   __shared__ uint16_t s_bias[kChunk];   // 1 + index of the last bias entry that names the token
   __shared__ int32_t s_node[kTreeMaxNodes];
-  __shared__ int16_t s_parent[kTreeMaxNodes];
+  __shared__ uint8_t s_parent[kTreeMaxNodes];
   __shared__ uint64_t s_in[kWords];               // nodes whose token lies in the chunk
   __shared__ uint64_t s_path[kTreeMaxNodes][kWords];  // those on each row's path
 
@@ -176,12 +178,13 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust_logits(AdjustArgs A) 
     if (tid < words * 64) {
       // row v's own node: the draft before row v, or the tree node's token
       int t = -1;
-      if (tid >= 1 && tid < A.R) t = A.tokens[b * A.tokens_stride + (A.tree ? tid : tid - 1)];
+      if (tid >= 1 && tid < A.R) t = A.tokens[b * A.tokens_stride + (kTree ? tid : tid - 1)];
       const bool in = t >= base && t < A.V && t - base < kChunk;
       s_node[tid] = t;
       // the walks below read parents from LDS: a step through the argument
       // block would cost a trip to memory each
-      s_parent[tid] = A.tree ? A.parent[tid] : static_cast<int16_t>(tid - 1);
+      s_parent[tid] = static_cast<uint8_t>(tid - 1);
+      if constexpr (kTree) s_parent[tid] = (tree.parent[tid], ...);
       const uint64_t bits = __ballot(in);
       if ((tid & 63) == 0) s_in[tid >> 6] = bits;
     }
@@ -317,19 +320,27 @@ namespace {
 
 constexpr int64_t kAdjustStreamBytes = 256ll << 20;
 
-template <int kMode>
-void launch_type(int dtype, const AdjustArgs &A, dim3 grid, hipStream_t st) {
-  if (dtype == DT_F32)
-    hipLaunchKernelGGL((k_adjust_logits<DT_F32, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
-  else if (dtype == DT_BF16)
-    hipLaunchKernelGGL((k_adjust_logits<DT_BF16, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
+template <int DT, int kMode>
+void launch_shape(const AdjustArgs &A, const TreeParents *parents, dim3 grid, hipStream_t st) {
+  if (parents)
+    hipLaunchKernelGGL((k_adjust_logits<DT, kMode, TreeParents>), grid, dim3(kAdjustThreads), 0, st, A, *parents);
   else
-    hipLaunchKernelGGL((k_adjust_logits<DT_F16, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
+    hipLaunchKernelGGL((k_adjust_logits<DT, kMode>), grid, dim3(kAdjustThreads), 0, st, A);
+}
+
+template <int kMode>
+void launch_type(int dtype, const AdjustArgs &A, const TreeParents *parents, dim3 grid, hipStream_t st) {
+  if (dtype == DT_F32)
+    launch_shape<DT_F32, kMode>(A, parents, grid, st);
+  else if (dtype == DT_BF16)
+    launch_shape<DT_BF16, kMode>(A, parents, grid, st);
+  else
+    launch_shape<DT_F16, kMode>(A, parents, grid, st);
 }
 
 }  // namespace
 
-void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st) {
+void launch_adjust_logits(int dtype, AdjustArgs A, const TreeParents *parents, int B, hipStream_t st) {
   A.chunks = adjust_chunks(dtype, A.V);
   // Few sequences and many rows (a tree): rows go to several workgroups, each
   // of which counts the history again.  Four at least stay together, which is
@@ -344,11 +355,11 @@ void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st) {
   // the verification that reads them.
   const int64_t bytes = 2 * static_cast<int64_t>(B) * A.R * A.V * (dtype == DT_F32 ? 4 : 2);
   if (A.in_place)
-    launch_type<ADJ_IN_PLACE>(dtype, A, grid, st);
+    launch_type<ADJ_IN_PLACE>(dtype, A, parents, grid, st);
   else if (bytes > kAdjustStreamBytes)
-    launch_type<ADJ_STREAM>(dtype, A, grid, st);
+    launch_type<ADJ_STREAM>(dtype, A, parents, grid, st);
   else
-    launch_type<ADJ_COPY>(dtype, A, grid, st);
+    launch_type<ADJ_COPY>(dtype, A, parents, grid, st);
 }
 
 }  // namespace sv

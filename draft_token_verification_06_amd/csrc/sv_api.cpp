@@ -86,6 +86,16 @@ int build_tree(const int32_t *parent, int32_t N, TreeMeta *meta) {
   return SV_OK;
 }
 
+// Parents of a valid tree, as the step operators' kernels take them.
+int tree_parents(const int32_t *parent, int32_t N, TreeParents *out) {
+  TreeMeta meta;
+  const int st = build_tree(parent, N, &meta);
+  if (st != SV_OK) return st;
+  std::memset(out, 0, sizeof(*out));
+  for (int v = 1; v < N; ++v) out->parent[v] = static_cast<uint8_t>(parent[v]);
+  return SV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -561,12 +571,10 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
   if (B < 1 || R < 1 || V < 1 || V > kMaxVocab) return SV_EINVAL;
   if (!logits || !out || !aligned(logits, eb) || !aligned(out, eb)) return SV_EINVAL;
   AdjustArgs A{};
+  TreeParents parents;
   if (parent_host) {
-    TreeMeta meta;
-    const int tst = build_tree(parent_host, R, &meta);
+    const int tst = tree_parents(parent_host, R, &parents);
     if (tst != SV_OK) return tst;
-    std::memcpy(A.parent, meta.parent, sizeof(A.parent));
-    A.tree = 1;
   } else if (R > SV_MAX_GAMMA + 1) {
     return SV_EINVAL;
   }
@@ -616,7 +624,7 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
   A.allowed = allowed;
   A.allowed_seq_stride = allowed_seq_stride;
   A.allowed_row_stride = allowed_row_stride;
-  launch_adjust_logits(dtype, A, B, stream);
+  launch_adjust_logits(dtype, A, parent_host ? &parents : nullptr, B, stream);
   return launch_status();
 }
 
@@ -689,12 +697,10 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
   if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
   if (!attention_sizes_ok(B, R, Hq, Hkv, D, P, max_ctx)) return SV_EINVAL;
   AttendArgs A{};
+  TreeParents parents;
   if (parent_host) {
-    TreeMeta meta;
-    const int tst = build_tree(parent_host, R, &meta);
+    const int tst = tree_parents(parent_host, R, &parents);
     if (tst != SV_OK) return tst;
-    std::memcpy(A.parent, meta.parent, sizeof(A.parent));
-    A.tree = 1;
   } else if (R > SV_MAX_GAMMA + 1) {
     return SV_EINVAL;
   }
@@ -745,7 +751,7 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
   A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + L.ml_off);
   A.out = static_cast<uint16_t *>(out);
   A.lse = lse;
-  launch_attend(dtype, D, A, L, stream);
+  launch_attend(dtype, D, A, parent_host ? &parents : nullptr, L, stream);
   return launch_status();
 }
 

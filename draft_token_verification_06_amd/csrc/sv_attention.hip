@@ -332,17 +332,19 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   }
 }
 
-__device__ __forceinline__ bool bad_len(const AttendArgs &A, int len) { return len < 0 || len > A.max_ctx; }
-__device__ __forceinline__ int live_rows(const AttendArgs &A, int b) {
+__device__ __forceinline__ bool bad_len(const AttendJoin &A, int len) { return len < 0 || len > A.max_ctx; }
+__device__ __forceinline__ int live_rows(const AttendJoin &A, int b) {
   return A.row_count ? min(max(A.row_count[b], 0), A.R) : A.R;
 }
 
-template <int DT, int D, int WQP, int WQO>
-__global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
+// tree: nothing for a window, or the TreeParents.
+template <int DT, int D, int WQP, int WQO, class... Tree>
+__global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A, Tree... tree) {
+  constexpr bool kTree = sizeof...(Tree) > 0;
   constexpr size_t kBytes = at_tile_bytes<D, WQP>() > at_tile_bytes<D, WQO>() ? at_tile_bytes<D, WQP>() : at_tile_bytes<D, WQO>();
   __shared__ uint4 s_tile[kBytes / sizeof(uint4)];
   __shared__ uint32_t s_anc[kTreeMaxNodes][8];
-  __shared__ int16_t s_parent[kTreeMaxNodes];
+  __shared__ uint8_t s_parent[kTreeMaxNodes];
   __shared__ float2 s_ml[128];  // [waves on the same rows][rows]
   char *lds = reinterpret_cast<char *>(s_tile);
   Item it{};
@@ -397,18 +399,19 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
   if (it.k1 > len) {
     // ancestor sets of the rows, one row per thread; parents go to LDS first,
     // as a walk through the argument block would cost a trip to memory a step
-    if (A.tree) {
-      for (int v = threadIdx.x; v < A.R; v += kAtThreads) s_parent[v] = A.parent[v];
+    if constexpr (kTree) {
+      for (int v = threadIdx.x; v < A.R; v += kAtThreads) s_parent[v] = (tree.parent[v], ...);
       __syncthreads();
     }
     for (int v = threadIdx.x; v < A.R; v += kAtThreads) {
       uint32_t w[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) w[x] = 0;
-      if (A.tree) {
-        for (int u = v; u >= 0; u = s_parent[u])
+      if constexpr (kTree) {
+        for (int u = v; u > 0; u = s_parent[u])
 #pragma unroll
           for (int x = 0; x < 8; ++x) w[x] |= x == (u >> 5) ? 1u << (u & 31) : 0u;
+        w[0] |= 1u;  // the root
       } else {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A) {
 // One wave per (row, head): the row's items in order, weighted by their
 // maxima; a sequence whose length is out of range gets NaN.
 template <int DT, int D>
-__global__ void __launch_bounds__(256) k_attend_combine(AttendArgs A) {
+__global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
   constexpr int E = D / 64;
   const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -464,36 +467,45 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendArgs A) {
 
 namespace {
 
-template <int DT, int D, int WQP>
-void launch_own(const AttendArgs &A, const AttendPlan &P, dim3 grid, hipStream_t st) {
-  if (P.own_waves == 4)
-    hipLaunchKernelGGL((k_attend<DT, D, WQP, 4>), grid, dim3(kAtThreads), 0, st, A);
-  else if (P.own_waves == 2)
-    hipLaunchKernelGGL((k_attend<DT, D, WQP, 2>), grid, dim3(kAtThreads), 0, st, A);
+template <int DT, int D, int WQP, int WQO>
+void launch_shape(const AttendArgs &A, const TreeParents *parents, dim3 grid, hipStream_t st) {
+  if (parents)
+    hipLaunchKernelGGL((k_attend<DT, D, WQP, WQO, TreeParents>), grid, dim3(kAtThreads), 0, st, A, *parents);
   else
-    hipLaunchKernelGGL((k_attend<DT, D, WQP, 1>), grid, dim3(kAtThreads), 0, st, A);
+    hipLaunchKernelGGL((k_attend<DT, D, WQP, WQO>), grid, dim3(kAtThreads), 0, st, A);
+}
+
+template <int DT, int D, int WQP>
+void launch_own(const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, dim3 grid, hipStream_t st) {
+  if (P.own_waves == 4)
+    launch_shape<DT, D, WQP, 4>(A, parents, grid, st);
+  else if (P.own_waves == 2)
+    launch_shape<DT, D, WQP, 2>(A, parents, grid, st);
+  else
+    launch_shape<DT, D, WQP, 1>(A, parents, grid, st);
 }
 
 template <int DT, int D>
-void launch_type(const AttendArgs &A, const AttendPlan &P, hipStream_t st) {
+void launch_type(const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks));
   if (P.prefix_waves == 4)
-    launch_own<DT, D, 4>(A, P, grid, st);
+    launch_own<DT, D, 4>(A, parents, P, grid, st);
   else
-    launch_own<DT, D, 1>(A, P, grid, st);
+    launch_own<DT, D, 1>(A, parents, P, grid, st);
   const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
-  hipLaunchKernelGGL((k_attend_combine<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, A);
+  hipLaunchKernelGGL((k_attend_combine<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st,
+                     static_cast<const AttendJoin &>(A));
 }
 
 }  // namespace
 
-void launch_attend(int dtype, int D, const AttendArgs &A, const AttendPlan &P, hipStream_t st) {
+void launch_attend(int dtype, int D, const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st) {
   if (dtype == DT_BF16) {
-    if (D == 64) launch_type<DT_BF16, 64>(A, P, st);
-    else launch_type<DT_BF16, 128>(A, P, st);
+    if (D == 64) launch_type<DT_BF16, 64>(A, parents, P, st);
+    else launch_type<DT_BF16, 128>(A, parents, P, st);
   } else {
-    if (D == 64) launch_type<DT_F16, 64>(A, P, st);
-    else launch_type<DT_F16, 128>(A, P, st);
+    if (D == 64) launch_type<DT_F16, 64>(A, parents, P, st);
+    else launch_type<DT_F16, 128>(A, parents, P, st);
   }
 }
 

@@ -94,6 +94,14 @@ struct LmDecideArgs {
   int32_t *arrive;               // arrival counters of the draw, zeroed here
 };
 
+// Parents of a tree's nodes (entry 0, the root's, unused), as the last part of
+// a kernel's arguments.  Window calls leave them out: a launch writes its
+// arguments across the bus, at about 2 us a kilobyte.
+struct TreeParents {
+  uint8_t parent[kTreeMaxNodes];
+};
+static_assert(kTreeMaxNodes <= 256, "a parent fits a byte");
+
 // Logits adjustment.  Row r of a sequence follows tokens[0 .. r - 1] (window)
 // or carries node r of the tree given by parent.
 struct AdjustArgs {
@@ -117,12 +125,11 @@ struct AdjustArgs {
   int32_t chunks;   // token chunks per row; rows split into groups of group_rows (set by the launcher)
   int32_t row_groups, group_rows;
   int32_t in_place; // out is in: only what changes is touched
-  int32_t tree;
-  int16_t parent[kTreeMaxNodes];
 };
 constexpr int kAdjustThreads = 256;
 int adjust_chunks(int dtype, int V);
-void launch_adjust_logits(int dtype, AdjustArgs A, int B, hipStream_t st);
+// parents: null for a window.
+void launch_adjust_logits(int dtype, AdjustArgs A, const TreeParents *parents, int B, hipStream_t st);
 
 // LM head on 4-bit weights: rows of h (stride lda elements) against w [V][K / 2]
 // with scales [V][K / group] of h's type and zeros [V][K / group] or null (8).
@@ -142,29 +149,33 @@ constexpr int kLmQuantThreads = 256;
 constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 64;  // of a workgroup's tile
 void launch_lm_quant(int dtype, const LmQuantArgs &A, hipStream_t st);
 
-// Attention of a step's rows.  Strides in elements; heads are D apart.
-struct AttendArgs {
+// Attention of a step's rows.  Strides in elements; heads are D apart.  What
+// the join of a row's items needs, and the rest.
+struct AttendJoin {
+  const int32_t *ctx_len, *row_count;
+  int32_t B, R, Hq;
+  int32_t max_ctx;
+  int32_t prefix_parts, own_chunk;
+  float scale_log2;  // magnitude of the score scale, times log2(e)
+  float *part_o;     // [parts][B R Hq][D] unnormalised outputs
+  float2 *part_ml;   // [parts][B R Hq] (largest product, sum)
+  uint16_t *out;     // [B][R][Hq][D]
+  float *lse;        // [B][R][Hq] or null
+};
+struct AttendArgs : AttendJoin {
   const uint16_t *q;
   int64_t q_row_stride;
   const uint16_t *k, *v;  // [B] caches of cap tokens
   int64_t seq_stride, tok_stride;
   const uint16_t *prefix_k, *prefix_v;
   int64_t prefix_tok_stride;
-  const int32_t *ctx_len, *row_count;
-  int32_t B, R, Hq, Hkv, n;  // n = Hq / Hkv
-  int32_t P, max_ctx;
-  int32_t prefix_parts, prefix_chunk, prefix_items;
-  int32_t own_parts, own_chunk, own_tiles;
-  float scale_log2;  // magnitude of the score scale, times log2(e)
+  int32_t Hkv, n;  // n = Hq / Hkv
+  int32_t P;
+  int32_t prefix_chunk, prefix_items;
+  int32_t own_parts, own_tiles;
   int32_t negate;    // the scale is negative
-  float *part_o;     // [parts][B R Hq][D] unnormalised outputs
-  float2 *part_ml;   // [parts][B R Hq] (largest product, sum)
-  uint16_t *out;     // [B][R][Hq][D]
-  float *lse;        // [B][R][Hq] or null
-  int32_t tree;
-  int16_t parent[kTreeMaxNodes];
 };
-void launch_attend(int dtype, int D, const AttendArgs &A, const AttendPlan &P, hipStream_t st);
+void launch_attend(int dtype, int D, const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st);
 
 // Launches the GEMMs of two problems (target rows, draft rows) as one grid.
 void launch_lm_gemm(LmGemmArgs A0, LmGemmArgs A1, hipStream_t st);
