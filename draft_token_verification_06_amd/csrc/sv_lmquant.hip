@@ -113,29 +113,39 @@ template <int DT> __device__ __forceinline__ void store_logit(const LmQuantArgs 
   else static_cast<_Float16 *>(A.out)[at] = static_cast<_Float16>(x);
 }
 
-// MT x NT tiles of 16 x 16 per wave; the waves of a workgroup lie side by
-// side along V and share the hidden rows, scales and zero points of kChunk
-// values of K in LDS.  kGroup: values per scale.  Weights go from memory to
-// registers a chunk ahead and stay in flight across the barriers.
-template <int DT, int MT, int NT, int kGroup, int kChunk>
-__global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(LmQuantArgs A) {
+// MT x NT tiles of 16 x 16 per wave; the waves of a team lie side by side along
+// V and share the hidden rows, scales and zero points of kChunk values of K in
+// LDS.  kGroup: values per scale.  Weights go from memory to registers a chunk
+// ahead and stay in flight across the barriers.  kSplit = 1: the workgroup is
+// one team.  kSplit = 4 (problems with too few columns to fill the chip): every
+// wave is a team of its own on the same columns, takes every fourth chunk of K
+// without any barrier, and the four sums are added in wave order at the end.
+template <int DT, int MT, int NT, int kGroup, int kChunk, int kSplit>
+__global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : 2) k_lm_quant(LmQuantArgs A) {
   using E = Elt<DT>;
   using Q = QuantElt<DT>;
-  constexpr int kRows = 16 * MT, kCols = 16 * NT * kQWaves;
+  constexpr int kTeamWaves = kQWaves / kSplit, kTeamThreads = kQThreads / kSplit;
+  constexpr int kRows = 16 * MT, kCols = 16 * NT * kTeamWaves;
   constexpr int kSteps = kChunk / kQStep;
   constexpr int kG = kQStep / kGroup, kGC = kChunk / kGroup;  // groups per step and chunk
   constexpr int kSub = kGroup / 32;                           // MFMAs per group and tile
   constexpr int kARow = kChunk + 8;                           // 16 bytes of padding spread the banks
   constexpr int kPieces = kChunk / 8;                         // 16-byte pieces per row of a chunk
-  constexpr int kRowsPerPass = kQThreads / kPieces;
+  constexpr int kRowsPerPass = kTeamThreads / kPieces;
   constexpr int kLoads = kRows / kRowsPerPass;
-  constexpr int kScales = (kGC * kCols + kQThreads - 1) / kQThreads;
+  constexpr int kScales = (kGC * kCols + kTeamThreads - 1) / kTeamThreads;
   static_assert(kRows % kRowsPerPass == 0, "whole passes");
-  __shared__ uint16_t s_a[kRows * kARow];
+  static_assert(kSplit == 1 || kSplit == kQWaves, "teams are the workgroup or its waves");
+  __shared__ uint16_t s_as[kSplit][kRows * kARow];
   __shared__ uint4 s_w[kQWaves][NT][128];  // a step's weights on their way to the lanes that multiply them
-  __shared__ float s_sum[kGC][kRows];    // sums of the hidden values per group
-  __shared__ float2 s_scale[kGC][kCols];  // scale, -(16 + zero)
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ float s_sums[kSplit][kGC][kRows];    // sums of the hidden values per group
+  __shared__ float2 s_scales[kSplit][kGC][kCols];  // scale, -(16 + zero)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int team = kSplit > 1 ? wave : 0, team_wave = kSplit > 1 ? 0 : wave;
+  const int tid = kSplit > 1 ? lane : threadIdx.x;  // within the team
+  uint16_t *s_a = s_as[team];
+  float(*s_sum)[kRows] = s_sums[team];
+  float2(*s_scale)[kCols] = s_scales[team];
   const int c16 = lane & 15, quad = lane >> 4;
   // column tiles round the XCDs, the row blocks of one column tile on one XCD
   const int ct = blockIdx.x / (8 * A.row_blocks) * 8 + blockIdx.x % 8;
@@ -177,7 +187,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
   auto load_scales = [&](int chunk) {
 #pragma unroll
     for (int j = 0; j < kScales; ++j) {
-      const int x = tid + j * kQThreads;
+      const int x = tid + j * kTeamThreads;
       const int64_t v = min(col0 + x / kGC, A.V - 1);
       const int g = min(chunk * kGC + x % kGC, groups - 1);
       rs[j] = E::raw(A.scales, v * groups + g);
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
   auto store_scales = [&]() {
 #pragma unroll
     for (int j = 0; j < kScales; ++j) {
-      const int x = tid + j * kQThreads;
+      const int x = tid + j * kTeamThreads;
       if (x < kGC * kCols) s_scale[x % kGC][x / kGC] = make_float2(E::dec(rs[j]), -16.0f - static_cast<float>(rz[j]));
     }
   };
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = i * 8 + (lane >> 3), block = (lane & 7) ^ (n >> 1);
-      woff[t][i] = static_cast<uint32_t>(min(wave * NT * 16 + t * 16 + n, A.V - 1 - col0)) * (A.K / 2) + block * 16;
+      woff[t][i] = static_cast<uint32_t>(min(team_wave * NT * 16 + t * 16 + n, A.V - 1 - col0)) * (A.K / 2) + block * 16;
       wtail[t][i] = woff[t][i] - max(last * 8 + block - (blocks - 1), 0) * 16;
     }
   auto load_w = [&](int slot, int pair) {
@@ -225,21 +235,25 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = q_f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  load_a(0);
-  load_scales(0);
+  auto team_barrier = [&]() {
+    if (kSplit > 1) __builtin_amdgcn_wave_barrier();
+    else lds_barrier();
+  };
+  load_a(min(team, chunks - 1));
+  load_scales(min(team, chunks - 1));
 #pragma unroll
-  for (int u = 0; u < kSteps; u += 2) load_w(u, u / 2);
-  for (int r = A.M - row0 + wave; r < kRows; r += kQWaves) {
+  for (int u = 0; u < kSteps; u += 2) load_w(u, (team * kSteps + u) / 2);
+  for (int r = A.M - row0 + team_wave; r < kRows; r += kTeamWaves) {
     for (int x = lane; x < kPieces; x += 64) *reinterpret_cast<uint4 *>(&s_a[r * kARow + x * 8]) = make_uint4(0, 0, 0, 0);
     if (lane < kGC) s_sum[lane][r] = 0.0f;
   }
-  for (int c = 0; c < chunks; ++c) {
-    if (c > 0) lds_barrier();  // every wave is done with the previous chunk
+  for (int c = team; c < chunks; c += kSplit) {
+    if (c >= kSplit) team_barrier();  // every wave is done with the previous chunk
     store_a();
     store_scales();
-    load_a(min(c + 1, chunks - 1));
-    load_scales(min(c + 1, chunks - 1));
-    lds_barrier();
+    load_a(min(c + kSplit, chunks - 1));
+    load_scales(min(c + kSplit, chunks - 1));
+    team_barrier();
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       uint32_t w[NT][4];
@@ -256,13 +270,13 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
         w[t][3] = x.w;
         exchange<kGroup>(w[t]);
       }
-      if (u % 2 == 0) load_w(u, ((c + 1) * kSteps + u) / 2);  // past the end: the last steps again, unused
+      if (u % 2 == 0) load_w(u, ((c + kSplit) * kSteps + u) / 2);  // past the end: the last steps again, unused
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         q_f32x4_t part[MT][NT];
         float2 sc[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sc[t] = s_scale[u * kG + g][(wave * NT + t) * 16 + c16];
+        for (int t = 0; t < NT; ++t) sc[t] = s_scale[u * kG + g][(team_wave * NT + t) * 16 + c16];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const float4 hs = *reinterpret_cast<const float4 *>(&s_sum[u * kG + g][m * 16 + quad * 4]);
@@ -292,9 +306,28 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
       }
     }
   }
+  if (kSplit > 1) {
+    // wave order: each adds its sums to those before it
+    __shared__ float4 s_acc[MT][NT][64];
+    for (int z = 0; z < kSplit; ++z) {
+      __syncthreads();
+      if (z != wave) continue;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (z > 0) {
+            const float4 x = s_acc[m][t][lane];
+            acc[m][t] = q_f32x4_t{x.x + acc[m][t][0], x.y + acc[m][t][1], x.z + acc[m][t][2], x.w + acc[m][t][3]};
+          }
+          s_acc[m][t][lane] = make_float4(acc[m][t][0], acc[m][t][1], acc[m][t][2], acc[m][t][3]);
+        }
+    }
+    if (wave != kSplit - 1) return;
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int v = col0 + (wave * NT + t) * 16 + c16;
+    const int v = col0 + (team_wave * NT + t) * 16 + c16;
     if (v >= A.V) continue;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -308,29 +341,36 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 ? 4 : 2) k_lm_quant(Lm
 
 namespace {
 
-template <int DT, int MT, int NT, int kChunk>
+template <int DT, int MT, int NT, int kChunk, int kSplit = 1>
 void launch_tiles(LmQuantArgs A, hipStream_t st) {
-  const int cols = 16 * NT * kQWaves;
+  const int cols = 16 * NT * kQWaves / kSplit;
   A.row_blocks = (A.M + 16 * MT - 1) / (16 * MT);
   const dim3 grid(static_cast<unsigned>((A.V + cols - 1) / cols + 7) / 8 * 8 * A.row_blocks);
   if (A.group == 32)
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 32, kChunk>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 32, kChunk, kSplit>), grid, dim3(kQThreads), 0, st, A);
   else if (A.group == 64)
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, kChunk>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, kChunk, kSplit>), grid, dim3(kQThreads), 0, st, A);
   else
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, kChunk>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, kChunk, kSplit>), grid, dim3(kQThreads), 0, st, A);
 }
 
 // Tiles by rows: the fewest 16-row tiles that hold them, as weights are
 // unpacked once per row block; past 64 rows in blocks of 64 or 80, whichever
-// pads less.
+// pads less.  Where 16-column workgroups whose waves split K fill the chip no
+// more than about twice, they run instead: K is long and little else can be
+// shared out (us at K = 4096: M = 4, V = 8000 11, not split 18; M = 24, V = 8000
+// 16 and 39; M = 64, V = 4000 17 and 37, V = 14000 55 and 43).
 template <int DT>
 void launch_type(const LmQuantArgs &A, hipStream_t st) {
-  const int64_t M = A.M;
-  if (M <= 16 && A.V < 512 * 128)
+  const int64_t M = A.M, tiles = (A.V + 15) / 16;
+  if (M <= 16 && tiles <= 640)
+    launch_tiles<DT, 1, 1, 256, 4>(A, st);
+  else if (M > 16 && tiles * ((M + 31) / 32) <= 1024)
+    launch_tiles<DT, 2, 1, 256, 4>(A, st);
+  else if (M <= 16 && A.V < 512 * 128)
     launch_tiles<DT, 1, 1, 512>(A, st);  // 64 columns: 128 would leave CUs idle (V = 32000: 11 us, 13 with 128)
   else if (M <= 16)
-    launch_tiles<DT, 1, 2, 256>(A, st);  // (V = 128256, M = 8: 58 us, 65 with 64 columns)
+    launch_tiles<DT, 1, 2, 256>(A, st);  // (V = 128256, M = 8: 54 us, 65 with 64 columns)
   else if (M <= 32)
     launch_tiles<DT, 2, 2, 256>(A, st);
   else if ((M + 63) / 64 * 64 <= (M + 79) / 80 * 80)
