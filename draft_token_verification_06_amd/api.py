@@ -454,12 +454,18 @@ def adjust_logits(logits, *, tokens=None, parent=None, history=None, history_len
     return out
 
 
-def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32, out=None):
+def lmhead_quant_workspace(M, K, group, device):
+    """A workspace for lmhead_quant calls of M rows, or None where they need none."""
+    nbytes = int(lib().sv_lmhead_quant_workspace(M, K, group))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32, out=None, ws=None):
     """Logits from hidden states on 4-bit weights with group scales:
     sv_lmhead_quant.  hidden (..., K) bf16 or fp16; weights (V, K / 2) uint8,
     scales (V, K / group) of hidden's dtype, zeros (V, K / group) uint8 or None.
     Returns (..., V) logits of out_dtype (float32 or hidden's dtype), or fills
-    out."""
+    out.  ws: a lmhead_quant_workspace, for more than 32 rows."""
     dtype, dev = hidden.dtype, hidden.device
     if (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda" or hidden.dim() < 1:
         raise ValueError("hidden: expected a bf16 or fp16 device tensor")
@@ -490,9 +496,13 @@ def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32
         raise ValueError("hidden: rows must be one stride apart") from None
     if rows.stride(1) != 1 or (M > 1 and rows.stride(0) < K):
         raise ValueError("hidden: rows must be contiguous and not overlap")
+    group = K // scales.shape[1]
+    if ws is None and M > 32:
+        ws = lmhead_quant_workspace(M, K, group, dev)
+    ws_bytes = 0 if ws is None else _ws_bytes(ws, dev)
     _launch(dev, lib().sv_lmhead_quant, rows.data_ptr(), rows.stride(0) if M > 1 else 0, _DTYPE_CODE[dtype],
             weights.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-            M, K, V, K // scales.shape[1], out.data_ptr(), 0, _DTYPE_CODE[out.dtype])
+            M, K, V, group, out.data_ptr(), 0, _DTYPE_CODE[out.dtype], None if ws is None else ws.data_ptr(), ws_bytes)
     return out
 
 

@@ -557,6 +557,19 @@ int sv_verify_window_lmhead(const void *hidden_target, const void *unembed_targe
   return launch_status();
 }
 
+}  // extern "C"
+
+namespace {
+
+bool quant_sizes_ok(int32_t K, int32_t group) {
+  if (group != 32 && group != 64 && group != 128) return false;
+  return K >= SV_LMHEAD_K_STEP && K <= SV_LMHEAD_MAX_HIDDEN && K % SV_LMHEAD_K_STEP == 0 && K % group == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
 int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t out_seq_stride, int dtype,
                      const int32_t *tokens, int64_t tokens_stride, const int32_t *parent_host,
                      const int32_t *row_count, int32_t B, int32_t R, int32_t V,
@@ -628,15 +641,19 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
   return launch_status();
 }
 
+size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t group) {
+  if (M < 1 || M > kMaxGridY || !quant_sizes_ok(K, group)) return 0;
+  return lm_quant_layout(M, K, group).total;
+}
+
 int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                     const uint8_t *weights, const void *scales, const uint8_t *zeros,
                     int32_t M, int32_t K, int32_t V, int32_t group,
-                    void *out, int64_t out_row_stride, int out_dtype, hipStream_t stream) {
+                    void *out, int64_t out_row_stride, int out_dtype,
+                    void *workspace, size_t workspace_bytes, hipStream_t stream) {
   if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
   if (out_dtype != SV_DT_F32 && out_dtype != dtype) return SV_EDTYPE;
-  if (M < 1 || V < 1 || V > kMaxVocab) return SV_EINVAL;
-  if (group != 32 && group != 64 && group != 128) return SV_EINVAL;
-  if (K < SV_LMHEAD_K_STEP || K > SV_LMHEAD_MAX_HIDDEN || K % SV_LMHEAD_K_STEP != 0 || K % group != 0) return SV_EINVAL;
+  if (M < 1 || M > kMaxGridY || V < 1 || V > kMaxVocab || !quant_sizes_ok(K, group)) return SV_EINVAL;
   if (!hidden || !weights || !scales || !out) return SV_EINVAL;
   if (hidden_row_stride == 0) hidden_row_stride = K;
   if (out_row_stride == 0) out_row_stride = V;
@@ -648,6 +665,11 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                      ((static_cast<int64_t>(M) + kLmQuantMinRows - 1) / kLmQuantMinRows),
                  kLmQuantThreads))
     return SV_EINVAL;
+  const LmQuantLayout L = lm_quant_layout(M, K, group);
+  if (L.total > 0) {
+    const int ws = check_workspace(workspace, workspace_bytes, L.total);
+    if (ws != SV_OK) return ws;
+  }
   LmQuantArgs A{};
   A.h = static_cast<const uint16_t *>(hidden);
   A.lda = hidden_row_stride;
@@ -661,6 +683,9 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
   A.out = out;
   A.out_stride = out_row_stride;
   A.out_f32 = out_dtype == SV_DT_F32;
+  A.padded = L.padded;
+  A.prepared = static_cast<uint16_t *>(workspace);
+  A.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + L.sums_off);
   launch_lm_quant(dtype, A, stream);
   return launch_status();
 }

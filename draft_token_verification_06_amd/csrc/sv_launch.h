@@ -144,9 +144,12 @@ struct LmQuantArgs {
   int64_t out_stride;
   int32_t out_f32;
   int32_t row_blocks;  // set by the launcher
+  // calls of more than kLmQuantDirectRows rows: the rows laid out, [M][padded], and their groups' sums, [padded / group][M]
+  int32_t padded;
+  uint16_t *prepared;
+  float *sums;
 };
 constexpr int kLmQuantThreads = 256;
-constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 64;  // of a workgroup's tile
 void launch_lm_quant(int dtype, const LmQuantArgs &A, hipStream_t st);
 
 // Attention of a step's rows.  Strides in elements; heads are D apart.  What

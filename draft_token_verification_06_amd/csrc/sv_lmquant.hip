@@ -73,6 +73,24 @@ template <int DT> __device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Eight hidden values in the order of unpack8, and their sum.
+__device__ __forceinline__ uint4 permute8(uint4 v) {
+  return make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                    __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
+}
+template <int DT> __device__ __forceinline__ float sum8(uint4 v) {
+  using Q = QuantElt<DT>;
+  return Q::sum2(v.x, Q::sum2(v.y, Q::sum2(v.z, Q::sum2(v.w, 0.0f))));
+}
+// Sum over the lanes (8 values each) that hold one group, in every one of them.
+template <int kGroup> __device__ __forceinline__ float group_sum(float s) {
+  s += dpp_f32<0xB1>(s);
+  s += dpp_f32<0x4E>(s);
+  if (kGroup >= 64) s += dpp_f32<0x141>(s);   // the other half of 8 lanes
+  if (kGroup >= 128) s += dpp_f32<0x140>(s);  // the other half of 16 lanes
+  return s;
+}
+
 // Rows of 16 lanes (quads) hold the 16-byte blocks b0..b3 of a step, 32 values
 // each.  One MFMA multiplies one register of all four, so dwords are exchanged
 // between the quads until a register holds values of one group only: not at
@@ -113,6 +131,24 @@ template <int DT> __device__ __forceinline__ void store_logit(const LmQuantArgs 
   else static_cast<_Float16 *>(A.out)[at] = static_cast<_Float16>(x);
 }
 
+// Hidden rows of a call with many of them, laid out once: permuted as the tiles
+// want them, zeros up to a whole chunk, and the sums of their groups
+// ([group][row]).  The product's workgroups then copy them as they are; doing
+// this in each of them took a third of their vector instructions.
+template <int DT>
+__global__ void __launch_bounds__(256) k_lm_prepare(LmQuantArgs A) {
+  const int piece = blockIdx.x * 256 + threadIdx.x, row = blockIdx.y;
+  const int pieces = A.padded / 8;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (piece * 8 < A.K) v = load_vec(A.h + row * A.lda + piece * 8);
+  const float s8 = sum8<DT>(v);
+  const float s32 = group_sum<32>(s8), s64 = group_sum<64>(s8), s128 = group_sum<128>(s8);
+  if (piece >= pieces) return;
+  const int per = A.group / 8;
+  if (piece % per == 0) A.sums[static_cast<int64_t>(piece / per) * A.M + row] = A.group == 32 ? s32 : A.group == 64 ? s64 : s128;
+  *reinterpret_cast<uint4 *>(A.prepared + static_cast<int64_t>(row) * A.padded + piece * 8) = permute8(v);
+}
+
 // MT x NT tiles of 16 x 16 per wave; the waves of a team lie side by side along
 // V and share the hidden rows, scales and zero points of kChunk values of K in
 // LDS.  kGroup: values per scale.  Weights go from memory to registers a chunk
@@ -120,8 +156,9 @@ template <int DT> __device__ __forceinline__ void store_logit(const LmQuantArgs 
 // one team.  kSplit = 4 (problems with too few columns to fill the chip): every
 // wave is a team of its own on the same columns, takes every fourth chunk of K
 // without any barrier, and the four sums are added in wave order at the end.
-template <int DT, int MT, int NT, int kGroup, int kChunk, int kSplit>
-__global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : 2) k_lm_quant(LmQuantArgs A) {
+// kPrepared: the hidden rows come from k_lm_prepare.
+template <int DT, int MT, int NT, int kGroup, int kChunk, int kSplit, bool kPrepared>
+__global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : MT == 2 && kSplit == 4 ? 1 : 2) k_lm_quant(LmQuantArgs A) {
   using E = Elt<DT>;
   using Q = QuantElt<DT>;
   constexpr int kTeamWaves = kQWaves / kSplit, kTeamThreads = kQThreads / kSplit;
@@ -157,30 +194,53 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : 2
 
   uint4 ra[kLoads];
   const int piece = tid % kPieces, first = tid / kPieces;
-  auto load_a = [&](int chunk) {
-    const bool in = chunk * kChunk + piece * 8 < A.K;
+  // prepared rows: offsets from the tile's first (past M: the last row again, whose products are not stored)
+  constexpr int kSums = (kGC * kRows + kTeamThreads - 1) / kTeamThreads;
+  float rsum[kSums];
+  uint32_t aoff[kLoads];
+  const uint16_t *atile = A.prepared + static_cast<int64_t>(row0) * A.padded;
+  if constexpr (kPrepared)
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int r = row0 + first + j * kRowsPerPass;
-      ra[j] = make_uint4(0, 0, 0, 0);
-      if (in && r < A.M) ra[j] = load_vec(A.h + r * A.lda + chunk * kChunk + piece * 8);
+    for (int j = 0; j < kLoads; ++j)
+      aoff[j] = static_cast<uint32_t>(min(first + j * kRowsPerPass, A.M - 1 - row0)) * A.padded + piece * 8;
+  auto load_a = [&](int chunk) {
+    if constexpr (kPrepared) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) ra[j] = load_vec(atile + chunk * kChunk + aoff[j]);
+#pragma unroll
+      for (int j = 0; j < kSums; ++j) {
+        const int x = min(tid + j * kTeamThreads, kGC * kRows - 1);
+        rsum[j] = as_global<float>(A.sums)[static_cast<int64_t>(chunk * kGC + x / kRows) * A.M + min(row0 + x % kRows, A.M - 1)];
+      }
+    } else {
+      const bool in = chunk * kChunk + piece * 8 < A.K;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int r = row0 + first + j * kRowsPerPass;
+        ra[j] = make_uint4(0, 0, 0, 0);
+        if (in && r < A.M) ra[j] = load_vec(A.h + r * A.lda + chunk * kChunk + piece * 8);
+      }
     }
   };
   auto store_a = [&]() {
+    if constexpr (kPrepared) {
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int r = first + j * kRowsPerPass;
-      if (row0 + r >= A.M) continue;  // these rows were zeroed once
-      float s = Q::sum2(ra[j].x, Q::sum2(ra[j].y, Q::sum2(ra[j].z, Q::sum2(ra[j].w, 0.0f))));
-      s += dpp_f32<0xB1>(s);
-      s += dpp_f32<0x4E>(s);
-      if (kGroup >= 64) s += dpp_f32<0x141>(s);   // the other half of 8 lanes
-      if (kGroup >= 128) s += dpp_f32<0x140>(s);  // the other half of 16 lanes
-      if (piece % (kGroup / 8) == 0) s_sum[piece / (kGroup / 8)][r] = s;
-      const uint4 v = ra[j];
-      const uint4 p = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                                 __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
-      *reinterpret_cast<uint4 *>(&s_a[r * kARow + piece * 8]) = p;
+      for (int j = 0; j < kLoads; ++j)
+        *reinterpret_cast<uint4 *>(&s_a[(first + j * kRowsPerPass) * kARow + piece * 8]) = ra[j];
+#pragma unroll
+      for (int j = 0; j < kSums; ++j) {
+        const int x = tid + j * kTeamThreads;
+        if (x < kGC * kRows) s_sum[x / kRows][x % kRows] = rsum[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int r = first + j * kRowsPerPass;
+        if (row0 + r >= A.M) continue;  // these rows were zeroed once
+        const float s = group_sum<kGroup>(sum8<DT>(ra[j]));
+        if (piece % (kGroup / 8) == 0) s_sum[piece / (kGroup / 8)][r] = s;
+        *reinterpret_cast<uint4 *>(&s_a[r * kARow + piece * 8]) = permute8(ra[j]);
+      }
     }
   };
   uint32_t rs[kScales], rz[kScales];
@@ -243,7 +303,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : 2
   load_scales(min(team, chunks - 1));
 #pragma unroll
   for (int u = 0; u < kSteps; u += 2) load_w(u, (team * kSteps + u) / 2);
-  for (int r = A.M - row0 + team_wave; r < kRows; r += kTeamWaves) {
+  for (int r = A.M - row0 + team_wave; !kPrepared && r < kRows; r += kTeamWaves) {
     for (int x = lane; x < kPieces; x += 64) *reinterpret_cast<uint4 *>(&s_a[r * kARow + x * 8]) = make_uint4(0, 0, 0, 0);
     if (lane < kGC) s_sum[lane][r] = 0.0f;
   }
@@ -341,17 +401,19 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : 2
 
 namespace {
 
-template <int DT, int MT, int NT, int kChunk, int kSplit = 1>
+template <int DT, int MT, int NT, int kChunk, int kSplit = 1, bool kPrepared = false>
 void launch_tiles(LmQuantArgs A, hipStream_t st) {
   const int cols = 16 * NT * kQWaves / kSplit;
   A.row_blocks = (A.M + 16 * MT - 1) / (16 * MT);
   const dim3 grid(static_cast<unsigned>((A.V + cols - 1) / cols + 7) / 8 * 8 * A.row_blocks);
+  if (kPrepared)
+    hipLaunchKernelGGL(k_lm_prepare<DT>, dim3((A.padded / 8 + 255) / 256, A.M), dim3(256), 0, st, A);
   if (A.group == 32)
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 32, kChunk, kSplit>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 32, kChunk, kSplit, kPrepared>), grid, dim3(kQThreads), 0, st, A);
   else if (A.group == 64)
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, kChunk, kSplit>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, kChunk, kSplit, kPrepared>), grid, dim3(kQThreads), 0, st, A);
   else
-    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, kChunk, kSplit>), grid, dim3(kQThreads), 0, st, A);
+    hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, kChunk, kSplit, kPrepared>), grid, dim3(kQThreads), 0, st, A);
 }
 
 // Tiles by rows: the fewest 16-row tiles that hold them, as weights are
@@ -374,9 +436,9 @@ void launch_type(const LmQuantArgs &A, hipStream_t st) {
   else if (M <= 32)
     launch_tiles<DT, 2, 2, 256>(A, st);
   else if ((M + 63) / 64 * 64 <= (M + 79) / 80 * 80)
-    launch_tiles<DT, 4, 2, 256>(A, st);
+    launch_tiles<DT, 4, 2, 256, 1, true>(A, st);
   else
-    launch_tiles<DT, 5, 2, 256>(A, st);
+    launch_tiles<DT, 5, 2, 256, 1, true>(A, st);
 }
 
 }  // namespace

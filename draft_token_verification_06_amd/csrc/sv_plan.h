@@ -73,7 +73,7 @@ constexpr int kLmGemmThreads = 512;
 // count, so a launch of `blocks` workgroups of `threads` along one dimension
 // must stay within it; the entry points reject calls whose grids would not.
 constexpr int64_t kMaxGridItems = 0xFFFFFFFFll;
-constexpr int64_t kMaxGridY = 65535;
+constexpr int64_t kMaxGridY = 65535;  // workgroups along a second dimension
 inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks >= 1 && blocks <= kMaxGridItems / threads; }
 
 struct RowPlan {
@@ -158,6 +158,23 @@ inline LmLayout make_lm_layout(int64_t B, int32_t gamma, int32_t V) {
   L.rows_d_off = off;
   off = align256(off + sizeof(float) * static_cast<size_t>(Md) * V);
   L.total = off;
+  return L;
+}
+
+// 4-bit LM head: the smallest tile of a workgroup, and the workspace of a call
+// with more rows than its workgroups lay out themselves (K padded to a chunk).
+constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 16;
+constexpr int kLmQuantDirectRows = 32;
+struct LmQuantLayout {
+  int32_t padded;
+  size_t sums_off, total;
+};
+inline LmQuantLayout lm_quant_layout(int64_t M, int32_t K, int32_t group) {
+  LmQuantLayout L{};
+  if (M <= kLmQuantDirectRows) return L;
+  L.padded = (K + 255) / 256 * 256;
+  L.sums_off = align256(static_cast<size_t>(M) * L.padded * 2);
+  L.total = align256(L.sums_off + static_cast<size_t>(M) * (L.padded / group) * sizeof(float));
   return L;
 }
 

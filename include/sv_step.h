@@ -86,12 +86,16 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
  *   out     [M] rows of out_row_stride elements (0 = V), SV_DT_F32 or hidden's
  *           type, not overlapping the inputs.  Dense rows of M = B * (gamma + 1)
  *           are the target_logits of sv_verify_window.
+ *   workspace of sv_lmhead_quant_workspace bytes; that is 0 (and NULL will do)
+ *           for up to 32 rows.
  * Weights enter the products exactly; sums are held in float32 and rounded
- * once.  M <= 1,048,560. */
+ * once.  M <= 65535. */
+size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t group);
 int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                     const uint8_t *weights, const void *scales, const uint8_t *zeros,
                     int32_t M, int32_t K, int32_t V, int32_t group,
-                    void *out, int64_t out_row_stride, int out_dtype, hipStream_t stream);
+                    void *out, int64_t out_row_stride, int out_dtype,
+                    void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Attention of a step's rows: every row of a window or tree over the prefix
  * the whole batch shares, its sequence's cached context and its own ancestors

@@ -15,6 +15,7 @@ int main(void) {
   } entry[] = {
       {"sv_adjust_logits", (any_fn)sv_adjust_logits},
       {"sv_lmhead_quant", (any_fn)sv_lmhead_quant},
+      {"sv_lmhead_quant_workspace", (any_fn)sv_lmhead_quant_workspace},
       {"sv_attention_workspace", (any_fn)sv_attention_workspace},
       {"sv_attention", (any_fn)sv_attention},
   };
@@ -24,8 +25,8 @@ int main(void) {
   printf("attention_ws_bad %zu\n", sv_attention_workspace(64, 9, 32, 7, 128, 8192, 1024));
   printf("adjust_null %d\n", sv_adjust_logits(NULL, 0, NULL, 0, SV_DT_BF16, NULL, 0, NULL, NULL, 2, 1, 100, NULL, 0, 0, NULL,
                                               NULL, NULL, NULL, NULL, NULL, NULL, 0, NULL, 0, 0, NULL));
-  printf("lmhead_null %d\n", sv_lmhead_quant(NULL, 0, SV_DT_F16, NULL, NULL, NULL, 1, 64, 100, 64, NULL, 0, SV_DT_F32, NULL));
-  printf("lmhead_dtype %d\n", sv_lmhead_quant(NULL, 0, SV_DT_F32, NULL, NULL, NULL, 1, 64, 100, 64, NULL, 0, SV_DT_F32, NULL));
+  printf("lmhead_null %d\n", sv_lmhead_quant(NULL, 0, SV_DT_F16, NULL, NULL, NULL, 1, 64, 100, 64, NULL, 0, SV_DT_F32, NULL, 0, NULL));
+  printf("lmhead_dtype %d\n", sv_lmhead_quant(NULL, 0, SV_DT_F32, NULL, NULL, NULL, 1, 64, 100, 64, NULL, 0, SV_DT_F32, NULL, 0, NULL));
   printf("attention_null %d\n", sv_attention(NULL, 0, SV_DT_BF16, NULL, NULL, 0, 0, 64, NULL, NULL, 0, 0, NULL, NULL, NULL,
                                              1, 1, 8, 8, 64, 10, 1.0f, NULL, NULL, NULL, 0, NULL));
   return 0;

@@ -10,7 +10,7 @@ FAKE = 0x100000  # never dereferenced: validation fails first
 
 def _call(**kw):
     a = dict(hidden=FAKE, stride=0, dtype=1, weights=FAKE, scales=FAKE, zeros=None, M=4, K=256, V=100, group=64,
-             out=FAKE, out_stride=0, out_dtype=0)
+             out=FAKE, out_stride=0, out_dtype=0, ws=None, ws_bytes=0)
     a.update(kw)
     return _lib.lib().sv_lmhead_quant(*a.values(), None)
 
@@ -20,7 +20,10 @@ def _call(**kw):
     (dict(dtype=5), -2),
     (dict(out_dtype=2), -2),                 # float16 rows from bf16 states
     (dict(M=0), -1),
-    (dict(M=1048561), -1),
+    (dict(M=65536), -1),
+    (dict(M=33), -3),                        # more rows than 32 need a workspace
+    (dict(M=33, ws=FAKE, ws_bytes=1024), -3),
+    (dict(M=33, ws=FAKE + 16, ws_bytes=1 << 20), -3),
     (dict(V=0), -1),
     (dict(V=(1 << 21) + 1), -1),
     (dict(group=16), -1),
@@ -43,6 +46,14 @@ def _call(**kw):
 ])
 def test_status(kw, status):
     assert _call(**kw) == status
+
+
+def test_workspace_rules():
+    L = _lib.lib()
+    assert L.sv_lmhead_quant_workspace(32, 4096, 128) == 0
+    assert L.sv_lmhead_quant_workspace(33, 4096, 128) >= 33 * (4096 * 2 + 32 * 4)
+    assert L.sv_lmhead_quant_workspace(33, 4096, 96) == 0
+    assert L.sv_lmhead_quant_workspace(0, 4096, 128) == 0
 
 
 def test_binding_refuses():
