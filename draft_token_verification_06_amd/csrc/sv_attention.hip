@@ -84,10 +84,14 @@ __device__ __forceinline__ float2 both_halves(float x) {
   return make_float2(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
-template <int D> constexpr int at_lds_row() { return D + 8; }  // elements; 16 bytes of padding spread the banks
+// LDS rows in elements.  The 128 bytes that one cycle serves are 8 lanes of 16
+// bytes in consecutive key rows (16 bytes of padding put them side by side),
+// or the 4 value rows of 32 bytes of a transposing read (32 bytes of padding).
+template <int D> constexpr int at_key_row() { return D + 8; }
+template <int D> constexpr int at_value_row() { return D + 16; }
 template <int D, int WQ> constexpr int at_tile_keys() { return WQ == 1 ? 128 : 64; }
 template <int D, int WQ> constexpr size_t at_tile_bytes() {
-  const size_t kv = 2 * static_cast<size_t>(at_tile_keys<D, WQ>()) * at_lds_row<D>() * 2;
+  const size_t kv = static_cast<size_t>(at_tile_keys<D, WQ>()) * (at_key_row<D>() + at_value_row<D>()) * 2;
   const size_t merge = WQ < 4 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
   return kv > merge ? kv : merge;
 }
@@ -115,7 +119,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   constexpr int WK = 4 / WQ;
   constexpr int KT = at_tile_keys<D, WQ>();
   constexpr int SB = KT / (32 * WK);      // 32-key blocks per wave and tile
-  constexpr int kRow = at_lds_row<D>();
+  constexpr int kRow = at_key_row<D>(), kVRow = at_value_row<D>();
   constexpr int kChunks = D / 8;          // 16-byte pieces per row
   constexpr int kLoads = KT * kChunks / kAtThreads;
   uint16_t *s_k = reinterpret_cast<uint16_t *>(lds);
@@ -192,7 +196,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
       *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 8) = rk[j];
-      *reinterpret_cast<uint4 *>(s_v + row * kRow + piece * 8) = v;
+      *reinterpret_cast<uint4 *>(s_v + row * kVRow + piece * 8) = v;
     }
     tile_barrier();
     if (t0 + KT < it.k1) load(t0 + KT);
@@ -253,11 +257,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
         const uint4 p = make_uint4(T::pack(s[sb][8 * ks], s[sb][8 * ks + 1]), T::pack(s[sb][8 * ks + 2], s[sb][8 * ks + 3]),
                                    T::pack(s[sb][8 * ks + 4], s[sb][8 * ks + 5]), T::pack(s[sb][8 * ks + 6], s[sb][8 * ks + 7]));
         // lane l: block of 4 keys x 16 values; its address is row (l % 16) / 4, values 4 (l % 4)
-        const uint16_t *base = s_v + (kb + ks * 16 + 4 * half + ((lane & 15) >> 2)) * kRow + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+        const uint16_t *base = s_v + (kb + ks * 16 + 4 * half + ((lane & 15) >> 2)) * kVRow + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
 #pragma unroll
         for (int t = 0; t < D / 32; ++t) {
           const at_i16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32));
-          const at_i16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32 + 8 * kRow));
+          const at_i16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(base + t * 32 + 8 * kVRow));
           const uint2 u0 = __builtin_bit_cast(uint2, a0), u1 = __builtin_bit_cast(uint2, a1);
           o[t] = T::mma(make_uint4(u0.x, u0.y, u1.x, u1.y), p, o[t]);
         }

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int n = i * 8 + (lane >> 3), block = (lane & 7) ^ (n >> 1);
+      const int n = i * 8 + (lane >> 3), block = (lane & 7) ^ (n & 7);
       woff[t][i] = static_cast<uint32_t>(min(team_wave * NT * 16 + t * 16 + n, A.V - 1 - col0)) * (A.K / 2) + block * 16;
       wtail[t][i] = woff[t][i] - max(last * 8 + block - (blocks - 1), 0) * 16;
     }
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
           s_w[wave][t][lane] = rw[u][t];
           s_w[wave][t][64 + lane] = rw[u + 1][t];
         }
-        const uint4 x = s_w[wave][t][c16 * 8 + ((u % 2 * 4 + quad) ^ (c16 >> 1))];
+        const uint4 x = s_w[wave][t][c16 * 8 + ((u % 2 * 4 + quad) ^ (c16 & 7))];
         w[t][0] = x.x;
         w[t][1] = x.y;
         w[t][2] = x.z;
