@@ -118,6 +118,15 @@ template <int kGroup> __device__ __forceinline__ int step_at(int s, int quad) {
   return quad * 32 + s * 8;
 }
 
+// Where the 16-byte piece p of a hidden row lies in its LDS row: exclusive-ored
+// with the row, so that the 16 lanes one cycle pair serves (rows 0-3 and 12-15
+// of one quad, 4-11 of the next) meet 16 different bank groups.  Neighbouring
+// quads' pieces differ in bit 2 (bit 0 for groups of 32), which rows 4-11 undo.
+template <int kGroup> __device__ __forceinline__ int a_slot(int p, int row) {
+  const int f = (row & 15) ^ (kGroup == 32 ? 0 : 4 * ((row >> 2 ^ row >> 3) & 1));
+  return p ^ f;
+}
+
 // A workgroup barrier that orders LDS only: global loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -166,14 +175,13 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
   constexpr int kSteps = kChunk / kQStep;
   constexpr int kG = kQStep / kGroup, kGC = kChunk / kGroup;  // groups per step and chunk
   constexpr int kSub = kGroup / 32;                           // MFMAs per group and tile
-  constexpr int kARow = kChunk + 8;                           // 16 bytes of padding spread the banks
   constexpr int kPieces = kChunk / 8;                         // 16-byte pieces per row of a chunk
   constexpr int kRowsPerPass = kTeamThreads / kPieces;
   constexpr int kLoads = kRows / kRowsPerPass;
   constexpr int kScales = (kGC * kCols + kTeamThreads - 1) / kTeamThreads;
   static_assert(kRows % kRowsPerPass == 0, "whole passes");
   static_assert(kSplit == 1 || kSplit == kQWaves, "teams are the workgroup or its waves");
-  __shared__ uint16_t s_as[kSplit][kRows * kARow];
+  __shared__ uint16_t s_as[kSplit][kRows * kChunk];
   __shared__ uint4 s_w[kQWaves][NT][128];  // a step's weights on their way to the lanes that multiply them
   __shared__ float s_sums[kSplit][kGC][kRows];    // sums of the hidden values per group
   __shared__ float2 s_scales[kSplit][kGC][kCols];  // scale, -(16 + zero)
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
     if constexpr (kPrepared) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
-        *reinterpret_cast<uint4 *>(&s_a[(first + j * kRowsPerPass) * kARow + piece * 8]) = ra[j];
+        *reinterpret_cast<uint4 *>(&s_a[(first + j * kRowsPerPass) * kChunk + a_slot<kGroup>(piece, first + j * kRowsPerPass) * 8]) = ra[j];
 #pragma unroll
       for (int j = 0; j < kSums; ++j) {
         const int x = tid + j * kTeamThreads;
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
         if (row0 + r >= A.M) continue;  // these rows were zeroed once
         const float s = group_sum<kGroup>(sum8<DT>(ra[j]));
         if (piece % (kGroup / 8) == 0) s_sum[piece / (kGroup / 8)][r] = s;
-        *reinterpret_cast<uint4 *>(&s_a[r * kARow + piece * 8]) = permute8(ra[j]);
+        *reinterpret_cast<uint4 *>(&s_a[r * kChunk + a_slot<kGroup>(piece, r) * 8]) = permute8(ra[j]);
       }
     }
   };
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
 #pragma unroll
   for (int u = 0; u < kSteps; u += 2) load_w(u, (team * kSteps + u) / 2);
   for (int r = A.M - row0 + team_wave; !kPrepared && r < kRows; r += kTeamWaves) {
-    for (int x = lane; x < kPieces; x += 64) *reinterpret_cast<uint4 *>(&s_a[r * kARow + x * 8]) = make_uint4(0, 0, 0, 0);
+    for (int x = lane; x < kPieces; x += 64) *reinterpret_cast<uint4 *>(&s_a[r * kChunk + x * 8]) = make_uint4(0, 0, 0, 0);
     if (lane < kGC) s_sum[lane][r] = 0.0f;
   }
   for (int c = team; c < chunks; c += kSplit) {
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
           for (int t = 0; t < NT; ++t) b[t] = unpack8<DT>(w[t][s], mask, one);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(&s_a[(m * 16 + c16) * kARow + u * kQStep + step_at<kGroup>(s, quad)]);
+            const uint4 a = *reinterpret_cast<const uint4 *>(&s_a[(m * 16 + c16) * kChunk + a_slot<kGroup>(u * (kQStep / 8) + step_at<kGroup>(s, quad) / 8, c16) * 8]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) part[m][t] = Q::mma(a, b[t], part[m][t]);
           }
