@@ -40,7 +40,7 @@ _SIGNATURES = {
 _STEP_SIGNATURES = {
     "sv_adjust_logits": (_c.c_int, [_P, _I64, _P, _I64, _c.c_int, _P, _I64, _P, _P, _I32, _I32, _I32,
                                     _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _P]),
-    "sv_lmhead_quant_workspace": (_SZ, [_I32] * 3),
+    "sv_lmhead_quant_workspace": (_SZ, [_I32] * 4),
     "sv_lmhead_quant": (_c.c_int, [_P, _I64, _c.c_int, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _c.c_int,
                                    _P, _SZ, _P]),
     "sv_attention_workspace": (_SZ, [_I32] * 7),

@@ -454,9 +454,9 @@ def adjust_logits(logits, *, tokens=None, parent=None, history=None, history_len
     return out
 
 
-def lmhead_quant_workspace(M, K, group, device):
-    """A workspace for lmhead_quant calls of M rows, or None where they need none."""
-    nbytes = int(lib().sv_lmhead_quant_workspace(M, K, group))
+def lmhead_quant_workspace(M, K, V, group, device):
+    """A workspace for lmhead_quant calls of these sizes, or None where they need none."""
+    nbytes = int(lib().sv_lmhead_quant_workspace(M, K, V, group))
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
@@ -498,7 +498,7 @@ def lmhead_quant(hidden, weights, scales, zeros=None, *, out_dtype=torch.float32
         raise ValueError("hidden: rows must be contiguous and not overlap")
     group = K // scales.shape[1]
     if ws is None and M > 32:
-        ws = lmhead_quant_workspace(M, K, group, dev)
+        ws = lmhead_quant_workspace(M, K, V, group, dev)
     ws_bytes = 0 if ws is None else _ws_bytes(ws, dev)
     _launch(dev, lib().sv_lmhead_quant, rows.data_ptr(), rows.stride(0) if M > 1 else 0, _DTYPE_CODE[dtype],
             weights.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),

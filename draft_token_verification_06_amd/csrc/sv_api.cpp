@@ -641,9 +641,9 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
   return launch_status();
 }
 
-size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t group) {
-  if (M < 1 || M > kMaxGridY || !quant_sizes_ok(K, group)) return 0;
-  return lm_quant_layout(M, K, group).total;
+size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t V, int32_t group) {
+  if (M < 1 || M > kMaxGridY || V < 1 || V > kMaxVocab || !quant_sizes_ok(K, group)) return 0;
+  return lm_quant_layout(M, K, V, group).total;
 }
 
 int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
@@ -665,7 +665,7 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                      ((static_cast<int64_t>(M) + kLmQuantMinRows - 1) / kLmQuantMinRows),
                  kLmQuantThreads))
     return SV_EINVAL;
-  const LmQuantLayout L = lm_quant_layout(M, K, group);
+  const LmQuantLayout L = lm_quant_layout(M, K, V, group);
   if (L.total > 0) {
     const int ws = check_workspace(workspace, workspace_bytes, L.total);
     if (ws != SV_OK) return ws;
@@ -686,6 +686,9 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
   A.padded = L.padded;
   A.prepared = static_cast<uint16_t *>(workspace);
   A.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + L.sums_off);
+  A.splits = L.splits;
+  A.split_chunks = L.split_chunks;
+  A.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + L.partial_off);
   launch_lm_quant(dtype, A, stream);
   return launch_status();
 }

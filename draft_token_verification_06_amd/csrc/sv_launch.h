@@ -148,6 +148,8 @@ struct LmQuantArgs {
   int32_t padded;
   uint16_t *prepared;
   float *sums;
+  int32_t splits, split_chunks;  // K shared out among workgroups: shares, chunks of 256 in each
+  float *partial;                // [splits][M][V] where there are several
 };
 constexpr int kLmQuantThreads = 256;
 void launch_lm_quant(int dtype, const LmQuantArgs &A, hipStream_t st);

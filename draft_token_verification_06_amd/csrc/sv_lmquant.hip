@@ -197,8 +197,11 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
   const int row0 = blockIdx.x / 8 % A.row_blocks * kRows;
   const int col0 = ct * kCols;
   if (col0 >= A.V) return;
-  const int chunks = (A.K + kChunk - 1) / kChunk;
+  const int chunks_all = (A.K + kChunk - 1) / kChunk;
   const int groups = A.K / kGroup, blocks = A.K / 32;
+  // this workgroup's chunks of K: all, or (prepared rows) blockIdx.y's share
+  const int begin = kPrepared ? blockIdx.y * A.split_chunks : 0;
+  const int chunks = kPrepared ? min(begin + A.split_chunks, chunks_all) : chunks_all;
 
   uint4 ra[kLoads];
   const int piece = tid % kPieces, first = tid / kPieces;
@@ -307,16 +310,16 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
     if (kSplit > 1) __builtin_amdgcn_wave_barrier();
     else lds_barrier();
   };
-  load_a(min(team, chunks - 1));
-  load_scales(min(team, chunks - 1));
+  load_a(min(begin + team, chunks - 1));
+  load_scales(min(begin + team, chunks - 1));
 #pragma unroll
-  for (int u = 0; u < kSteps; u += 2) load_w(u, (team * kSteps + u) / 2);
+  for (int u = 0; u < kSteps; u += 2) load_w(u, ((begin + team) * kSteps + u) / 2);
   for (int r = A.M - row0 + team_wave; !kPrepared && r < kRows; r += kTeamWaves) {
     for (int x = lane; x < kPieces; x += 64) *reinterpret_cast<uint4 *>(&s_a[r * kChunk + x * 8]) = make_uint4(0, 0, 0, 0);
     if (lane < kGC) s_sum[lane][r] = 0.0f;
   }
-  for (int c = team; c < chunks; c += kSplit) {
-    if (c >= kSplit) team_barrier();  // every wave is done with the previous chunk
+  for (int c = begin + team; c < chunks; c += kSplit) {
+    if (c >= begin + kSplit) team_barrier();  // every wave is done with the previous chunk
     store_a();
     store_scales();
     load_a(min(c + kSplit, chunks - 1));
@@ -402,9 +405,24 @@ __global__ void __launch_bounds__(kQThreads, MT * NT <= 2 && kSplit == 1 ? 4 : M
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = row0 + m * 16 + quad * 4 + e;
-        if (r < A.M) store_logit<DT>(A, r * A.out_stride + v, acc[m][t][e]);
+        if (r >= A.M) continue;
+        if (kPrepared && A.splits > 1)
+          A.partial[(static_cast<int64_t>(blockIdx.y) * A.M + r) * A.V + v] = acc[m][t][e];
+        else
+          store_logit<DT>(A, r * A.out_stride + v, acc[m][t][e]);
       }
   }
+}
+
+// The shares of K of every logit, added in order.
+template <int DT>
+__global__ void __launch_bounds__(256) k_lm_join(LmQuantArgs A) {
+  const int v = blockIdx.x * 256 + threadIdx.x, r = blockIdx.y;
+  if (v >= A.V) return;
+  const float *p = A.partial + static_cast<int64_t>(r) * A.V + v;
+  float x = p[0];
+  for (int s = 1; s < A.splits; ++s) x += p[static_cast<int64_t>(s) * A.M * A.V];
+  store_logit<DT>(A, r * A.out_stride + v, x);
 }
 
 namespace {
@@ -413,7 +431,8 @@ template <int DT, int MT, int NT, int kChunk, int kSplit = 1, bool kPrepared = f
 void launch_tiles(LmQuantArgs A, hipStream_t st) {
   const int cols = 16 * NT * kQWaves / kSplit;
   A.row_blocks = (A.M + 16 * MT - 1) / (16 * MT);
-  const dim3 grid(static_cast<unsigned>((A.V + cols - 1) / cols + 7) / 8 * 8 * A.row_blocks);
+  dim3 grid(static_cast<unsigned>((A.V + cols - 1) / cols + 7) / 8 * 8 * A.row_blocks);
+  grid.y = kPrepared ? A.splits : 1;
   if (kPrepared)
     hipLaunchKernelGGL(k_lm_prepare<DT>, dim3((A.padded / 8 + 255) / 256, A.M), dim3(256), 0, st, A);
   if (A.group == 32)
@@ -422,28 +441,31 @@ void launch_tiles(LmQuantArgs A, hipStream_t st) {
     hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 64, kChunk, kSplit, kPrepared>), grid, dim3(kQThreads), 0, st, A);
   else
     hipLaunchKernelGGL((k_lm_quant<DT, MT, NT, 128, kChunk, kSplit, kPrepared>), grid, dim3(kQThreads), 0, st, A);
+  if (kPrepared && A.splits > 1)
+    hipLaunchKernelGGL(k_lm_join<DT>, dim3((A.V + 255) / 256, A.M), dim3(256), 0, st, A);
 }
 
 // Tiles by rows: the fewest 16-row tiles that hold them, as weights are
-// unpacked once per row block; past 64 rows in blocks of 64 or 80, whichever
-// pads less.  Where 16-column workgroups whose waves split K fill the chip no
-// more than about twice, they run instead: K is long and little else can be
-// shared out (us at K = 4096: M = 4, V = 8000 11, not split 18; M = 24, V = 8000
-// 16 and 39; M = 64, V = 4000 17 and 37, V = 14000 55 and 43).
+// unpacked once per row block; past 32 rows in blocks of 64 or 80.  Small
+// vocabularies share K out: among a workgroup's waves up to 32 rows, while
+// 16-column workgroups fill the chip about twice at most (us at K = 4096: M = 4,
+// V = 8000 11, not shared 18; M = 16, V = 16000 20 and 14; M = 24, V = 8000 16 and
+// 39), among workgroups beyond (M = 64, V = 8000 25 and 42; M = 200, V = 4000 35
+// and 52), see lm_quant_layout.
 template <int DT>
 void launch_type(const LmQuantArgs &A, hipStream_t st) {
   const int64_t M = A.M, tiles = (A.V + 15) / 16;
   if (M <= 16 && tiles <= 640)
     launch_tiles<DT, 1, 1, 256, 4>(A, st);
-  else if (M > 16 && tiles * ((M + 31) / 32) <= 1024)
-    launch_tiles<DT, 2, 1, 256, 4>(A, st);
   else if (M <= 16 && A.V < 512 * 128)
     launch_tiles<DT, 1, 1, 512>(A, st);  // 64 columns: 128 would leave CUs idle (V = 32000: 11 us, 13 with 128)
   else if (M <= 16)
-    launch_tiles<DT, 1, 2, 256>(A, st);  // (V = 128256, M = 8: 54 us, 65 with 64 columns)
-  else if (M <= 32)
+    launch_tiles<DT, 1, 2, 256>(A, st);  // (V = 128256, M = 8: 55 us, 65 with 64 columns)
+  else if (M <= kLmQuantDirectRows && tiles <= 1024)
+    launch_tiles<DT, 2, 1, 256, 4>(A, st);
+  else if (M <= kLmQuantDirectRows)
     launch_tiles<DT, 2, 2, 256>(A, st);
-  else if ((M + 63) / 64 * 64 <= (M + 79) / 80 * 80)
+  else if (lm_quant_rows(M) == 64)
     launch_tiles<DT, 4, 2, 256, 1, true>(A, st);
   else
     launch_tiles<DT, 5, 2, 256, 1, true>(A, st);

@@ -165,16 +165,33 @@ inline LmLayout make_lm_layout(int64_t B, int32_t gamma, int32_t V) {
 // with more rows than its workgroups lay out themselves (K padded to a chunk).
 constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 16;
 constexpr int kLmQuantDirectRows = 32;
+constexpr int kLmQuantCols = 128;       // columns of a workgroup with more rows than that
+constexpr int64_t kLmQuantSlots = 512;  // of those run at once: 2 on each of 256 CUs
+// Rows of a workgroup: blocks of 64 or 80, whichever pads less.
+inline int lm_quant_rows(int64_t M) { return (M + 63) / 64 * 64 <= (M + 79) / 80 * 80 ? 64 : 80; }
 struct LmQuantLayout {
-  int32_t padded;
-  size_t sums_off, total;
+  int32_t padded, splits, split_chunks;
+  size_t sums_off, partial_off, total;
 };
-inline LmQuantLayout lm_quant_layout(int64_t M, int32_t K, int32_t group) {
+inline LmQuantLayout lm_quant_layout(int64_t M, int32_t K, int32_t V, int32_t group) {
   LmQuantLayout L{};
+  L.splits = 1;
   if (M <= kLmQuantDirectRows) return L;
-  L.padded = (K + 255) / 256 * 256;
+  const int chunks = (K + 255) / 256;
+  L.padded = chunks * 256;
+  // Few tiles leave most of the chip idle for as long as K is: K is then shared
+  // out too, two chunks at least to a workgroup.
+  const int64_t rows = lm_quant_rows(M);
+  const int64_t tiles = (static_cast<int64_t>(V) + kLmQuantCols - 1) / kLmQuantCols * ((M + rows - 1) / rows);
+  int64_t splits = (kLmQuantSlots + tiles - 1) / tiles;
+  if (splits > (chunks + 1) / 2) splits = (chunks + 1) / 2;
+  if (splits > 8) splits = 8;
+  if (4 * tiles > 3 * kLmQuantSlots) splits = 1;
+  L.split_chunks = static_cast<int32_t>((chunks + splits - 1) / splits);
+  L.splits = (chunks + L.split_chunks - 1) / L.split_chunks;
   L.sums_off = align256(static_cast<size_t>(M) * L.padded * 2);
-  L.total = align256(L.sums_off + static_cast<size_t>(M) * (L.padded / group) * sizeof(float));
+  L.partial_off = align256(L.sums_off + static_cast<size_t>(M) * (L.padded / group) * sizeof(float));
+  L.total = L.partial_off + (L.splits > 1 ? align256(static_cast<size_t>(L.splits) * M * V * sizeof(float)) : 0);
   return L;
 }
 

@@ -59,6 +59,9 @@ CASES = [
     (130, 256, 129, 128, "f16", True, "f32"),
     (256, 1280, 200, 64, "bf16", False, "f32"),
     (1, 8192, 999, 128, "bf16", True, "f32"),
+    (40, 4096, 20000, 64, "bf16", True, "f32"),      # K shared out among workgroups
+    (150, 1600, 6001, 32, "f16", True, "same"),
+    (96, 64, 30000, 64, "bf16", False, "f32"),
     (5, 4096, 50257, 128, "bf16", True, "f32"),
 ]
 

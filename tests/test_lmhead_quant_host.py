@@ -50,10 +50,14 @@ def test_status(kw, status):
 
 def test_workspace_rules():
     L = _lib.lib()
-    assert L.sv_lmhead_quant_workspace(32, 4096, 128) == 0
-    assert L.sv_lmhead_quant_workspace(33, 4096, 128) >= 33 * (4096 * 2 + 32 * 4)
-    assert L.sv_lmhead_quant_workspace(33, 4096, 96) == 0
-    assert L.sv_lmhead_quant_workspace(0, 4096, 128) == 0
+    size = L.sv_lmhead_quant_workspace
+    assert size(32, 4096, 5000, 128) == 0
+    assert size(33, 4096, 200000, 128) >= 33 * (4096 * 2 + 32 * 4)
+    assert size(33, 4096, 200000, 128) % 256 == 0
+    assert size(200, 4096, 4000, 128) >= 200 * (4096 * 2 + 32 * 4) + 2 * 200 * 4000 * 4  # K shared out
+    assert size(33, 4096, 5000, 96) == 0
+    assert size(0, 4096, 5000, 128) == 0
+    assert size(33, 4096, 0, 128) == 0
 
 
 def test_binding_refuses():
