@@ -672,7 +672,41 @@ def side_workloads(torch, sv, synth, dev):
     out["hierarchy_64_streams_V128256_bf16"] = {
         "stage1_us": s1_ms * 1e3, "stage1_GBps": S * 17 * V * 2 / (s1_ms * 1e-3) / 1e9,
         "stage2_us": s2_ms * 1e3, "rollback_us": rb_ms * 1e3}
+    del h, bt, bl, w1, w2, r1, r2
+    out["step_B64_g8_P8192_Hq32_Hkv8_D128_V128256"] = step_workload(torch, sv, dev, reps)
     return out
+
+
+def step_workload(torch, sv, dev, reps):
+    """The target's side of one verification step of 64 windows (gamma = 8)
+    behind a shared prefix of 8192 tokens: attention (32 query heads on 8 kv
+    heads of 128, own caches of 1024), LM head on 4-bit weights with groups of
+    128, penalties over 1024-token histories, greedy verification; one time per
+    operator."""
+    Bs, R, Hq, Hkv, D, P, ctx, G = 64, GAMMA + 1, 32, 8, 128, 8192, 1024, 128
+    bf, K = torch.bfloat16, Hq * D
+    rnd = lambda *s: torch.randn(*s, device=dev, dtype=bf)  # noqa: E731
+    q, k, v, pk, pv = rnd(Bs, R, Hq, D), rnd(Bs, ctx + R, Hkv, D), rnd(Bs, ctx + R, Hkv, D), rnd(P, Hkv, D), rnd(P, Hkv, D)
+    lens = torch.full((Bs,), ctx, dtype=torch.int32, device=dev)
+    wq = torch.randint(0, 256, (V, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.rand(V, K // G, device=dev).to(bf) * 0.02
+    tokens = torch.randint(0, V, (Bs, GAMMA), dtype=torch.int32, device=dev)
+    history = torch.randint(0, V, (Bs, 1024), dtype=torch.int32, device=dev)
+    penalty = torch.full((Bs,), 1.1, device=dev)
+    ws = sv.attention_workspace(Bs, R, Hq, Hkv, D, P, ctx, dev)
+    hws = sv.lmhead_quant_workspace(Bs * R, K, V, G, dev)
+    vws = sv.workspace(sv.SV_OP_GREEDY, Bs, GAMMA, V, bf, dev)
+    att = sv.attention(q, k, v, lens, prefix_k=pk, prefix_v=pv, ws=ws)
+    hidden = att.out.view(Bs, R, K)
+    logits = sv.lmhead_quant(hidden, wq, scales, out_dtype=bf, ws=hws)
+    rows = torch.empty_like(logits)
+    calls = {
+        "attention": lambda: sv.attention(q, k, v, lens, prefix_k=pk, prefix_v=pv, out=att, ws=ws),
+        "lmhead_quant": lambda: sv.lmhead_quant(hidden, wq, scales, out=logits, ws=hws),
+        "adjust_logits": lambda: sv.adjust_logits(logits, tokens=tokens, history=history, repetition=penalty, out=rows),
+        "verify_greedy": lambda: sv.verify_greedy(rows, tokens, ws=vws),
+    }
+    return {name + "_us": event_time_ms(torch, call, reps) * 1e3 for name, call in calls.items()}
 
 
 if __name__ == "__main__":

@@ -22,6 +22,17 @@
 // tile.  A workgroup's four waves split the tile's rows (WQ = 4: 128 rows, for
 // the prefix of a batch), the keys of a tile (WQ = 1: 32 rows, for the few rows
 // of one sequence, where cache bandwidth is the bound), or both (WQ = 2: 64).
+// Two workgroups share a CU: 220 registers per lane, up to 81 KB of LDS.
+//
+// Measured (bf16, 32 query heads on 8 kv heads of 128):
+// - 128 single tokens over own caches of 1000 to 4000 tokens and a prefix of
+//   2048 (1.34 GB): 235 us + 6 us for the join, 5.6 TB/s.  Bound: memory and the
+//   start and end of each range; ranges of 512 to 2048 keys differ by 5%.
+// - 64 windows of 9 rows, prefix 8192, own caches of 256 to 1024 (84 GFLOP):
+//   135 + 15 us, 560 TFLOP/s.  Bound: the loads and their way through LDS, which
+//   alone take 108 us, then the vector work of the exponentials.
+// - one token over 333 + 700 keys: 7.5 + 5 us; bound: two launches and the trips
+//   to memory of one range.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -329,7 +340,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
         const float2 v = s_ml[w * kRows + q];
-        if (v.x != kNegInf) L += v.y * exp2_fast((v.x - Mq) * A.scale_log2);
+        L += v.x == kNegInf ? v.y : v.y * exp2_fast((v.x - Mq) * A.scale_log2);  // (no maximum: zero, or NaN)
       }
       A.part_ml[at] = make_float2(Mq, L);
     }
@@ -439,7 +450,7 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
   const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  if (row >= rows) return;
+  if (row >= rows) return;  // (bound: the partial outputs, 4 D bytes a row and range, written and read once)
   const int64_t br = row / A.Hq;
   const int b = static_cast<int>(br / A.R), r = static_cast<int>(br % A.R);
   const int live = live_rows(A, b);

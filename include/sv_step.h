@@ -89,7 +89,8 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
  *   workspace of sv_lmhead_quant_workspace bytes; that is 0 (and NULL will do)
  *           for up to 32 rows.
  * Weights enter the products exactly; sums are held in float32 and rounded
- * once.  M <= 65535. */
+ * once.  Hidden values must be finite (an infinite one makes its row NaN).
+ * M <= 65535. */
 size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t V, int32_t group);
 int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                     const uint8_t *weights, const void *scales, const uint8_t *zeros,

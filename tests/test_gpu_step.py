@@ -85,7 +85,8 @@ def check_step(s):
         tol = moved * float(s["rep"][b])  # the penalty multiplies a logit by at most that
         fine = np.isfinite(y)
         assert np.array_equal(np.isfinite(got[b]), fine)
-        assert (np.abs(got[b] - y)[fine] <= tol[fine]).all(), float((np.abs(got[b] - y)[fine] / tol[fine]).max())
+        err = np.abs(got[b][fine] - y[fine])
+        assert (err <= tol[fine]).all(), float((err / tol[fine]).max())
         for r in range(R):
             top = int(np.argmax(y[r]))
             rest = np.delete(y[r] + np.where(np.isfinite(y[r]), tol[r], 0), top).max()
