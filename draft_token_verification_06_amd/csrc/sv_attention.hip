@@ -169,14 +169,27 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   constexpr bool kApart = WQ == 1;
   constexpr int kRowsPerPass = (kApart ? 64 : kAtThreads) / kChunks;
   const int piece = tid % kChunks, first = kApart ? wave * 32 + lane / kChunks : tid / kChunks;
+  // one sequence's cache is read once: streamed
+  auto fetch = [&](const uint16_t *p) { return kApart ? load_stream(reinterpret_cast<const uint4 *>(p)) : load_vec(p); };
+  const bool near = it.tok_stride < (1 << 22);  // a tile's offsets fit 32 bits
+  const uint32_t lane_off = static_cast<uint32_t>(first) * static_cast<uint32_t>(it.tok_stride) + piece * 8;
   auto load = [&](int t0) {
+    if (near && t0 + KT <= it.k1) {
+      // whole tiles: one offset per lane, everything else scalar
+      const uint16_t *pk = it.k + t0 * it.tok_stride, *pv = it.v + t0 * it.tok_stride;
+      const int64_t pass = kRowsPerPass * it.tok_stride;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int64_t key = min(t0 + first + j * kRowsPerPass, it.k1 - 1);
-      const uint16_t *pk = it.k + key * it.tok_stride + piece * 8, *pv = it.v + key * it.tok_stride + piece * 8;
-      // one sequence's cache is read once: streamed
-      rk[j] = kApart ? load_stream(reinterpret_cast<const uint4 *>(pk)) : load_vec(pk);
-      rv[j] = kApart ? load_stream(reinterpret_cast<const uint4 *>(pv)) : load_vec(pv);
+      for (int j = 0; j < kLoads; ++j) {
+        rk[j] = fetch(pk + j * pass + lane_off);
+        rv[j] = fetch(pv + j * pass + lane_off);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int64_t key = min(t0 + first + j * kRowsPerPass, it.k1 - 1);
+        rk[j] = fetch(it.k + key * it.tok_stride + piece * 8);
+        rv[j] = fetch(it.v + key * it.tok_stride + piece * 8);
+      }
     }
   };
   auto tile_barrier = [&]() {
@@ -196,7 +209,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
     for (int j = 0; j < kLoads; ++j) {
       const int row = first + j * kRowsPerPass;
       uint4 v = rv[j];
-      if (t0 + row >= it.k1) v = make_uint4(0, 0, 0, 0);
+      if (t0 + KT > it.k1 && t0 + row >= it.k1) v = make_uint4(0, 0, 0, 0);
       if (masked && t0 + row >= it.draft && t0 + row < it.k1) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

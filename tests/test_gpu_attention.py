@@ -152,6 +152,34 @@ def test_row_count_and_bad_lengths():
     check(sub, q[ok], k[ok], v[ok], [lens[b] for b in ok], pk=pk, pv=pv, row_count=[rc[b] for b in ok])
 
 
+def test_max_ctx_bounds_the_lengths():
+    """max_ctx below the cache's room: the results are those of the default,
+    and a longer sequence is out of range."""
+    q, k, v, pk, pv = make(3, 2, 4, 2, 64, 9, 600, "f16", 21)
+    n = torch.tensor([100, 0, 101], dtype=torch.int32, device=DEV)
+    a = sv.attention(q, k, v, n, prefix_k=pk, prefix_v=pv, max_ctx=100, return_lse=True)
+    torch.cuda.synchronize()
+    check(sv.AttentionResult(a.out[:2], a.lse[:2]), q[:2], k[:2], v[:2], [100, 0], pk=pk, pv=pv)
+    assert torch.isnan(a.out[2]).all() and torch.isnan(a.lse[2]).all()
+
+
+def test_many_sequences_and_ranges():
+    """Enough sequences for ranges of 1024 keys, all rows of some of them
+    checked; and a long prefix split into many ranges for few rows."""
+    B, cap = 128, 2300
+    q, k, v, pk, pv = make(B, 1, 16, 8, 64, 3000, cap, "bf16", 31)
+    lens = [(37 * b) % 2290 for b in range(B)]
+    res = sv.attention(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV), prefix_k=pk, prefix_v=pv, return_lse=True)
+    torch.cuda.synchronize()
+    for b in (0, 1, 61, 62, 127):
+        one = sv.AttentionResult(res.out[b:b + 1], res.lse[b:b + 1])
+        check(one, q[b:b + 1], k[b:b + 1], v[b:b + 1], lens[b:b + 1], pk=pk, pv=pv)
+    q, k, v, pk, pv = make(1, 2, 4, 1, 128, 20000, 40, "f16", 32)
+    res = sv.attention(q, k, v, torch.tensor([31], dtype=torch.int32, device=DEV), prefix_k=pk, prefix_v=pv, return_lse=True)
+    torch.cuda.synchronize()
+    check(res, q, k, v, [31], pk=pk, pv=pv)
+
+
 def test_infinities_and_nan_in_masked_nodes():
     """A node's infinite or NaN key and value reach only the rows that see it."""
     parent = [-1, 0, 0, 1, 2, 2]

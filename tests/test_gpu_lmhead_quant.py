@@ -120,6 +120,20 @@ def test_large_means_and_infinite_scales():
     assert torch.equal(again[:, keep], got[:, keep]) and not torch.isfinite(again[:, 5]).any()
 
 
+def test_given_workspace():
+    """A workspace kept between calls, its contents from another call, changes
+    nothing; one too small is refused."""
+    h, w, s, z = make(90, 1024, 3000, 64, "bf16", True, 6)
+    want = sv.lmhead_quant(h, w, s, z)
+    ws = sv.lmhead_quant_workspace(90, 1024, 3000, 64, DEV)
+    ws.fill_(255)
+    for _ in range(2):
+        assert torch.equal(sv.lmhead_quant(h, w, s, z, ws=ws), want)
+    assert sv.lmhead_quant_workspace(32, 1024, 3000, 64, DEV) is None
+    with pytest.raises(sv.SvError):
+        sv.lmhead_quant(h, w, s, z, ws=ws[:1024])
+
+
 def test_window_from_quantised_hidden_states():
     """The logits feed sv_verify_window: (B, gamma + 1, V) in one call."""
     B, g, V = 3, 4, 5000
