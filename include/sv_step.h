@@ -29,7 +29,8 @@ extern "C" {
  * is drawn from them).
  *   logits, out [B][R][V], `dtype`; rows of one sequence contiguous, sequences
  *               seq_stride / out_seq_stride ELEMENTS apart (0 = dense).  out is
- *               logits itself (same stride: in place) or does not overlap it.
+ *               logits itself (same stride: in place), or the two lie apart
+ *               (from first row to last, also where only their gaps overlap).
  *   tokens      [B] rows of tokens_stride (0 = dense) int32, the drafts.
  *   parent_host NULL: a window; row i follows tokens[b][0 .. i-1] (R - 1 are
  *               read), so target rows (R = gamma + 1) and draft rows
