@@ -53,10 +53,15 @@ constexpr int kAtThreads = kAttendThreads;
 template <int DT> struct AtElt;
 template <> struct AtElt<DT_BF16> {
   static constexpr uint32_t kExp = 0x7F80u;  // exponent of infinities and NaN
+  static constexpr float kLift = 0.0f;
   __device__ static __forceinline__ at_f32x16_t mma(uint4 a, uint4 b, at_f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8_t, a), __builtin_bit_cast(at_bf16x8_t, b), c, 0, 0, 0);
   }
-  // Two exponentials in [0, 1] to the storage type, rounded to nearest.
+  // Two exponentials to the storage type, rounded to nearest: the matrix units
+  // take two operands of one type, and the values come in that type.  It costs
+  // half a step of each weight (2^-8 in bfloat16), as much as rounding the
+  // output does; a second product for what the rounding leaves would double
+  // the matrix work of the values.
   __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, v2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
@@ -65,6 +70,10 @@ template <> struct AtElt<DT_BF16> {
 };
 template <> struct AtElt<DT_F16> {
   static constexpr uint32_t kExp = 0x7C00u;
+  // Exponentials of rows in float16 are held 2^15 times larger, sums and
+  // outputs with them: weights down to 2^-29 of the largest stay normal
+  // numbers (down to 2^-14 otherwise, and thousands of smaller ones add up).
+  static constexpr float kLift = 15.0f;
   __device__ static __forceinline__ at_f32x16_t mma(uint4 a, uint4 b, at_f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(at_f16x8_t, a), __builtin_bit_cast(at_f16x8_t, b), c, 0, 0, 0);
   }
@@ -263,13 +272,17 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
         for (int e = 0; e < 16; ++e) o[t][e] *= alpha;
       m = mn;
     }
-    const float mu = m == kNegInf ? 0.0f : m * A.scale_log2;
+    // The lifted exponent is taken from the difference to the maximum, so that
+    // the largest is 2^15 exactly however far the scores are (65504 ends the
+    // type); unlifted, one multiply-add does.
+    const float top_s = m == kNegInf ? 0.0f : m, mu = top_s * A.scale_log2;
     float sum = 0.0f;
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[sb][e] = exp2_fast(__builtin_fmaf(s[sb][e], A.scale_log2, -mu));
+        s[sb][e] = exp2_fast(T::kLift > 0 ? __builtin_fmaf(s[sb][e] - top_s, A.scale_log2, T::kLift)
+                                          : __builtin_fmaf(s[sb][e], A.scale_log2, -mu));
         sum += s[sb][e];
       }
     l += sum;
@@ -490,7 +503,7 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
   uint16_t *out = A.out + row * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = AtElt<DT>::bits(acc[e] / L);
-  if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L)) * 0.6931471805599453f;
+  if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L * (AtElt<DT>::kLift > 0 ? 0x1p-15f : 1.0f))) * 0.6931471805599453f;
 }
 
 namespace {

@@ -275,3 +275,51 @@ def test_binding_refuses_on_device():
             sv.attention(q, k, v, n, **kw)
     with pytest.raises(ValueError):
         sv.attention(q[..., :32].contiguous(), k[..., :32].contiguous(), v[..., :32].contiguous(), n)  # no workspace for D = 32
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [1, 4, 40])
+def test_small_weights_keep_their_share(rows, dtype):
+    """One key far above a thousand others (their weights lie below float16's
+    normal numbers, their sum does not vanish).  One product per score, so
+    scores are exact up to their scaling: an exponent's argument is off by at
+    most (2 + 2 A) 2^-24, the sums over N weights by N 2^-24 each, the weights
+    and the output by half a step each, a float16 output by 2^-25 at least."""
+    D, N = 64, 1000
+    B, R = (1, 1) if rows == 1 else (rows // 4 if rows > 4 else 1, 4)
+    h = HALF_STEP[DT[dtype]]
+    for strong in (3, 777):
+        for A in (8.0, 15.0, 15.5, 16.0):
+            q = torch.zeros(B, R, 4, D, device=DEV, dtype=DT[dtype])
+            q[..., 0] = 8
+            k = torch.zeros(N, 1, D, device=DEV, dtype=DT[dtype])
+            v = torch.ones_like(k)
+            k[strong, 0, 0], v[strong] = A, 0
+            cache = torch.zeros(B, 2 * R, 1, D, device=DEV, dtype=DT[dtype])
+            n = torch.zeros(B, dtype=torch.int32, device=DEV)
+            res = sv.attention(q, cache, torch.ones_like(cache), n, prefix_k=k, prefix_v=v, scale=0.125, return_lse=True)
+            torch.cuda.synchronize()
+            for r in range(R):
+                w = (N + r) * math.exp(-A)
+                want = w / (1 + w)
+                tol = (2 * h + 2 * (N + R + 2 + 2 * A) * 2.0 ** -24) * want * (1 + 2.0 ** -6) + 2.0 ** -25
+                got = host(res.out[:, r])
+                assert np.abs(got - want).max() <= tol, (strong, A, r, float(np.abs(got - want).max() / tol))
+                lse = A + math.log1p(w)
+                assert np.abs(host(res.lse[:, r]) - lse).max() <= 2 * (N + R + 8 + 4 * A) * 2.0 ** -24 + 2.0 ** -23 * lse
+
+
+def test_far_scores_stay_finite():
+    """Scores of 2^26 and more (float16 inputs in the hundreds): the largest
+    key takes all the weight, in a tile of its own or beside others."""
+    D = 128
+    for dtype in ("f16", "bf16"):
+        q = torch.full((1, 4, 4, D), 1024.0, device=DEV, dtype=DT[dtype])
+        k = torch.full((1, 300, 1, D), 512.0, device=DEV, dtype=DT[dtype])
+        v = torch.zeros(1, 300, 1, D, device=DEV, dtype=DT[dtype])
+        k[0, 7], v[0, 7] = 1024.0, 3.0
+        for scale in (0.5, 1.0, 3.0):
+            res = sv.attention(q, k, v, torch.tensor([290], dtype=torch.int32, device=DEV), scale=scale, return_lse=True)
+            torch.cuda.synchronize()
+            assert (res.out == 3).all(), (dtype, scale)
+            assert (res.lse / (scale * D * 1024.0 * 1024.0) - 1).abs().max() <= 2.0 ** -20
