@@ -212,3 +212,31 @@ def test_binding_refuses_on_device():
     flat = torch.zeros(2 * 3 * 40 + 1, device=DEV)
     with pytest.raises(sv.SvError):
         sv.adjust_logits(flat[:-1].view(2, 3, 40), out=flat[1:].view(2, 3, 40))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_neighbours_keep_their_bits(dtype, inplace):
+    """Beside a biased token, a penalised one, one of the path and a masked one
+    every other element keeps its bits, signalling NaN (which float32
+    arithmetic would quieten), subnormals and signed zeros among them."""
+    V, R = 96, 3
+    bits_of = {"f32": (torch.int32, [0x7F800001, -0x007FFFFE, 1, -0x7FFFFFFF, -0x80000000]),
+               "bf16": (torch.int16, [0x7F81, -0x7E, 1, -0x7FFF, -0x8000]), "f16": (torch.int16, [0x7C01, -0x3FE, 1, -0x7FFF, -0x8000])}
+    int_t, odd = bits_of[dtype]
+    for extra in range(len(odd)):
+        raw = torch.full((1, R, V), odd[extra], dtype=int_t, device=DEV)
+        touched = torch.zeros(R, V, dtype=torch.bool, device=DEV)
+        for t in (1, 8, 21, 38):  # bias, history, the draft (rows 1, 2), the mask
+            raw.view(DT[dtype])[0, :, t] = 1.5
+        touched[:, 1] = touched[:, 8] = touched[1:, 21] = touched[:, 38] = True
+        ok = np.ones((1, 1, V), dtype=bool)
+        ok[..., 38] = False
+        words = torch.from_numpy(np.packbits(ok, axis=-1, bitorder="little").view(np.int32).copy()).to(DEV).expand(1, R, 3)
+        x = raw.clone().view(DT[dtype])
+        y = sv.adjust_logits(x, tokens=_i32([[21, 50 * V]]), history=_i32([[8, 8]]), repetition=_f32([2.0]), frequency=_f32([0.25]),
+                             bias_tokens=_i32([[1]]), bias_values=_f32([[1.0]]), allowed=words, out=x if inplace else None)
+        torch.cuda.synchronize()
+        got = y.view(int_t)[0]
+        assert (got[~touched] == raw[0][~touched]).all(), extra
+        assert (y[0, :, 1] == 2.5).all() and (y[0, :, 8] == 0.25).all() and (y[0, 1:, 21] == 0.5).all() and torch.isinf(y[0, :, 38]).all()
