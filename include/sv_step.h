@@ -60,8 +60,10 @@ extern "C" {
  * in float32, rounded once to dtype.  Tokens outside [0, V) anywhere are
  * skipped.  A disallowed logit is -inf whatever it was (NaN included); a row
  * that allows nothing becomes all -inf (a greedy argmax of 0).  Logits that
- * nothing applies to keep their bits; in place they are neither read nor
- * written.  tokens may be NULL when R = 1 or no penalty is given. */
+ * nothing applies to keep their bits.  In place, rows are read and written back
+ * in groups of 8 tokens (4 in float32, counted from token 0), and only the
+ * groups that something applies to: nothing else may write to those while the
+ * call runs.  tokens may be NULL when R = 1 or no penalty is given. */
 int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t out_seq_stride, int dtype,
                      const int32_t *tokens, int64_t tokens_stride, const int32_t *parent_host,
                      const int32_t *row_count, int32_t B, int32_t R, int32_t V,
