@@ -561,9 +561,11 @@ int sv_verify_window_lmhead(const void *hidden_target, const void *unembed_targe
 
 namespace {
 
-bool quant_sizes_ok(int32_t K, int32_t group) {
+bool quant_sizes_ok(int32_t M, int32_t K, int32_t V, int32_t group) {
+  if (M < 1 || M > kMaxGridY || V < 1 || V > kMaxVocab) return false;
   if (group != 32 && group != 64 && group != 128) return false;
-  return K >= SV_LMHEAD_K_STEP && K <= SV_LMHEAD_MAX_HIDDEN && K % SV_LMHEAD_K_STEP == 0 && K % group == 0;
+  if (K < SV_LMHEAD_K_STEP || K > SV_LMHEAD_MAX_HIDDEN || K % SV_LMHEAD_K_STEP != 0 || K % group != 0) return false;
+  return grid_fits(lm_quant_blocks(M, V), kLmQuantThreads);
 }
 
 }  // namespace
@@ -642,7 +644,7 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
 }
 
 size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t V, int32_t group) {
-  if (M < 1 || M > kMaxGridY || V < 1 || V > kMaxVocab || !quant_sizes_ok(K, group)) return 0;
+  if (!quant_sizes_ok(M, K, V, group)) return 0;
   return lm_quant_layout(M, K, V, group).total;
 }
 
@@ -653,17 +655,12 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                     void *workspace, size_t workspace_bytes, hipStream_t stream) {
   if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
   if (out_dtype != SV_DT_F32 && out_dtype != dtype) return SV_EDTYPE;
-  if (M < 1 || M > kMaxGridY || V < 1 || V > kMaxVocab || !quant_sizes_ok(K, group)) return SV_EINVAL;
+  if (!quant_sizes_ok(M, K, V, group)) return SV_EINVAL;
   if (!hidden || !weights || !scales || !out) return SV_EINVAL;
   if (hidden_row_stride == 0) hidden_row_stride = K;
   if (out_row_stride == 0) out_row_stride = V;
   if (M > 1 && (hidden_row_stride < K || hidden_row_stride % 8 != 0 || out_row_stride < V)) return SV_EINVAL;
   if (!aligned(hidden, 16) || !aligned(weights, 16) || !aligned(scales, 2) || !aligned(out, elem_bytes(out_dtype)))
-    return SV_EINVAL;
-  // one workgroup per column and row tile (column tiles in eights), counted with the smallest tile
-  if (!grid_fits(((static_cast<int64_t>(V) + kLmQuantMinCols - 1) / kLmQuantMinCols + 7) / 8 * 8 *
-                     ((static_cast<int64_t>(M) + kLmQuantMinRows - 1) / kLmQuantMinRows),
-                 kLmQuantThreads))
     return SV_EINVAL;
   const LmQuantLayout L = lm_quant_layout(M, K, V, group);
   if (L.total > 0) {

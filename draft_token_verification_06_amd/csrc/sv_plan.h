@@ -161,14 +161,21 @@ inline LmLayout make_lm_layout(int64_t B, int32_t gamma, int32_t V) {
   return L;
 }
 
-// 4-bit LM head: the smallest tile of a workgroup, and the workspace of a call
+// 4-bit LM head: the narrowest tile of a workgroup, and the workspace of a call
 // with more rows than its workgroups lay out themselves (K padded to a chunk).
-constexpr int kLmQuantMinRows = 16, kLmQuantMinCols = 16;
+constexpr int kLmQuantMinCols = 16;
 constexpr int kLmQuantDirectRows = 32;
 constexpr int kLmQuantCols = 128;       // columns of a workgroup with more rows than that
 constexpr int64_t kLmQuantSlots = 512;  // of those run at once: 2 on each of 256 CUs
 // Rows of a workgroup: blocks of 64 or 80, whichever pads less.
 inline int lm_quant_rows(int64_t M) { return (M + 63) / 64 * 64 <= (M + 79) / 80 * 80 ? 64 : 80; }
+// Workgroups of a launch along its first dimension, at most: all rows in one
+// row block up to kLmQuantDirectRows, and column tiles in eights.
+inline int64_t lm_quant_blocks(int64_t M, int64_t V) {
+  const int64_t cols = M <= kLmQuantDirectRows ? kLmQuantMinCols : kLmQuantCols;
+  const int64_t rows = M <= kLmQuantDirectRows ? kLmQuantDirectRows : lm_quant_rows(M);
+  return ((V + cols - 1) / cols + 7) / 8 * 8 * ((M + rows - 1) / rows);
+}
 struct LmQuantLayout {
   int32_t padded, splits, split_chunks;
   size_t sums_off, partial_off, total;

@@ -90,10 +90,11 @@ int sv_adjust_logits(const void *logits, int64_t seq_stride, void *out, int64_t 
  *           type, not overlapping the inputs.  Dense rows of M = B * (gamma + 1)
  *           are the target_logits of sv_verify_window.
  *   workspace of sv_lmhead_quant_workspace bytes; that is 0 (and NULL will do)
- *           for up to 32 rows.
+ *           for up to 32 rows (and for sizes outside the rules).
  * Weights enter the products exactly; sums are held in float32 and rounded
  * once.  Hidden values must be finite (an infinite one makes its row NaN).
- * M <= 65535. */
+ * M <= 65535; what a dispatch cannot hold (ceil(V / 128) * ceil(M / 64) >=
+ * 2^24, only the largest M and V together) is SV_EINVAL. */
 size_t sv_lmhead_quant_workspace(int32_t M, int32_t K, int32_t V, int32_t group);
 int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
                     const uint8_t *weights, const void *scales, const uint8_t *zeros,

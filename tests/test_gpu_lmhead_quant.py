@@ -159,3 +159,14 @@ def test_binding_refuses_on_device():
         sv.lmhead_quant(h, w, s, z, out=torch.empty(4, 41, device=DEV))
     with pytest.raises(sv.SvError):
         sv.lmhead_quant(h, w, s[:, :1].contiguous(), None)   # group 256
+
+
+def test_many_rows_past_32_bit_offsets():
+    """40000 rows of 128256 logits: more than 2^32 elements; rows at both ends
+    and on both sides of that offset."""
+    M, K, V, G = 40000, 64, 128256, 64
+    h, w, s, z = make(M, K, V, G, "bf16", True, 8)
+    got = sv.lmhead_quant(h, w, s, z, out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    rows = [0, 63, 64, 2 ** 32 // V - 1, 2 ** 32 // V, 2 ** 32 // V + 1, M - 65, M - 1]
+    check(got[rows], h[rows], w, s, z, G)

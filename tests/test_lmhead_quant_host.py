@@ -67,3 +67,13 @@ def test_binding_refuses():
         sv.lmhead_quant(h, w, s)             # host memory
     with pytest.raises(ValueError):
         sv.lmhead_quant(h.float(), w, s)
+
+
+def test_every_size_of_the_rules_is_accepted():
+    """Calls of many rows go by the tiles they launch (64 or 80 rows, 128
+    columns), and the workspace is sized for what a call accepts."""
+    size = _lib.lib().sv_lmhead_quant_workspace
+    for M, V in ((40000, 128256), (65535, 128256), (65535, 1 << 20), (9000, 1 << 21), (32, 1 << 21)):
+        assert M <= 32 or _call(M=M, V=V) == -3              # only the workspace is missing
+        assert (size(M, 256, V, 64) > 0) == (M > 32)
+    assert _call(M=65535, V=1 << 21) == -1 and size(65535, 256, 1 << 21, 64) == 0   # 2^24 workgroups of 256 work-items
