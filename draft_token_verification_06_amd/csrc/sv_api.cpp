@@ -694,13 +694,14 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
 
 namespace {
 
-bool attention_sizes_ok(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
+// False for sizes outside the rules; else their plan.
+bool attention_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, AttendPlan *L) {
   if (B < 1 || R < 1 || R > SV_TREE_MAX_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > SV_ATTENTION_MAX_HEADS) return false;
   if (D != 64 && D != 128) return false;
   if (P < 0 || P > SV_ATTENTION_MAX_KEYS || max_ctx < 0 || max_ctx > SV_ATTENTION_MAX_KEYS) return false;
   if (static_cast<int64_t>(B) * R > (int64_t{1} << 30) / Hq) return false;
-  const AttendPlan L = plan_attention(B, R, Hq, Hkv, D, P, max_ctx);
-  return grid_fits(L.prefix_items + L.own_blocks, kAttendThreads) &&
+  *L = plan_attention(B, R, Hq, Hkv, D, P, max_ctx);
+  return grid_fits(L->prefix_items + L->own_blocks, kAttendThreads) &&
          grid_fits((static_cast<int64_t>(B) * R * Hq + 3) / 4, 256);
 }
 
@@ -709,8 +710,8 @@ bool attention_sizes_ok(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D
 extern "C" {
 
 size_t sv_attention_workspace(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
-  if (!attention_sizes_ok(B, R, Hq, Hkv, D, P, max_ctx)) return 0;
-  return plan_attention(B, R, Hq, Hkv, D, P, max_ctx).total;
+  AttendPlan L;
+  return attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &L) ? L.total : 0;
 }
 
 int sv_attention(const void *q, int64_t q_row_stride, int dtype,
@@ -720,7 +721,8 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
                  int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_ctx, float scale,
                  void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
   if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
-  if (!attention_sizes_ok(B, R, Hq, Hkv, D, P, max_ctx)) return SV_EINVAL;
+  AttendPlan L;
+  if (!attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &L)) return SV_EINVAL;
   AttendArgs A{};
   TreeParents parents;
   if (parent_host) {
@@ -742,7 +744,6 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
     return SV_EINVAL;
   if (P > 0 && (!aligned(prefix_k, 16) || !aligned(prefix_v, 16))) return SV_EINVAL;
-  const AttendPlan L = plan_attention(B, R, Hq, Hkv, D, P, max_ctx);
   const int ws = check_workspace(workspace, workspace_bytes, L.total);
   if (ws != SV_OK) return ws;
   A.q = static_cast<const uint16_t *>(q);
@@ -767,7 +768,7 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
   A.prefix_chunk = L.prefix_chunk;
   A.prefix_items = static_cast<int32_t>(L.prefix_items);
   A.own_parts = L.own_parts;
-  A.own_chunk = L.own_chunk;
+  A.split = L.split;
   A.own_tiles = L.own_tiles;
   // never zero: masked products are -inf, and 0 * -inf is no number
   A.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);

@@ -5,7 +5,7 @@
 // The keys of a row are split among work items: the prefix into ranges that
 // all rows of a kv head share (so its keys and values are read once per tile
 // of rows of the whole batch, not once per sequence), and each sequence's
-// cache, the step's own keys at its end, into ranges of chunk_own keys.  An
+// cache, the step's own keys at its end, into ranges by its length.  An
 // item runs one pass over its range with a running maximum and sum and leaves
 // an unnormalised float32 output with (maximum, sum); k_attend_combine joins
 // the items of a row in a fixed order.
@@ -422,16 +422,25 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A, Tree... 
   const int tile = j % per % A.own_tiles;
   it.kvh = j % per / A.own_tiles;
   const int split = range / A.B;  // every sequence's first range, then the second ..: full ones go first
-  const int b = range % A.B;
+  // moved on from split to split: where B is a multiple of 8, all ranges of a
+  // long sequence would lie on one XCD (one of 60000 keys among 31 of 500: 243
+  // us, 121 spread out)
+  int b = range - split * A.B;
+  if (A.B >= 8) {
+    b += split & 7;
+    if (b >= A.B) b -= A.B;
+  }
   const int len = A.ctx_len[b];
   const int live = live_rows(A, b);
   if (bad_len(A, len) || live == 0) return;
-  it.k0 = split * A.own_chunk;
-  it.k1 = min(it.k0 + A.own_chunk, len + live);
-  it.draft = len;
+  const int keys = __builtin_amdgcn_readfirstlane(len + live);  // (the same for the workgroup: scalar from here)
+  const int own = attend_own_range(A.split, keys);
   it.row0 = tile * (32 * WQO);
   it.rows = live * A.n;
-  if (it.k0 >= it.k1 || it.row0 >= it.rows) return;
+  if (static_cast<int64_t>(split) * own >= keys || it.row0 >= it.rows) return;
+  it.k0 = split * own;
+  it.k1 = min(it.k0 + own, keys);
+  it.draft = len;
   it.part = A.prefix_parts + split;
   it.base_row = static_cast<int64_t>(b) * A.R;
   it.k = A.k + b * A.seq_stride + it.kvh * D;
@@ -489,7 +498,10 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = L;
   } else {
-    const int parts = A.prefix_parts + (len + live + A.own_chunk - 1) / A.own_chunk;
+    // the same for the wave: counted in scalar registers
+    const int keys = __builtin_amdgcn_readfirstlane(len + live), own = attend_own_range(A.split, keys);
+    int parts = A.prefix_parts;
+    for (int k0 = 0; k0 < keys; k0 += own) ++parts;
     for (int p = 0; p < parts; ++p) M = fmaxf(M, A.part_ml[p * rows + row].x);
     for (int p = 0; p < parts; ++p) {
       const float2 ml = A.part_ml[p * rows + row];

@@ -160,7 +160,8 @@ struct AttendJoin {
   const int32_t *ctx_len, *row_count;
   int32_t B, R, Hq;
   int32_t max_ctx;
-  int32_t prefix_parts, own_chunk;
+  int32_t prefix_parts;
+  AttendSplit split;
   float scale_log2;  // magnitude of the score scale, times log2(e)
   float *part_o;     // [parts][B R Hq][D] unnormalised outputs
   float2 *part_ml;   // [parts][B R Hq] (largest product, sum)

@@ -210,36 +210,63 @@ constexpr int kAttendThreads = 256;
 constexpr int kAttendWideRows = 64;        // more stacked rows than this: tiles of 128
 constexpr int64_t kAttendSlots = 512;      // workgroups that run at once: 2 on each of 256 CUs
 constexpr int kAttendMinKeys = 128;        // keys per range at least (a tile)
+// A sequence's own keys (context and live rows) are split by their number
+// alone, so that neither the ranges nor the results follow the capacity of the
+// cache: lengths up to 128, 256, 512 .. each have their range, in tiles of 128
+// keys (16 bits: no division in the kernel).
+constexpr int kAttendBuckets = 19;  // 128 << 18 holds the longest
+struct AttendSplit {
+  uint64_t tiles[5];
+};
+constexpr int attend_bucket(int keys) { return keys <= 128 ? 0 : 32 - __builtin_clz(static_cast<unsigned>(keys - 1) >> 7); }
+// Keys per range of a sequence with `keys` of its own.
+constexpr int attend_own_range(const AttendSplit &S, int keys) {
+  const int j = attend_bucket(keys);
+  const uint64_t word = j < 8 ? (j < 4 ? S.tiles[0] : S.tiles[1]) : j < 12 ? S.tiles[2] : j < 16 ? S.tiles[3] : S.tiles[4];
+  return static_cast<int>(word >> (16 * (j & 3)) & 0xFFFF) * 128;
+}
 struct AttendPlan {
   int prefix_waves, own_waves;  // waves along the rows
-  int prefix_parts, prefix_chunk, own_parts, own_chunk, own_tiles;
+  int prefix_parts, prefix_chunk, own_parts, own_tiles;  // own_parts: most ranges of a sequence
+  AttendSplit split;
   int64_t prefix_items, own_blocks;
   size_t ml_off, total;
 };
 
+// Keys of a range when `keys` are split into `parts`: whole tiles.
+inline int64_t attend_range(int64_t keys, int64_t parts) { return ((keys + parts - 1) / parts + 127) / 128 * 128; }
+
 // Ranges of `keys` keys for `items` items of `rows` rows each: the number that
 // ends first when rounds of kAttendSlots items take turns.  An item costs its
 // keys, a tile's start and end, and its partial output, written and read
-// again: two keys' bytes per row.  Where the launch has work for many rounds
-// already (many), ranges of about `most_keys` keep the items few and even.
-inline void split_keys(int64_t keys, int64_t items, int64_t rows, bool many, int64_t most_keys, int *parts, int *chunk) {
-  auto chunk_of = [&](int64_t p) { return ((keys + p - 1) / p + 127) / 128 * 128; };
-  int64_t c = chunk_of((keys + most_keys - 1) / most_keys);
-  if (!many) {
-    int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys;
-    if (most > 256) most = 256;
-    int64_t best = -1;
-    for (int64_t p = 1; p <= most; ++p) {
-      const int64_t rounds = (items * p + kAttendSlots - 1) / kAttendSlots;
-      const int64_t cost = rounds * (chunk_of(p) + kAttendMinKeys + 2 * rows);
-      if (best < 0 || cost < best) {
-        best = cost;
-        c = chunk_of(p);
-      }
+// again: two keys' bytes per row; a round that fills half of the slots at most,
+// one item per CU, takes 13 twentieths of a full one (8 windows of 9 rows over
+// 4000 keys: 4 ranges 32 us, 8 ranges 35).  Every range costs the join of a row two
+// trips to memory after each other, as long as 64 keys take (one token of 32
+// heads over 4000 keys: 32 ranges 27 us, 7 ranges 19, 2 ranges 32).  Where
+// there is work for many rounds already (crowded), ranges of about 1024 keys
+// keep the items even; longer sequences then have longer ranges, 16 of them or
+// what fills the chip once, so that partial outputs do not follow the length.
+inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded) {
+  if (crowded) {
+    const int64_t fill = (kAttendSlots + items - 1) / items, cap = fill > 16 ? fill : 16;
+    const int64_t p = (keys + 1023) / 1024;
+    return static_cast<int>(p < cap ? p : cap);
+  }
+  int64_t most = (keys + kAttendMinKeys - 1) / kAttendMinKeys, best = -1;
+  if (most > 256) most = 256;
+  int parts = 1;
+  for (int64_t p = 1, step = 1; p <= most; p += step) {
+    if (p == 8 * step) step *= 2;  // eight candidates, then four per doubling
+    const int64_t last = items * p % kAttendSlots;
+    const int64_t rounds = items * p / kAttendSlots * 20 + (last == 0 ? 0 : last <= kAttendSlots / 2 ? 13 : 20);
+    const int64_t cost = rounds * (attend_range(keys, p) + kAttendMinKeys + 2 * rows) + 20 * 64 * p;
+    if (best < 0 || cost < best) {
+      best = cost;
+      parts = static_cast<int>(p);
     }
   }
-  *chunk = static_cast<int>(c);
-  *parts = static_cast<int>((keys + c - 1) / c);
+  return parts;
 }
 
 inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx) {
@@ -251,13 +278,23 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
   const int64_t prefix_rows = 32 * L.prefix_waves, own_rows = 32 * L.own_waves;
   const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
   L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
-  const int64_t own_keys = max_ctx + R, own_items = B * Hkv * L.own_tiles;
-  const bool own_many = own_items * ((own_keys + 1023) / 1024) >= 4 * kAttendSlots;
-  split_keys(own_keys, own_items, own < own_rows ? own : own_rows, own_many, 1024, &L.own_parts, &L.own_chunk);
+  const int64_t own_items = B * Hkv * L.own_tiles;
+  const int longest = attend_bucket(static_cast<int>(max_ctx + R));
+  for (int j = 0; j <= longest; ++j) {
+    const int64_t keys = int64_t{128} << j;
+    const bool crowded = own_items * ((keys + 1023) / 1024) >= 4 * kAttendSlots;
+    const int64_t range = attend_range(keys, attend_parts(keys, own_items, own < own_rows ? own : own_rows, crowded));
+    L.split.tiles[j / 4] |= static_cast<uint64_t>(range / 128) << (16 * (j % 4));  // (crowded: 16 parts at least; else under 2^21 keys)
+    const int parts = static_cast<int>((keys + range - 1) / range);
+    if (parts > L.own_parts) L.own_parts = parts;
+  }
   L.prefix_chunk = 1;
   if (P > 0) {
-    const bool many = own_many || tiles * Hkv * ((P + 1023) / 1024) >= 4 * kAttendSlots;
-    split_keys(P, tiles * Hkv, all < prefix_rows ? all : prefix_rows, many, 1024, &L.prefix_parts, &L.prefix_chunk);
+    // The prefix's items run beside the sequences' own; whatever their lengths,
+    // those alone are two rounds where there are as many.
+    const bool crowded = own_items >= 2 * kAttendSlots;
+    L.prefix_chunk = static_cast<int>(attend_range(P, attend_parts(P, tiles * Hkv, all < prefix_rows ? all : prefix_rows, crowded)));
+    L.prefix_parts = static_cast<int>((P + L.prefix_chunk - 1) / L.prefix_chunk);
     L.prefix_items = tiles * Hkv * L.prefix_parts;
   }
   L.own_blocks = (B * L.own_parts + 7) / 8 * 8 * Hkv * L.own_tiles;

@@ -115,9 +115,10 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
  *   prefix_k, prefix_v  P tokens prefix_tok_stride elements apart (0 = Hkv *
  *            D), seen by every row of every sequence; P = 0: none.
  *   ctx_len  [B] int32 in [0, max_ctx]; max_ctx + R <= cap.  max_ctx only
- *            bounds the lengths (the work follows the lengths themselves).  A
- *            sequence whose length is outside gets rows of NaN, and nothing of
- *            its cache is read.
+ *            bounds the lengths: work and results follow the lengths
+ *            themselves, and the workspace stops growing with it after some
+ *            tens of thousands.  A sequence whose length is outside gets rows
+ *            of NaN, and nothing of its cache is read.
  *   row_count  [B] or NULL (= R): rows of each sequence to compute (clamped
  *            to [0, R]); the others of out and lse are left as they were, and
  *            their keys and values are not used.

@@ -323,3 +323,34 @@ def test_far_scores_stay_finite():
             torch.cuda.synchronize()
             assert (res.out == 3).all(), (dtype, scale)
             assert (res.lse / (scale * D * 1024.0 * 1024.0) - 1).abs().max() <= 2.0 ** -20
+
+
+def test_results_do_not_depend_on_the_capacity():
+    """The same lengths under capacities from just enough to millions of
+    tokens: the same bits, for lengths of every number of ranges, window and
+    tree, few sequences and many."""
+    g = torch.Generator(device=DEV).manual_seed(77)
+    for B, R, parent, lens in ((1, 1, None, [4000]), (5, 3, None, [0, 100, 1021, 2500, 5000]), (2, 9, [-1, 0, 0, 1, 1, 2, 2, 3, 3], [128, 900]),
+                               (70, 1, None, [(977 * b) % 3000 for b in range(70)])):
+        Hq, Hkv, D, P, cap = 16, 8, 64, 700, max(lens) + R
+        rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+        q, k, v, pk, pv = rnd(B, R, Hq, D), rnd(B, cap, Hkv, D), rnd(B, cap, Hkv, D), rnd(P, Hkv, D), rnd(P, Hkv, D)
+        n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        tight = sv.attention(q, k, v, n, prefix_k=pk, prefix_v=pv, parent=parent, return_lse=True)
+        torch.cuda.synchronize()
+        check(sv.AttentionResult(tight.out[-1:], tight.lse[-1:]), q[-1:], k[-1:], v[-1:], lens[-1:], pk=pk, pv=pv, parent=parent)
+        for big in (9000, 40000):
+            kk, vv = (torch.full((B, big, Hkv, D), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+            kk[:, :cap], vv[:, :cap] = k, v
+            res = sv.attention(q, kk, vv, n, prefix_k=pk, prefix_v=pv, parent=parent, return_lse=True)
+            torch.cuda.synchronize()
+            assert torch.equal(res.out, tight.out) and torch.equal(res.lse, tight.lse), (B, big)
+    # one sequence in a cache of millions of tokens (2^31 bytes of keys and more)
+    q, n = torch.randn(1, 1, 4, 64, generator=g, device=DEV).to(torch.bfloat16), torch.tensor([3000], dtype=torch.int32, device=DEV)
+    k, v = (torch.empty(1, 9 << 20, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for t in (k, v):
+        t[:, :3001] = torch.randn(1, 3001, 2, 64, generator=g, device=DEV)
+    big, tight = sv.attention(q, k, v, n), sv.attention(q, k[:, :3001], v[:, :3001], n)
+    torch.cuda.synchronize()
+    assert torch.equal(big.out, tight.out)
+    check(big, q, k, v, [3000])
