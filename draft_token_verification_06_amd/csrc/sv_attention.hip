@@ -530,8 +530,9 @@ void launch_shape(const AttendArgs &A, const TreeParents *parents, dim3 grid, hi
 
 template <int DT, int D, int WQP>
 void launch_own(const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, dim3 grid, hipStream_t st) {
-  if (P.own_waves == 4)
-    launch_shape<DT, D, WQP, 4>(A, parents, grid, st);
+  // (a sequence's rows are no more than the batch's: 4 waves on them mean 4 on the prefix)
+  if (WQP == 4 && P.own_waves == 4)
+    launch_shape<DT, D, 4, 4>(A, parents, grid, st);
   else if (P.own_waves == 2)
     launch_shape<DT, D, WQP, 2>(A, parents, grid, st);
   else
