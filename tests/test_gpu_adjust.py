@@ -240,3 +240,43 @@ def test_neighbours_keep_their_bits(dtype, inplace):
         got = y.view(int_t)[0]
         assert (got[~touched] == raw[0][~touched]).all(), extra
         assert (y[0, :, 1] == 2.5).all() and (y[0, :, 8] == 0.25).all() and (y[0, 1:, 21] == 0.5).all() and torch.isinf(y[0, :, 38]).all()
+
+
+LARGE = [
+    # more than 256 MiB read and written, rows off the 16-byte grid: B, R, parent, V, dtype, history, bias, mask
+    (60, 9, None, 128257, "bf16", 500, 20, None),
+    (33, 41, "432", 50257, "f16", 200, 8, 0.5),
+    (30, 9, None, 128257, "f32", 300, 0, 0.9),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "-".join(map(str, c)))
+def test_large_copies(case):
+    """Copies that stream past the caches; the first sequences, one in the
+    middle and the last against the definition, rows past row_count left."""
+    print("adjust", case, flush=True)
+    B, R, kind, V, dtype, hist, n_bias, mask = case
+    parent = _parent(kind, R)
+    rng = np.random.default_rng(B)
+    g = torch.Generator(device=DEV).manual_seed(B)
+    x = torch.empty(B, R, V, dtype=DT[dtype], device=DEV)
+    for b in range(B):
+        x[b] = torch.randn(R, V, generator=g, device=DEV) * 3
+    _, kw, _ = _inputs(B, 2, None, V, "f32", hist, n_bias, None, False, 5)
+    kw["tokens"], kw["parent"] = _i32((rng.random((B, R)) ** 3 * V).astype(np.int64)), parent
+    ok = None
+    if mask is not None:
+        one, words = _bits(rng, 1, 1, V, mask)  # one mask for all rows
+        ok, kw["allowed"] = np.broadcast_to(one, (B, R, V)), words.expand(B, R, -1)
+    rc = np.full(B, R)
+    rc[1], rc[B // 2] = R - 2, 0
+    before = torch.full((1, R, V), 5.0, dtype=DT[dtype], device=DEV)
+    out = before.expand(B, R, V).clone()
+    got = sv.adjust_logits(x, **kw, row_count=_i32(rc), out=out)
+    torch.cuda.synchronize()
+    kw.pop("allowed", None)
+    kw.pop("parent")
+    for b in (0, 1, B // 2, B - 1):
+        part = {k: v[b:b + 1] for k, v in kw.items()}
+        check(got[b:b + 1], x[b:b + 1], dtype, parent=parent, ok=None if ok is None else ok[b:b + 1], row_count=rc[b:b + 1],
+              before=before, **part)

@@ -354,3 +354,40 @@ def test_results_do_not_depend_on_the_capacity():
     torch.cuda.synchronize()
     assert torch.equal(big.out, tight.out)
     check(big, q, k, v, [3000])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scales_of_both_signs(dtype):
+    """Outputs and lse against the definition for scales of both signs, windows
+    and trees, tiles of 32, 64 and 128 rows."""
+    for R, parent, Hq, Hkv in ((3, None, 4, 2), (12, None, 8, 2), (20, [-1] + [v // 2 for v in range(19)], 16, 4)):
+        q, k, v, pk, pv = make(2, R, Hq, Hkv, 64, 150, 260, dtype, 40 + R)
+        lens = [230, 77]
+        n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        for scale in (-0.125, 0.125, -0.6, 0.6):
+            res = sv.attention(q, k, v, n, prefix_k=pk, prefix_v=pv, parent=parent, scale=scale, return_lse=True)
+            torch.cuda.synchronize()
+            check(res, q, k, v, lens, pk=pk, pv=pv, parent=parent, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_one_key_takes_all(dtype):
+    """Whole numbers as queries and keys, so that scores are exact products, 40
+    apart at least: the row is the mean of the values of its largest keys
+    (others weigh at most 493 e^-40), for scales of both signs."""
+    g = torch.Generator(device=DEV).manual_seed(50)
+    whole = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, generator=g, device=DEV).to(DT[dtype])  # noqa: E731
+    q, k, pk = whole(-2, 2, 1, 3, 4, 64), whole(-1, 1, 1, 300, 2, 64), whole(-1, 1, 200, 2, 64)
+    q[0, 1, 2], q[0, 0, 1] = 0, -q[0, 0, 0]     # a row of equal scores, a pair of opposite rows
+    v, pv = (torch.randn(*s, generator=g, device=DEV).to(DT[dtype]) for s in ((1, 300, 2, 64), (200, 2, 64)))
+    n = torch.tensor([290], dtype=torch.int32, device=DEV)
+    h = HALF_STEP[DT[dtype]]
+    for scale in (50.0, -50.0, 40.0):
+        res = sv.attention(q, k, v, n, prefix_k=pk, prefix_v=pv, scale=scale, return_lse=True)
+        torch.cuda.synchronize()
+        want, lse = oracle.attention(host(q[0]), host(k[0]), host(v[0]), 290, prefix_k=host(pk), prefix_v=host(pv), scale=scale)
+        # the exponent's scaling and shift: off by 2^-24 of scores up to 128 |scale|, twice; then weights and output by half a step
+        arg = 4 * 128 * abs(scale) * 2.0 ** -24
+        tol = (h + arg + 2 * 500 * 2.0 ** -24) * np.abs(host(v)).max() * (1 + 2.0 ** -6) + h * np.abs(want)
+        assert (np.abs(host(res.out[0]) - want) <= tol).all(), scale
+        assert (np.abs(host(res.lse[0]) - lse) <= arg + 500 * 2.0 ** -24 + 2.0 ** -23 * np.abs(lse)).all()

@@ -170,3 +170,55 @@ def test_many_rows_past_32_bit_offsets():
     torch.cuda.synchronize()
     rows = [0, 63, 64, 2 ** 32 // V - 1, 2 ** 32 // V, 2 ** 32 // V + 1, M - 65, M - 1]
     check(got[rows], h[rows], w, s, z, G)
+
+
+TILES = [
+    # every tile of the launcher with every group, K and V off its sizes: M, K, V, G, dtype, zeros, out
+    (4, 448, 4099, 64, "bf16", True, "f32"),        # 16 rows, K shared out among waves
+    (16, 1088, 10003, 32, "f16", True, "f32"),
+    (11, 640, 9001, 128, "f16", False, "same"),
+    (7, 1088, 12001, 32, "f16", True, "f32"),       # 16 rows, 64 columns
+    (16, 704, 20011, 64, "bf16", False, "f32"),
+    (9, 896, 30001, 128, "bf16", True, "same"),
+    (8, 256, 65553, 128, "bf16", True, "f32"),      # 16 rows, 128 columns
+    (13, 320, 65601, 64, "f16", True, "same"),
+    (16, 288 + 32, 70001, 32, "bf16", False, "f32"),
+    (24, 320, 16377, 32, "f16", True, "f32"),       # 32 rows, K shared out among waves
+    (32, 384, 9999, 128, "bf16", True, "same"),
+    (20, 576, 5003, 64, "bf16", False, "f32"),
+    (24, 320, 16401, 32, "f16", True, "f32"),       # 32 rows, 128 columns
+    (17, 384, 17001, 128, "bf16", True, "f32"),
+    (31, 192, 20003, 64, "f16", False, "same"),
+    (64, 320, 70003, 32, "bf16", True, "f32"),      # 64 rows
+    (120, 576, 40009, 64, "f16", True, "f32"),
+    (250, 384, 20001, 128, "bf16", False, "same"),
+    (72, 576, 60001, 64, "bf16", True, "f32"),      # 80 rows
+    (79, 320, 66001, 32, "f16", False, "f32"),
+    (155, 384, 30001, 128, "bf16", True, "same"),
+]
+
+
+@pytest.mark.parametrize("case", TILES, ids=lambda c: "-".join(map(str, c)))
+def test_every_tile(case):
+    print("lmhead_quant", case, flush=True)
+    M, K, V, G, dtype, zeros, out = case
+    h, w, s, z = make(M, K, V, G, dtype, zeros, M + 7 * K)
+    got = sv.lmhead_quant(h, w, s, z, out_dtype=torch.float32 if out == "f32" else DT[dtype])
+    torch.cuda.synchronize()
+    check(got, h, w, s, z, G)
+
+
+@pytest.mark.parametrize("M", [3, 20, 40])
+def test_subnormal_hidden_values(M):
+    """float16 rows of subnormal values (but for the few of the channel that
+    stands out): the sums of the groups keep them as the products do (the
+    correction for 16 + q would not cancel otherwise)."""
+    h, w, s, z = make(M, 256, 90, 64, "f16", True, 31)
+    h = (h.float() * 2.0 ** -18).to(torch.float16)
+    assert (h.abs() < 2.0 ** -14).float().mean() > 0.99 and (h != 0).any()
+    s = torch.ones_like(s)
+    got = sv.lmhead_quant(h, w, s, z)
+    torch.cuda.synchronize()
+    want, size = oracle.lmhead_quant(h.double().cpu().numpy(), w.cpu().numpy(), s.double().cpu().numpy(), z.cpu().numpy())
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= (2 * 64 + 256 // 64 + 4) * 2.0 ** -24 * (62 / 24) * size).all()
