@@ -19,9 +19,9 @@
 // restricted to the chunk, nearly always empty, so a row costs its load, its
 // mask byte and its store.
 //
-// Measured: B = 256, 9 rows of 128256 bf16, histories of 2048, biases: 221 us,
-// 5.3 TB/s (a plain copy of 2 GiB: 4.9); 267 us while the first rows waited for
-// the counting.  Workgroups of 512 threads, 333 us: fewer of them cover the
+// Measured: B = 256, 9 rows of 128256 bf16, histories of 2048, biases: 226 us,
+// 5.2 TB/s (a plain copy of 2 GiB: 4.9); 45 us more while the first rows waited
+// for the counting.  Workgroups of 512 threads, 333 us: fewer of them cover the
 // counting's barriers.  Grammar masks alone, in place on 32 windows: 24 us for
 // 79 MB of mask and -inf.  Tree of 41 rows of 50257 fp16, 4 sequences: 17 us.
 #include <hip/hip_runtime.h>

@@ -26,13 +26,13 @@
 //
 // Measured (bf16, 32 query heads on 8 kv heads of 128):
 // - 128 single tokens over own caches of 1000 to 4000 tokens and a prefix of
-//   2048 (1.34 GB): 230 us + 6 us for the join, 5.6 TB/s.  Bound: memory and the
+//   2048 (1.34 GB): 229 us + 7 us for the join, 5.7 TB/s.  Bound: memory and the
 //   start and end of each range; ranges of 512 to 2048 keys differ by 5%.
 // - 64 windows of 9 rows, prefix 8192, own caches of 256 to 1024 (84 GFLOP):
-//   127 + 15 us, 590 TFLOP/s.  Bound: the loads and their way through LDS, which
-//   alone take 108 us, then the vector work of the exponentials.
-// - one token over 333 + 700 keys: 7.5 + 5 us; bound: two launches and the trips
-//   to memory of one range.
+//   122 + 15 us, 610 TFLOP/s.  Bound: the loads and their way through LDS (108 us
+//   alone when the whole took 150), then the vector work of the exponentials.
+// - one token over 333 + 700 keys: 9 + 5 us; bound: two launches, the trips to
+//   memory of one range, and those of the join, two for each range in turn.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
