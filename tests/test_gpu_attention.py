@@ -391,3 +391,21 @@ def test_one_key_takes_all(dtype):
         tol = (h + arg + 2 * 500 * 2.0 ** -24) * np.abs(host(v)).max() * (1 + 2.0 ** -6) + h * np.abs(want)
         assert (np.abs(host(res.out[0]) - want) <= tol).all(), scale
         assert (np.abs(host(res.lse[0]) - lse) <= arg + 500 * 2.0 ** -24 + 2.0 ** -23 * np.abs(lse)).all()
+
+
+def test_row_count_of_trees():
+    """Trees cut off after a sequence's first nodes: the others' rows stay as
+    they were, and their queries, keys and values do not matter."""
+    parent = [-1, 0, 0, 1, 1, 2, 3, 3, 5, 6, 0]
+    B, R = 5, len(parent)
+    q, k, v, pk, pv = make(B, R, 6, 2, 64, 45, 400, "f16", 61)
+    lens, rc = [0, 127, 120, 389, 300], [1, 4, 9, 11, 0]
+    for b in range(B):
+        q[b, rc[b]:], k[b, lens[b] + rc[b]:], v[b, lens[b] + rc[b]:] = (float("nan"),) * 3
+    res = sv.AttentionResult(torch.full((B, R, 6, 64), 3.0, dtype=torch.float16, device=DEV), torch.full((B, R, 6), 3.0, device=DEV))
+    sv.attention(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV), prefix_k=pk, prefix_v=pv, parent=parent,
+                 row_count=torch.tensor(rc, dtype=torch.int32, device=DEV), out=res)
+    torch.cuda.synchronize()
+    for b in range(B):
+        assert (res.out[b, rc[b]:] == 3).all() and (res.lse[b, rc[b]:] == 3).all()
+    check(res, q, k, v, lens, pk=pk, pv=pv, parent=parent, row_count=rc)
