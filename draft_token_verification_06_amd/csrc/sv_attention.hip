@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A, Tree... 
   it.kvh = j % per / A.own_tiles;
   const int split = range / A.B;  // every sequence's first range, then the second ..: full ones go first
   // moved on from split to split: where B is a multiple of 8, all ranges of a
-  // long sequence would lie on one XCD (one of 60000 keys among 31 of 500: 243
-  // us, 121 spread out)
+  // long sequence would lie on one XCD (one of 60000 keys among 31 of 500 took
+  // 235 us, 122 spread out)
   int b = range - split * A.B;
   if (A.B >= 8) {
     b += split & 7;
@@ -482,12 +482,11 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A, Tree... 
 template <int DT, int D>
 __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
   constexpr int E = D / 64;
-  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int rows = A.B * A.R * A.Hq;  // at most 2^30
+  const int row = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // scalar: the same for the wave
   const int lane = threadIdx.x & 63;
   if (row >= rows) return;  // (bound: the partial outputs, 4 D bytes a row and range, written and read once)
-  const int64_t br = row / A.Hq;
-  const int b = static_cast<int>(br / A.R), r = static_cast<int>(br % A.R);
+  const int br = row / A.Hq, b = br / A.R, r = br % A.R;
   const int live = live_rows(A, b);
   if (r >= live) return;
   const int len = A.ctx_len[b];
@@ -498,21 +497,21 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = L;
   } else {
-    // the same for the wave: counted in scalar registers
-    const int keys = __builtin_amdgcn_readfirstlane(len + live), own = attend_own_range(A.split, keys);
+    const int keys = len + live, own = attend_own_range(A.split, keys);
     int parts = A.prefix_parts;
     for (int k0 = 0; k0 < keys; k0 += own) ++parts;
-    for (int p = 0; p < parts; ++p) M = fmaxf(M, A.part_ml[p * rows + row].x);
+    for (int p = 0; p < parts; ++p) M = fmaxf(M, A.part_ml[static_cast<int64_t>(p) * rows + row].x);
     for (int p = 0; p < parts; ++p) {
-      const float2 ml = A.part_ml[p * rows + row];
+      const int64_t at = static_cast<int64_t>(p) * rows + row;
+      const float2 ml = A.part_ml[at];
       const float f = ml.x == kNegInf ? 0.0f : exp2_fast((ml.x - M) * A.scale_log2);
       L += f * ml.y;
-      const float *po = A.part_o + (p * rows + row) * D + lane * E;
+      const float *po = A.part_o + at * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] += f * po[e];
     }
   }
-  uint16_t *out = A.out + row * D + lane * E;
+  uint16_t *out = A.out + static_cast<int64_t>(row) * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = AtElt<DT>::bits(acc[e] / L);
   if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L * (AtElt<DT>::kLift > 0 ? 0x1p-15f : 1.0f))) * 0.6931471805599453f;

@@ -22,9 +22,9 @@
 // Measured at K = 4096, groups of 128: V = 128256 (263 MB of weights), M = 8: 54
 // us, 5.1 TB/s; M = 72: 121 us, where vector work (39%), matrix work (29%) and
 // LDS (32%) take turns, as registers leave room for two waves per SIMD; M =
-// 576: 823 to 850 us, 710 TFLOP/s and more, as every 64 rows unpack the weights again; V =
-// 50257, M = 256: 160 us, 650 TFLOP/s, and 235 us with groups of 32, whose
-// scaling is four times the vector work.
+// 576: 823 to 850 us, 710 to 736 TFLOP/s, as every 64 rows unpack the weights
+// again; V = 50257, M = 256: 160 us, 650 TFLOP/s, and 235 us with groups of
+// 32, whose scaling is four times the vector work.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

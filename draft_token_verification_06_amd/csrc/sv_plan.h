@@ -241,9 +241,10 @@ inline int64_t attend_range(int64_t keys, int64_t parts) { return ((keys + parts
 // keys, a tile's start and end, and its partial output, written and read
 // again: two keys' bytes per row; a round that fills half of the slots at most,
 // one item per CU, takes 13 twentieths of a full one (8 windows of 9 rows over
-// 4000 keys: 4 ranges 32 us, 8 ranges 35).  Every range costs the join of a row two
-// trips to memory after each other, as long as 64 keys take (one token of 32
-// heads over 4000 keys: 32 ranges 27 us, 7 ranges 19, 2 ranges 32).  Where
+// 4000 keys: 4 ranges 32 us, 8 ranges 35).  Every range costs the join of a row
+// two trips to memory after each other, 0.75 us or some 64 keys (one token of 32
+// heads over 4000 keys: 32 ranges 27 us, 7 ranges 19, 2 ranges 32; with 42 keys 64
+// windows behind 16384 tokens get 7 ranges for 3, 239 us for 223).  Where
 // there is work for many rounds already (crowded), ranges of about 1024 keys
 // keep the items even; longer sequences then have longer ranges, 16 of them or
 // what fills the chip once, so that partial outputs do not follow the length.
@@ -284,7 +285,7 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
     const int64_t keys = int64_t{128} << j;
     const bool crowded = own_items * ((keys + 1023) / 1024) >= 4 * kAttendSlots;
     const int64_t range = attend_range(keys, attend_parts(keys, own_items, own < own_rows ? own : own_rows, crowded));
-    L.split.tiles[j / 4] |= static_cast<uint64_t>(range / 128) << (16 * (j % 4));  // (crowded: 16 parts at least; else under 2^21 keys)
+    L.split.tiles[j / 4] |= static_cast<uint64_t>(range / 128) << (16 * (j % 4));  // (crowded: 1024 keys or a 16th at most; else below 2^21 keys)
     const int parts = static_cast<int>((keys + range - 1) / range);
     if (parts > L.own_parts) L.own_parts = parts;
   }
