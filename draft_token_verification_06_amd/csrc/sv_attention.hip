@@ -29,9 +29,9 @@
 //   2048 (1.34 GB): 229 us + 7 us for the join, 5.7 TB/s.  Bound: memory and the
 //   start and end of each range; ranges of 512 to 2048 keys differ by 5%.
 // - 64 windows of 9 rows, prefix 8192, own caches of 256 to 1024 (84 GFLOP):
-//   122 + 15 us, 610 TFLOP/s.  Bound: the loads and their way through LDS (108 us
+//   122 + 13 us, 620 TFLOP/s.  Bound: the loads and their way through LDS (108 us
 //   alone when the whole took 150), then the vector work of the exponentials.
-// - one token over 333 + 700 keys: 9 + 5 us; bound: two launches, the trips to
+// - one token over 333 + 700 keys: 9 + 4 us; bound: two launches, the trips to
 //   memory of one range, and those of the join, two for each range in turn.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
