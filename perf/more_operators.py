@@ -1,0 +1,593 @@
+"""Workloads of the paged cache of a verification step: rotary positions,
+appending a step's keys and values, attention over the pages (held in 16 bits
+or in 8 with a scale for each block of tokens and head), and moving a tree's
+accepted path behind the context.
+
+Each case is a dict of plain values.  ``prepare`` makes a case's inputs from a
+seed, ``run`` takes one pass through the operator: in its plain form (torch
+operations in float32) or, with ``own`` set, through this package's call.
+``exact`` gives the same outputs in float64 from the definitions.
+"""
+import math
+
+import torch
+
+own = False
+DEV = "cuda"
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+BYTES = {"f32": 4, "bf16": 2, "f16": 2}
+F8 = torch.float8_e4m3fn
+F8_MAX = 448.0
+NEG_INF = float("-inf")
+
+
+def listed():
+    return [
+        # -- rotary positions -------------------------------------------------
+        # the queries of a step of 8 windows: latency
+        {"name": "rotary_step_b8", "op": "rotary", "B": 8, "R": 9, "tree": "", "H": 32, "D": 128, "rot": 128, "layout": "half",
+         "scaling": "none", "dtype": "bf16", "pos": 4000},
+        # four long prompts far behind the trained length, half of each head rotated, interleaved pairs
+        {"name": "rotary_prompt_b4", "op": "rotary", "B": 4, "R": 8191, "tree": "", "H": 32, "D": 128, "rot": 64,
+         "layout": "interleaved", "scaling": "ramp", "dtype": "f16", "pos": 1000000},
+        # -- appending to the pages -------------------------------------------
+        # one token of one sequence: the draft model's own step, latency only
+        {"name": "append_single_b1", "op": "append", "B": 1, "R": 1, "tree": "", "ragged": False, "Hq": 32, "Hkv": 8, "D": 128, "rot": 128,
+         "layout": "half", "scaling": "none", "dtype": "bf16", "cache": "f8", "page": 16, "block": 16, "ctx": 1033, "shared": 512},
+        # windows of 64 sequences behind one system prompt, 8-bit pages
+        {"name": "append_window_b64", "op": "append", "B": 64, "R": 9, "tree": "", "ragged": False, "Hq": 32, "Hkv": 8, "D": 128, "rot": 128,
+         "layout": "half", "scaling": "linear", "dtype": "bf16", "cache": "f8", "page": 64, "block": 64, "ctx": 1024, "shared": 896},
+        # prompts of four sequences, of different lengths, half of the head rotated
+        {"name": "append_prompt_b4", "op": "append", "B": 4, "R": 4096, "tree": "", "ragged": True, "Hq": 32, "Hkv": 8, "D": 128, "rot": 64,
+         "layout": "interleaved", "scaling": "none", "dtype": "bf16", "cache": "f8", "page": 64, "block": 32, "ctx": 100, "shared": 0},
+        # tree (4, 3, 2) of four sequences, 20 heads of 64 without grouping, 16-bit pages
+        {"name": "append_tree_b4", "op": "append", "B": 4, "R": 41, "tree": "4,3,2", "ragged": False, "Hq": 20, "Hkv": 20, "D": 64, "rot": 32,
+         "layout": "half", "scaling": "none", "dtype": "f16", "cache": "16", "page": 32, "block": 32, "ctx": 983, "shared": 512},
+        # -- keeping the accepted path ----------------------------------------
+        # the same trees after their verification, one layer: latency
+        {"name": "commit_tree_b4", "op": "commit", "L": 1, "B": 4, "tree": "4,3,2", "Hkv": 20, "D": 64, "dtype": "f16", "cache": "16",
+         "page": 32, "block": 32, "ctx": 983, "shared": 512},
+        # 64 trees in the 8-bit pages of 32 layers at once
+        {"name": "commit_tree_b64_layers", "op": "commit", "L": 32, "B": 64, "tree": "4,3,2", "Hkv": 8, "D": 128, "dtype": "bf16",
+         "cache": "f8", "page": 64, "block": 64, "ctx": 1024, "shared": 896},
+        # -- attention over the pages -----------------------------------------
+        # one token of one sequence in small pages, latency only
+        {"name": "attend_paged_single", "op": "attend", "B": 1, "R": 1, "tree": "", "Hq": 32, "Hkv": 8, "D": 128, "P": 0, "ctx": 1033,
+         "dtype": "bf16", "cache": "f8", "page": 16, "block": 16},
+        # tree (4, 3, 2) of four sequences, 20 heads of 64 without grouping, 16-bit pages
+        {"name": "attend_paged_tree_b4", "op": "attend", "B": 4, "R": 41, "tree": "4,3,2", "Hq": 20, "Hkv": 20, "D": 64, "P": 0, "ctx": 983,
+         "dtype": "f16", "cache": "16", "page": 32, "block": 32},
+        # windows of 64 sequences behind one long prompt: the prefix is matrix work
+        {"name": "attend_paged_window_b64", "op": "attend", "B": 64, "R": 9, "tree": "", "Hq": 32, "Hkv": 8, "D": 128, "P": 8192, "ctx": 1024,
+         "dtype": "bf16", "cache": "f8", "page": 64, "block": 64},
+        # single tokens of 128 sequences with long caches of their own: the pages are the traffic
+        {"name": "attend_paged_decode_b128", "op": "attend", "B": 128, "R": 1, "tree": "", "Hq": 32, "Hkv": 8, "D": 128, "P": 2048, "ctx": 4000,
+         "dtype": "bf16", "cache": "f8", "page": 64, "block": 64},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _log_int0(rng, lo, hi):
+    """0 in one case out of four, else log-spread over [lo, hi]."""
+    return 0 if rng.random() < 0.25 else _log_int(rng, lo, hi)
+
+
+def _draw_rotation(rng, D):
+    return {"rot": rng.choice([D, D, D // 2, D // 4, 48 if D >= 64 else D]), "layout": rng.choice(["half", "interleaved"]),
+            "scaling": rng.choice(["none", "linear", "ramp"])}
+
+
+def _draw_pages(rng):
+    page = rng.choice([16, 32, 64, 128])
+    return {"cache": rng.choice(["f8", "f8", "16"]), "page": page, "block": rng.choice([b for b in (16, 32, 64) if b <= page])}
+
+
+def draw(rng):
+    op = rng.choice(["rotary", "append", "commit", "attend", "attend"])
+    tree = rng.choice(["", "", "4,3,2", "2,2,2", "3,1,1"])
+    if op == "rotary":
+        D = rng.choice([64, 80, 128, 256])
+        H = rng.choice([1, 5, 8, 20, 32])
+        R = len(_parents(tree)) if tree else _log_int(rng, 1, 8192)
+        B = max(1, min(_log_int(rng, 1, 256), 4 * 8191 * 32 * 128 // (R * H * D)))
+        dtype = rng.choice(["bf16", "f16", "f32"]) if B * R * H * D < 1 << 26 else "bf16"
+        return {"op": op, "B": B, "R": R, "tree": tree, "H": H, "D": D, **_draw_rotation(rng, D), "dtype": dtype, "pos": _log_int(rng, 10, 1 << 20)}
+    if op == "append":
+        Hkv, D = rng.choice([1, 2, 4, 8, 20]), rng.choice([64, 128])
+        Hq = Hkv * rng.choice([0, 1, 2, 4, 7])
+        R = len(_parents(tree)) if tree else _log_int(rng, 1, 4096)
+        B = max(1, min(_log_int(rng, 1, 256), 4 * 4096 * 48 * 128 // (R * (Hq + 2 * Hkv) * D)))
+        ctx = _log_int0(rng, 16, 4000)
+        return {"op": op, "B": B, "R": R, "tree": tree, "ragged": not tree and rng.random() < 0.5, "Hq": Hq, "Hkv": Hkv, "D": D,
+                **_draw_rotation(rng, D), "dtype": rng.choice(["bf16", "f16"]), **_draw_pages(rng), "ctx": ctx, "shared": ctx // 2}
+    if op == "commit":
+        tree = tree or "8,1,1,1,1,1"
+        Hkv, D, L = rng.choice([1, 2, 4, 8, 20]), rng.choice([64, 128]), _log_int(rng, 1, 32)
+        B = max(1, min(_log_int(rng, 1, 64), 32 * 64 * 8 * 128 // (L * Hkv * D)))
+        ctx = _log_int0(rng, 16, 4000)
+        return {"op": op, "L": L, "B": B, "tree": tree, "Hkv": Hkv, "D": D, "dtype": rng.choice(["bf16", "f16"]), **_draw_pages(rng), "ctx": ctx,
+                "shared": max(0, ctx - 128)}
+    R = len(_parents(tree)) if tree else rng.randint(1, 17)
+    Hkv, D = rng.choice([1, 2, 4, 8, 20]), rng.choice([64, 128])
+    Hq = Hkv * rng.choice([1, 2, 4, 7, 8])
+    P, ctx = _log_int0(rng, 16, 8192), _log_int0(rng, 16, 4000)
+    B = _log_int(rng, 1, 128)
+    B = max(1, min(B, 64 * 9 * 32 * 128 * 9000 // (R * Hq * D * (P + ctx + R)), 128 * 4000 * 8 * 128 // ((ctx + R) * Hkv * D)))
+    return {"op": op, "B": B, "R": R, "tree": tree, "Hq": Hq, "Hkv": Hkv, "D": D, "P": P, "ctx": ctx, "dtype": rng.choice(["bf16", "f16"]),
+            **_draw_pages(rng)}
+
+
+def _pow2(e):
+    """2^e for whole e, exactly (torch.ldexp goes through a rounded power)."""
+    return torch.exp2(e.double())
+
+
+# -- the rows of a step ----------------------------------------------------------
+def _parents(tree):
+    """Parent array of a tree given by its branching factors, breadth first."""
+    parent, level = [-1], [0]
+    for f in (int(x) for x in tree.split(",")):
+        level = [len(parent) + i for i in range(len(level) * f)]
+        parent += [p for p in range(level[0] - len(level) // f, level[0]) for _ in range(f)]
+    return parent
+
+
+def _row_parents(c):
+    return _parents(c["tree"]) if c["tree"] else list(range(-1, c["R"] - 1))
+
+
+def _depths(parent):
+    depth = []
+    for p in parent:
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    return depth
+
+
+def _ancestors(parent):
+    """anc[v][w]: w is v or an ancestor of v."""
+    R = len(parent)
+    anc = torch.zeros(R, R, dtype=torch.bool)
+    for v, p in enumerate(parent):
+        if p >= 0:
+            anc[v] = anc[p]
+        anc[v, v] = True
+    return anc
+
+
+def _lens(lo, hi, B, g):
+    """B lengths spread evenly over [lo, hi], in an order of the seed's."""
+    at = torch.randperm(B, generator=g, device=DEV)
+    return (lo + (hi - lo) * (at + 1) // B).to(torch.int32)
+
+
+# -- inputs ----------------------------------------------------------------------
+def _frequencies(c):
+    """Radians a position (float64, host) and the factor on the rotated values."""
+    n, base, factor = c["rot"], 10000.0, 8.0
+    f = base ** (-torch.arange(0, n, 2, dtype=torch.float64) / n)
+    if c["scaling"] == "linear":
+        return f / factor, 1.0
+    if c["scaling"] == "ramp":
+        # fast pairs stay, slow ones are divided, a ramp over the turns within 4096 positions between them
+        turns = 4096 * f / (2 * math.pi)
+        keep = ((turns - 1) / (32 - 1)).clamp(0, 1)
+        return f * keep + f / factor * (1 - keep), 0.1 * math.log(factor) + 1
+    return f, 1.0
+
+
+def _turns(f):
+    """Fractions of a turn a position, in units of 2^-64 (int64 bits of the unsigned numbers)."""
+    words = [int(math.ldexp(x / (2 * math.pi), 64)) % (1 << 64) for x in f.tolist()]
+    return torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64, device=DEV)
+
+
+def _rotation(c, s):
+    s["freq"], s["magnitude"] = _frequencies(c)
+    s["turns"] = _turns(s["freq"])
+    s["freq"] = s["freq"].to(DEV)
+    s["depth"] = torch.tensor(_depths(_row_parents(c)), device=DEV)
+
+
+def _pages(B, tokens, shared, page, g):
+    """A page table (B, pages) for `tokens` tokens, the first `shared` of which
+    lie in pages common to all, in an order of the seed's, and the number of
+    pages.  Page 0 belongs to nobody."""
+    n, common = (tokens + page - 1) // page, shared // page
+    total = 1 + common + B * (n - common)
+    ids = 1 + torch.randperm(total - 1, generator=g, device=DEV)
+    table = torch.empty(B, n, dtype=torch.int32, device=DEV)
+    table[:, :common] = ids[:common]
+    table[:, common:] = ids[common:].view(B, n - common)
+    return table, total
+
+
+def _cache(c, lead, total, g):
+    """Pages of keys and values (.., page, Hkv, D), the heads of a page apart,
+    with scales (.., page / block, Hkv) where they hold 8 bits."""
+    s = {}
+    for n in ("k", "v"):
+        shape = (*lead, total, c["Hkv"], c["page"], c["D"])
+        x = torch.empty(shape, dtype=F8 if c["cache"] == "f8" else DTYPES[c["dtype"]], device=DEV)
+        flat, step = x.view(-1, c["D"]), max(1, (1 << 25) // c["D"])
+        for i in range(0, flat.shape[0], step):
+            v = torch.randn(min(step, flat.shape[0] - i), c["D"], generator=g, device=DEV)
+            flat[i:i + step] = (v * 80 if c["cache"] == "f8" else v).to(x.dtype)
+        s[n] = x.transpose(-2, -3)
+        s[n + "_scale"] = None
+        if c["cache"] == "f8":
+            e = torch.randint(-8, -5, (*lead, total, c["page"] // c["block"], c["Hkv"]), generator=g, device=DEV)
+            s[n + "_scale"] = _pow2(e).float()
+    return s
+
+
+def prepare(c, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return {"rotary": _prepare_rotary, "append": _prepare_append, "commit": _prepare_commit, "attend": _prepare_attend}[c["op"]](c, g)
+
+
+def _prepare_rotary(c, g):
+    s = {"c": c, "parent": _row_parents(c) if c["tree"] else None}
+    _rotation(c, s)
+    s["x"] = torch.randn(c["B"], c["R"], c["H"], c["D"], generator=g, device=DEV).to(DTYPES[c["dtype"]])
+    s["pos"] = _lens(c["pos"] // 4, c["pos"], c["B"], g).long()
+    return s
+
+
+def _prepare_append(c, g):
+    B, R, Hq, Hkv, D = c["B"], c["R"], c["Hq"], c["Hkv"], c["D"]
+    s = {"c": c, "parent": _row_parents(c) if c["tree"] else None}
+    _rotation(c, s)
+    # one projection's output holds the heads of queries, keys and values of a row
+    x = torch.randn(B, R, Hq + 2 * Hkv, D, generator=g, device=DEV)
+    x[..., torch.randint(0, D, (2,), generator=g, device=DEV)] *= 6  # a few channels stand out
+    x = x.to(DTYPES[c["dtype"]])
+    s["q"], s["kn"], s["vn"] = x[:, :, :Hq] if Hq else None, x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+    s["q_out"] = torch.zeros(B, R, Hq, D, dtype=x.dtype, device=DEV) if Hq else None  # rows behind a sequence's last stay as they are
+    s["len"] = _lens(c["shared"], c["ctx"], B, g)
+    s["rows"] = _lens(R // 4, R, B, g) if c["ragged"] else None
+    s["table"], total = _pages(B, c["ctx"] + R, c["shared"], c["page"], g)
+    return {**s, **_cache(c, (), total, g)}
+
+
+def _prepare_commit(c, g):
+    B, parent = c["B"], _parents(c["tree"])
+    s = {"c": c, "R": len(parent)}
+    s["len"] = _lens(c["shared"], c["ctx"], B, g)
+    # Accepted paths of 0 .. depth nodes.  A node is where it goes already or
+    # behind all accepted ones, so that repeated passes move the same rows (a
+    # block that begins with a path may get a scale of its own each time).
+    depth, most = _depths(parent), max(_depths(parent))
+    paths = [p for v, d in enumerate(depth) if d == most for p in [_path(parent, v)] if all(w == i + 1 or w > most for i, w in enumerate(p))]
+    pick = torch.randint(0, len(paths), (B,), generator=g, device=DEV)
+    s["n"] = torch.randint(0, most + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    s["nodes"] = torch.tensor(paths, dtype=torch.int32, device=DEV)[pick]
+    s["nodes"] = torch.where(torch.arange(most, device=DEV) < s["n"][:, None], s["nodes"], -1).to(torch.int32)
+    s["table"], total = _pages(B, c["ctx"] + s["R"], c["shared"], c["page"], g)
+    return {**s, **_cache(c, (c["L"],), total, g)}
+
+
+def _path(parent, v):
+    return _path(parent, parent[v]) + [v] if v > 0 else []
+
+
+def _prepare_attend(c, g):
+    B, R, Hq, D, P = c["B"], c["R"], c["Hq"], c["D"], c["P"]
+    s = {"c": c, "parent": _row_parents(c) if c["tree"] else None, "anc": _ancestors(_row_parents(c)).to(DEV)}
+    s["q"] = (1.5 * torch.randn(B, R, Hq, D, generator=g, device=DEV)).to(DTYPES[c["dtype"]])
+    s["len"] = _lens(c["ctx"] // 4, c["ctx"], B, g)
+    s["table"], total = _pages(B, c["ctx"] + R, 0, c["page"], g)
+    n = (P + c["page"] - 1) // c["page"]
+    s["prefix"] = (total + torch.randperm(n, generator=g, device=DEV)).to(torch.int32) if P else None
+    return {**s, **_cache(c, (), total + n, g)}
+
+
+# -- one pass --------------------------------------------------------------------
+def run(s):
+    return {"rotary": _run_rotary, "append": _run_append, "commit": _run_commit, "attend": _run_attend}[s["c"]["op"]](s)
+
+
+def _own_cache(s):
+    import draft_token_verification_06_amd as sv
+    return sv, sv.PagedCache(s["k"], s["v"], s["k_scale"], s["v_scale"])
+
+
+def _rotated(s, x, base):
+    """x (B, R, H, D) turned by its rows' positions, in float32: angles in 64 bits."""
+    c, n = s["c"], s["c"]["rot"]
+    angle = ((base[:, None] + s["depth"])[..., None] * s["freq"])[:, :, None]
+    cos, sin = (angle.cos() * s["magnitude"]).float(), (angle.sin() * s["magnitude"]).float()
+    x = x.float()
+    if c["layout"] == "half":
+        a, b = x[..., :n // 2], x[..., n // 2:n]
+        return torch.cat([a * cos - b * sin, b * cos + a * sin, x[..., n:]], -1)
+    a, b = x[..., 0:n:2], x[..., 1:n:2]
+    return torch.cat([torch.stack([a * cos - b * sin, b * cos + a * sin], -1).flatten(-2), x[..., n:]], -1)
+
+
+def _run_rotary(s):
+    if own:
+        import draft_token_verification_06_amd as sv
+        return sv.rotary(s["x"], s["turns"], s["pos"], parent=s["parent"], interleaved=s["c"]["layout"] == "interleaved",
+                         magnitude=s["magnitude"])
+    return _rotated(s, s["x"], s["pos"]).to(s["x"].dtype)
+
+
+def _store(s, pages, scales, x, first, rows):
+    """Rows x (L, B, N, H, D), float32, to slots first[b] .. first[b] + rows[b] - 1 of pages (L, pages, page, H, D)."""
+    c, table, at = s["c"], s["table"].long(), torch.arange
+    L, B, N, H, D = x.shape
+    page, block = c["page"], c["block"]
+    # the blocks that the rows may touch, whole: slot, page and row of each of their tokens
+    n = (N + block - 2) // block + 1
+    slot = first[:, None].long() // block * block + at(n * block, device=DEV)
+    row = slot - first[:, None]
+    new = (row >= 0) & (row < rows[:, None])
+    row = row.clamp(0, N - 1)
+    which = at(B, device=DEV)[:, None].expand_as(row)
+    y = x[:, which, row]
+    touched = new.view(B, n, block).any(2)
+    # a block without a row of this call stands for the page that belongs to nobody
+    live = touched[..., None].expand(B, n, block).reshape(B, n * block)
+    home = torch.where(live, table.gather(1, (slot // page).clamp(max=table.shape[1] - 1)), 0)
+    if scales is None:
+        old = pages[:, home, slot % page]
+        pages[:, home, slot % page] = torch.where(new[..., None, None], y.to(pages.dtype), old)
+        return
+    old = pages.view(torch.uint8)[:, home, slot % page]
+    earlier = (slot < first[:, None]).view(B, n, block).any(2)[..., None]
+    top = torch.where(new[..., None, None], y.abs(), 0.0).view(L, B, n, block, H, D).amax((3, 5))
+    m, e = torch.frexp(top)  # top = m 2^e, m in [0.5, 1): 448 = 0.875 2^9
+    need = _pow2(torch.where(top > 0, (e - 9 + (m > 0.875).int()).clamp(min=-100), -100)).float()
+    spot, part = home[:, ::block], (slot % page // block)[:, ::block]
+    had = scales[:, spot, part]
+    m, e = torch.frexp(top / had)
+    grown = had * _pow2(torch.where(top > 0, (e - 9 + (m > 0.875).int()).clamp(min=0), 0)).float()
+    now = torch.where(earlier, grown, need)
+    scales[:, spot, part] = torch.where(touched[..., None], now, had)
+    wide = lambda t: t.repeat_interleave(block, 2)[..., None]  # noqa: E731
+    again = (old.view(F8).float() * wide(had / now)).to(F8).view(torch.uint8)
+    fresh = (y / wide(now)).to(F8).view(torch.uint8)
+    keep = (slot < first[:, None]) & live
+    pages.view(torch.uint8)[:, home, slot % page] = torch.where(new[..., None, None], fresh, torch.where(keep[..., None, None], again, old))
+
+
+def _run_append(s):
+    c = s["c"]
+    if own:
+        sv, cache = _own_cache(s)
+        q = sv.cache_append(cache, s["table"], s["len"], s["kn"], s["vn"], q=s["q"], turns=s["turns"], parent=s["parent"],
+                            interleaved=c["layout"] == "interleaved", magnitude=s["magnitude"], row_count=s["rows"], q_out=s["q_out"])
+    else:
+        rows = s["rows"] if s["rows"] is not None else torch.full_like(s["len"], c["R"])
+        for n, x in (("k", _rotated(s, s["kn"], s["len"])), ("v", s["vn"].float())):
+            _store(s, s[n][None], s[n + "_scale"][None] if c["cache"] == "f8" else None, x[None], s["len"], rows)
+        q = s["q_out"]
+        if q is not None:
+            live = torch.arange(c["R"], device=DEV) < rows[:, None]
+            q.copy_(torch.where(live[..., None, None], _rotated(s, s["q"], s["len"]), q.float()))
+    return {"q": q, "k": s["k"], "v": s["v"], "k_scale": s["k_scale"], "v_scale": s["v_scale"]}
+
+
+def _run_commit(s):
+    c = s["c"]
+    if own:
+        sv, cache = _own_cache(s)
+        length = sv.cache_commit(cache, s["table"], s["len"], s["nodes"], s["n"], rows=s["R"])
+    else:
+        slot = (s["len"][:, None] + s["nodes"].clamp(min=0)).long()
+        home, at = s["table"].long().gather(1, slot // c["page"]), slot % c["page"]
+        for n in ("k", "v"):
+            x = s[n].view(torch.uint8)[:, home, at].view(F8).float() if c["cache"] == "f8" else s[n][:, home, at].float()
+            if c["cache"] == "f8":
+                x = x * s[n + "_scale"][:, home, at // c["block"]][..., None]
+            _store(s, s[n], s[n + "_scale"], x, s["len"] + 1, s["n"])
+        length = s["len"] + s["n"] + 1
+    return {"len": length, "k": s["k"], "v": s["v"], "k_scale": s["k_scale"], "v_scale": s["v_scale"]}
+
+
+def _dense(s, n, table):
+    """Keys or values (.., tokens, H, D) of a page table, in float32."""
+    c, home = s["c"], table.long()
+    x = s[n].view(torch.uint8)[home].view(F8).float() if c["cache"] == "f8" else s[n][home].float()
+    if c["cache"] == "f8":
+        x = x * s[n + "_scale"][home].repeat_interleave(c["block"], -2)[..., None]
+    return x.flatten(-4, -3)
+
+
+def _run_attend(s):
+    c, q = s["c"], s["q"]
+    B, R, Hq, D = q.shape
+    Hkv, P, scale = c["Hkv"], c["P"], 1 / math.sqrt(D)
+    if own:
+        sv, cache = _own_cache(s)
+        r = sv.paged_attention(q, cache, s["table"], s["len"], prefix_table=s["prefix"], prefix_len=P, parent=s["parent"], scale=scale,
+                               return_lse=True)
+        return r.out, r.lse
+    n = Hq // Hkv
+    # rows (b, r, head of the group) of each kv head
+    x = q.float().view(B, R, Hkv, n, D).permute(0, 2, 1, 3, 4).reshape(B, Hkv, R * n, D)
+    k, v = (_dense(s, i, s["table"]).permute(0, 2, 1, 3).contiguous() for i in ("k", "v"))
+    L = k.shape[2]
+    score = torch.matmul(x, k.transpose(2, 3).contiguous()) * scale
+    rel = torch.arange(L, device=DEV) - s["len"][:, None]
+    seen = torch.zeros(B, R, L, dtype=torch.bool, device=DEV) | (rel < 0)[:, None]
+    draft = ((rel >= 0) & (rel < R))[:, None].expand(B, R, L)
+    seen |= draft & torch.gather(s["anc"].expand(B, R, R), 2, rel.clamp(0, R - 1)[:, None].expand(B, R, L))
+    score = score.masked_fill_(~seen.repeat_interleave(n, 1)[:, None], NEG_INF)
+    if P:
+        pk, pv = (_dense(s, i, s["prefix"])[:P].permute(1, 0, 2).contiguous() for i in ("k", "v"))
+        xp = x.permute(1, 0, 2, 3).reshape(Hkv, B * R * n, D)
+        before = torch.matmul(xp, pk.transpose(1, 2).contiguous()) * scale
+        score = torch.cat([before.view(Hkv, B, R * n, P).transpose(0, 1), score], 3)
+    top = score.amax(3, keepdim=True)
+    e = (score - top).exp_()
+    total = e.sum(3, keepdim=True)
+    o = torch.matmul(e[..., P:], v)
+    if P:
+        before = e[..., :P].transpose(0, 1).reshape(Hkv, B * R * n, P)
+        o += torch.matmul(before, pv).view(Hkv, B, R * n, D).transpose(0, 1)
+    o = (o / total).view(B, Hkv, R, n, D).permute(0, 2, 1, 3, 4).reshape(B, R, Hq, D).to(q.dtype)
+    lse = (top + total.log()).view(B, Hkv, R, n).permute(0, 2, 1, 3).reshape(B, R, Hq)
+    return o, lse
+
+
+def _lens_sum(lo, hi, B):
+    return sum(lo + (hi - lo) * (i + 1) // B for i in range(B))
+
+
+def work(c):
+    e = BYTES[c["dtype"]]
+    if c["op"] == "rotary":
+        values = c["B"] * c["R"] * c["H"] * c["D"]
+        return {"bytes": 2 * values * e, "flops": 3 * values * c["rot"] // c["D"]}
+    held = 1 if c["cache"] == "f8" else e
+    if c["op"] == "append":
+        rows = _lens_sum(c["R"] // 4, c["R"], c["B"]) if c["ragged"] else c["B"] * c["R"]
+        return {"bytes": rows * c["D"] * (2 * c["Hq"] * e + 2 * c["Hkv"] * (e + held)), "flops": 3 * rows * c["rot"] * (c["Hq"] + c["Hkv"])}
+    if c["op"] == "commit":
+        moved = c["L"] * c["B"] * len(c["tree"].split(",")) / 2
+        return {"bytes": moved * 2 * c["Hkv"] * c["D"] * 2 * held, "flops": 0}
+    B, R, Hq, Hkv, D, P = c["B"], c["R"], c["Hq"], c["Hkv"], c["D"], c["P"]
+    own_keys = _lens_sum(c["ctx"] // 4, c["ctx"], B)
+    pairs = B * R * P + R * own_keys + B * int(_ancestors(_row_parents(c)).sum())
+    scales = 4 / c["block"] if c["cache"] == "f8" else 0
+    return {"bytes": 2 * B * R * Hq * D * e + 4 * B * R * Hq + 2 * Hkv * (D * held + scales) * (P + own_keys + B * R), "flops": 4 * D * Hq * pairs}
+
+
+# -- the definitions in 64 bits --------------------------------------------------
+def exact(c, seed):
+    s = prepare(c, seed)
+    return {"rotary": _exact_rotary, "append": _exact_append, "commit": _exact_commit, "attend": _exact_attend}[c["op"]](c, s)
+
+
+def _exact_turn(c, s, x, pos):
+    """One sequence's rows x (R, H, D) as complex numbers times e^(i angle); pos (R,)."""
+    n = c["rot"]
+    z = torch.polar(torch.full((1,), s["magnitude"], dtype=torch.float64, device=DEV), pos.double()[:, None] * s["freq"])[:, None]
+    y = x.double().clone()
+    lo, hi = (slice(0, n // 2), slice(n // 2, n)) if c["layout"] == "half" else (slice(0, n, 2), slice(1, n, 2))
+    w = torch.complex(y[..., lo].clone(), y[..., hi].clone()) * z
+    y[..., lo], y[..., hi] = w.real, w.imag
+    return y
+
+
+def _exact_rotary(c, s):
+    return torch.stack([_exact_turn(c, s, s["x"][b], s["pos"][b] + s["depth"]) for b in range(c["B"])])
+
+
+def _round_f8(x):
+    """The nearest 8-bit values (4 exponent, 3 fraction bits, ties to even) of |x| <= 448."""
+    _, e = torch.frexp(x)
+    step = _pow2((e - 1).clamp(min=-6) - 3)
+    return torch.round(x / step) * step
+
+
+def _exact_store(c, pages, scales, table, x, first):
+    """One sequence's rows x (N, H, D) to slots first .. of float64 pages (pages, page, H, D), in place."""
+    page, block = c["page"], c["block"]
+    done = 0
+    while done < len(x):
+        slot = first + done
+        n = min(block - slot % block, len(x) - done)
+        at, home, y = slot % page, int(table[slot // page]), x[done:done + n]
+        done += n
+        if scales is None:
+            pages[home, at:at + n] = y
+            continue
+        top = y.abs().amax((0, 2))
+        s = scales[home, at // block]
+        earlier = at % block
+        ratio = top / F8_MAX if earlier == 0 else top / (F8_MAX * s)
+        up = torch.ceil(torch.log2(ratio))
+        up = up + (torch.exp2(up) < ratio).double() - (torch.exp2(up - 1) >= ratio).double()  # the logarithm's rounding
+        if earlier:
+            grow = torch.exp2(up.clamp(min=0))
+            pages[home, at - earlier:at] = _round_f8(pages[home, at - earlier:at] / grow[:, None])
+            now = s * grow
+        else:
+            now = torch.exp2(up.clamp(min=-100))
+        scales[home, at // block] = now
+        pages[home, at:at + n] = _round_f8(y / now[:, None])
+
+
+def _too_long(c, s):
+    """More blocks than twenty seconds hold, one after the other."""
+    rows = c["R"] if c["op"] == "append" else max(_depths(_parents(c["tree"])))
+    return c["B"] * (rows // c["block"] + 2) > 1024 * 2 or s["k"].numel() > 1 << 30
+
+
+def _exact_append(c, s):
+    if _too_long(c, s):
+        return None
+    k, v = s["k"].double(), s["v"].double()
+    ks, vs = (None, None) if c["cache"] != "f8" else (s["k_scale"].double(), s["v_scale"].double())
+    q = torch.zeros(c["B"], c["R"], c["Hq"], c["D"], dtype=torch.float64, device=DEV) if c["Hq"] else None
+    lens, rows = s["len"].tolist(), s["rows"].tolist() if s["rows"] is not None else [c["R"]] * c["B"]
+    for b, (n, r) in enumerate(zip(lens, rows)):
+        pos, table = n + s["depth"][:r], s["table"][b].tolist()
+        _exact_store(c, k, ks, table, _exact_turn(c, s, s["kn"][b, :r], pos), n)
+        _exact_store(c, v, vs, table, s["vn"][b, :r].double(), n)
+        if q is not None:
+            q[b, :r] = _exact_turn(c, s, s["q"][b, :r], pos)
+    return {"q": q, "k": k, "v": v, "k_scale": ks, "v_scale": vs}
+
+
+def _exact_commit(c, s):
+    if _too_long(c, s):
+        return None
+    out = {}
+    for n in ("k", "v"):
+        pages = s[n].double()
+        scales = s[n + "_scale"].double() if c["cache"] == "f8" else None
+        P, H, D = c["page"], c["Hkv"], c["D"]
+        # layers as more heads: (pages, page, L H, D)
+        flat = pages.permute(1, 2, 0, 3, 4).reshape(-1, P, c["L"] * H, D)
+        flat_scales = None if scales is None else scales.permute(1, 2, 0, 3).reshape(flat.shape[0], -1, c["L"] * H)
+        for b, (length, count) in enumerate(zip(s["len"].tolist(), s["n"].tolist())):
+            table, rows = s["table"][b].tolist(), []
+            for w in s["nodes"][b, :count].tolist():
+                home, at = table[(length + w) // P], (length + w) % P
+                rows.append(flat[home, at] * (1 if scales is None else flat_scales[home, at // c["block"]][:, None]))
+            if rows:
+                _exact_store(c, flat, flat_scales, table, torch.stack(rows), length + 1)
+        out[n] = flat.view(-1, P, c["L"], H, D).permute(2, 0, 1, 3, 4)
+        out[n + "_scale"] = None if scales is None else flat_scales.view(flat.shape[0], -1, c["L"], H).permute(2, 0, 1, 3)
+    return {"len": None, **out}
+
+
+def _exact_tokens(c, s, n, table, count):
+    """The first `count` keys or values of a page table, float64."""
+    found = []
+    for i, home in enumerate(table.tolist()[:(count + c["page"] - 1) // c["page"]]):
+        x = s[n][home].double()
+        if c["cache"] == "f8":
+            scale = s[n + "_scale"][home].double()
+            x = (x.view(-1, c["block"], *x.shape[1:]) * scale[:, None, :, None]).reshape(x.shape)
+        found.append(x)
+    return torch.cat(found)[:count]
+
+
+def _exact_attend(c, s):
+    B, R, Hq, Hkv, D, P = c["B"], c["R"], c["Hq"], c["Hkv"], c["D"], c["P"]
+    o = torch.empty(B, R, Hq, D, dtype=torch.float64, device=DEV)
+    lse = torch.empty(B, R, Hq, dtype=torch.float64, device=DEV)
+    n = Hq // Hkv
+    before = {i: _exact_tokens(c, s, i, s["prefix"], P) for i in ("k", "v")} if P else None
+    for b in range(B):
+        L = int(s["len"][b])
+        k, v = (_exact_tokens(c, s, i, s["table"][b], L + R) for i in ("k", "v"))
+        if P:
+            k, v = torch.cat([before["k"], k]), torch.cat([before["v"], v])
+        ok = torch.ones(R, P + L + R, dtype=torch.bool, device=DEV)
+        ok[:, P + L:] = s["anc"]
+        for h in range(Hkv):
+            q = s["q"][b, :, h * n:(h + 1) * n].double().reshape(R * n, D)
+            a = (q @ k[:, h].t().contiguous()) / math.sqrt(D)
+            a[~ok.repeat_interleave(n, 0)] = NEG_INF
+            z = torch.logsumexp(a, 1)
+            lse[b, :, h * n:(h + 1) * n] = z.view(R, n)
+            o[b, :, h * n:(h + 1) * n] = ((a - z[:, None]).exp() @ v[:, h]).view(R, n, D)
+    return o, lse
