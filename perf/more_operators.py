@@ -214,7 +214,7 @@ def _cache(c, lead, total, g):
         flat, step = x.view(-1, c["D"]), max(1, (1 << 25) // c["D"])
         for i in range(0, flat.shape[0], step):
             v = torch.randn(min(step, flat.shape[0] - i), c["D"], generator=g, device=DEV)
-            flat[i:i + step] = (v * 80 if c["cache"] == "f8" else v).to(x.dtype)
+            flat[i:i + step] = ((v * 80).clamp_(-F8_MAX, F8_MAX) if c["cache"] == "f8" else v).to(x.dtype)
         s[n] = x.transpose(-2, -3)
         s[n + "_scale"] = None
         if c["cache"] == "f8":
