@@ -24,6 +24,15 @@ from .api import (  # noqa: F401
     AttentionResult,
     lmhead_quant,
     lmhead_quant_workspace,
+    PagedCache,
+    paged_cache,
+    rotary,
+    rotary_frequencies,
+    rotary_turns,
+    cache_append,
+    cache_commit,
+    paged_attention,
+    paged_attention_workspace,
     probe_read,
     SV_OP_WINDOW,
     SV_OP_GREEDY,
@@ -34,5 +43,7 @@ from .api import (  # noqa: F401
 __all__ = [
     "SvError", "WindowResult", "TreeResult", "workspace_size", "workspace",
     "verify_window", "verify_window_noalloc", "verify_window_lmhead", "verify_greedy", "verify_tree", "tree_max_depth", "rollback",
-    "adjust_logits", "attention", "attention_workspace", "AttentionResult", "lmhead_quant", "lmhead_quant_workspace", "probe_read",
+    "adjust_logits", "attention", "attention_workspace", "AttentionResult", "lmhead_quant", "lmhead_quant_workspace",
+    "PagedCache", "paged_cache", "rotary", "rotary_frequencies", "rotary_turns", "cache_append", "cache_commit",
+    "paged_attention", "paged_attention_workspace", "probe_read",
 ]

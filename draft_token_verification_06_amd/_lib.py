@@ -48,8 +48,33 @@ _STEP_SIGNATURES = {
                                 _I32, _I32, _I32, _I32, _I32, _I32, _c.c_float, _P, _P, _P, _SZ, _P]),
 }
 
+
+
+class PagedCacheArgs(ctypes.Structure):
+    """sv_paged_cache of include/sv_cache.h."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P)] + \
+        [(n, _I32) for n in ("dtype", "num_pages", "page", "block", "Hkv", "D")] + \
+        [(n, _I64) for n in ("page_stride", "token_stride", "head_stride")]
+
+
+_PC = _c.POINTER(PagedCacheArgs)
+
+# include/sv_cache.h
+_CACHE_SIGNATURES = {
+    "sv_rotary_turns": (_c.c_int, [_c.POINTER(_c.c_double), _I32, _c.POINTER(_U64)]),
+    "sv_rotary": (_c.c_int, [_P, _I64, _P, _I64, _c.c_int, _P, _I32, _c.c_int, _c.c_int, _c.c_float, _P, _P, _P,
+                             _I32, _I32, _I32, _I32, _P]),
+    "sv_cache_append": (_c.c_int, [_PC, _P, _I64, _I32, _P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _c.c_int,
+                                   _P, _I32, _c.c_int, _c.c_float, _I32, _I32, _I32, _P]),
+    "sv_paged_attention_workspace": (_SZ, [_I32] * 7),
+    "sv_paged_attention": (_c.c_int, [_P, _I64, _c.c_int, _PC, _P, _I64, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
+                                      _c.c_float, _P, _P, _P, _SZ, _P]),
+    "sv_cache_commit": (_c.c_int, [_PC, _I32, _I64, _P, _I64, _I32, _P, _P, _I64, _I32, _P, _I32, _I32, _P, _P]),
+}
+
 EXPORTED = tuple(_SIGNATURES)
 STEP_EXPORTED = tuple(_STEP_SIGNATURES)
+CACHE_EXPORTED = tuple(_CACHE_SIGNATURES)
 
 _lib = None
 
@@ -76,7 +101,7 @@ def lib():
     import torch  # noqa: F401  -- torch's HIP runtime must be the one the library binds to
 
     handle = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in (*_SIGNATURES.items(), *_STEP_SIGNATURES.items()):
+    for name, (res, args) in (*_SIGNATURES.items(), *_STEP_SIGNATURES.items(), *_CACHE_SIGNATURES.items()):
         fn = getattr(handle, name)
         fn.restype = res
         fn.argtypes = args

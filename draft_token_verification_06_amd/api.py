@@ -1,22 +1,26 @@
-"""Python binding of the C ABI in include/sv.h: argument marshalling only.
+"""Python binding of the C ABI in include/sv.h, sv_step.h and sv_cache.h:
+argument marshalling only.
 
 Tensors must live on a ROCm device; every computation runs in the HIP
 library on the current torch stream of that device.  Results come back as
 device tensors; nothing synchronises.
 """
 import ctypes
+import math
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from ._lib import lib
+from ._lib import PagedCacheArgs, lib
 
 SV_OP_WINDOW, SV_OP_GREEDY, SV_OP_TREE, SV_OP_LMHEAD = 0, 1, 2, 3
 SV_TREE_GREEDY, SV_TREE_STOCHASTIC, SV_TREE_MULTI_CANDIDATE = 0, 1, 2
 _TREE_MODES = {"greedy": SV_TREE_GREEDY, "stochastic": SV_TREE_STOCHASTIC,
                "multi_candidate": SV_TREE_MULTI_CANDIDATE}
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+SV_DT_F8E4M3 = 3
+_PAGE_CODE = {torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: SV_DT_F8E4M3}
 
 
 class SvError(RuntimeError):
@@ -602,6 +606,289 @@ def attention(q, k_cache, v_cache, ctx_len, *, prefix_k=None, prefix_v=None, par
         _out_tensor(out.lse, torch.float32, (B, R, Hq), dev, "lse")
     _launch(dev, L.sv_attention, q.data_ptr(), q_stride, _DTYPE_CODE[dtype], k_cache.data_ptr(), v_cache.data_ptr(),
             seq_stride, tok_stride, cap, pk, pv, prefix_stride, P, len_ptr, rows_ptr, par, B, R, Hq, Hkv, D, max_ctx, scale,
+            out.out.data_ptr(), None if out.lse is None else out.lse.data_ptr(), ws.data_ptr(), ws_bytes)
+    return out
+
+
+class PagedCache:
+    """Pages of keys and values: sv_paged_cache of include/sv_cache.h.
+
+    k, v (num_pages, page, Hkv, D) in any non-overlapping order with unit
+    stride along D: bf16 or fp16, or float8_e4m3fn with k_scale, v_scale
+    (num_pages, page / block, Hkv) float32, contiguous.  One more leading
+    dimension on all of them holds the layers of a model (layer(i) is one of
+    them).  A handle on those tensors: they keep their storage while it is used.
+    paged_cache() allocates one."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "layers", "layer_stride", "args", "ref")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        code = _PAGE_CODE.get(k.dtype)
+        if code is None or k.device.type != "cuda" or k.dim() not in (4, 5):
+            raise ValueError("k: expected a bf16, fp16 or float8_e4m3fn device tensor of shape (num_pages, page, Hkv, D), or (layers, ..)")
+        st = k.stride()
+        if v.dtype != k.dtype or v.device != k.device or v.shape != k.shape or v.stride() != st:
+            raise ValueError("v must match k in dtype, device, shape and strides")
+        num_pages, page, Hkv, D = k.shape[-4:]
+        if st[-1] != 1:
+            raise ValueError("k and v: the values of a head must be contiguous")
+        self.layers, self.layer_stride = (k.shape[0], st[0]) if k.dim() == 5 else (0, 0)
+        if k.numel() == 0 or (self.layers > 1 and st[0] <= 0):
+            raise ValueError("k and v: expected pages that do not overlap")
+        block, ks, vs = 0, None, None
+        if code == SV_DT_F8E4M3:
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t is None or t.dtype != torch.float32 or t.device != k.device or not t.is_contiguous() or t.dim() != k.dim() - 1 \
+                        or t.shape[:-2] != k.shape[:-3] or t.shape[-1] != Hkv or not 0 < t.shape[-2] <= page or page % t.shape[-2]:
+                    raise ValueError(f"{name}: 8-bit pages need a contiguous float32 tensor (.., num_pages, page / block, Hkv) on {k.device}")
+            if k_scale.shape != v_scale.shape:
+                raise ValueError("k_scale and v_scale must have one shape")
+            block, ks, vs = page // k_scale.shape[-2], k_scale.data_ptr(), v_scale.data_ptr()
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("16-bit pages have no scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        # strides of dimensions of one entry do not matter: any multiple that overlaps nothing (0: dense)
+        self.args = PagedCacheArgs(k.data_ptr(), v.data_ptr(), ks, vs, code, num_pages, page, block, Hkv, D,
+                                   st[-4] if num_pages > 1 else 0, st[-3], st[-2] if Hkv > 1 else 0)
+        self.ref = ctypes.byref(self.args)
+
+    def layer(self, i):
+        """The pages of layer i, on the same memory."""
+        if not 0 <= i < self.layers:
+            raise IndexError(f"layer {i} of {self.layers}")
+        return PagedCache(self.k[i], self.v[i], *(None if t is None else t[i] for t in (self.k_scale, self.v_scale)))
+
+
+def paged_cache(num_pages, page, Hkv, D, dtype, device, *, block=None, layers=None):
+    """A PagedCache of zeros, the tokens of a head and page contiguous.  dtype
+    torch.float8_e4m3fn: with a scale for each `block` tokens (default: the
+    page, 64 at most)."""
+    lead = (num_pages,) if layers is None else (layers, num_pages)
+    k, v = (torch.zeros((*lead, Hkv, page, D), dtype=dtype, device=device).transpose(-2, -3) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return PagedCache(k, v)
+    block = min(page, 64) if block is None else block
+    return PagedCache(k, v, *(torch.zeros((*lead, page // block, Hkv), device=device) for _ in range(2)))
+
+
+def rotary_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, trained=4096, fast=32.0, slow=1.0):
+    """(inv_freq, magnitude) of rot turned values: radians per position, as a
+    list of rot / 2 floats, and the factor on the turned values.
+
+    scaling None: base ** (-2 i / rot).  For contexts `factor` times longer than
+    the `trained` length: "linear" divides every frequency by factor, "base"
+    raises the base by factor ** (rot / (rot - 2)) (the fastest pair stays, the
+    slowest is divided by factor), "ramp" keeps the pairs that make more than
+    `fast` turns within the trained length, divides those that make fewer than
+    `slow` by factor, blends linearly in between, and scales the values by 0.1
+    log(factor) + 1."""
+    if rot < 2 or rot % 2 or base <= 0 or factor <= 0:
+        raise ValueError("rot must be even and positive, base and factor positive")
+    if scaling == "base":
+        base *= factor ** (rot / (rot - 2)) if rot > 2 else factor
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    if scaling is None or scaling == "base":
+        return f, 1.0
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling != "ramp":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if fast <= slow:
+        raise ValueError("fast must exceed slow")
+    keep = [min(max((trained * x / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0) for x in f]
+    return [x * w + x / factor * (1 - w) for x, w in zip(f, keep)], (0.1 * math.log(factor) + 1 if factor > 1 else 1.0)
+
+
+def rotary_turns(inv_freq, device):
+    """The frequencies (a host sequence, radians per position) as rotary and
+    cache_append take them, a device int64 tensor: sv_rotary_turns."""
+    n = len(inv_freq)
+    src, out = (ctypes.c_double * n)(*inv_freq), (ctypes.c_uint64 * n)()
+    _check(lib().sv_rotary_turns(src, n, out))
+    return torch.tensor([x - (1 << 64) if x >> 63 else x for x in out], dtype=torch.int64).to(device)
+
+
+def _turns(turns, D, dev):
+    """(address, turned values) of a frequency tensor, or (None, 0)."""
+    if turns is None:
+        return None, 0
+    if turns.dtype != torch.int64 or turns.device != dev or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError(f"turns: expected a contiguous int64 tensor of shape (rot / 2,) on {dev}")
+    return turns.data_ptr(), 2 * turns.shape[0]
+
+
+def _rows(t, B, R, H, D, dtype, dev, name):
+    """Row stride of a (B, R, H, D) tensor with dense heads and rows one stride apart (0 = dense)."""
+    if t.dtype != dtype or t.device != dev or t.shape != (B, R, H, D):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape ({B}, {R}, {H}, {D}) on {dev}, got {t.dtype} {tuple(t.shape)}")
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (H > 1 and s2 != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    row = s1 if R > 1 else s0 if B > 1 else 0
+    if (B > 1 and R > 1 and s0 != R * row) or (B * R > 1 and row < H * D):
+        raise ValueError(f"{name}: rows must be one stride apart and not overlap")
+    return row
+
+
+def rotary(x, turns, base_pos=None, *, parent=None, interleaved=False, magnitude=1.0, inverse=False, row_count=None, out=None):
+    """Rows turned to their positions: sv_rotary.
+
+    x (B, R, H, D) float32, bf16 or fp16; turns: rotary_turns of the pairs'
+    frequencies, (rot / 2,) int64.  Row r stands at base_pos[b] + r, or with
+    parent (a host sequence) at base_pos[b] + its depth; base_pos (B,) int64 or
+    None (0).  inverse turns back: with the same magnitude, the gradient.  out:
+    a tensor like x (x itself: in place), a new one when None."""
+    dtype, dev = x.dtype, x.device
+    if x.dim() != 4 or dtype not in _DTYPE_CODE or dev.type != "cuda":
+        raise ValueError("x: expected a float32, bf16 or fp16 device tensor of shape (B, R, H, D)")
+    B, R, H, D = x.shape
+    stride = _rows(x, B, R, H, D, dtype, dev, "x")
+    if turns is None:
+        raise ValueError("turns is required")
+    turns_ptr, rot = _turns(turns, D, dev)
+    if out is None:
+        out, out_stride = torch.empty((B, R, H, D), dtype=dtype, device=dev), 0
+    else:
+        out_stride = _rows(out, B, R, H, D, dtype, dev, "out")
+    _launch(dev, lib().sv_rotary, x.data_ptr(), stride, out.data_ptr(), out_stride, _DTYPE_CODE[dtype], turns_ptr, rot,
+            bool(interleaved), bool(inverse), magnitude, _vec(base_pos, torch.int64, B, dev, "base_pos"),
+            _vec(row_count, torch.int32, B, dev, "row_count"), _parents(parent, R), B, R, H, D)
+    return out
+
+
+def _one_layer(cache, dev):
+    if cache.k.device != dev:
+        raise ValueError(f"cache is on {cache.k.device}, expected {dev}")
+    if cache.layers:
+        raise ValueError("cache: expected one layer (cache.layer(i))")
+    return cache.args
+
+
+def cache_append(cache, page_table, ctx_len, k, v, *, q=None, turns=None, base_pos=None, parent=None, interleaved=False,
+                 magnitude=1.0, row_count=None, q_out=None):
+    """Stores rows' keys, turned, and values in their sequences' pages, and turns
+    their queries: sv_cache_append.
+
+    cache: a PagedCache (one layer); page_table (B, pages) int32; row r becomes
+    token ctx_len[b] + r.  k, v (B, R, Hkv, D) bf16 or fp16, q (B, R, Hq, D) or
+    None (each may be a part of one projection's rows).  turns, base_pos, parent,
+    interleaved, magnitude as in rotary (turns None: not turned; base_pos None:
+    ctx_len).  Returns q_out (a new tensor when None; q itself: in place), or
+    None without q."""
+    dtype, dev = k.dtype, k.device
+    if k.dim() != 4 or (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda":
+        raise ValueError("k: expected a bf16 or fp16 device tensor of shape (B, R, Hkv, D)")
+    a = _one_layer(cache, dev)
+    B, R = k.shape[:2]
+    Hkv, D = a.Hkv, a.D
+    k_stride, v_stride = _rows(k, B, R, Hkv, D, dtype, dev, "k"), _rows(v, B, R, Hkv, D, dtype, dev, "v")
+    if a.dtype != SV_DT_F8E4M3 and cache.k.dtype != dtype:
+        raise ValueError(f"k and v: 16-bit pages hold {cache.k.dtype}")
+    table_stride = _rows_i32(page_table, B, 1, dev, "page_table")
+    if ctx_len is None:
+        raise ValueError("ctx_len is required")
+    turns_ptr, rot = _turns(turns, D, dev)
+    Hq = q_stride = out_stride = 0
+    q_ptr = out_ptr = None
+    if q is not None:
+        Hq = q.shape[2] if q.dim() == 4 else 0
+        q_stride = _rows(q, B, R, Hq, D, dtype, dev, "q")
+        if q_out is None:
+            q_out = torch.empty((B, R, Hq, D), dtype=dtype, device=dev)
+        else:
+            out_stride = _rows(q_out, B, R, Hq, D, dtype, dev, "q_out")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _launch(dev, lib().sv_cache_append, cache.ref, page_table.data_ptr(), table_stride, page_table.shape[1],
+            _vec(ctx_len, torch.int32, B, dev, "ctx_len"), _vec(row_count, torch.int32, B, dev, "row_count"), _parents(parent, R),
+            _vec(base_pos, torch.int64, B, dev, "base_pos"), k.data_ptr(), k_stride, v.data_ptr(), v_stride, q_ptr, q_stride,
+            out_ptr, out_stride, _DTYPE_CODE[dtype], turns_ptr, rot, bool(interleaved), magnitude, B, R, Hq)
+    return q_out
+
+
+def cache_commit(cache, page_table, ctx_len, nodes, n_accepted, *, rows, new_len=None):
+    """Moves an accepted path's keys and values behind the context, in all layers
+    of the cache, and advances the lengths: sv_cache_commit.
+
+    nodes, n_accepted: out_nodes and n_accepted of verify_tree (nodes None: a
+    window, only the lengths); rows: the rows of the step.  Returns new_len (a
+    new tensor when None; ctx_len itself: in place)."""
+    dev = cache.k.device
+    if ctx_len is None or n_accepted is None:
+        raise ValueError("ctx_len and n_accepted are required")
+    B = page_table.shape[0]
+    table_stride = _rows_i32(page_table, B, 1, dev, "page_table")
+    nodes_ptr, nodes_stride, most = None, 0, 0
+    if nodes is not None and nodes.shape[-1] > 0:
+        nodes_stride = _rows_i32(nodes, B, 1, dev, "nodes")
+        nodes_ptr, most = nodes.data_ptr(), nodes.shape[1]
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    _launch(dev, lib().sv_cache_commit, cache.ref, max(cache.layers, 1), cache.layer_stride if cache.layers > 1 else 0,
+            page_table.data_ptr(), table_stride, page_table.shape[1], _vec(ctx_len, torch.int32, B, dev, "ctx_len"), nodes_ptr,
+            nodes_stride, most, _vec(n_accepted, torch.int32, B, dev, "n_accepted"), B, rows,
+            _vec(new_len, torch.int32, B, dev, "new_len"))
+    return new_len
+
+
+def paged_attention_workspace(B, R, Hq, Hkv, D, P, max_ctx, device):
+    """A workspace for paged_attention calls of these sizes."""
+    nbytes = int(lib().sv_paged_attention_workspace(B, R, Hq, Hkv, D, P, max_ctx))
+    if nbytes == 0:
+        raise ValueError("invalid sizes for an attention workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def paged_attention(q, cache, page_table, ctx_len, *, prefix_table=None, prefix_len=0, parent=None, row_count=None,
+                    scale=None, max_ctx=None, return_lse=False, out=None, ws=None):
+    """Attention of a window's or tree's rows over paged caches: sv_paged_attention.
+
+    As attention(), with keys and values in the pages of cache (a PagedCache, one
+    layer): page_table (B, pages) int32 for the sequences' own tokens, prefix_table
+    (ceil(prefix_len / page),) int32 for the prefix_len tokens in front that all
+    share.  max_ctx defaults to the table's room for a context."""
+    dtype, dev = q.dtype, q.device
+    if q.dim() != 4 or (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda":
+        raise ValueError("q: expected a bf16 or fp16 device tensor of shape (B, R, Hq, D)")
+    a = _one_layer(cache, dev)
+    B, R, Hq, D = q.shape
+    q_stride = _rows(q, B, R, Hq, a.D, dtype, dev, "q")
+    if a.dtype != SV_DT_F8E4M3 and cache.k.dtype != dtype:
+        raise ValueError(f"q: 16-bit pages hold {cache.k.dtype}")
+    if Hq % a.Hkv:
+        raise ValueError("the query heads must be a multiple of the kv heads")
+    table_stride = _rows_i32(page_table, B, 1, dev, "page_table")
+    prefix_ptr = None
+    if prefix_len:
+        if prefix_table is None or prefix_table.dtype != torch.int32 or prefix_table.device != dev or prefix_table.dim() != 1 \
+                or not prefix_table.is_contiguous() or prefix_table.shape[0] * a.page < prefix_len:
+            raise ValueError(f"prefix_table: expected a contiguous int32 tensor of the {prefix_len} tokens' pages on {dev}")
+        prefix_ptr = prefix_table.data_ptr()
+    if ctx_len is None:
+        raise ValueError("ctx_len is required")
+    if max_ctx is None:
+        max_ctx = min(page_table.shape[1] * a.page - R, 1 << 24)
+    if scale is None:
+        scale = D ** -0.5
+    L = lib()
+    if ws is None:
+        ws_bytes = L.sv_paged_attention_workspace(B, R, Hq, a.Hkv, D, prefix_len, max_ctx)
+        if ws_bytes == 0:
+            raise ValueError("sizes outside the rules of sv_paged_attention")
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        ws_bytes = _ws_bytes(ws, dev)
+    if out is None:
+        out = AttentionResult(torch.empty((B, R, Hq, D), dtype=dtype, device=dev),
+                              torch.empty((B, R, Hq), dtype=torch.float32, device=dev) if return_lse else None)
+    else:
+        if out.out is None:
+            raise ValueError("out is a required output")
+        _out_tensor(out.out, dtype, (B, R, Hq, D), dev, "out")
+        _out_tensor(out.lse, torch.float32, (B, R, Hq), dev, "lse")
+    _launch(dev, L.sv_paged_attention, q.data_ptr(), q_stride, _DTYPE_CODE[dtype], cache.ref, page_table.data_ptr(), table_stride,
+            page_table.shape[1], prefix_ptr, prefix_len, _vec(ctx_len, torch.int32, B, dev, "ctx_len"),
+            _vec(row_count, torch.int32, B, dev, "row_count"), _parents(parent, R), B, R, Hq, max_ctx, scale,
             out.out.data_ptr(), None if out.lse is None else out.lse.data_ptr(), ws.data_ptr(), ws_bytes)
     return out
 

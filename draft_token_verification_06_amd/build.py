@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = [os.path.join(CSRC, "sv_rows.hip"), os.path.join(CSRC, "sv_kernels.hip"),
            os.path.join(CSRC, "sv_lmhead.hip"), os.path.join(CSRC, "sv_noalloc.hip"),
            os.path.join(CSRC, "sv_adjust.hip"), os.path.join(CSRC, "sv_lmquant.hip"),
-           os.path.join(CSRC, "sv_attention.hip"),
+           os.path.join(CSRC, "sv_attention.hip"), os.path.join(CSRC, "sv_paged.hip"),
+           os.path.join(CSRC, "sv_cache.hip"),
            os.path.join(CSRC, "sv_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "sv.h"
+#include "sv_cache.h"
 #include "sv_launch.h"
 #include "sv_plan.h"
 #include "sv_step.h"
@@ -778,6 +779,308 @@ int sv_attention(const void *q, int64_t q_row_stride, int dtype,
   A.out = static_cast<uint16_t *>(out);
   A.lse = lse;
   launch_attend(dtype, D, A, parent_host ? &parents : nullptr, L, stream);
+  return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+bool power_of_two(int32_t x, int32_t lo, int32_t hi) { return x >= lo && x <= hi && (x & (x - 1)) == 0; }
+
+// Whether no two tokens or heads of [num_pages][page][Hkv] vectors of D values
+// share memory: with strides in ascending order each passes what lies inside.
+bool disjoint(const sv_paged_cache &c) {
+  struct { int64_t stride, count; } dim[3] = {
+    {c.page_stride, c.num_pages}, {c.token_stride, c.page}, {c.head_stride, c.Hkv}};
+  std::sort(dim, dim + 3, [](const auto &a, const auto &b) { return a.stride < b.stride; });
+  int64_t extent = c.D;
+  for (const auto &d : dim) {
+    if (d.count == 1) continue;
+    if (d.stride < extent || d.stride > (int64_t{1} << 40)) return false;
+    extent += (d.count - 1) * d.stride;
+    if (extent > int64_t{1} << 46) return false;
+  }
+  return true;
+}
+
+// Checks a cache and describes it to the kernels; fills in dense strides.
+int cache_pool(const sv_paged_cache *cache, int dtype, sv_paged_cache *full, PagedPool *P) {
+  if (!cache) return SV_EINVAL;
+  sv_paged_cache c = *cache;
+  const bool f8 = c.dtype == SV_DT_F8E4M3;
+  if (!f8 && c.dtype != SV_DT_BF16 && c.dtype != SV_DT_F16) return SV_EDTYPE;
+  if (dtype >= 0 && !f8 && c.dtype != dtype) return SV_EDTYPE;
+  if (!c.k || !c.v || c.num_pages < 1 || c.Hkv < 1 || c.Hkv > SV_ATTENTION_MAX_HEADS) return SV_EINVAL;
+  if ((c.D != 64 && c.D != 128) || !power_of_two(c.page, 16, SV_CACHE_MAX_PAGE)) return SV_EINVAL;
+  if (f8) {
+    if (!c.k_scale || !c.v_scale || !power_of_two(c.block, 16, SV_CACHE_MAX_BLOCK) || c.block > c.page) return SV_EINVAL;
+    if (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4)) return SV_EINVAL;
+  } else {
+    c.block = std::min<int32_t>(c.page, SV_CACHE_MAX_BLOCK);
+  }
+  if (c.token_stride == 0) c.token_stride = c.D;
+  if (c.head_stride == 0) c.head_stride = static_cast<int64_t>(c.page) * c.D;
+  if (c.page_stride == 0) c.page_stride = static_cast<int64_t>(c.Hkv) * c.page * c.D;
+  const int bytes = f8 ? 1 : 2, step = 16 / bytes;
+  if (c.page_stride < 0 || c.token_stride < 0 || c.head_stride < 0 || c.page_stride % step || c.token_stride % step || c.head_stride % step)
+    return SV_EINVAL;
+  if (c.token_stride > 1 << 24 || !disjoint(c)) return SV_EINVAL;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16)) return SV_EINVAL;
+  P->k = static_cast<uint8_t *>(c.k);
+  P->v = static_cast<uint8_t *>(c.v);
+  P->k_scale = f8 ? c.k_scale : nullptr;
+  P->v_scale = f8 ? c.v_scale : nullptr;
+  P->page_bytes = c.page_stride * bytes;
+  P->token_bytes = c.token_stride * bytes;
+  P->head_bytes = c.head_stride * bytes;
+  P->num_pages = c.num_pages;
+  P->page_shift = __builtin_ctz(c.page);
+  P->block_shift = __builtin_ctz(c.block);
+  P->Hkv = c.Hkv;
+  *full = c;
+  return SV_OK;
+}
+
+// A table of B rows of table_pages page numbers.  Tokens are counted in 30 bits.
+bool table_ok(const int32_t *table, int64_t *stride, int32_t table_pages, int32_t page, int32_t B) {
+  if (!table || table_pages < 1 || table_pages > (1 << 30) / page) return false;
+  if (*stride == 0) *stride = table_pages;
+  return B == 1 || *stride >= table_pages;
+}
+
+// Depths of a valid tree's nodes.
+int tree_depths(const int32_t *parent, int32_t N, TreeDepths *out) {
+  TreeMeta meta;
+  const int st = build_tree(parent, N, &meta);
+  if (st != SV_OK) return st;
+  std::memcpy(out->depth, meta.depth, sizeof(out->depth));
+  return SV_OK;
+}
+
+// step: what the number of turned values is a multiple of.
+bool rotation_ok(const uint64_t *turns, int32_t rot, int32_t step, int32_t D, float magnitude) {
+  return aligned(turns, 8) && rot >= step && rot <= D && rot % step == 0 && std::isfinite(magnitude);
+}
+
+// [rows] of `elems` elements `stride` apart.
+bool rows_ok(const void *p, int64_t *stride, int64_t elems, int64_t rows, int bytes) {
+  if (!p || !aligned(p, 16)) return false;
+  if (*stride == 0) *stride = elems;
+  return rows == 1 || (*stride >= elems && *stride * bytes % 16 == 0 && *stride <= int64_t{1} << 40);
+}
+
+// out is in with the same stride, or the two spans are disjoint.
+bool in_place_or_apart(const void *in, int64_t in_stride, const void *out, int64_t out_stride, int64_t elems, int64_t rows, int bytes) {
+  if (in == out) return rows == 1 || in_stride == out_stride;
+  const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
+  return i0 + ((rows - 1) * in_stride + elems) * bytes <= o0 || o0 + ((rows - 1) * out_stride + elems) * bytes <= i0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sv_rotary_turns(const double *inv_freq, int32_t n, uint64_t *turns) {
+  if (!inv_freq || !turns || n < 1) return SV_EINVAL;
+  for (int32_t i = 0; i < n; ++i)
+    if (!std::isfinite(inv_freq[i])) return SV_EINVAL;
+  for (int32_t i = 0; i < n; ++i) {
+    const double turn = inv_freq[i] / 6.283185307179586477, part = std::fabs(turn) - std::floor(std::fabs(turn));
+    const uint64_t units = static_cast<uint64_t>(std::ldexp(part, 64));  // (part < 1: below 2^64)
+    turns[i] = turn < 0 ? 0 - units : units;
+  }
+  return SV_OK;
+}
+
+int sv_rotary(const void *x, int64_t x_row_stride, void *out, int64_t out_row_stride, int dtype,
+              const uint64_t *turns, int32_t rot, int interleaved, int inverse, float magnitude,
+              const int64_t *base_pos, const int32_t *row_count, const int32_t *parent_host,
+              int32_t B, int32_t R, int32_t H, int32_t D, hipStream_t stream) {
+  const int eb = elem_bytes(dtype);
+  if (eb == 0) return SV_EDTYPE;
+  if (B < 1 || R < 1 || H < 1 || H > SV_ATTENTION_MAX_HEADS || D < 16 || D > SV_ROTARY_MAX_DIM || D % 16) return SV_EINVAL;
+  const int64_t rows = static_cast<int64_t>(B) * R, elems = static_cast<int64_t>(H) * D;
+  if (!turns || !rotation_ok(turns, rot, 2, D, magnitude) || !aligned(base_pos, 8)) return SV_EINVAL;
+  TreeDepths depths;
+  if (parent_host) {
+    const int st = tree_depths(parent_host, R, &depths);
+    if (st != SV_OK) return st;
+  }
+  if (!grid_fits((rows + kRotaryTokens - 1) / kRotaryTokens, kRotaryThreads)) return SV_EINVAL;
+  if (!rows_ok(x, &x_row_stride, elems, rows, eb) || !rows_ok(out, &out_row_stride, elems, rows, eb)) return SV_EINVAL;
+  if (!in_place_or_apart(x, x_row_stride, out, out_row_stride, elems, rows, eb)) return SV_EINVAL;
+  RotaryArgs A{};
+  A.rotation = {turns, base_pos, rot, interleaved != 0, inverse != 0, magnitude};
+  A.x = static_cast<const char *>(x);
+  A.out = static_cast<char *>(out);
+  A.x_stride = x_row_stride;
+  A.out_stride = out_row_stride;
+  A.row_count = row_count;
+  A.R = R;
+  A.H = H;
+  A.D = D;
+  A.in_place = x == out;
+  A.rows = rows;
+  launch_rotary(dtype, A, parent_host ? &depths : nullptr, stream);
+  return launch_status();
+}
+
+int sv_cache_append(const sv_paged_cache *cache, const int32_t *page_table, int64_t table_stride, int32_t table_pages,
+                    const int32_t *ctx_len, const int32_t *row_count, const int32_t *parent_host, const int64_t *base_pos,
+                    const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                    const void *q, int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int dtype,
+                    const uint64_t *turns, int32_t rot, int interleaved, float magnitude,
+                    int32_t B, int32_t R, int32_t Hq, hipStream_t stream) {
+  if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
+  AppendArgs A{};
+  sv_paged_cache c;
+  const int cst = cache_pool(cache, dtype, &c, &A.pool);
+  if (cst != SV_OK) return cst;
+  if (B < 1 || R < 1 || R > 1 << 24 || Hq < 0 || Hq > SV_ATTENTION_MAX_HEADS || !ctx_len) return SV_EINVAL;
+  TreeDepths depths;
+  if (parent_host) {
+    const int st = tree_depths(parent_host, R, &depths);
+    if (st != SV_OK) return st;
+  }
+  if (!table_ok(page_table, &table_stride, table_pages, c.page, B)) return SV_EINVAL;
+  const int64_t rows = static_cast<int64_t>(B) * R, kv = static_cast<int64_t>(c.Hkv) * c.D, elems = static_cast<int64_t>(Hq) * c.D;
+  if (!rows_ok(k, &k_row_stride, kv, rows, 2) || !rows_ok(v, &v_row_stride, kv, rows, 2)) return SV_EINVAL;
+  if (Hq > 0) {
+    if (!rows_ok(q, &q_row_stride, elems, rows, 2) || !rows_ok(q_out, &q_out_row_stride, elems, rows, 2)) return SV_EINVAL;
+    if (!in_place_or_apart(q, q_row_stride, q_out, q_out_row_stride, elems, rows, 2)) return SV_EINVAL;
+  } else if (q || q_out) {
+    return SV_EINVAL;
+  }
+  if (turns ? !rotation_ok(turns, rot, 16, c.D, magnitude) : rot != 0) return SV_EINVAL;
+  if (!aligned(base_pos, 8)) return SV_EINVAL;
+  const int64_t blocks = append_blocks(R, c.block);
+  if (!grid_fits(B * blocks, kAppendThreads)) return SV_EINVAL;
+  A.rotation = {turns, base_pos, rot, interleaved != 0, 0, magnitude};
+  A.table = page_table;
+  A.table_stride = table_stride;
+  A.table_pages = table_pages;
+  A.ctx_len = ctx_len;
+  A.row_count = row_count;
+  A.k = static_cast<const uint16_t *>(k);
+  A.v = static_cast<const uint16_t *>(v);
+  A.q = static_cast<const uint16_t *>(q);
+  A.q_out = static_cast<uint16_t *>(q_out);
+  A.k_stride = k_row_stride;
+  A.v_stride = v_row_stride;
+  A.q_stride = q_row_stride;
+  A.q_out_stride = q_out_row_stride;
+  A.B = B;
+  A.R = R;
+  A.Hq = Hq;
+  A.D = c.D;
+  A.blocks = static_cast<int32_t>(blocks);
+  launch_append(dtype, c.dtype == SV_DT_F8E4M3, A, parent_host ? &depths : nullptr, stream);
+  return launch_status();
+}
+
+int sv_cache_commit(const sv_paged_cache *cache, int32_t layers, int64_t layer_stride,
+                    const int32_t *page_table, int64_t table_stride, int32_t table_pages,
+                    const int32_t *ctx_len, const int32_t *nodes, int64_t nodes_stride, int32_t max_nodes,
+                    const int32_t *n_accepted, int32_t B, int32_t R, int32_t *new_len, hipStream_t stream) {
+  CommitArgs A{};
+  sv_paged_cache c;
+  const int cst = cache_pool(cache, -1, &c, &A.pool);
+  if (cst != SV_OK) return cst;
+  if (B < 1 || R < 1 || layers < 1 || layers > 65535 || !ctx_len || !n_accepted) return SV_EINVAL;
+  if (!table_ok(page_table, &table_stride, table_pages, c.page, B)) return SV_EINVAL;
+  if (max_nodes < 0 || max_nodes > kTreeMaxDepth || (max_nodes > 0) != (nodes != nullptr)) return SV_EINVAL;
+  if (nodes && nodes_stride == 0) nodes_stride = max_nodes;
+  if (nodes && B > 1 && nodes_stride < max_nodes) return SV_EINVAL;
+  if (!nodes && !new_len) return SV_EINVAL;
+  const uintptr_t n0 = reinterpret_cast<uintptr_t>(new_len), c0 = reinterpret_cast<uintptr_t>(ctx_len);
+  if (new_len && n0 != c0 && n0 < c0 + 4 * static_cast<uintptr_t>(B) && c0 < n0 + 4 * static_cast<uintptr_t>(B)) return SV_EINVAL;
+  const int bytes = c.dtype == SV_DT_F8E4M3 ? 1 : 2;
+  const int64_t dense = static_cast<int64_t>(c.num_pages) * c.Hkv * c.page * c.D;
+  if (layer_stride == 0) layer_stride = dense;
+  // layers lie apart: behind each other, whatever the order inside
+  const int64_t extent = (c.num_pages - 1) * c.page_stride + (c.page - 1) * c.token_stride + (c.Hkv - 1) * c.head_stride + c.D;
+  if (layers > 1 && (layer_stride < extent || layer_stride * bytes % 16 || layer_stride > int64_t{1} << 46)) return SV_EINVAL;
+  if (!grid_fits(static_cast<int64_t>((2 * c.Hkv + 3) / 4) * B * layers, kCommitThreads)) return SV_EINVAL;
+  A.layer_bytes = layer_stride * bytes;
+  A.layer_scales = static_cast<int64_t>(c.num_pages) * (c.page / c.block) * c.Hkv;
+  A.table = page_table;
+  A.table_stride = table_stride;
+  A.table_pages = table_pages;
+  A.ctx_len = ctx_len;
+  A.nodes = nodes;
+  A.n_accepted = n_accepted;
+  A.nodes_stride = nodes_stride;
+  A.max_nodes = max_nodes;
+  A.B = B;
+  A.R = R;
+  A.D = c.D;
+  A.layers = layers;
+  A.new_len = new_len;
+  launch_commit(c.dtype == SV_DT_F8E4M3, A, stream);
+  return launch_status();
+}
+
+size_t sv_paged_attention_workspace(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
+  AttendPlan L;
+  return attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &L) ? L.total : 0;
+}
+
+int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_paged_cache *cache,
+                       const int32_t *page_table, int64_t table_stride, int32_t table_pages,
+                       const int32_t *prefix_table, int32_t P,
+                       const int32_t *ctx_len, const int32_t *row_count, const int32_t *parent_host,
+                       int32_t B, int32_t R, int32_t Hq, int32_t max_ctx, float scale,
+                       void *out, float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (dtype != SV_DT_BF16 && dtype != SV_DT_F16) return SV_EDTYPE;
+  PagedAttendArgs A{};
+  sv_paged_cache c;
+  const int cst = cache_pool(cache, dtype, &c, &A.pool);
+  if (cst != SV_OK) return cst;
+  AttendPlan L;
+  if (!attention_plan(B, R, Hq, c.Hkv, c.D, P, max_ctx, &L)) return SV_EINVAL;
+  TreeParents parents;
+  if (parent_host) {
+    const int tst = tree_parents(parent_host, R, &parents);
+    if (tst != SV_OK) return tst;
+  } else if (R > SV_MAX_GAMMA + 1) {
+    return SV_EINVAL;
+  }
+  if (!ctx_len || !out || !table_ok(page_table, &table_stride, table_pages, c.page, B)) return SV_EINVAL;
+  if ((P > 0) != (prefix_table != nullptr)) return SV_EINVAL;
+  if (static_cast<int64_t>(max_ctx) + R > static_cast<int64_t>(table_pages) * c.page) return SV_EINVAL;
+  if (!(scale == scale) || scale - scale != 0.0f) return SV_EINVAL;
+  if (!rows_ok(q, &q_row_stride, static_cast<int64_t>(Hq) * c.D, static_cast<int64_t>(B) * R, 2)) return SV_EINVAL;
+  if (!aligned(out, 16) || (lse && !aligned(lse, 4))) return SV_EINVAL;
+  const int ws = check_workspace(workspace, workspace_bytes, L.total);
+  if (ws != SV_OK) return ws;
+  A.q = static_cast<const uint16_t *>(q);
+  A.q_row_stride = q_row_stride;
+  A.table = page_table;
+  A.table_stride = table_stride;
+  A.prefix_table = prefix_table;
+  A.ctx_len = ctx_len;
+  A.row_count = row_count;
+  A.B = B;
+  A.R = R;
+  A.Hq = Hq;
+  A.n = Hq / c.Hkv;
+  A.P = P;
+  A.max_ctx = max_ctx;
+  A.prefix_parts = L.prefix_parts;
+  A.prefix_chunk = L.prefix_chunk;
+  A.prefix_items = static_cast<int32_t>(L.prefix_items);
+  A.own_parts = L.own_parts;
+  A.split = L.split;
+  A.own_tiles = L.own_tiles;
+  // never zero: masked products are -inf, and 0 * -inf is no number
+  A.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  A.negate = scale < 0.0f;
+  A.part_o = static_cast<float *>(workspace);
+  A.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + L.ml_off);
+  A.out = static_cast<uint16_t *>(out);
+  A.lse = lse;
+  launch_paged_attend(dtype, c.dtype == SV_DT_F8E4M3, c.D, A, parent_host ? &parents : nullptr, L, stream);
   return launch_status();
 }
 

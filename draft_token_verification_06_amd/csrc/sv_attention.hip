@@ -36,53 +36,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "sv_device.h"
-#include "sv_launch.h"
-#include "sv_plan.h"
+#include "sv_attend.h"
 
 namespace sv {
-
-typedef __bf16 at_bf16x8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 at_f16x8_t __attribute__((ext_vector_type(8)));
-typedef float at_f32x16_t __attribute__((ext_vector_type(16)));
-typedef short at_i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) at_i16x4_t *lds_i16x4_t;
-
-constexpr int kAtThreads = kAttendThreads;
-
-template <int DT> struct AtElt;
-template <> struct AtElt<DT_BF16> {
-  static constexpr uint32_t kExp = 0x7F80u;  // exponent of infinities and NaN
-  static constexpr float kLift = 0.0f;
-  __device__ static __forceinline__ at_f32x16_t mma(uint4 a, uint4 b, at_f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8_t, a), __builtin_bit_cast(at_bf16x8_t, b), c, 0, 0, 0);
-  }
-  // Two exponentials to the storage type, rounded to nearest: the matrix units
-  // take two operands of one type, and the values come in that type.  It costs
-  // half a step of each weight (2^-8 in bfloat16), as much as rounding the
-  // output does; a second product for what the rounding leaves would double
-  // the matrix work of the values.
-  __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
-    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, v2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
-  }
-  __device__ static __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
-};
-template <> struct AtElt<DT_F16> {
-  static constexpr uint32_t kExp = 0x7C00u;
-  // Exponentials of rows in float16 are held 2^15 times larger, sums and
-  // outputs with them: weights down to 2^-29 of the largest stay normal
-  // numbers (down to 2^-14 otherwise, and thousands of smaller ones add up).
-  static constexpr float kLift = 15.0f;
-  __device__ static __forceinline__ at_f32x16_t mma(uint4 a, uint4 b, at_f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(at_f16x8_t, a), __builtin_bit_cast(at_f16x8_t, b), c, 0, 0, 0);
-  }
-  __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
-    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, v2{static_cast<_Float16>(lo), static_cast<_Float16>(hi)});
-  }
-  __device__ static __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x)); }
-};
 
 // What one work item computes: rows [row0, row0 + rows) of a stack of rows
 // (stack row i is query row base_row + i / n, head kvh n + i % n) over keys
@@ -97,12 +53,6 @@ struct Item {
   int k0, k1, draft;
   int part;
 };
-
-// The values of lanes l and l ^ 32 (in either order): one lane-swap instruction.
-__device__ __forceinline__ float2 both_halves(float x) {
-  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return make_float2(__uint_as_float(p[0]), __uint_as_float(p[1]));
-}
 
 // LDS rows in elements.  The 128 bytes that one cycle serves are 8 lanes of 16
 // bytes in consecutive key rows (16 bytes of padding put them side by side),
@@ -373,15 +323,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs &A, const Item &it,
   }
 }
 
-__device__ __forceinline__ bool bad_len(const AttendJoin &A, int len) { return len < 0 || len > A.max_ctx; }
-__device__ __forceinline__ int live_rows(const AttendJoin &A, int b) {
-  return A.row_count ? min(max(A.row_count[b], 0), A.R) : A.R;
-}
-
 // tree: nothing for a window, or the TreeParents.
 template <int DT, int D, int WQP, int WQO, class... Tree>
 __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A, Tree... tree) {
-  constexpr bool kTree = sizeof...(Tree) > 0;
   constexpr size_t kBytes = at_tile_bytes<D, WQP>() > at_tile_bytes<D, WQO>() ? at_tile_bytes<D, WQP>() : at_tile_bytes<D, WQO>();
   __shared__ uint4 s_tile[kBytes / sizeof(uint4)];
   __shared__ uint32_t s_anc[kTreeMaxNodes][8];
@@ -446,33 +390,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_attend(AttendArgs A, Tree... 
   it.k = A.k + b * A.seq_stride + it.kvh * D;
   it.v = A.v + b * A.seq_stride + it.kvh * D;
   it.tok_stride = A.tok_stride;
-  if (it.k1 > len) {
-    // ancestor sets of the rows, one row per thread; parents go to LDS first,
-    // as a walk through the argument block would cost a trip to memory a step
-    if constexpr (kTree) {
-      for (int v = threadIdx.x; v < A.R; v += kAtThreads) s_parent[v] = (tree.parent[v], ...);
-      __syncthreads();
-    }
-    for (int v = threadIdx.x; v < A.R; v += kAtThreads) {
-      uint32_t w[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) w[x] = 0;
-      if constexpr (kTree) {
-        for (int u = v; u > 0; u = s_parent[u])
-#pragma unroll
-          for (int x = 0; x < 8; ++x) w[x] |= x == (u >> 5) ? 1u << (u & 31) : 0u;
-        w[0] |= 1u;  // the root
-      } else {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int n = v + 1 - 32 * x;
-          w[x] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) s_anc[v][x] = w[x];
-    }
-  }
+  if (it.k1 > len) ancestor_sets(A.R, s_anc, s_parent, tree...);
   __syncthreads();
   attend_item<DT, D, WQO>(A, it, lds, s_anc, s_ml);
 }
@@ -517,6 +435,18 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
   if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L * (AtElt<DT>::kLift > 0 ? 0x1p-15f : 1.0f))) * 0.6931471805599453f;
 }
 
+void launch_attend_join(int dtype, int D, const AttendJoin &A, hipStream_t st) {
+  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4)), threads(256);
+  if (dtype == DT_BF16) {
+    if (D == 64) hipLaunchKernelGGL((k_attend_combine<DT_BF16, 64>), grid, threads, 0, st, A);
+    else hipLaunchKernelGGL((k_attend_combine<DT_BF16, 128>), grid, threads, 0, st, A);
+  } else {
+    if (D == 64) hipLaunchKernelGGL((k_attend_combine<DT_F16, 64>), grid, threads, 0, st, A);
+    else hipLaunchKernelGGL((k_attend_combine<DT_F16, 128>), grid, threads, 0, st, A);
+  }
+}
+
 namespace {
 
 template <int DT, int D, int WQP, int WQO>
@@ -545,9 +475,7 @@ void launch_type(const AttendArgs &A, const TreeParents *parents, const AttendPl
     launch_own<DT, D, 4>(A, parents, P, grid, st);
   else
     launch_own<DT, D, 1>(A, parents, P, grid, st);
-  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
-  hipLaunchKernelGGL((k_attend_combine<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st,
-                     static_cast<const AttendJoin &>(A));
+  launch_attend_join(DT, D, A, st);
 }
 
 }  // namespace

@@ -182,6 +182,85 @@ struct AttendArgs : AttendJoin {
   int32_t negate;    // the scale is negative
 };
 void launch_attend(int dtype, int D, const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st);
+void launch_attend_join(int dtype, int D, const AttendJoin &A, hipStream_t st);
+
+// The paged cache.  Strides in bytes; page and block are powers of two (tokens
+// of a page; tokens that share a scale, or are handled together in 16-bit pages).
+struct PagedPool {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;  // [num_pages][page / block][Hkv], 8-bit pages
+  int64_t page_bytes, token_bytes, head_bytes;
+  int32_t num_pages, page_shift, block_shift, Hkv;
+};
+// Depths of a tree's nodes, by value as TreeParents.
+struct TreeDepths {
+  uint8_t depth[kTreeMaxNodes];
+};
+// Rotation of rows: turns [rot / 2] or null.
+struct Rotation {
+  const uint64_t *turns;
+  const int64_t *base_pos;
+  int32_t rot, interleaved, inverse;
+  float magnitude;
+};
+struct RotaryArgs {
+  Rotation rotation;
+  const char *x;
+  char *out;
+  int64_t x_stride, out_stride;  // elements
+  const int32_t *row_count;
+  int32_t R, H, D, in_place;
+  int64_t rows;  // B * R
+};
+constexpr int kRotaryThreads = 256;
+constexpr int kRotaryTokens = 16;  // rows of a workgroup
+void launch_rotary(int dtype, const RotaryArgs &A, const TreeDepths *depths, hipStream_t st);
+
+struct AppendArgs {
+  PagedPool pool;
+  Rotation rotation;
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t table_pages;
+  const int32_t *ctx_len, *row_count;
+  const uint16_t *k, *v, *q;
+  uint16_t *q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  int32_t B, R, Hq, D;
+  int32_t blocks;  // of a sequence that rows may touch (set by the host)
+};
+constexpr int kAppendThreads = 256;
+inline int64_t append_blocks(int64_t R, int block) { return (R + block - 2) / block + 1; }
+void launch_append(int dtype, bool f8, const AppendArgs &A, const TreeDepths *depths, hipStream_t st);
+
+struct CommitArgs {
+  PagedPool pool;
+  int64_t layer_bytes, layer_scales;
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t table_pages;
+  const int32_t *ctx_len, *nodes, *n_accepted;
+  int64_t nodes_stride;
+  int32_t max_nodes, B, R, D, layers;
+  int32_t *new_len;
+};
+constexpr int kCommitThreads = 256;
+void launch_commit(bool f8, const CommitArgs &A, hipStream_t st);
+
+// Attention over pages: the plan, the ranges and the join of AttendArgs.
+struct PagedAttendArgs : AttendJoin {
+  PagedPool pool;  // (const here)
+  const uint16_t *q;
+  int64_t q_row_stride;
+  const int32_t *table, *prefix_table;
+  int64_t table_stride;
+  int32_t n;  // query heads of a kv head
+  int32_t P;
+  int32_t prefix_chunk, prefix_items;
+  int32_t own_parts, own_tiles;
+  int32_t negate;
+};
+void launch_paged_attend(int dtype, bool f8, int D, const PagedAttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st);
 
 // Launches the GEMMs of two problems (target rows, draft rows) as one grid.
 void launch_lm_gemm(LmGemmArgs A0, LmGemmArgs A1, hipStream_t st);

@@ -43,6 +43,7 @@ from .verify import (
     hierarchy_three_stage,
 )
 from .operators import row_paths, adjust_logits, lmhead_quant, attention
+from . import cache
 
 __all__ = [
     "philox4x64_10",
@@ -66,4 +67,5 @@ __all__ = [
     "adjust_logits",
     "lmhead_quant",
     "attention",
+    "cache",
 ]

@@ -1,0 +1,46 @@
+"""The paged cache's ABI (include/sv_cache.h): every declared function is
+exported and bound, and links from C11, whose host-only results equal those
+the Python side gets through ctypes; no GPU is needed."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from draft_token_verification_06_amd import _lib
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "draft_token_verification_06_amd")
+ROCM_INCLUDE = "/opt/rocm/include"
+
+
+def _declared():
+    text = open(os.path.join(ROOT, "include", "sv_cache.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    return set(re.findall(r"\b(sv_[a-z_]+)\s*\(", text))
+
+
+def test_every_declared_function_is_exported_and_bound():
+    L = _lib.lib()
+    assert _declared() == set(_lib.CACHE_EXPORTED)
+    for name in _declared():
+        assert hasattr(L, name), name
+
+
+def test_c_client(tmp_path):
+    gcc = shutil.which("gcc")
+    if not gcc or not os.path.isdir(ROCM_INCLUDE) or not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("needs gcc, the ROCm headers and the built library")
+    exe = str(tmp_path / "client")
+    subprocess.run([gcc, "-std=c11", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I", ROCM_INCLUDE,
+                    "-I", os.path.join(ROOT, "include"), os.path.join(ROOT, "tests", "cache_abi_client.c"), "-o", exe,
+                    "-L", PKG, "-lspecverify", f"-Wl,-rpath,{PKG}"], check=True, capture_output=True, text=True)
+    run = subprocess.run([exe], check=True, capture_output=True, text=True, timeout=120)
+    got = [line.split(" ", 1) for line in run.stdout.splitlines()]
+    assert {v.split()[0] for k, v in got if k == "linked" and v.split()[1] == "1"} == _declared()
+    got = {k: int(v) for k, v in got if k != "linked"}
+    assert got == {"turns": 0, "quarter": 1, "back": 1, "struct_bytes": ctypes.sizeof(_lib.PagedCacheArgs),
+                   "attention_ws": _lib.lib().sv_paged_attention_workspace(64, 9, 32, 8, 128, 8192, 1024), "attention_ws_bad": 0,
+                   "rotary_null": -1, "append_null": -1, "attention_null": -1, "commit_null": -1}

@@ -1,0 +1,164 @@
+"""Rotary positions on the GPU against the float64 definition.
+
+Tolerance.  Cosines and sines carry half a float32 step each, a product and the
+fused multiply-add half a step each, the storage type's rounding h half steps of
+the result; the float64 angle itself is off by 2^-52 of its size in the oracle
+(as is the frequency that both are given):
+  |out - exact| <= m (|a| + |b|) (3 * 2^-24 + 2^-51 |angle|) + h |out| + the type's least number / 2."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_06_amd as sv
+from draft_token_verification_06_amd import synth
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+LEAST = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -24}
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def check(got, x, pos, f, dtype, *, interleaved=False, magnitude=1.0, inverse=False):
+    """One sequence's rows (R, H, D)."""
+    want = oc.rotate(x, pos, f, interleaved=interleaved, magnitude=magnitude, inverse=inverse)
+    n = len(f)
+    a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    size = np.zeros_like(want)
+    angle = np.abs(np.asarray(pos, dtype=np.float64))[:, None, None] * np.abs(np.array(f))
+    pair = (np.abs(x[..., a]) + np.abs(x[..., b])) * abs(magnitude) * (3 * 2.0 ** -24 + 2.0 ** -51 * angle)
+    size[..., a] = size[..., b] = pair
+    tol = size * (1 + 2.0 ** -6) + HALF[dtype] * np.abs(want) + LEAST[dtype] / 2
+    err = np.abs(got - want)
+    assert (err <= tol).all(), float((err / np.maximum(tol, 1e-300)).max())
+    assert np.array_equal(got[..., 2 * n:], x[..., 2 * n:])
+
+
+CASES = [
+    # B, R, H, D, rot, interleaved, dtype, positions up to
+    (1, 1, 1, 16, 16, False, "f32", 3),
+    (1, 1, 1, 64, 64, True, "bf16", 0),
+    (2, 9, 4, 128, 128, False, "bf16", 5000),
+    (3, 5, 7, 80, 32, False, "f16", 1 << 20),
+    (2, 17, 3, 96, 96, True, "f32", 1 << 20),
+    (2, 3, 5, 256, 64, True, "bf16", 1000),
+    (1, 33, 2, 512, 512, False, "f16", 77),
+    (2, 3, 1, 112, 48, True, "f16", -900),
+    (5, 7, 2, 64, 16, False, "f32", 1 << 26),
+    (2, 5, 3, 80, 40, False, "bf16", 4000),
+    (3, 17, 2, 80, 20, True, "f16", 4000),
+    (1, 2, 5, 48, 2, False, "f32", 100),
+    (2, 3, 1, 160, 158, False, "f16", 100),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("in_place", [False, True])
+def test_against_definition(case, in_place):
+    B, R, H, D, rot, inter, dtype, far = case
+    print("rotary", case, in_place, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(R * D)
+    x = (torch.randn(B, R, H, D, generator=g, device=DEV) * 3).to(DT[dtype])
+    f, m = sv.rotary_frequencies(rot, scaling="ramp", factor=8.0)
+    turns = sv.rotary_turns(f, DEV)
+    pos = torch.arange(B, device=DEV) * (far // max(B, 1)) + far // 3
+    before = x.clone()
+    out = sv.rotary(x, turns, pos, interleaved=inter, magnitude=m, out=x if in_place else None)
+    torch.cuda.synchronize()
+    assert in_place or torch.equal(x, before)
+    for b in range(B):
+        check(host(out[b]), host(before[b]), int(pos[b]) + np.arange(R), f, dtype, interleaved=inter, magnitude=m)
+
+
+def test_tree_rows_stand_at_their_depth():
+    parent = list(synth.bfs_tree((3, 2, 2)))
+    R = len(parent)
+    x = torch.randn(2, R, 3, 64, device=DEV)
+    f, _ = sv.rotary_frequencies(64)
+    turns = sv.rotary_turns(f, DEV)
+    pos = torch.tensor([11, 4000], device=DEV)
+    out = sv.rotary(x, turns, pos, parent=parent)
+    for b in range(2):
+        check(host(out[b]), host(x[b]), int(pos[b]) + np.array(oc.depths(R, parent)), f, "f32")
+
+
+def test_row_count_strides_and_no_positions():
+    """Rows of a wider projection into another layout; rows behind a sequence's last stay."""
+    wide = torch.randn(3, 6, 10, 32, device=DEV).to(torch.float16)
+    x = wide[:, :, 2:7]
+    room = torch.full((3, 6, 8, 32), 9.0, dtype=torch.float16, device=DEV)
+    out = room[:, :, :5]
+    f, _ = sv.rotary_frequencies(32)
+    rows = torch.tensor([0, 4, 99], dtype=torch.int32, device=DEV)
+    sv.rotary(x, sv.rotary_turns(f, DEV), None, row_count=rows, out=out)
+    torch.cuda.synchronize()
+    assert (room[:, :, 5:] == 9).all() and (room[0] == 9).all() and (room[1, 4:] == 9).all()
+    for b, n in ((1, 4), (2, 6)):
+        check(host(out[b, :n]), host(x[b, :n]), np.arange(n), f, "f16")
+
+
+def test_gradient():
+    """The inverse with the same magnitude is the transpose: by the formula, and by differences."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x, w = (torch.randn(2, 3, 2, 32, generator=g, device=DEV) for _ in range(2))
+    f, _ = sv.rotary_frequencies(16)
+    turns = sv.rotary_turns(f, DEV)
+    pos = torch.tensor([100, 7], device=DEV)
+    for inter in (False, True):
+        kw = dict(interleaved=inter, magnitude=1.25)
+        grad = sv.rotary(w, turns, pos, inverse=True, **kw)
+        for b in range(2):
+            check(host(grad[b]), host(w[b]), int(pos[b]) + np.arange(3), f, "f32", inverse=True, **kw)
+        for at in ((0, 0, 0, 0), (1, 2, 1, 9), (0, 1, 0, 15), (1, 0, 1, 31)):
+            step = torch.zeros_like(x)
+            step[at] = 0.5
+            up, down = (sv.rotary(x + s * step, turns, pos, **kw).double() for s in (1, -1))
+            slope = float(((up - down) * w.double()).sum())
+            # the operator is linear: what is left are roundings of x + step and of the outputs
+            size = float((up.abs() * w.abs()).sum())
+            assert abs(slope - float(grad[at])) <= 16 * 2.0 ** -24 * size
+
+
+def test_far_positions_keep_their_phase():
+    """At position 2^40 the turns' own product is the definition."""
+    f = [1.0, 0.37, 1e-3, 3e-5, 2.0, 0.011, 0.9, 0.05]
+    turns = sv.rotary_turns(f, DEV)
+    x = torch.zeros(1, 2, 1, 16, device=DEV)
+    x[..., :8] = 1
+    base = (1 << 40) + 12345
+    out = host(sv.rotary(x, turns, torch.tensor([base], device=DEV)))[0]
+    units = [t % (1 << 64) for t in turns.tolist()]
+    for r in range(2):
+        for i, u in enumerate(units):
+            t = 2 * math.pi * (((base + r) * u) % (1 << 64)) / 2.0 ** 64
+            assert abs(out[r, 0, i] - math.cos(t)) <= 2.0 ** -23 and abs(out[r, 0, 8 + i] - math.sin(t)) <= 2.0 ** -23
+
+
+def test_values_that_are_no_numbers_stay_in_their_pair():
+    x = torch.ones(1, 1, 2, 32, device=DEV)
+    x[0, 0, 0, 3] = float("nan")
+    x[0, 0, 1, 20] = float("inf")
+    out = sv.rotary(x, sv.rotary_turns(sv.rotary_frequencies(32)[0], DEV), torch.tensor([5], device=DEV))
+    bad = ~torch.isfinite(out[0, 0]).cpu()
+    want = torch.zeros(2, 32, dtype=torch.bool)
+    want[0, 3] = want[0, 19] = want[1, 4] = want[1, 20] = True
+    assert torch.equal(bad, want)
+
+
+def test_refusals_on_the_device():
+    x = torch.zeros(2, 3, 2, 32, device=DEV)
+    turns = sv.rotary_turns(sv.rotary_frequencies(32)[0], DEV)
+    for kw in (dict(x=x.double()), dict(x=x[..., :24]), dict(turns=None), dict(turns=turns.float()), dict(base_pos=torch.zeros(3, dtype=torch.int64, device=DEV)),
+               dict(base_pos=torch.zeros(2, dtype=torch.int32, device=DEV)), dict(out=x[:, :, :1]), dict(out=x.half()), dict(x=x.transpose(1, 2)),
+               dict(parent=[-1, 0]), dict(turns=torch.zeros(17, dtype=torch.int64, device=DEV))):
+        a = dict(x=x, turns=turns, base_pos=None)
+        a.update(kw)
+        with pytest.raises((ValueError, sv.SvError)):
+            sv.rotary(a.pop("x"), a.pop("turns"), a.pop("base_pos"), **a)
