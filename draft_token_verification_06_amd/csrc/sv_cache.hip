@@ -156,7 +156,7 @@ namespace {
 template <class... Tree>
 __device__ __forceinline__ int rotary_angles(const RotaryArgs &A, int64_t row0, float2 *s_cs, const Tree &...tree) {
   const Rotation &T = A.rotation;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kRotaryTokens), A.rows - row0));
+  const int rows = static_cast<int>(min(static_cast<int64_t>(A.group), A.rows - row0));
   const int half = T.rot / 2;
   for (int e = threadIdx.x; e < rows * half; e += kRotaryThreads) {
     const int64_t row = row0 + e / half;
@@ -182,9 +182,9 @@ template <int DT> __device__ __forceinline__ void store_value(char *row, int i, 
 
 template <int DT, class... Tree>
 __global__ void __launch_bounds__(kRotaryThreads) k_rotary(RotaryArgs A, Tree... tree) {
-  extern __shared__ float2 s_cs[];  // [kRotaryTokens][rot / 2]
+  extern __shared__ float2 s_cs[];  // [group][rot / 2]
   const Rotation &T = A.rotation;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRotaryTokens;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * A.group;
   const int rows = rotary_angles(A, row0, s_cs, tree...);
   const int half = T.rot / 2;
   constexpr int EB = Elt<DT>::kBytes, EPV = Elt<DT>::kEPV;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kRotaryThreads) k_rotary(RotaryArgs A, Tree...
 template <int DT, class... Tree>
 __global__ void __launch_bounds__(kRotaryThreads) k_rotary_pairs(RotaryArgs A, Tree... tree) {
   extern __shared__ float2 s_cs[];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRotaryTokens;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * A.group;
   const int rows = rotary_angles(A, row0, s_cs, tree...);
   constexpr int EB = Elt<DT>::kBytes;
   const int half = A.rotation.rot / 2, pairs = A.in_place ? half : A.D / 2;
@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kRotaryThreads) k_rotary_pairs(RotaryArgs A, T
 namespace {
 
 // Lanes of a wave on a block: D / 16 lanes per token, so many tokens a pass.
+// Kernels are built for 1, 2, 4 or 8 passes (registers are what a wave holds).
 template <int D> constexpr int kUnits = D / 16;
 template <int D> constexpr int kPassTokens = 64 / kUnits<D>;
-template <int D> constexpr int kPasses = 64 / kPassTokens<D>;
 
 // The largest of the wave's (non-negative) values, in every lane.
 __device__ __forceinline__ float wave_max(float v) {
@@ -281,13 +281,13 @@ __device__ __forceinline__ float wave_max(float v) {
 // The wave's values y (pass p, token p T + lane / units, 16 of it) whose bit in
 // `live` is set, to the block at `block` (token 0, this head): token u goes to
 // place u + shift.  Places below `first` hold earlier tokens, scaled by *scale.
-template <int D>
-__device__ void store_f8(const float (&y)[kPasses<D>][16], uint32_t live, int shift, int first, uint8_t *block, int64_t token_bytes,
-                         float *scale, int2 piece) {
+template <int D, int kP>
+__device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live, int shift, int first, uint8_t *block,
+                                         int64_t token_bytes, float *scale, int2 piece) {
   const int lane = threadIdx.x & 63, t_lane = lane / kUnits<D>;
   float a = 0.0f;
 #pragma unroll
-  for (int p = 0; p < kPasses<D>; ++p)
+  for (int p = 0; p < kP; ++p)
     if (live >> p & 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) a = fmaxf(a, finite(y[p][i]) ? fabsf(y[p][i]) : 0.0f);
@@ -295,7 +295,7 @@ __device__ void store_f8(const float (&y)[kPasses<D>][16], uint32_t live, int sh
   float base = kF8LeastScale;
   bool earlier = false;
   if (first > 0) {
-    const float s0 = *scale;
+    const float s0 = read_lane_f32(*scale, 0);  // (the same in every lane: decisions on it are scalar)
     earlier = s0 > 0.0f && finite(s0);
     if (earlier) base = s0;
   }
@@ -324,20 +324,27 @@ __device__ void store_f8(const float (&y)[kPasses<D>][16], uint32_t live, int sh
     }
   }
   if (lane == 0 && (!earlier || j > 0)) *scale = now;
-  // a power of two (anything but a scale of the caller's own) divides exactly as its inverse
-  const bool exact = (__float_as_uint(now) & 0x7FFFFF) == 0 && now >= 0x1p-126f;
+  // A power of two (anything but a scale of the caller's own) divides exactly as
+  // its inverse; other quotients are formed one by one.
+  const bool exact = __builtin_amdgcn_readfirstlane((__float_as_uint(now) & 0x7FFFFF) == 0 && now >= 0x1p-126f);
   const float inverse = 1.0f / now;
 #pragma unroll
-  for (int p = 0; p < kPasses<D>; ++p) {
+  for (int p = 0; p < kP; ++p) {
     if (!(live >> p & 1)) continue;
+    float x[16];
+    if (exact) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = y[p][i] * inverse;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = y[p][i] / now;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = exact ? y[p][4 * i + k] * inverse : y[p][4 * i + k] / now;
-      w[i] = pack_f8(x[0], x[1], x[2], x[3]);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = pack_f8(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     uint8_t *at = block + (p * kPassTokens<D> + t_lane + shift) * token_bytes;
     *reinterpret_cast<uint2 *>(at + piece.x * 8) = make_uint2(w[0], w[1]);
     *reinterpret_cast<uint2 *>(at + piece.y * 8) = make_uint2(w[2], w[3]);
@@ -350,9 +357,16 @@ __device__ void store_f8(const float (&y)[kPasses<D>][16], uint32_t live, int sh
 // Appending.  A workgroup takes the rows that fall into one block of one
 // sequence; its waves take heads in turn: keys, values, queries.
 // ---------------------------------------------------------------------------
-template <int DT, bool F8, int D, class... Tree>
-__global__ void __launch_bounds__(kAppendThreads, 2) k_append(AppendArgs A, Tree... tree) {
-  extern __shared__ float2 s_cs[];  // [block][rot / 2], then what float32 leaves of them (8-bit pages)
+namespace {
+// Angles of a row in LDS: two more than there are, so that rows begin 16 bytes
+// apart in the banks and the lanes of a pass, 64 bytes apart, do not meet.
+__host__ __device__ constexpr int append_row_angles(int rot) { return rot / 2 + 2; }
+}  // namespace
+
+template <int DT, bool F8, int D, int kP, class... Tree>
+__global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4) k_append(AppendArgs A, Tree... tree) {
+  // [tokens][row_angles], then what float32 leaves of them (8-bit pages)
+  extern __shared__ __attribute__((aligned(16))) float2 s_cs[];
   const Rotation &T = A.rotation;
   const int b = blockIdx.x / A.blocks;
   const int ctx = A.ctx_len[b];
@@ -366,19 +380,21 @@ __global__ void __launch_bounds__(kAppendThreads, 2) k_append(AppendArgs A, Tree
   const int row0 = static_cast<int>(slot0 - ctx);  // row of the block's first token (negative where it is an earlier one)
   const int page = A.table[b * A.table_stride + (slot0 >> A.pool.page_shift)];
   const int half = T.rot / 2;
-  float2 *s_lo = s_cs + block * half;
+  const int row_angles = append_row_angles(T.rot);
+  float2 *s_lo = s_cs + min(A.R, block) * row_angles;
   const int64_t pos0 = T.base_pos ? T.base_pos[b] : ctx;
   for (int e = threadIdx.x; e < (t1 - t0) * half; e += kAppendThreads) {
     const int t = t0 + e / half, i = e % half;
     float2 lo;
-    angle(T, pos0 + row_depth(row0 + t, tree...), i, &s_cs[t * half + i], &lo);
-    if (F8) s_lo[t * half + i] = lo;
+    const int at = (t - t0) * row_angles + i;
+    angle(T, pos0 + row_depth(row0 + t, tree...), i, &s_cs[at], &lo);
+    if (F8) s_lo[at] = lo;
   }
   __syncthreads();
 
-  constexpr int kU = kUnits<D>, kT = kPassTokens<D>, kP = kPasses<D>;
+  constexpr int kU = kUnits<D>, kT = kPassTokens<D>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int j = lane % kU, t_lane = lane / kU;
+  const int j = lane % kU, t_lane = t0 + lane / kU;  // (passes begin at the first row)
   const int2 piece = unit_pieces(T, j);
   const bool turned = j < T.rot / 16;
   const int heads = A.pool.Hkv;
@@ -391,54 +407,67 @@ __global__ void __launch_bounds__(kAppendThreads, 2) k_append(AppendArgs A, Tree
     const int h = query ? task - 2 * heads : value ? task - heads : task;
     const uint16_t *x = query ? A.q : value ? A.v : A.k;
     const int64_t stride = query ? A.q_stride : value ? A.v_stride : A.k_stride;
-    uint4 ra[kP], rb[kP];
-    uint32_t live = 0;
+    constexpr int kG = kP < 4 ? kP : 4;  // passes loaded together
+    uint4 ra[kG], rb[kG];
+    auto fetch = [&](int p0) {
 #pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      const int t = p * kT + t_lane;
-      if (t >= t0 && t < t1) {
-        live |= 1u << p;
+      for (int p = 0; p < kG; ++p) {
+        const int t = (p0 + p) * kT + t_lane;
+        if (t >= t1) continue;
         const uint16_t *row = x + (seq_row + t) * stride + h * D;
         ra[p] = load_vec(row + piece.x * 8);
         rb[p] = load_vec(row + piece.y * 8);
       }
-    }
+    };
     if (F8 && !query) {
       float y[kP][16];
+      uint32_t live = 0;
 #pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        if (!(live >> p & 1)) continue;
-        Elt<DT>::vec(ra[p], y[p]);
-        Elt<DT>::vec(rb[p], y[p] + 8);
-        const int at = (p * kT + t_lane) * half + j * 8;
-        if (!value && turned) turn_unit_odd(T.interleaved, s_cs + at, s_lo + at, y[p], y[p] + 8);
+      for (int p0 = 0; p0 < kP; p0 += kG) {
+        fetch(p0);
+#pragma unroll
+        for (int p = p0; p < p0 + kG; ++p) {
+          const int t = p * kT + t_lane;
+          if (t < t1) {
+            live |= 1u << p;
+            Elt<DT>::vec(ra[p - p0], y[p]);
+            Elt<DT>::vec(rb[p - p0], y[p] + 8);
+            const int at = (t - t0) * row_angles + j * 8;
+            if (!value && turned) turn_unit_odd(T.interleaved, s_cs + at, s_lo + at, y[p], y[p] + 8);
+          }
+          __builtin_amdgcn_sched_barrier(0);  // one pass's float64 values at a time
+        }
       }
       uint8_t *dst = (value ? A.pool.v : A.pool.k) + page * A.pool.page_bytes + in_page * A.pool.token_bytes + h * A.pool.head_bytes;
       const int64_t at = ((static_cast<int64_t>(page) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * heads + h;
-      store_f8<D>(y, live, 0, t0, dst, A.pool.token_bytes, (value ? A.pool.v_scale : A.pool.k_scale) + at, piece);
+      store_f8<D, kP>(y, live, t0, t0, dst, A.pool.token_bytes, (value ? A.pool.v_scale : A.pool.k_scale) + at, piece);
       continue;
     }
 #pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      if (!(live >> p & 1)) continue;
-      const int t = p * kT + t_lane;
-      if (!value && turned) {
-        float v[16];
-        Elt<DT>::vec(ra[p], v);
-        Elt<DT>::vec(rb[p], v + 8);
-        turn_unit(T.interleaved, s_cs + t * half + j * 8, v, v + 8);
-        ra[p] = pack8<DT>(v);
-        rb[p] = pack8<DT>(v + 8);
+    for (int p0 = 0; p0 < kP; p0 += kG) {
+      fetch(p0);
+#pragma unroll
+      for (int p = 0; p < kG; ++p) {
+        const int t = (p0 + p) * kT + t_lane;
+        if (t >= t1) continue;
+        if (!value && turned) {
+          float v[16];
+          Elt<DT>::vec(ra[p], v);
+          Elt<DT>::vec(rb[p], v + 8);
+          turn_unit(T.interleaved, s_cs + (t - t0) * row_angles + j * 8, v, v + 8);
+          ra[p] = pack8<DT>(v);
+          rb[p] = pack8<DT>(v + 8);
+        }
+        uint16_t *out;
+        if (query) {
+          out = A.q_out + (seq_row + t) * A.q_out_stride + h * D;
+        } else {
+          uint8_t *dst = (value ? A.pool.v : A.pool.k) + page * A.pool.page_bytes + (in_page + t) * A.pool.token_bytes + h * A.pool.head_bytes;
+          out = reinterpret_cast<uint16_t *>(dst);
+        }
+        *reinterpret_cast<uint4 *>(out + piece.x * 8) = ra[p];
+        *reinterpret_cast<uint4 *>(out + piece.y * 8) = rb[p];
       }
-      uint16_t *out;
-      if (query) {
-        out = A.q_out + (seq_row + t) * A.q_out_stride + h * D;
-      } else {
-        uint8_t *dst = (value ? A.pool.v : A.pool.k) + page * A.pool.page_bytes + (in_page + t) * A.pool.token_bytes + h * A.pool.head_bytes;
-        out = reinterpret_cast<uint16_t *>(dst);
-      }
-      *reinterpret_cast<uint4 *>(out + piece.x * 8) = ra[p];
-      *reinterpret_cast<uint4 *>(out + piece.y * 8) = rb[p];
     }
   }
 }
@@ -461,9 +490,9 @@ __device__ __forceinline__ int path_length(const CommitArgs &A, int b, int ctx) 
 
 }  // namespace
 
-template <bool F8, int D>
-__global__ void __launch_bounds__(kCommitThreads, 2) k_commit(CommitArgs A) {
-  constexpr int kU = kUnits<D>, kT = kPassTokens<D>, kP = kPasses<D>;
+template <bool F8, int D, int kP>
+__global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
+  constexpr int kU = kUnits<D>, kT = kPassTokens<D>;
   const int lane = threadIdx.x & 63;
   const int j = lane % kU, t_lane = lane / kU;
   const int heads = A.pool.Hkv;
@@ -544,7 +573,7 @@ __global__ void __launch_bounds__(kCommitThreads, 2) k_commit(CommitArgs A) {
         if (t >= 0 && t < block) here |= live & 1u << p;
       }
       if (!__any(here != 0)) continue;
-      store_f8<D>(y, here, first - slot0, max(first - slot0, 0), token(to, slot0), A.pool.token_bytes, scale_at(to, slot0),
+      store_f8<D, kP>(y, here, first - slot0, max(first - slot0, 0), token(to, slot0), A.pool.token_bytes, scale_at(to, slot0),
                   make_int2(2 * j, 2 * j + 1));
     }
   }
@@ -561,9 +590,12 @@ __global__ void __launch_bounds__(64) k_advance(CommitArgs A) {
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-void launch_rotary(int dtype, const RotaryArgs &A, const TreeDepths *depths, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((A.rows + kRotaryTokens - 1) / kRotaryTokens)), threads(kRotaryThreads);
-  const unsigned lds = kRotaryTokens * (A.rotation.rot / 2) * sizeof(float2);
+void launch_rotary(int dtype, RotaryArgs A, const TreeDepths *depths, hipStream_t st) {
+  // few rows: a workgroup each, as long as that fills no more than the chip
+  A.group = kRotaryTokens;
+  while (A.group > 1 && A.rows / A.group < 1024) A.group /= 2;
+  const dim3 grid(static_cast<unsigned>((A.rows + A.group - 1) / A.group)), threads(kRotaryThreads);
+  const unsigned lds = A.group * (A.rotation.rot / 2) * sizeof(float2);
   auto go = [&](auto plain, auto tree) {
     if (depths) hipLaunchKernelGGL(tree, grid, threads, lds, st, A, *depths);
     else hipLaunchKernelGGL(plain, grid, threads, lds, st, A);
@@ -581,16 +613,26 @@ void launch_rotary(int dtype, const RotaryArgs &A, const TreeDepths *depths, hip
 
 namespace {
 
-template <int DT, bool F8, int D>
-void launch_append_shape(const AppendArgs &A, const TreeDepths *depths, hipStream_t st) {
+template <int DT, bool F8, int D, int kP>
+void launch_append_passes(const AppendArgs &A, const TreeDepths *depths, hipStream_t st) {
   const int64_t x = static_cast<int64_t>(A.B) * A.blocks;
   const int64_t tasks = (2 * A.pool.Hkv + A.Hq + kAppendThreads / 64 - 1) / (kAppendThreads / 64);
   // few blocks: their heads are spread over workgroups (each forms the block's angles again)
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(tasks, 2048 / x));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y)), threads(kAppendThreads);
-  const unsigned lds = (1u << A.pool.block_shift) * (A.rotation.rot / 2) * sizeof(float2) * (F8 ? 2 : 1);
-  if (depths) hipLaunchKernelGGL((k_append<DT, F8, D, TreeDepths>), grid, threads, lds, st, A, *depths);
-  else hipLaunchKernelGGL((k_append<DT, F8, D>), grid, threads, lds, st, A);
+  const unsigned lds = std::min(A.R, 1 << A.pool.block_shift) * append_row_angles(A.rotation.rot) * sizeof(float2) * (F8 ? 2 : 1);
+  if (depths) hipLaunchKernelGGL((k_append<DT, F8, D, kP, TreeDepths>), grid, threads, lds, st, A, *depths);
+  else hipLaunchKernelGGL((k_append<DT, F8, D, kP>), grid, threads, lds, st, A);
+}
+
+// Passes over what a block can hold of a call's rows.
+template <int DT, bool F8, int D>
+void launch_append_shape(const AppendArgs &A, const TreeDepths *depths, hipStream_t st) {
+  const int tokens = std::min(A.R, 1 << A.pool.block_shift);
+  if (tokens <= kPassTokens<D>) launch_append_passes<DT, F8, D, 1>(A, depths, st);
+  else if (tokens <= 2 * kPassTokens<D>) launch_append_passes<DT, F8, D, 2>(A, depths, st);
+  else if (D == 64 || tokens <= 4 * kPassTokens<D>) launch_append_passes<DT, F8, D, 4>(A, depths, st);
+  else launch_append_passes<DT, F8, D, D == 64 ? 4 : 8>(A, depths, st);
 }
 
 template <int DT, bool F8>
@@ -611,19 +653,34 @@ void launch_append(int dtype, bool f8, const AppendArgs &A, const TreeDepths *de
   }
 }
 
+namespace {
+
+template <bool F8, int D, int kP>
+void launch_commit_passes(const CommitArgs &A, hipStream_t st) {
+  const int64_t groups = (2 * A.pool.Hkv + kCommitThreads / 64 - 1) / (kCommitThreads / 64);
+  hipLaunchKernelGGL((k_commit<F8, D, kP>), dim3(static_cast<unsigned>(groups * A.B * A.layers)), dim3(kCommitThreads), 0, st, A);
+}
+
+template <bool F8, int D>
+void launch_commit_shape(const CommitArgs &A, hipStream_t st) {
+  if (A.max_nodes <= kPassTokens<D>) launch_commit_passes<F8, D, 1>(A, st);
+  else if (A.max_nodes <= 2 * kPassTokens<D>) launch_commit_passes<F8, D, 2>(A, st);
+  else launch_commit_passes<F8, D, D == 64 ? 4 : 8>(A, st);
+}
+
+}  // namespace
+
 void launch_commit(bool f8, const CommitArgs &A, hipStream_t st) {
   const bool in_place = A.new_len == A.ctx_len;
   if (A.nodes) {
     CommitArgs M = A;
     if (in_place) M.new_len = nullptr;
-    const int64_t groups = (2 * A.pool.Hkv + kCommitThreads / 64 - 1) / (kCommitThreads / 64);
-    const dim3 grid(static_cast<unsigned>(groups * A.B * A.layers)), threads(kCommitThreads);
     if (f8) {
-      if (A.D == 64) hipLaunchKernelGGL((k_commit<true, 64>), grid, threads, 0, st, M);
-      else hipLaunchKernelGGL((k_commit<true, 128>), grid, threads, 0, st, M);
+      if (A.D == 64) launch_commit_shape<true, 64>(M, st);
+      else launch_commit_shape<true, 128>(M, st);
     } else {
-      if (A.D == 64) hipLaunchKernelGGL((k_commit<false, 64>), grid, threads, 0, st, M);
-      else hipLaunchKernelGGL((k_commit<false, 128>), grid, threads, 0, st, M);
+      if (A.D == 64) launch_commit_shape<false, 64>(M, st);
+      else launch_commit_shape<false, 128>(M, st);
     }
   }
   if (A.new_len && (in_place || !A.nodes)) hipLaunchKernelGGL(k_advance, dim3((A.B + 63) / 64), dim3(64), 0, st, A);

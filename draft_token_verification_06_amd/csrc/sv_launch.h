@@ -211,10 +211,11 @@ struct RotaryArgs {
   const int32_t *row_count;
   int32_t R, H, D, in_place;
   int64_t rows;  // B * R
+  int32_t group; // rows of a workgroup (set by the launcher)
 };
 constexpr int kRotaryThreads = 256;
-constexpr int kRotaryTokens = 16;  // rows of a workgroup
-void launch_rotary(int dtype, const RotaryArgs &A, const TreeDepths *depths, hipStream_t st);
+constexpr int kRotaryTokens = 16;  // rows of a workgroup, at most
+void launch_rotary(int dtype, RotaryArgs A, const TreeDepths *depths, hipStream_t st);
 
 struct AppendArgs {
   PagedPool pool;
