@@ -849,6 +849,14 @@ bool table_ok(const int32_t *table, int64_t *stride, int32_t table_pages, int32_
   return B == 1 || *stride >= table_pages;
 }
 
+// False for sizes outside the rules; else their plan.
+bool paged_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, PagedPlan *L) {
+  AttendPlan same;  // the rules are sv_attention's
+  if (!attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &same)) return false;
+  *L = plan_paged(B, R, Hq, Hkv, D, P, max_ctx);
+  return L->prefix_items <= INT32_MAX && grid_fits(L->prefix_items + L->own_blocks, 1024);
+}
+
 // Depths of a valid tree's nodes.
 int tree_depths(const int32_t *parent, int32_t N, TreeDepths *out) {
   TreeMeta meta;
@@ -1022,8 +1030,8 @@ int sv_cache_commit(const sv_paged_cache *cache, int32_t layers, int64_t layer_s
 }
 
 size_t sv_paged_attention_workspace(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
-  AttendPlan L;
-  return attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &L) ? L.total : 0;
+  PagedPlan L;
+  return paged_plan(B, R, Hq, Hkv, D, P, max_ctx, &L) ? L.total : 0;
 }
 
 int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_paged_cache *cache,
@@ -1037,8 +1045,8 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
   sv_paged_cache c;
   const int cst = cache_pool(cache, dtype, &c, &A.pool);
   if (cst != SV_OK) return cst;
-  AttendPlan L;
-  if (!attention_plan(B, R, Hq, c.Hkv, c.D, P, max_ctx, &L)) return SV_EINVAL;
+  PagedPlan L;
+  if (!paged_plan(B, R, Hq, c.Hkv, c.D, P, max_ctx, &L)) return SV_EINVAL;
   TreeParents parents;
   if (parent_host) {
     const int tst = tree_parents(parent_host, R, &parents);
@@ -1073,6 +1081,7 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
   A.own_parts = L.own_parts;
   A.split = L.split;
   A.own_tiles = L.own_tiles;
+  A.direct = L.direct;
   // never zero: masked products are -inf, and 0 * -inf is no number
   A.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
   A.negate = scale < 0.0f;

@@ -435,18 +435,6 @@ __global__ void __launch_bounds__(256) k_attend_combine(AttendJoin A) {
   if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L * (AtElt<DT>::kLift > 0 ? 0x1p-15f : 1.0f))) * 0.6931471805599453f;
 }
 
-void launch_attend_join(int dtype, int D, const AttendJoin &A, hipStream_t st) {
-  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4)), threads(256);
-  if (dtype == DT_BF16) {
-    if (D == 64) hipLaunchKernelGGL((k_attend_combine<DT_BF16, 64>), grid, threads, 0, st, A);
-    else hipLaunchKernelGGL((k_attend_combine<DT_BF16, 128>), grid, threads, 0, st, A);
-  } else {
-    if (D == 64) hipLaunchKernelGGL((k_attend_combine<DT_F16, 64>), grid, threads, 0, st, A);
-    else hipLaunchKernelGGL((k_attend_combine<DT_F16, 128>), grid, threads, 0, st, A);
-  }
-}
-
 namespace {
 
 template <int DT, int D, int WQP, int WQO>
@@ -475,7 +463,9 @@ void launch_type(const AttendArgs &A, const TreeParents *parents, const AttendPl
     launch_own<DT, D, 4>(A, parents, P, grid, st);
   else
     launch_own<DT, D, 1>(A, parents, P, grid, st);
-  launch_attend_join(DT, D, A, st);
+  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  hipLaunchKernelGGL((k_attend_combine<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st,
+                     static_cast<const AttendJoin &>(A));
 }
 
 }  // namespace

@@ -182,7 +182,6 @@ struct AttendArgs : AttendJoin {
   int32_t negate;    // the scale is negative
 };
 void launch_attend(int dtype, int D, const AttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st);
-void launch_attend_join(int dtype, int D, const AttendJoin &A, hipStream_t st);
 
 // The paged cache.  Strides in bytes; page and block are powers of two (tokens
 // of a page; tokens that share a scale, or are handled together in 16-bit pages).
@@ -260,8 +259,9 @@ struct PagedAttendArgs : AttendJoin {
   int32_t prefix_chunk, prefix_items;
   int32_t own_parts, own_tiles;
   int32_t negate;
+  int32_t direct;    // sequences of one range write their outputs themselves
 };
-void launch_paged_attend(int dtype, bool f8, int D, const PagedAttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st);
+void launch_paged_attend(int dtype, bool f8, int D, const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st);
 
 // Launches the GEMMs of two problems (target rows, draft rows) as one grid.
 void launch_lm_gemm(LmGemmArgs A0, LmGemmArgs A1, hipStream_t st);

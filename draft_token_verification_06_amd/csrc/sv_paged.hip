@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sv_attend.h"
 
 namespace sv {
@@ -109,6 +111,436 @@ __device__ float4 add_odd_paged(const PagedAttendArgs &A, const PagedItem &it, c
 
 }  // namespace
 
+typedef float pg_f32x4_t __attribute__((ext_vector_type(4)));
+typedef int pg_i32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) pg_i32x2_t *lds_i32x2_t;
+
+namespace {
+
+// 8 bytes as an operand of 8 values (exact).
+template <int DT> __device__ __forceinline__ uint4 widen8(uint2 raw) {
+  if constexpr (DT == DT_BF16)
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.x, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.x, 1.0f, true)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.y, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.y, 1.0f, true)));
+  else
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw.x, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw.x, 1.0f, true)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw.y, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw.y, 1.0f, true)));
+}
+
+template <int DT> __device__ __forceinline__ pg_f32x4_t mma16(uint4 a, uint4 b, pg_f32x4_t c) {
+  if constexpr (DT == DT_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(at_bf16x8_t, a), __builtin_bit_cast(at_bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(at_f16x8_t, a), __builtin_bit_cast(at_f16x8_t, b), c, 0, 0, 0);
+}
+
+// The sum / maximum over the lanes that hold one row: l ^ 32 (32 rows), and l ^ 16 (16 rows).
+template <int ROWS> __device__ __forceinline__ float row_max(float x) {
+  const float2 h = both_halves(x);
+  x = fmaxf(h.x, h.y);
+  if (ROWS == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  return x;
+}
+template <int ROWS> __device__ __forceinline__ float row_sum(float x) {
+  const float2 h = both_halves(x);
+  x = h.x + h.y;
+  if (ROWS == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return x;
+}
+
+// Bytes between rows of LDS.  Key rows of 16 bytes more put the rows that 8 lanes
+// read 16 bytes of side by side; a transposing read takes 8 rows of 16 bytes (8
+// bits: 16 bytes more) or 4 of 32 (16 bits: 32 bytes more).
+template <bool F8, int D> constexpr int few_key_pitch() { return F8 ? D + 16 : 2 * D + 16; }
+template <bool F8, int D> constexpr int few_value_pitch() { return F8 ? D + 16 : 2 * D + 32; }
+template <bool F8, int D, int ROWS, bool SHARED, int WAVES> constexpr size_t few_bytes() {
+  const size_t tile = static_cast<size_t>(SHARED ? 64 : 32 * WAVES) * (few_key_pitch<F8, D>() + few_value_pitch<F8, D>());
+  const size_t merge = SHARED ? 0 : static_cast<size_t>(WAVES) * ROWS * (64 + 4) * 4;
+  return tile > merge ? tile : merge;
+}
+
+}  // namespace
+
+// Few rows: tiles of 16 or 32 stacked rows.  Keys and values lie in LDS as the
+// pages hold them and become operands in registers.  Apart (SHARED = false): every
+// wave has blocks of 32 keys of its own for the same rows, so the waves run
+// without barriers until the end; SHARED: the workgroup's waves have rows of
+// their own and read the same 64 keys.
+//
+// The k order of a product may be any that both operands share, and so may the
+// keys' order in the score tile.  Keys are placed in LDS such that a lane's
+// exponentials belong to 8 (twice 8) consecutive keys: the operand of the second
+// product as they are, under one scale each, against values whose transposing
+// read takes 8 consecutive rows (no bank conflicts).
+template <int DT, bool F8, int D, int ROWS, bool SHARED, int WAVES>
+__device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedItem &it, char *lds, const uint32_t (*s_anc)[8],
+                                         float2 *s_ml, bool direct) {
+  using T = AtElt<DT>;
+  constexpr bool k16 = ROWS == 16;
+  constexpr int KB = SHARED ? 2 : 1;                 // blocks of 32 keys of a wave and tile
+  constexpr int KT = SHARED ? 64 : 32 * WAVES;
+  constexpr int kWaveKeys = SHARED ? KT / WAVES : 32;  // keys that a wave fetches
+  constexpr int kBytes = F8 ? 1 : 2;
+  constexpr int kChunks = D * kBytes / 16;           // 16-byte pieces of a row
+  constexpr int kWaveRows = 64 / kChunks;            // rows of one load of a wave: within a strip
+  constexpr int kLoads = kWaveKeys / kWaveRows;
+  constexpr int NK = k16 ? 8 : 16;                   // keys of a lane and block
+  constexpr int kKP = few_key_pitch<F8, D>(), kVP = few_value_pitch<F8, D>();
+  constexpr bool kRelative = F8 && T::kLift > 0;
+  static_assert(kWaveKeys % kWaveRows == 0 && kLoads >= 1, "whole loads");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & (ROWS - 1), grp = lane / ROWS;
+  char *s_k = lds + (SHARED ? 0 : wave * 32 * (kKP + kVP));
+  char *s_v = s_k + (SHARED ? KT : 32) * kKP;
+
+  // this lane's row, its query fragments
+  const int i = it.row0 + (SHARED ? wave * ROWS : 0) + col;
+  const int ic = min(i, it.rows - 1);
+  const int64_t qrow = it.base_row + ic / A.n;
+  const int head = it.kvh * A.n + ic % A.n;
+  constexpr int kSteps = D / (k16 ? 32 : 16);        // matrix steps of a score
+  uint4 qf[kSteps];
+  {
+    const uint16_t *p = A.q + qrow * A.q_row_stride + head * D;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      // 8 bits: a 16-byte read of keys is two steps' operands
+      const int d = F8 ? (s >> 1) * (k16 ? 64 : 32) + 16 * grp + 8 * (s & 1) : s * (k16 ? 32 : 16) + 8 * grp;
+      qf[s] = load_vec(p + d);
+      // a negative scale acts on the queries' signs, so that larger products are larger scores
+      if (A.negate) qf[s] = make_uint4(qf[s].x ^ 0x80008000u, qf[s].y ^ 0x80008000u, qf[s].z ^ 0x80008000u, qf[s].w ^ 0x80008000u);
+    }
+  }
+  const int r = static_cast<int>(qrow % A.R);
+
+  constexpr int kTiles = D / ROWS, kOut = k16 ? 4 : 16;  // output tiles, values of a lane in each
+  typename std::conditional<k16, pg_f32x4_t, at_f32x16_t>::type o[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int e = 0; e < kOut; ++e) o[t][e] = 0.0f;
+  float m = kNegInf, l = 0.0f;  // l: this lane's keys only
+  float ref = kRelative ? 0.0f : 1.0f;
+
+  // the strips of the look-up that begins at token c0, one per lane
+  int c0 = it.k0, pages = 0;
+  float kscale = 1.0f, vscale = 1.0f;
+  bool bad = false;
+  const int last = (it.k1 - 1) & -kStrip;
+  auto look_up = [&](int at) {
+    c0 = at;
+    const int key = min(at + lane * kStrip, last);
+    pages = it.table[key >> A.pool.page_shift];
+    if (static_cast<uint32_t>(pages) >= static_cast<uint32_t>(A.pool.num_pages)) pages = 0, bad = true;
+    if (F8) {
+      const int in_page = key & ((1 << A.pool.page_shift) - 1);
+      const int64_t s = ((static_cast<int64_t>(pages) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * A.pool.Hkv + it.kvh;
+      kscale = A.pool.k_scale[s];
+      vscale = A.pool.v_scale[s];
+    }
+  };
+  look_up(it.k0);
+
+  uint4 rk[kLoads], rv[kLoads];
+  float ks[2 * KB], vs[2 * KB], ks_next[2 * KB], vs_next[2 * KB];  // scales of this wave's strips, of the tile and of the one loaded
+  const int piece = lane % kChunks, row_lane = lane / kChunks;
+  const uint32_t lane_off = static_cast<uint32_t>(row_lane) * static_cast<uint32_t>(A.pool.token_bytes) + piece * 16;
+  const int page_mask = (1 << A.pool.page_shift) - 1;
+  const int64_t head_off = it.kvh * A.pool.head_bytes;
+  // one sequence's pages are read once: streamed
+  auto fetch = [&](const uint8_t *p) { return SHARED ? load_vec(p) : load_stream(reinterpret_cast<const uint4 *>(p)); };
+  auto load = [&](int t0) {
+    if (t0 - c0 >= kLookup) look_up(t0);
+#pragma unroll
+    for (int g = 0; g < kLoads * kWaveRows / kStrip; ++g) {
+      const int key = min(t0 + wave * kWaveKeys + g * kStrip, last);
+      const int page = __builtin_amdgcn_readlane(pages, (key - c0) / kStrip);
+      const int64_t off = page * A.pool.page_bytes + (key & page_mask) * A.pool.token_bytes + head_off;
+#pragma unroll
+      for (int x = 0; x < kStrip / kWaveRows; ++x) {
+        const int j = g * (kStrip / kWaveRows) + x;
+        rk[j] = fetch(A.pool.k + off + x * kWaveRows * A.pool.token_bytes + lane_off);
+        rv[j] = fetch(A.pool.v + off + x * kWaveRows * A.pool.token_bytes + lane_off);
+      }
+    }
+    if (F8)
+#pragma unroll
+      for (int g = 0; g < 2 * KB; ++g) {
+        const int at = (min(t0 + (SHARED ? 0 : wave * 32) + g * kStrip, last) - c0) / kStrip;
+        ks_next[g] = read_lane_f32(kscale, at);
+        vs_next[g] = read_lane_f32(vscale, at);
+      }
+  };
+  auto tile_barrier = [&]() {
+    if (SHARED) __syncthreads();
+    else __builtin_amdgcn_wave_barrier();
+  };
+  // LDS row of the tile's key: see above
+  auto key_row = [](int key) {
+    const int a = key & 31;
+    const int at = k16 ? 16 * ((a >> 2) & 1) + 4 * (a >> 3) + (a & 3) : 8 * (2 * (a >> 4) + ((a >> 2) & 1)) + 4 * ((a >> 3) & 1) + (a & 3);
+    return (key & ~31) + at;
+  };
+  bool odd = false;
+  load(it.k0);
+  for (int t0 = it.k0; t0 < it.k1; t0 += KT) {
+    const int w0 = t0 + (SHARED ? 0 : wave * 32);  // the wave's first key
+    // Keys past the range get zero values: their exponentials are zero, but
+    // zero times what a page holds behind the last token need not be.
+    // Infinities and NaN among the step's own values, which must reach only the
+    // rows that see them, are left out here and added at the end.
+    const bool masked = t0 + KT > it.draft;
+    tile_barrier();
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int at = (SHARED ? wave * kWaveKeys : 0) + j * kWaveRows + row_lane;  // key within the LDS rows
+      const int key = w0 + at;
+      uint4 v = rv[j];
+      if (t0 + KT > it.k1 && key >= it.k1) v = make_uint4(0, 0, 0, 0);
+      if (masked && key >= it.draft && key < it.k1) v = drop_odd<DT, F8>(v, &odd);
+      *reinterpret_cast<uint4 *>(s_k + key_row(at) * kKP + piece * 16) = rk[j];
+      *reinterpret_cast<uint4 *>(s_v + at * kVP + piece * 16) = v;
+    }
+#pragma unroll
+    for (int g = 0; g < 2 * KB; ++g) ks[g] = ks_next[g], vs[g] = vs_next[g];
+    tile_barrier();
+    if (t0 + KT < it.k1) load(t0 + KT);
+    if (w0 >= it.k1) continue;  // nothing of this tile for this wave
+    // products of the wave's blocks: element e of a lane is key 8 grp + e (16 rows),
+    // 16 (e / 8) + 8 grp + e % 8 (32 rows) of the block
+    float s[KB][NK];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      if constexpr (k16) {
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau) {
+          pg_f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          const char *row = s_k + (b * 32 + tau * 16 + col) * kKP + grp * 16;
+          if constexpr (F8) {
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(row + x * 64);
+              acc = mma16<DT>(widen8<DT>(make_uint2(w.x, w.y)), qf[2 * x], acc);
+              acc = mma16<DT>(widen8<DT>(make_uint2(w.z, w.w)), qf[2 * x + 1], acc);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) acc = mma16<DT>(*reinterpret_cast<const uint4 *>(row + x * 64), qf[x], acc);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][4 * tau + e] = acc[e];
+        }
+      } else {
+        at_f32x16_t acc;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+        const char *row = s_k + (b * 32 + col) * kKP + grp * 16;
+        if constexpr (F8) {
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(row + x * 32);
+            acc = T::mma(widen8<DT>(make_uint2(w.x, w.y)), qf[2 * x], acc);
+            acc = T::mma(widen8<DT>(make_uint2(w.z, w.w)), qf[2 * x + 1], acc);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) acc = T::mma(*reinterpret_cast<const uint4 *>(row + x * 32), qf[x], acc);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[b][e] = acc[e];
+      }
+    }
+    if (masked || t0 + KT > it.k1) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int e = 0; e < NK; ++e) {
+          const int key = w0 + b * 32 + 16 * (e >> 3) + 8 * grp + (e & 7);
+          const int own = key - it.draft;
+          const bool ok = key < it.k1 && (own < 0 || ((s_anc[r][(own & 255) >> 5] >> (own & 31)) & 1));
+          s[b][e] = ok ? s[b][e] : kNegInf;
+        }
+    }
+    // the scales of a lane's 8 (twice 8) keys
+    float kf[KB][NK / 8], vf[KB][NK / 8];
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int x = 0; x < NK / 8; ++x) {
+        kf[b][x] = !F8 ? 1.0f : k16 ? (grp < 2 ? ks[2 * b] : ks[2 * b + 1]) : ks[2 * b + x];
+        vf[b][x] = !F8 ? 1.0f : k16 ? (grp < 2 ? vs[2 * b] : vs[2 * b + 1]) : vs[2 * b + x];
+      }
+    float top = kNegInf;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int x = 0; x < NK / 8; ++x) {
+        float most = s[b][8 * x];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) most = fmaxf(most, s[b][8 * x + e]);
+        top = fmaxf(top, F8 ? most * kf[b][x] : most);
+      }
+    const float mn = fmaxf(m, row_max<ROWS>(top));
+    // Outputs are rescaled only when some row's maximum rose: 1 is exact.
+    if (__any(mn > m)) {
+      const float alpha = m == kNegInf ? 0.0f : exp2_fast((m - mn) * A.scale_log2);
+      l *= alpha;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) o[t][e] *= alpha;
+      m = mn;
+    }
+    if (kRelative) {
+      float most = vs[0];
+#pragma unroll
+      for (int g = 1; g < 2 * KB; ++g) most = fmaxf(most, vs[g]);
+      if (most > ref) {
+        const float down = ref / most;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int e = 0; e < kOut; ++e) o[t][e] *= down;
+        ref = most;
+      }
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int x = 0; x < NK / 8; ++x) vf[b][x] /= ref;
+    }
+    // One multiply-add per exponent, the key scale in its factor (never zero:
+    // masked products are -inf).  In float16 the largest is 2^15, held there
+    // however far the scores are and whatever their rounding (65504 ends the type).
+    const float mu = m == kNegInf ? 0.0f : m * A.scale_log2;
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int x = 0; x < NK / 8; ++x) {
+        const float c = F8 ? fmaxf(A.scale_log2 * kf[b][x], __FLT_MIN__) : A.scale_log2;
+#pragma unroll
+        for (int e = 8 * x; e < 8 * x + 8; ++e) {
+          const float arg = __builtin_fmaf(s[b][e], c, T::kLift - mu);
+          s[b][e] = exp2_fast(T::kLift > 0 && arg > T::kLift ? T::kLift : arg);  // (NaN stays)
+          sum += s[b][e];
+          if (F8) s[b][e] *= vf[b][x];
+        }
+      }
+    l += sum;
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+#pragma unroll
+      for (int x = 0; x < NK / 8; ++x) {
+        const float *e = &s[b][8 * x];
+        const uint4 p = make_uint4(T::pack(e[0], e[1]), T::pack(e[2], e[3]), T::pack(e[4], e[5]), T::pack(e[6], e[7]));
+        // values of keys 8 grp .. + 7 of these 32 (16) keys
+        const char *row = s_v + (b * 32 + 16 * x + 8 * grp + ((lane & 15) >> (F8 ? 1 : 2))) * kVP +
+                          (F8 ? (lane & 1) * 8 : (lane & 3) * 8) + (k16 ? 0 : ((lane >> 4) & 1) * 16 * kBytes);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          uint4 v;
+          if constexpr (F8) {
+            const pg_i32x2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(row + t * ROWS));
+            v = widen8<DT>(__builtin_bit_cast(uint2, w));
+          } else {
+            const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * ROWS * 2)));
+            const uint2 c = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * ROWS * 2 + 4 * kVP)));
+            v = make_uint4(a.x, a.y, c.x, c.y);
+          }
+          if constexpr (k16) o[t] = mma16<DT>(v, p, o[t]);
+          else o[t] = T::mma(v, p, o[t]);
+        }
+      }
+    }
+  }
+  // (also: every wave is done with the tiles)
+  const bool any_odd = it.k1 > it.draft ? __syncthreads_or(odd) : (__syncthreads(), false);
+  l = row_sum<ROWS>(l);
+  if (__any(bad)) l = __builtin_nanf("");  // a page that is none: the rows are no numbers
+
+  const int64_t rows_all = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  // value f of a lane's float4 number q: d = (k16 ? 16 t : 32 t + 8 q) + 4 grp + f
+  auto quad = [&](int t, int q, float f) { return make_float4(o[t][4 * q] * f, o[t][4 * q + 1] * f, o[t][4 * q + 2] * f, o[t][4 * q + 3] * f); };
+  if constexpr (SHARED) {
+    if (i < it.rows) {
+      const int64_t at = it.part * rows_all + qrow * A.Hq + head;
+      float *po = A.part_o + at * D;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int q = 0; q < kOut / 4; ++q) {
+          const int d = t * ROWS + 8 * q + 4 * grp;
+          float4 a = quad(t, q, ref);
+          if (any_odd) a = add_odd_paged<DT, F8>(A, it, s_anc[r], d, a);
+          *reinterpret_cast<float4 *>(po + d) = a;
+        }
+      if (grp == 0) A.part_ml[at] = make_float2(m, l);
+    }
+    return;
+  }
+  // The waves hold the same rows over different keys: joined in wave order, 64
+  // values of a row at a time.
+  float *s_o = reinterpret_cast<float *>(lds);
+  const int live = min(ROWS, it.rows - it.row0);
+  if (grp == 0) s_ml[wave * ROWS + col] = make_float2(m, l);
+  __syncthreads();
+  float M = kNegInf;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) M = fmaxf(M, s_ml[w * ROWS + col].x);
+  const float f = m == kNegInf ? 0.0f : exp2_fast((m - M) * A.scale_log2) * ref;
+#pragma unroll
+  for (int part = 0; part < D / 64; ++part) {
+    if (part > 0) __syncthreads();
+    if (col < live)
+#pragma unroll
+      for (int t = part * (64 / ROWS); t < (part + 1) * (64 / ROWS); ++t)
+#pragma unroll
+        for (int q = 0; q < kOut / 4; ++q)
+          *reinterpret_cast<float4 *>(s_o + (wave * ROWS + col) * (64 + 4) + t * ROWS - part * 64 + 8 * q + 4 * grp) = quad(t, q, f);
+    __syncthreads();
+    for (int z = tid; z < live * 16; z += 64 * WAVES) {
+      const int q = z / 16, c = z % 16, d = part * 64 + c * 4;
+      const int qi = it.row0 + q;
+      float4 a = *reinterpret_cast<const float4 *>(s_o + q * (64 + 4) + c * 4);
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) {
+        const float4 b = *reinterpret_cast<const float4 *>(s_o + (w * ROWS + q) * (64 + 4) + c * 4);
+        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+      }
+      if (any_odd) a = add_odd_paged<DT, F8>(A, it, s_anc[qi / A.n], d, a);
+      float Mq = kNegInf, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) Mq = fmaxf(Mq, s_ml[w * ROWS + q].x);
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const float2 v = s_ml[w * ROWS + q];
+        L += v.x == kNegInf ? v.y : v.y * exp2_fast((v.x - Mq) * A.scale_log2);  // (no maximum: zero, or NaN)
+      }
+      const int64_t row = (it.base_row + qi / A.n) * A.Hq + it.kvh * A.n + qi % A.n;
+      if (direct) {
+        const uint32_t lo = T::bits(a.x / L) | static_cast<uint32_t>(T::bits(a.y / L)) << 16;
+        const uint32_t hi = T::bits(a.z / L) | static_cast<uint32_t>(T::bits(a.w / L)) << 16;
+        *reinterpret_cast<uint2 *>(A.out + row * D + d) = make_uint2(lo, hi);
+        if (A.lse && d == 0) A.lse[row] = (Mq * A.scale_log2 + log2f(L * (T::kLift > 0 ? 0x1p-15f : 1.0f))) * 0.6931471805599453f;
+      } else {
+        const int64_t at = it.part * rows_all + row;
+        *reinterpret_cast<float4 *>(A.part_o + at * D + d) = a;
+        if (d == 0) A.part_ml[at] = make_float2(Mq, L);
+      }
+    }
+  }
+}
+
 template <int DT, bool F8, int D, int WQ>
 __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const PagedItem &it, char *lds, const uint32_t (*s_anc)[8],
                                            float2 *s_ml) {
@@ -120,7 +552,6 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   constexpr int kBytes = F8 ? 1 : 2;
   constexpr int kChunks = D * kBytes / 16;   // 16-byte pieces of a row
   constexpr int kWaveRows = 64 / kChunks;    // rows of one load of a wave: within a strip
-  constexpr bool kApart = WQ == 1;
   constexpr int kLoads = KT * kChunks / kAtThreads;
   constexpr bool kRelative = F8 && T::kLift > 0;
   uint16_t *s_k = reinterpret_cast<uint16_t *>(lds);
@@ -176,23 +607,21 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   uint4 rk[kLoads], rv[kLoads];
   float ks[2 * SB], vs[2 * SB], ks_next[2 * SB], vs_next[2 * SB];  // scales of this wave's strips, of the tile and of the one loaded
   const int piece = lane % kChunks;
-  constexpr int kStep = kApart ? kWaveRows : 4 * kWaveRows;
-  const int row0 = kApart ? wave * 32 : wave * kWaveRows;  // of this wave's first load
+  constexpr int kStep = 4 * kWaveRows;
+  const int row0 = wave * kWaveRows;  // of this wave's first load
   const int row_lane = lane / kChunks;
   const uint32_t lane_off = static_cast<uint32_t>(row_lane) * static_cast<uint32_t>(A.pool.token_bytes) + piece * 16;
   const int page_mask = (1 << A.pool.page_shift) - 1;
-  // one sequence's pages are read once: streamed
-  auto fetch = [&](const uint8_t *p) { return kApart ? load_stream(reinterpret_cast<const uint4 *>(p)) : load_vec(p); };
   auto load = [&](int t0) {
     if (t0 - c0 >= kLookup) look_up(t0);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const int key = t0 + row0 + j * kStep;  // (the wave's first row: rows follow within a strip)
-      const int strip = min(key, last + (key & (kStrip - 1))) ;
+      const int strip = min(key, last + (key & (kStrip - 1)));
       const int page = __builtin_amdgcn_readlane(pages, (strip - c0) / kStrip);
       const int64_t off = page * A.pool.page_bytes + (strip & page_mask) * A.pool.token_bytes + it.kvh * A.pool.head_bytes;
-      rk[j] = fetch(A.pool.k + off + lane_off);
-      rv[j] = fetch(A.pool.v + off + lane_off);
+      rk[j] = load_vec(A.pool.k + off + lane_off);
+      rv[j] = load_vec(A.pool.v + off + lane_off);
     }
     if (F8)
 #pragma unroll
@@ -202,10 +631,6 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
         vs_next[g] = read_lane_f32(vscale, at);
       }
   };
-  auto tile_barrier = [&]() {
-    if (kApart) __builtin_amdgcn_wave_barrier();
-    else __syncthreads();
-  };
   bool odd = false;
   load(it.k0);
   for (int t0 = it.k0; t0 < it.k1; t0 += KT) {
@@ -214,7 +639,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
     // Infinities and NaN among the step's own values, which must reach only the
     // rows that see them, are left out here and added at the end.
     const bool masked = t0 + KT > it.draft;
-    tile_barrier();
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const int row = row0 + j * kStep + row_lane;
@@ -236,7 +661,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
     }
 #pragma unroll
     for (int g = 0; g < 2 * SB; ++g) ks[g] = ks_next[g], vs[g] = vs_next[g];
-    tile_barrier();
+    __syncthreads();
     if (t0 + KT < it.k1) load(t0 + KT);
     if (t0 + wk * SB * 32 >= it.k1) continue;  // nothing of this tile for this wave
     // products of the wave's blocks of 32 keys
@@ -401,46 +826,32 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   }
 }
 
-// tree: nothing for a window, or the TreeParents.
-template <int DT, bool F8, int D, int WQP, int WQO, class... Tree>
-__global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs A, Tree... tree) {
-  constexpr size_t kBytes = pg_tile_bytes<D, WQP>() > pg_tile_bytes<D, WQO>() ? pg_tile_bytes<D, WQP>() : pg_tile_bytes<D, WQO>();
-  __shared__ uint4 s_tile[kBytes / sizeof(uint4)];
-  __shared__ uint32_t s_anc[kTreeMaxNodes][8];
-  __shared__ uint8_t s_parent[kTreeMaxNodes];
-  __shared__ float2 s_ml[128];  // [waves on the same rows][rows]
-  char *lds = reinterpret_cast<char *>(s_tile);
-  PagedItem it{};
-  const int heads = A.pool.Hkv;
-  int id = blockIdx.x;
-  if (id < A.prefix_items) {
-    // row tiles of one (kv head, range) are Hkv * parts apart: a multiple of 8
-    // of those keeps them on one XCD
-    const int pairs = heads * A.prefix_parts;
-    const int pair = id % pairs;
-    it.kvh = pair % heads;
-    it.part = pair / heads;
-    it.row0 = id / pairs * (32 * WQP);
-    it.rows = A.B * A.R * A.n;
-    it.base_row = 0;
-    it.table = A.prefix_table;
-    it.k0 = it.part * A.prefix_chunk;
-    it.k1 = min(it.k0 + A.prefix_chunk, A.P);
-    it.draft = it.k1 + (1 << 30);
-    if (A.P - it.k0 <= 0) return;
-    paged_item<DT, F8, D, WQP>(A, it, lds, s_anc, s_ml);
-    return;
+// A sequence whose length is out of range: its rows of this head are no numbers
+// (calls without a join; else the join says so).
+template <int DT, int D>
+__device__ void no_numbers(const PagedAttendArgs &A, int b, int live, int kvh) {
+  for (int z = threadIdx.x; z < live * A.n * (D / 4); z += blockDim.x) {
+    const int q = z / (D / 4), c = z % (D / 4);
+    const int64_t row = (static_cast<int64_t>(b) * A.R + q / A.n) * A.Hq + kvh * A.n + q % A.n;
+    const uint32_t nan2 = DT == DT_BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+    *reinterpret_cast<uint2 *>(A.out + row * D + c * 4) = make_uint2(nan2, nan2);
+    if (A.lse && c == 0) A.lse[row] = __builtin_nanf("");
   }
-  id -= A.prefix_items;
-  // All heads and row tiles of a range of one sequence's tokens follow each
-  // other on one XCD (8 blocks apart), every sequence's first range first, the
-  // next moved on by one: see k_attend.
+}
+
+// The own item of block `id`: false where there is none.  All heads and row
+// tiles of a range of one sequence's tokens follow each other on one XCD (8
+// blocks apart), every sequence's first range first, the next moved on by one:
+// see k_attend.
+template <int DT, int D>
+__device__ __forceinline__ bool own_item(const PagedAttendArgs &A, int id, int tile_rows, PagedItem *it, bool *direct) {
+  const int heads = A.pool.Hkv;
   const int per = heads * A.own_tiles;
   const int j = id / 8;
   const int range = j / per * 8 + id % 8;
-  if (range >= A.B * A.own_parts) return;
+  if (range >= A.B * A.own_parts) return false;
   const int tile = j % per % A.own_tiles;
-  it.kvh = j % per / A.own_tiles;
+  it->kvh = j % per / A.own_tiles;
   const int split = range / A.B;
   int b = range - split * A.B;
   if (A.B >= 8) {
@@ -449,63 +860,198 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs 
   }
   const int len = A.ctx_len[b];
   const int live = live_rows(A, b);
-  if (bad_len(A, len) || live == 0) return;
+  if (live == 0) return false;
+  if (bad_len(A, len)) {
+    if (A.direct && split == 0 && tile == 0) no_numbers<DT, D>(A, b, live, it->kvh);
+    return false;
+  }
   const int keys = __builtin_amdgcn_readfirstlane(len + live);
   const int own = attend_own_range(A.split, keys);
-  it.row0 = tile * (32 * WQO);
-  it.rows = live * A.n;
-  if (static_cast<int64_t>(split) * own >= keys || it.row0 >= it.rows) return;
-  it.k0 = split * own;
-  it.k1 = min(it.k0 + own, keys);
-  it.draft = len;
-  it.part = A.prefix_parts + split;
-  it.base_row = static_cast<int64_t>(b) * A.R;
-  it.table = A.table + b * A.table_stride;
-  if (it.k1 > len) ancestor_sets(A.R, s_anc, s_parent, tree...);
+  it->row0 = tile * tile_rows;
+  it->rows = live * A.n;
+  if (static_cast<int64_t>(split) * own >= keys || it->row0 >= it->rows) return false;
+  *direct = A.direct && own >= keys;
+  it->k0 = split * own;
+  it->k1 = min(it->k0 + own, keys);
+  it->draft = len;
+  it->part = A.prefix_parts + split;
+  it->base_row = static_cast<int64_t>(b) * A.R;
+  it->table = A.table + b * A.table_stride;
+  return true;
+}
+
+__device__ __forceinline__ void prefix_item(const PagedAttendArgs &A, int id, int tile_rows, PagedItem *it) {
+  // row tiles of one (kv head, range) are Hkv * parts apart: a multiple of 8
+  // of those keeps them on one XCD
+  const int heads = A.pool.Hkv, pairs = heads * A.prefix_parts;
+  const int pair = id % pairs;
+  it->kvh = pair % heads;
+  it->part = pair / heads;
+  it->row0 = id / pairs * tile_rows;
+  it->rows = A.B * A.R * A.n;
+  it->base_row = 0;
+  it->table = A.prefix_table;
+  it->k0 = it->part * A.prefix_chunk;
+  it->k1 = min(it->k0 + A.prefix_chunk, A.P);
+  it->draft = it->k1 + (1 << 30);
+}
+
+// Up to 16 stacked rows of a sequence.  PREFIX: 0 none, 1 tiles of 16 rows, 2
+// tiles of 64 (rows of the whole batch).  tree: nothing for a window, or the
+// TreeParents.
+template <int DT, bool F8, int D, int PREFIX, int WAVES, class... Tree>
+__global__ void __launch_bounds__(64 * WAVES, F8 ? 4 : 2) k_paged_few(PagedAttendArgs A, Tree... tree) {
+  constexpr size_t kOwn = few_bytes<F8, D, 16, false, WAVES>(), kPrefix = PREFIX == 2 ? few_bytes<F8, D, 16, true, WAVES>() : 0;
+  __shared__ uint4 s_tile[(kOwn > kPrefix ? kOwn : kPrefix) / sizeof(uint4)];
+  __shared__ uint32_t s_anc[16][8];  // (16 stacked rows are 16 rows at most)
+  __shared__ uint8_t s_parent[16];
+  __shared__ float2 s_ml[16 * WAVES];
+  char *lds = reinterpret_cast<char *>(s_tile);
+  PagedItem it{};
+  if constexpr (PREFIX > 0) {
+    if (static_cast<int>(blockIdx.x) < A.prefix_items) {
+      prefix_item(A, blockIdx.x, PREFIX == 2 ? 16 * WAVES : 16, &it);
+      few_item<DT, F8, D, 16, PREFIX == 2, WAVES>(A, it, lds, s_anc, s_ml, false);
+      return;
+    }
+  }
+  bool direct = false;
+  if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 16, &it, &direct)) return;
+  if (it.k1 > it.draft) ancestor_sets<64 * WAVES>(A.R, s_anc, s_parent, tree...);
   __syncthreads();
-  paged_item<DT, F8, D, WQO>(A, it, lds, s_anc, s_ml);
+  few_item<DT, F8, D, 16, false, WAVES>(A, it, lds, s_anc, s_ml, direct);
+}
+
+// More rows: tiles of 32, 64 or 128 stacked rows on 1, 2 or 4 waves, WQP of the
+// prefix and WQO of the sequences.
+template <int DT, bool F8, int D, int WQP, int WQO, class... Tree>
+__global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs A, Tree... tree) {
+  constexpr size_t kP = WQP == 1 ? few_bytes<F8, D, 32, false, 4>() : pg_tile_bytes<D, WQP>();
+  constexpr size_t kO = WQO == 1 ? few_bytes<F8, D, 32, false, 4>() : pg_tile_bytes<D, WQO>();
+  __shared__ uint4 s_tile[(kP > kO ? kP : kO) / sizeof(uint4)];
+  __shared__ uint32_t s_anc[kTreeMaxNodes][8];
+  __shared__ uint8_t s_parent[kTreeMaxNodes];
+  __shared__ float2 s_ml[128];  // [waves on the same rows][rows]
+  char *lds = reinterpret_cast<char *>(s_tile);
+  PagedItem it{};
+  if (static_cast<int>(blockIdx.x) < A.prefix_items) {
+    prefix_item(A, blockIdx.x, 32 * WQP, &it);
+    if constexpr (WQP == 1) few_item<DT, F8, D, 32, false, 4>(A, it, lds, s_anc, s_ml, false);
+    else paged_item<DT, F8, D, WQP>(A, it, lds, s_anc, s_ml);
+    return;
+  }
+  bool direct = false;
+  if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 32 * WQO, &it, &direct)) return;
+  if (it.k1 > it.draft) ancestor_sets(A.R, s_anc, s_parent, tree...);
+  __syncthreads();
+  if constexpr (WQO == 1) few_item<DT, F8, D, 32, false, 4>(A, it, lds, s_anc, s_ml, direct);
+  else paged_item<DT, F8, D, WQO>(A, it, lds, s_anc, s_ml);
+}
+
+// One wave per (row, head): the row's items joined.  Their maxima and sums are
+// read by the lanes, one each, and the outputs 8 at a time, all of them in
+// flight; the sums' order is the items'.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) k_paged_join(AttendJoin A, int direct) {
+  constexpr int E = D / 64;
+  const int rows = A.B * A.R * A.Hq;  // at most 2^30
+  const int row = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= rows) return;
+  const int br = row / A.Hq, b = br / A.R, r = br % A.R;
+  const int live = live_rows(A, b);
+  if (r >= live) return;
+  const int len = A.ctx_len[b];
+  float acc[E] = {};
+  float M = kNegInf, L = 0.0f;
+  if (bad_len(A, len)) {
+    M = L = __builtin_nanf("");
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = L;
+  } else {
+    const int keys = len + live, own = attend_own_range(A.split, keys);
+    const int parts = A.prefix_parts + (keys + own - 1) / own;
+    if (direct && parts == 1) return;
+    for (int p0 = 0; p0 < parts; p0 += 64) {
+      const int n = min(64, parts - p0);
+      const float2 ml = lane < n ? A.part_ml[static_cast<int64_t>(p0 + lane) * rows + row] : make_float2(kNegInf, 0.0f);
+      float top = ml.x;
+#pragma unroll
+      for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+      const float mn = fmaxf(M, top);
+      const float alpha = M == kNegInf ? 0.0f : exp2_fast((M - mn) * A.scale_log2);
+      M = mn;
+      L *= alpha;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= alpha;
+      const float f = ml.x == kNegInf ? 0.0f : exp2_fast((ml.x - M) * A.scale_log2);
+      // (no maximum: the sum is zero, or NaN, which stays)
+      L += wave_sum(ml.x == kNegInf ? ml.y : f * ml.y);
+      const float *po = A.part_o + (static_cast<int64_t>(p0) * rows + row) * D + lane * E;
+      const int64_t step = static_cast<int64_t>(rows) * D;
+      for (int p = 0; p < n; p += 8) {
+        float v[8][E];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[x][e] = p + x < n ? po[(p + x) * step + e] : 0.0f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float w = read_lane_f32(f, min(p + x, 63));
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(w, v[x][e], acc[e]);
+        }
+      }
+    }
+  }
+  uint16_t *out = A.out + static_cast<int64_t>(row) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = AtElt<DT>::bits(acc[e] / L);
+  if (A.lse && lane == 0) A.lse[row] = (M * A.scale_log2 + log2f(L * (AtElt<DT>::kLift > 0 ? 0x1p-15f : 1.0f))) * 0.6931471805599453f;
 }
 
 namespace {
 
-template <int DT, bool F8, int D, int WQP, int WQO>
-void launch_shape(const PagedAttendArgs &A, const TreeParents *parents, dim3 grid, hipStream_t st) {
-  if (parents)
-    hipLaunchKernelGGL((k_paged_attend<DT, F8, D, WQP, WQO, TreeParents>), grid, dim3(kAtThreads), 0, st, A, *parents);
-  else
-    hipLaunchKernelGGL((k_paged_attend<DT, F8, D, WQP, WQO>), grid, dim3(kAtThreads), 0, st, A);
-}
-
-template <int DT, bool F8, int D, int WQP>
-void launch_own(const PagedAttendArgs &A, const TreeParents *parents, const AttendPlan &P, dim3 grid, hipStream_t st) {
-  // (a sequence's rows are no more than the batch's: 4 waves on them mean 4 on the prefix)
-  if (WQP == 4 && P.own_waves == 4)
-    launch_shape<DT, F8, D, 4, 4>(A, parents, grid, st);
-  else if (P.own_waves == 2)
-    launch_shape<DT, F8, D, WQP, 2>(A, parents, grid, st);
-  else
-    launch_shape<DT, F8, D, WQP, 1>(A, parents, grid, st);
+// kernel(A) or kernel(A, parents).
+template <class Plain, class Tree>
+void launch(Plain plain, Tree tree, const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st, int waves = 4) {
+  const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks)), threads(64 * waves);
+  if (parents) hipLaunchKernelGGL(tree, grid, threads, 0, st, A, *parents);
+  else hipLaunchKernelGGL(plain, grid, threads, 0, st, A);
 }
 
 template <int DT, bool F8, int D>
-void launch_dim(const PagedAttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks));
-  if (P.prefix_waves == 4)
-    launch_own<DT, F8, D, 4>(A, parents, P, grid, st);
-  else
-    launch_own<DT, F8, D, 1>(A, parents, P, grid, st);
-  launch_attend_join(DT, D, A, st);
+void launch_dim(const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
+  using T = TreeParents;
+  if (P.few == 16) {
+    constexpr int kWide = F8 ? 16 : 8;  // (16-bit keys and values fill the LDS with 8 waves)
+    if (P.wide) launch(k_paged_few<DT, F8, D, 0, kWide>, k_paged_few<DT, F8, D, 0, kWide, T>, A, parents, P, st, kWide);
+    else if (P.prefix_items == 0 || P.prefix_waves == 1) launch(k_paged_few<DT, F8, D, 1, 4>, k_paged_few<DT, F8, D, 1, 4, T>, A, parents, P, st);
+    else launch(k_paged_few<DT, F8, D, 2, 4>, k_paged_few<DT, F8, D, 2, 4, T>, A, parents, P, st);
+  } else if (P.prefix_waves == 4) {
+    // (a sequence's rows are no more than the batch's: 4 waves on them mean 4 on the prefix)
+    if (P.own_waves == 4) launch(k_paged_attend<DT, F8, D, 4, 4>, k_paged_attend<DT, F8, D, 4, 4, T>, A, parents, P, st);
+    else if (P.own_waves == 2) launch(k_paged_attend<DT, F8, D, 4, 2>, k_paged_attend<DT, F8, D, 4, 2, T>, A, parents, P, st);
+    else launch(k_paged_attend<DT, F8, D, 4, 1>, k_paged_attend<DT, F8, D, 4, 1, T>, A, parents, P, st);
+  } else {
+    if (P.own_waves == 2) launch(k_paged_attend<DT, F8, D, 1, 2>, k_paged_attend<DT, F8, D, 1, 2, T>, A, parents, P, st);
+    else launch(k_paged_attend<DT, F8, D, 1, 1>, k_paged_attend<DT, F8, D, 1, 1, T>, A, parents, P, st);
+  }
+  if (P.direct && P.own_parts == 1) return;
+  const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;
+  hipLaunchKernelGGL((k_paged_join<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st,
+                     static_cast<const AttendJoin &>(A), A.direct);
 }
 
 template <int DT, bool F8>
-void launch_cache(int D, const PagedAttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st) {
+void launch_cache(int D, const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
   if (D == 64) launch_dim<DT, F8, 64>(A, parents, P, st);
   else launch_dim<DT, F8, 128>(A, parents, P, st);
 }
 
 }  // namespace
 
-void launch_paged_attend(int dtype, bool f8, int D, const PagedAttendArgs &A, const TreeParents *parents, const AttendPlan &P, hipStream_t st) {
+void launch_paged_attend(int dtype, bool f8, int D, const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
   if (dtype == DT_BF16) {
     if (f8) launch_cache<DT_BF16, true>(D, A, parents, P, st);
     else launch_cache<DT_BF16, false>(D, A, parents, P, st);

@@ -248,9 +248,9 @@ inline int64_t attend_range(int64_t keys, int64_t parts) { return ((keys + parts
 // there is work for many rounds already (crowded), ranges of about 1024 keys
 // keep the items even; longer sequences then have longer ranges, 16 of them or
 // what fills the chip once, so that partial outputs do not follow the length.
-inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded) {
+inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded, int64_t slots = kAttendSlots) {
   if (crowded) {
-    const int64_t fill = (kAttendSlots + items - 1) / items, cap = fill > 16 ? fill : 16;
+    const int64_t fill = (slots + items - 1) / items, cap = fill > 16 ? fill : 16;
     const int64_t p = (keys + 1023) / 1024;
     return static_cast<int>(p < cap ? p : cap);
   }
@@ -259,8 +259,8 @@ inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded)
   int parts = 1;
   for (int64_t p = 1, step = 1; p <= most; p += step) {
     if (p == 8 * step) step *= 2;  // eight candidates, then four per doubling
-    const int64_t last = items * p % kAttendSlots;
-    const int64_t rounds = items * p / kAttendSlots * 20 + (last == 0 ? 0 : last <= kAttendSlots / 2 ? 13 : 20);
+    const int64_t last = items * p % slots;
+    const int64_t rounds = items * p / slots * 20 + (last == 0 ? 0 : last <= slots / 2 ? 13 : 20);
     const int64_t cost = rounds * (attend_range(keys, p) + kAttendMinKeys + 2 * rows) + 20 * 64 * p;
     if (best < 0 || cost < best) {
       best = cost;
@@ -302,6 +302,63 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
   const size_t slots = static_cast<size_t>(L.prefix_parts + L.own_parts) * static_cast<size_t>(B * R * Hq);
   L.ml_off = align256(slots * static_cast<size_t>(D) * sizeof(float));
   L.total = align256(L.ml_off + slots * 2 * sizeof(float));
+  return L;
+}
+
+// Attention over pages.  The rows of a sequence (times the heads of a group)
+// choose the kernel: up to 16 or 32 of them stay one tile (few), more go by
+// tiles of 64 or 128 as above.  Tiles of 16 rows hold half of the registers,
+// four workgroups on a CU; where there are no more items than CUs and no prefix,
+// a workgroup is 8 or 16 waves instead (wide), so that some thousands of keys need
+// no join.
+constexpr int64_t kPagedFewSlots = 1024;
+constexpr int64_t kPagedWideItems = 256;
+constexpr int64_t kPagedWideKeys = 2048;  // keys that such a workgroup takes alone
+struct PagedPlan : AttendPlan {
+  int few;
+  bool wide;
+  bool direct;  // a sequence of one range needs no partial outputs
+};
+
+inline PagedPlan plan_paged(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx) {
+  PagedPlan L{};
+  const int64_t n = Hq / Hkv, all = B * R * n, own = R * n;
+  L.few = own <= 16 ? 16 : own <= 32 ? 32 : 0;
+  L.wide = L.few == 16 && P == 0 && B * Hkv <= kPagedWideItems;
+  L.direct = L.few > 0 && P == 0;
+  L.own_waves = own > kAttendWideRows ? 4 : own > 32 ? 2 : 1;
+  L.prefix_waves = all > kAttendWideRows ? 4 : 1;
+  const int64_t own_rows = L.few > 0 ? L.few : 32 * L.own_waves;
+  const int64_t prefix_rows = L.few == 16 ? (L.prefix_waves == 4 ? 64 : 16) : 32 * L.prefix_waves;
+  const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
+  const int64_t slots = L.wide ? kPagedWideItems : L.few == 16 ? kPagedFewSlots : kAttendSlots;
+  L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
+  const int64_t own_items = B * Hkv * L.own_tiles;
+  const int longest = attend_bucket(static_cast<int>(max_ctx + R));
+  for (int j = 0; j <= longest; ++j) {
+    const int64_t keys = int64_t{128} << j;
+    const bool crowded = own_items * ((keys + 1023) / 1024) >= 4 * slots;
+    int64_t parts = attend_parts(keys, own_items, own < own_rows ? own : own_rows, crowded, slots);
+    if (L.wide) {
+      const int64_t most = (keys + kPagedWideKeys / 2 - 1) / (kPagedWideKeys / 2);
+      parts = keys <= kPagedWideKeys ? 1 : parts < most ? parts : most;
+    }
+    const int64_t range = attend_range(keys, parts);
+    L.split.tiles[j / 4] |= static_cast<uint64_t>(range / 128) << (16 * (j % 4));
+    parts = (keys + range - 1) / range;
+    if (parts > L.own_parts) L.own_parts = static_cast<int>(parts);
+  }
+  L.prefix_chunk = 1;
+  if (P > 0) {
+    const bool crowded = own_items >= 2 * slots;
+    L.prefix_chunk = static_cast<int>(attend_range(P, attend_parts(P, tiles * Hkv, all < prefix_rows ? all : prefix_rows, crowded, slots)));
+    L.prefix_parts = static_cast<int>((P + L.prefix_chunk - 1) / L.prefix_chunk);
+    L.prefix_items = tiles * Hkv * L.prefix_parts;
+  }
+  L.own_blocks = (B * L.own_parts + 7) / 8 * 8 * Hkv * L.own_tiles;
+  const size_t parts = static_cast<size_t>(L.prefix_parts + L.own_parts) * static_cast<size_t>(B * R * Hq);
+  L.ml_off = align256(parts * static_cast<size_t>(D) * sizeof(float));
+  L.total = align256(L.ml_off + parts * 2 * sizeof(float));
   return L;
 }
 
