@@ -2,6 +2,7 @@
 built: there is no fallback path."""
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspecverify.so")
 
@@ -50,26 +51,21 @@ _STEP_SIGNATURES = {
 
 
 
-class PagedCacheArgs(ctypes.Structure):
-    """sv_paged_cache of include/sv_cache.h."""
-    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P)] + \
-        [(n, _I32) for n in ("dtype", "num_pages", "page", "block", "Hkv", "D")] + \
-        [(n, _I64) for n in ("page_stride", "token_stride", "head_stride")]
-
-
-_PC = _c.POINTER(PagedCacheArgs)
+# sv_paged_cache of include/sv_cache.h: four addresses, dtype, num_pages, page,
+# block, Hkv, D and three strides.
+PAGED_CACHE = struct.Struct("4P6i3q")
 
 # include/sv_cache.h
 _CACHE_SIGNATURES = {
     "sv_rotary_turns": (_c.c_int, [_c.POINTER(_c.c_double), _I32, _c.POINTER(_U64)]),
     "sv_rotary": (_c.c_int, [_P, _I64, _P, _I64, _c.c_int, _P, _I32, _c.c_int, _c.c_int, _c.c_float, _P, _P, _P,
                              _I32, _I32, _I32, _I32, _P]),
-    "sv_cache_append": (_c.c_int, [_PC, _P, _I64, _I32, _P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _c.c_int,
+    "sv_cache_append": (_c.c_int, [_P, _P, _I64, _I32, _P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _c.c_int,
                                    _P, _I32, _c.c_int, _c.c_float, _I32, _I32, _I32, _P]),
     "sv_paged_attention_workspace": (_SZ, [_I32] * 7),
-    "sv_paged_attention": (_c.c_int, [_P, _I64, _c.c_int, _PC, _P, _I64, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
+    "sv_paged_attention": (_c.c_int, [_P, _I64, _c.c_int, _P, _P, _I64, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
                                       _c.c_float, _P, _P, _P, _SZ, _P]),
-    "sv_cache_commit": (_c.c_int, [_PC, _I32, _I64, _P, _I64, _I32, _P, _P, _I64, _I32, _P, _I32, _I32, _P, _P]),
+    "sv_cache_commit": (_c.c_int, [_P, _I32, _I64, _P, _I64, _I32, _P, _P, _I64, _I32, _P, _I32, _I32, _P, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)

@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import PagedCacheArgs, lib
+from ._lib import PAGED_CACHE, lib
 
 SV_OP_WINDOW, SV_OP_GREEDY, SV_OP_TREE, SV_OP_LMHEAD = 0, 1, 2, 3
 SV_TREE_GREEDY, SV_TREE_STOCHASTIC, SV_TREE_MULTI_CANDIDATE = 0, 1, 2
@@ -619,37 +619,45 @@ class PagedCache:
     dimension on all of them holds the layers of a model (layer(i) is one of
     them).  A handle on those tensors: they keep their storage while it is used.
     paged_cache() allocates one."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "layers", "layer_stride", "args", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "layers", "layer_stride", "code", "page", "heads", "dim", "device", "args")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        code = _PAGE_CODE.get(k.dtype)
-        if code is None or k.device.type != "cuda" or k.dim() not in (4, 5):
+        # (small calls are bound by the host: one comparison a property)
+        dtype, dev, shape, st = k.dtype, k.device, k.shape, k.stride()
+        code = _PAGE_CODE.get(dtype)
+        if code is None or dev.type != "cuda" or len(shape) not in (4, 5):
             raise ValueError("k: expected a bf16, fp16 or float8_e4m3fn device tensor of shape (num_pages, page, Hkv, D), or (layers, ..)")
-        st = k.stride()
-        if v.dtype != k.dtype or v.device != k.device or v.shape != k.shape or v.stride() != st:
+        if v.dtype != dtype or v.device != dev or v.shape != shape or v.stride() != st:
             raise ValueError("v must match k in dtype, device, shape and strides")
-        num_pages, page, Hkv, D = k.shape[-4:]
-        if st[-1] != 1:
+        if len(shape) == 4:
+            num_pages, page, Hkv, D = shape
+            page_stride, token_stride, head_stride, unit = st
+            self.layers = self.layer_stride = 0
+        else:
+            self.layers, num_pages, page, Hkv, D = shape
+            self.layer_stride, page_stride, token_stride, head_stride, unit = st
+            if self.layers > 1 and self.layer_stride <= 0:
+                raise ValueError("k and v: layers overlap")
+        if unit != 1:
             raise ValueError("k and v: the values of a head must be contiguous")
-        self.layers, self.layer_stride = (k.shape[0], st[0]) if k.dim() == 5 else (0, 0)
-        if k.numel() == 0 or (self.layers > 1 and st[0] <= 0):
-            raise ValueError("k and v: expected pages that do not overlap")
-        block, ks, vs = 0, None, None
+        if 0 in shape:
+            raise ValueError("k and v: expected pages")
+        block, ks, vs = 0, 0, 0
         if code == SV_DT_F8E4M3:
-            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if t is None or t.dtype != torch.float32 or t.device != k.device or not t.is_contiguous() or t.dim() != k.dim() - 1 \
-                        or t.shape[:-2] != k.shape[:-3] or t.shape[-1] != Hkv or not 0 < t.shape[-2] <= page or page % t.shape[-2]:
-                    raise ValueError(f"{name}: 8-bit pages need a contiguous float32 tensor (.., num_pages, page / block, Hkv) on {k.device}")
-            if k_scale.shape != v_scale.shape:
-                raise ValueError("k_scale and v_scale must have one shape")
-            block, ks, vs = page // k_scale.shape[-2], k_scale.data_ptr(), v_scale.data_ptr()
+            blocks = k_scale.shape[-2] if k_scale is not None and k_scale.dim() > 2 else 0
+            want = (*shape[:-3], blocks, Hkv)
+            if not 0 < blocks <= page or page % blocks or v_scale is None or k_scale.shape != want or v_scale.shape != want \
+                    or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.device != dev or v_scale.device != dev \
+                    or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+                raise ValueError(f"k_scale, v_scale: 8-bit pages need contiguous float32 tensors (.., num_pages, page / block, Hkv) on {dev}")
+            block, ks, vs = page // blocks, k_scale.data_ptr(), v_scale.data_ptr()
         elif k_scale is not None or v_scale is not None:
             raise ValueError("16-bit pages have no scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        # strides of dimensions of one entry do not matter: any multiple that overlaps nothing (0: dense)
-        self.args = PagedCacheArgs(k.data_ptr(), v.data_ptr(), ks, vs, code, num_pages, page, block, Hkv, D,
-                                   st[-4] if num_pages > 1 else 0, st[-3], st[-2] if Hkv > 1 else 0)
-        self.ref = ctypes.byref(self.args)
+        self.code, self.page, self.heads, self.dim, self.device = code, page, Hkv, D, dev
+        # strides of dimensions of one entry do not matter (0: dense)
+        self.args = PAGED_CACHE.pack(k.data_ptr(), v.data_ptr(), ks, vs, code, num_pages, page, block, Hkv, D,
+                                     page_stride if num_pages > 1 else 0, token_stride, head_stride if Hkv > 1 else 0)
 
     def layer(self, i):
         """The pages of layer i, on the same memory."""
@@ -755,12 +763,14 @@ def rotary(x, turns, base_pos=None, *, parent=None, interleaved=False, magnitude
     return out
 
 
-def _one_layer(cache, dev):
-    if cache.k.device != dev:
-        raise ValueError(f"cache is on {cache.k.device}, expected {dev}")
+def _one_layer(cache, dtype, dev):
+    """Refuses caches on another device, of several layers, or of 16-bit pages of another type than dtype."""
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
     if cache.layers:
         raise ValueError("cache: expected one layer (cache.layer(i))")
-    return cache.args
+    if cache.code != SV_DT_F8E4M3 and cache.code != _DTYPE_CODE[dtype]:
+        raise ValueError(f"16-bit pages hold {cache.k.dtype}, the rows are {dtype}")
 
 
 def cache_append(cache, page_table, ctx_len, k, v, *, q=None, turns=None, base_pos=None, parent=None, interleaved=False,
@@ -777,12 +787,9 @@ def cache_append(cache, page_table, ctx_len, k, v, *, q=None, turns=None, base_p
     dtype, dev = k.dtype, k.device
     if k.dim() != 4 or (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda":
         raise ValueError("k: expected a bf16 or fp16 device tensor of shape (B, R, Hkv, D)")
-    a = _one_layer(cache, dev)
-    B, R = k.shape[:2]
-    Hkv, D = a.Hkv, a.D
+    _one_layer(cache, dtype, dev)
+    B, R, Hkv, D = k.shape[0], k.shape[1], cache.heads, cache.dim
     k_stride, v_stride = _rows(k, B, R, Hkv, D, dtype, dev, "k"), _rows(v, B, R, Hkv, D, dtype, dev, "v")
-    if a.dtype != SV_DT_F8E4M3 and cache.k.dtype != dtype:
-        raise ValueError(f"k and v: 16-bit pages hold {cache.k.dtype}")
     table_stride = _rows_i32(page_table, B, 1, dev, "page_table")
     if ctx_len is None:
         raise ValueError("ctx_len is required")
@@ -799,7 +806,7 @@ def cache_append(cache, page_table, ctx_len, k, v, *, q=None, turns=None, base_p
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _launch(dev, lib().sv_cache_append, cache.ref, page_table.data_ptr(), table_stride, page_table.shape[1],
+    _launch(dev, lib().sv_cache_append, cache.args, page_table.data_ptr(), table_stride, page_table.shape[1],
             _vec(ctx_len, torch.int32, B, dev, "ctx_len"), _vec(row_count, torch.int32, B, dev, "row_count"), _parents(parent, R),
             _vec(base_pos, torch.int64, B, dev, "base_pos"), k.data_ptr(), k_stride, v.data_ptr(), v_stride, q_ptr, q_stride,
             out_ptr, out_stride, _DTYPE_CODE[dtype], turns_ptr, rot, bool(interleaved), magnitude, B, R, Hq)
@@ -813,7 +820,7 @@ def cache_commit(cache, page_table, ctx_len, nodes, n_accepted, *, rows, new_len
     nodes, n_accepted: out_nodes and n_accepted of verify_tree (nodes None: a
     window, only the lengths); rows: the rows of the step.  Returns new_len (a
     new tensor when None; ctx_len itself: in place)."""
-    dev = cache.k.device
+    dev = cache.device
     if ctx_len is None or n_accepted is None:
         raise ValueError("ctx_len and n_accepted are required")
     B = page_table.shape[0]
@@ -824,7 +831,7 @@ def cache_commit(cache, page_table, ctx_len, nodes, n_accepted, *, rows, new_len
         nodes_ptr, most = nodes.data_ptr(), nodes.shape[1]
     if new_len is None:
         new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    _launch(dev, lib().sv_cache_commit, cache.ref, max(cache.layers, 1), cache.layer_stride if cache.layers > 1 else 0,
+    _launch(dev, lib().sv_cache_commit, cache.args, max(cache.layers, 1), cache.layer_stride if cache.layers > 1 else 0,
             page_table.data_ptr(), table_stride, page_table.shape[1], _vec(ctx_len, torch.int32, B, dev, "ctx_len"), nodes_ptr,
             nodes_stride, most, _vec(n_accepted, torch.int32, B, dev, "n_accepted"), B, rows,
             _vec(new_len, torch.int32, B, dev, "new_len"))
@@ -850,29 +857,27 @@ def paged_attention(q, cache, page_table, ctx_len, *, prefix_table=None, prefix_
     dtype, dev = q.dtype, q.device
     if q.dim() != 4 or (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda":
         raise ValueError("q: expected a bf16 or fp16 device tensor of shape (B, R, Hq, D)")
-    a = _one_layer(cache, dev)
+    _one_layer(cache, dtype, dev)
     B, R, Hq, D = q.shape
-    q_stride = _rows(q, B, R, Hq, a.D, dtype, dev, "q")
-    if a.dtype != SV_DT_F8E4M3 and cache.k.dtype != dtype:
-        raise ValueError(f"q: 16-bit pages hold {cache.k.dtype}")
-    if Hq % a.Hkv:
+    q_stride = _rows(q, B, R, Hq, cache.dim, dtype, dev, "q")
+    if Hq % cache.heads:
         raise ValueError("the query heads must be a multiple of the kv heads")
     table_stride = _rows_i32(page_table, B, 1, dev, "page_table")
     prefix_ptr = None
     if prefix_len:
         if prefix_table is None or prefix_table.dtype != torch.int32 or prefix_table.device != dev or prefix_table.dim() != 1 \
-                or not prefix_table.is_contiguous() or prefix_table.shape[0] * a.page < prefix_len:
+                or not prefix_table.is_contiguous() or prefix_table.shape[0] * cache.page < prefix_len:
             raise ValueError(f"prefix_table: expected a contiguous int32 tensor of the {prefix_len} tokens' pages on {dev}")
         prefix_ptr = prefix_table.data_ptr()
     if ctx_len is None:
         raise ValueError("ctx_len is required")
     if max_ctx is None:
-        max_ctx = min(page_table.shape[1] * a.page - R, 1 << 24)
+        max_ctx = min(page_table.shape[1] * cache.page - R, 1 << 24)
     if scale is None:
         scale = D ** -0.5
     L = lib()
     if ws is None:
-        ws_bytes = L.sv_paged_attention_workspace(B, R, Hq, a.Hkv, D, prefix_len, max_ctx)
+        ws_bytes = L.sv_paged_attention_workspace(B, R, Hq, cache.heads, D, prefix_len, max_ctx)
         if ws_bytes == 0:
             raise ValueError("sizes outside the rules of sv_paged_attention")
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
@@ -886,7 +891,7 @@ def paged_attention(q, cache, page_table, ctx_len, *, prefix_table=None, prefix_
             raise ValueError("out is a required output")
         _out_tensor(out.out, dtype, (B, R, Hq, D), dev, "out")
         _out_tensor(out.lse, torch.float32, (B, R, Hq), dev, "lse")
-    _launch(dev, L.sv_paged_attention, q.data_ptr(), q_stride, _DTYPE_CODE[dtype], cache.ref, page_table.data_ptr(), table_stride,
+    _launch(dev, L.sv_paged_attention, q.data_ptr(), q_stride, _DTYPE_CODE[dtype], cache.args, page_table.data_ptr(), table_stride,
             page_table.shape[1], prefix_ptr, prefix_len, _vec(ctx_len, torch.int32, B, dev, "ctx_len"),
             _vec(row_count, torch.int32, B, dev, "row_count"), _parents(parent, R), B, R, Hq, max_ctx, scale,
             out.out.data_ptr(), None if out.lse is None else out.lse.data_ptr(), ws.data_ptr(), ws_bytes)

@@ -854,7 +854,7 @@ bool paged_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_
   AttendPlan same;  // the rules are sv_attention's
   if (!attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &same)) return false;
   *L = plan_paged(B, R, Hq, Hkv, D, P, max_ctx);
-  return L->prefix_items <= INT32_MAX && grid_fits(L->prefix_items + L->own_blocks, 1024);
+  return L->prefix_items <= INT32_MAX && grid_fits(L->prefix_items + L->own_blocks, kAttendThreads);
 }
 
 // Depths of a valid tree's nodes.

@@ -67,14 +67,14 @@ __device__ __forceinline__ int live_rows(const AttendJoin &A, int b) {
 // Ancestor sets of the rows, one row per thread; parents go to LDS first, as a
 // walk through the argument block would cost a trip to memory a step.  (A
 // barrier follows at the caller's.)  tree: nothing for a window, or the TreeParents.
-template <int THREADS = kAtThreads, class... Tree>
+template <class... Tree>
 __device__ __forceinline__ void ancestor_sets(int R, uint32_t (*s_anc)[8], uint8_t *s_parent, const Tree &...tree) {
   constexpr bool kTree = sizeof...(Tree) > 0;
   if constexpr (kTree) {
-    for (int v = threadIdx.x; v < R; v += THREADS) s_parent[v] = (tree.parent[v], ...);
+    for (int v = threadIdx.x; v < R; v += kAtThreads) s_parent[v] = (tree.parent[v], ...);
     __syncthreads();
   }
-  for (int v = threadIdx.x; v < R; v += THREADS) {
+  for (int v = threadIdx.x; v < R; v += kAtThreads) {
     uint32_t w[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) w[x] = 0;

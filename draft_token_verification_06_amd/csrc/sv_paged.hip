@@ -24,6 +24,7 @@ namespace sv {
 
 namespace {
 
+constexpr int kFewWaves = kAtThreads / 64;
 constexpr int kStrip = 16;               // tokens that share page and scale
 constexpr int kLookup = 64 * kStrip;     // tokens of one look-up
 
@@ -47,18 +48,18 @@ template <int D, int WQ> constexpr size_t pg_tile_bytes() {
   return kv > merge ? kv : merge;
 }
 
-// 16 bytes as 16 values of the storage type (exact).
-template <int DT> __device__ __forceinline__ void widen(uint4 raw, uint4 *lo, uint4 *hi) {
+// 16 bytes as 16 values of the storage type, times a power of two (exact).
+template <int DT> __device__ __forceinline__ void widen(uint4 raw, float scale, uint4 *lo, uint4 *hi) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (DT == DT_BF16) {
-      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false));
-      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true));
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, true));
     } else {
-      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], 1.0f, false));
-      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], 1.0f, true));
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], scale, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], scale, true));
     }
   }
   *lo = make_uint4(o[0], o[1], o[2], o[3]);
@@ -163,9 +164,9 @@ template <int ROWS> __device__ __forceinline__ float row_sum(float x) {
 // bits: 16 bytes more) or 4 of 32 (16 bits: 32 bytes more).
 template <bool F8, int D> constexpr int few_key_pitch() { return F8 ? D + 16 : 2 * D + 16; }
 template <bool F8, int D> constexpr int few_value_pitch() { return F8 ? D + 16 : 2 * D + 32; }
-template <bool F8, int D, int ROWS, bool SHARED, int WAVES> constexpr size_t few_bytes() {
-  const size_t tile = static_cast<size_t>(SHARED ? 64 : 32 * WAVES) * (few_key_pitch<F8, D>() + few_value_pitch<F8, D>());
-  const size_t merge = SHARED ? 0 : static_cast<size_t>(WAVES) * ROWS * (64 + 4) * 4;
+template <bool F8, int D, int ROWS, bool SHARED> constexpr size_t few_bytes() {
+  const size_t tile = static_cast<size_t>(SHARED ? 64 : 32 * kFewWaves) * (few_key_pitch<F8, D>() + few_value_pitch<F8, D>());
+  const size_t merge = SHARED ? 0 : static_cast<size_t>(kFewWaves) * ROWS * (64 + 4) * 4;
   return tile > merge ? tile : merge;
 }
 
@@ -182,12 +183,13 @@ template <bool F8, int D, int ROWS, bool SHARED, int WAVES> constexpr size_t few
 // exponentials belong to 8 (twice 8) consecutive keys: the operand of the second
 // product as they are, under one scale each, against values whose transposing
 // read takes 8 consecutive rows (no bank conflicts).
-template <int DT, bool F8, int D, int ROWS, bool SHARED, int WAVES>
+template <int DT, bool F8, int D, int ROWS, bool SHARED>
 __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedItem &it, char *lds, const uint32_t (*s_anc)[8],
                                          float2 *s_ml, bool direct) {
   using T = AtElt<DT>;
   constexpr bool k16 = ROWS == 16;
   constexpr int KB = SHARED ? 2 : 1;                 // blocks of 32 keys of a wave and tile
+  constexpr int WAVES = kFewWaves;
   constexpr int KT = SHARED ? 64 : 32 * WAVES;
   constexpr int kWaveKeys = SHARED ? KT / WAVES : 32;  // keys that a wave fetches
   constexpr int kBytes = F8 ? 1 : 2;
@@ -299,17 +301,21 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
     // zero times what a page holds behind the last token need not be.
     // Infinities and NaN among the step's own values, which must reach only the
     // rows that see them, are left out here and added at the end.
-    const bool masked = t0 + KT > it.draft;
+    const bool masked = t0 + KT > it.draft, plain = !masked && t0 + KT <= it.k1;
     tile_barrier();
+    if (!plain) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int key = w0 + (SHARED ? wave * kWaveKeys : 0) + j * kWaveRows + row_lane;
+        if (key >= it.k1) rv[j] = make_uint4(0, 0, 0, 0);
+        else if (key >= it.draft) rv[j] = drop_odd<DT, F8>(rv[j], &odd);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const int at = (SHARED ? wave * kWaveKeys : 0) + j * kWaveRows + row_lane;  // key within the LDS rows
-      const int key = w0 + at;
-      uint4 v = rv[j];
-      if (t0 + KT > it.k1 && key >= it.k1) v = make_uint4(0, 0, 0, 0);
-      if (masked && key >= it.draft && key < it.k1) v = drop_odd<DT, F8>(v, &odd);
       *reinterpret_cast<uint4 *>(s_k + key_row(at) * kKP + piece * 16) = rk[j];
-      *reinterpret_cast<uint4 *>(s_v + at * kVP + piece * 16) = v;
+      *reinterpret_cast<uint4 *>(s_v + at * kVP + piece * 16) = rv[j];
     }
 #pragma unroll
     for (int g = 0; g < 2 * KB; ++g) ks[g] = ks_next[g], vs[g] = vs_next[g];
@@ -360,7 +366,7 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
         for (int e = 0; e < 16; ++e) s[b][e] = acc[e];
       }
     }
-    if (masked || t0 + KT > it.k1) {
+    if (!plain) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -446,19 +452,25 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
         // values of keys 8 grp .. + 7 of these 32 (16) keys
         const char *row = s_v + (b * 32 + 16 * x + 8 * grp + ((lane & 15) >> (F8 ? 1 : 2))) * kVP +
                           (F8 ? (lane & 1) * 8 : (lane & 3) * 8) + (k16 ? 0 : ((lane >> 4) & 1) * 16 * kBytes);
+        if constexpr (F8) {
+          pg_i32x2_t w[kTiles];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          uint4 v;
-          if constexpr (F8) {
-            const pg_i32x2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(row + t * ROWS));
-            v = widen8<DT>(__builtin_bit_cast(uint2, w));
-          } else {
+          for (int t = 0; t < kTiles; ++t) w[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(row + t * ROWS));
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            const uint4 v = widen8<DT>(__builtin_bit_cast(uint2, w[t]));
+            if constexpr (k16) o[t] = mma16<DT>(v, p, o[t]);
+            else o[t] = T::mma(v, p, o[t]);
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
             const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * ROWS * 2)));
             const uint2 c = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * ROWS * 2 + 4 * kVP)));
-            v = make_uint4(a.x, a.y, c.x, c.y);
+            const uint4 v = make_uint4(a.x, a.y, c.x, c.y);
+            if constexpr (k16) o[t] = mma16<DT>(v, p, o[t]);
+            else o[t] = T::mma(v, p, o[t]);
           }
-          if constexpr (k16) o[t] = mma16<DT>(v, p, o[t]);
-          else o[t] = T::mma(v, p, o[t]);
         }
       }
     }
@@ -554,23 +566,28 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   constexpr int kWaveRows = 64 / kChunks;    // rows of one load of a wave: within a strip
   constexpr int kLoads = KT * kChunks / kAtThreads;
   constexpr bool kRelative = F8 && T::kLift > 0;
+  constexpr bool kFolded = F8 && DT == DT_BF16;  // scales' powers of two enter as values are widened (bf16 holds them all)
   uint16_t *s_k = reinterpret_cast<uint16_t *>(lds);
   uint16_t *s_v = s_k + KT * kRow;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wq = wave % WQ, wk = wave / WQ;
   const int q32 = lane & 31, half = lane >> 5;
 
-  // this lane's row, its query fragments: d = 16 s + 8 half ..
+  // A row's 16-byte pieces in LDS: those of 8-bit pages widen to two, the first
+  // ones side by side and the second ones behind them, so that 8 lanes write 128
+  // bytes.  Place x of a row (8 values) holds d = place_d(x) ..
+  auto place_d = [](int x) { return F8 ? 16 * (x % kChunks) + 8 * (x / kChunks) : 8 * x; };
+  // this lane's row, its query fragments: places 2 s + half
   const int i = it.row0 + wq * 32 + q32;
   const int ic = min(i, it.rows - 1);
   const int64_t qrow = it.base_row + ic / A.n;
   const int head = it.kvh * A.n + ic % A.n;
   uint4 qf[D / 16];
   {
-    const uint16_t *p = A.q + qrow * A.q_row_stride + head * D + half * 8;
+    const uint16_t *p = A.q + qrow * A.q_row_stride + head * D;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      qf[s] = load_vec(p + s * 16);
+      qf[s] = load_vec(p + place_d(2 * s + half));
       // a negative scale acts on the queries' signs, so that larger products are larger scores
       if (A.negate) qf[s] = make_uint4(qf[s].x ^ 0x80008000u, qf[s].y ^ 0x80008000u, qf[s].z ^ 0x80008000u, qf[s].w ^ 0x80008000u);
     }
@@ -588,7 +605,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   // the strips of the look-up that begins at token c0, one per lane
   int c0 = it.k0, pages = 0;
   float kscale = 1.0f, vscale = 1.0f;
-  bool bad = false;
+  bool bad = false, whole = true;
   const int last = (it.k1 - 1) & -kStrip;
   auto look_up = [&](int at) {
     c0 = at;
@@ -600,12 +617,19 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
       const int64_t s = ((static_cast<int64_t>(pages) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * A.pool.Hkv + it.kvh;
       kscale = A.pool.k_scale[s];
       vscale = A.pool.v_scale[s];
+      // powers of two alone, as cache_append leaves them, need no products
+      if (kFolded) whole = __all(((__float_as_uint(kscale) | __float_as_uint(vscale)) & 0x7FFFFFu) == 0);
     }
   };
+  auto power = [](float x) { return __uint_as_float(__float_as_uint(x) & 0x7F800000u); };
+  auto rest = [](float x) { return __uint_as_float((__float_as_uint(x) & 0x7FFFFFu) | 0x3F800000u); };
   look_up(it.k0);
 
   uint4 rk[kLoads], rv[kLoads];
-  float ks[2 * SB], vs[2 * SB], ks_next[2 * SB], vs_next[2 * SB];  // scales of this wave's strips, of the tile and of the one loaded
+  // scales: of this wave's strips to compute with, of the tile and of the one
+  // loaded; of its strips to widen, of the one loaded; whether those of the tile are all powers of two
+  float ks[2 * SB], vs[2 * SB], ks_next[2 * SB], vs_next[2 * SB], kw[kLoads], vw[kLoads];
+  bool plain_scales = true, plain_next = true;
   const int piece = lane % kChunks;
   constexpr int kStep = 4 * kWaveRows;
   const int row0 = wave * kWaveRows;  // of this wave's first load
@@ -623,12 +647,19 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
       rk[j] = load_vec(A.pool.k + off + lane_off);
       rv[j] = load_vec(A.pool.v + off + lane_off);
     }
-    if (F8)
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int at = (min(t0 + row0 + j * kStep, last) - c0) / kStrip;
+      kw[j] = kFolded ? power(read_lane_f32(kscale, at)) : 1.0f;
+      vw[j] = kFolded ? power(read_lane_f32(vscale, at)) : 1.0f;
+    }
+    plain_next = whole;
+    if (F8 && !(kFolded && whole))
 #pragma unroll
       for (int g = 0; g < 2 * SB; ++g) {
         const int at = (min(t0 + wk * SB * 32 + g * kStrip, last) - c0) / kStrip;
-        ks_next[g] = read_lane_f32(kscale, at);
-        vs_next[g] = read_lane_f32(vscale, at);
+        ks_next[g] = kFolded ? rest(read_lane_f32(kscale, at)) : read_lane_f32(kscale, at);
+        vs_next[g] = kFolded ? rest(read_lane_f32(vscale, at)) : read_lane_f32(vscale, at);
       }
   };
   bool odd = false;
@@ -648,12 +679,12 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
       if (masked && t0 + row >= it.draft && t0 + row < it.k1) v = drop_odd<DT, F8>(v, &odd);
       if constexpr (F8) {
         uint4 lo, hi;
-        widen<DT>(rk[j], &lo, &hi);
-        *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 16) = lo;
-        *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 16 + 8) = hi;
-        widen<DT>(v, &lo, &hi);
-        *reinterpret_cast<uint4 *>(s_v + row * kVRow + piece * 16) = lo;
-        *reinterpret_cast<uint4 *>(s_v + row * kVRow + piece * 16 + 8) = hi;
+        widen<DT>(rk[j], kw[j], &lo, &hi);
+        *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 8) = lo;
+        *reinterpret_cast<uint4 *>(s_k + row * kRow + (kChunks + piece) * 8) = hi;
+        widen<DT>(v, vw[j], &lo, &hi);
+        *reinterpret_cast<uint4 *>(s_v + row * kVRow + piece * 8) = lo;
+        *reinterpret_cast<uint4 *>(s_v + row * kVRow + (kChunks + piece) * 8) = hi;
       } else {
         *reinterpret_cast<uint4 *>(s_k + row * kRow + piece * 8) = rk[j];
         *reinterpret_cast<uint4 *>(s_v + row * kVRow + piece * 8) = v;
@@ -661,6 +692,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
     }
 #pragma unroll
     for (int g = 0; g < 2 * SB; ++g) ks[g] = ks_next[g], vs[g] = vs_next[g];
+    plain_scales = plain_next;
     __syncthreads();
     if (t0 + KT < it.k1) load(t0 + KT);
     if (t0 + wk * SB * 32 >= it.k1) continue;  // nothing of this tile for this wave
@@ -673,10 +705,12 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
         s[sb] = T::mma(*reinterpret_cast<const uint4 *>(s_k + ((wk * SB + sb) * 32 + q32) * kRow + d * 16 + half * 8), qf[d], s[sb]);
-      if (F8)
+    }
+    if (F8 && !(kFolded && plain_scales))
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[sb][e] *= ks[2 * sb + (e >> 3)];
-    }
     if (masked || t0 + KT > it.k1) {
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb)
@@ -735,9 +769,13 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
         s[sb][e] = exp2_fast(T::kLift > 0 ? __builtin_fmaf(s[sb][e] - top_s, A.scale_log2, T::kLift)
                                           : __builtin_fmaf(s[sb][e], A.scale_log2, -mu));
         sum += s[sb][e];
-        if (F8) s[sb][e] *= wt[2 * sb + (e >> 3)];
       }
     l += sum;
+    if (F8 && !(kFolded && plain_scales))
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[sb][e] *= wt[2 * sb + (e >> 3)];
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb) {
       const int kb = (wk * SB + sb) * 32;  // this block's first key in the tile
@@ -773,7 +811,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           float4 a = make_float4(o[t][4 * f] * ref, o[t][4 * f + 1] * ref, o[t][4 * f + 2] * ref, o[t][4 * f + 3] * ref);
-          const int d = t * 32 + 8 * f + 4 * half;
+          const int d = place_d(t * 4 + f) + 4 * half;
           if (any_odd) a = add_odd_paged<DT, F8>(A, it, s_anc[r], d, a);
           *reinterpret_cast<float4 *>(po + d) = a;
         }
@@ -797,7 +835,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
     for (int t = 0; t < D / 32; ++t)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<float4 *>(s_o + (wk * kRows + row) * (D + 4) + t * 32 + 8 * g + 4 * half) =
+        *reinterpret_cast<float4 *>(s_o + (wk * kRows + row) * (D + 4) + place_d(t * 4 + g) + 4 * half) =
           make_float4(o[t][4 * g] * f, o[t][4 * g + 1] * f, o[t][4 * g + 2] * f, o[t][4 * g + 3] * f);
   __syncthreads();
   for (int z = tid; z < live * (D / 4); z += kAtThreads) {
@@ -896,38 +934,36 @@ __device__ __forceinline__ void prefix_item(const PagedAttendArgs &A, int id, in
   it->draft = it->k1 + (1 << 30);
 }
 
-// Up to 16 stacked rows of a sequence.  PREFIX: 0 none, 1 tiles of 16 rows, 2
-// tiles of 64 (rows of the whole batch).  tree: nothing for a window, or the
-// TreeParents.
-template <int DT, bool F8, int D, int PREFIX, int WAVES, class... Tree>
-__global__ void __launch_bounds__(64 * WAVES, F8 ? 4 : 2) k_paged_few(PagedAttendArgs A, Tree... tree) {
-  constexpr size_t kOwn = few_bytes<F8, D, 16, false, WAVES>(), kPrefix = PREFIX == 2 ? few_bytes<F8, D, 16, true, WAVES>() : 0;
+// Up to 16 stacked rows of a sequence.  PREFIX: 1 tiles of 16 rows (none where
+// there is no prefix), 2 tiles of 64 (rows of the whole batch).  tree: nothing
+// for a window, or the TreeParents.
+template <int DT, bool F8, int D, int PREFIX, class... Tree>
+__global__ void __launch_bounds__(kAtThreads, F8 ? 4 : 2) k_paged_few(PagedAttendArgs A, Tree... tree) {
+  constexpr size_t kOwn = few_bytes<F8, D, 16, false>(), kPrefix = PREFIX == 2 ? few_bytes<F8, D, 16, true>() : 0;
   __shared__ uint4 s_tile[(kOwn > kPrefix ? kOwn : kPrefix) / sizeof(uint4)];
   __shared__ uint32_t s_anc[16][8];  // (16 stacked rows are 16 rows at most)
   __shared__ uint8_t s_parent[16];
-  __shared__ float2 s_ml[16 * WAVES];
+  __shared__ float2 s_ml[16 * kFewWaves];
   char *lds = reinterpret_cast<char *>(s_tile);
   PagedItem it{};
-  if constexpr (PREFIX > 0) {
-    if (static_cast<int>(blockIdx.x) < A.prefix_items) {
-      prefix_item(A, blockIdx.x, PREFIX == 2 ? 16 * WAVES : 16, &it);
-      few_item<DT, F8, D, 16, PREFIX == 2, WAVES>(A, it, lds, s_anc, s_ml, false);
-      return;
-    }
+  if (static_cast<int>(blockIdx.x) < A.prefix_items) {
+    prefix_item(A, blockIdx.x, PREFIX == 2 ? 16 * kFewWaves : 16, &it);
+    few_item<DT, F8, D, 16, PREFIX == 2>(A, it, lds, s_anc, s_ml, false);
+    return;
   }
   bool direct = false;
   if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 16, &it, &direct)) return;
-  if (it.k1 > it.draft) ancestor_sets<64 * WAVES>(A.R, s_anc, s_parent, tree...);
+  if (it.k1 > it.draft) ancestor_sets(A.R, s_anc, s_parent, tree...);
   __syncthreads();
-  few_item<DT, F8, D, 16, false, WAVES>(A, it, lds, s_anc, s_ml, direct);
+  few_item<DT, F8, D, 16, false>(A, it, lds, s_anc, s_ml, direct);
 }
 
 // More rows: tiles of 32, 64 or 128 stacked rows on 1, 2 or 4 waves, WQP of the
 // prefix and WQO of the sequences.
 template <int DT, bool F8, int D, int WQP, int WQO, class... Tree>
 __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs A, Tree... tree) {
-  constexpr size_t kP = WQP == 1 ? few_bytes<F8, D, 32, false, 4>() : pg_tile_bytes<D, WQP>();
-  constexpr size_t kO = WQO == 1 ? few_bytes<F8, D, 32, false, 4>() : pg_tile_bytes<D, WQO>();
+  constexpr size_t kP = WQP == 1 ? few_bytes<F8, D, 32, false>() : pg_tile_bytes<D, WQP>();
+  constexpr size_t kO = WQO == 1 ? few_bytes<F8, D, 32, false>() : pg_tile_bytes<D, WQO>();
   __shared__ uint4 s_tile[(kP > kO ? kP : kO) / sizeof(uint4)];
   __shared__ uint32_t s_anc[kTreeMaxNodes][8];
   __shared__ uint8_t s_parent[kTreeMaxNodes];
@@ -936,7 +972,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs 
   PagedItem it{};
   if (static_cast<int>(blockIdx.x) < A.prefix_items) {
     prefix_item(A, blockIdx.x, 32 * WQP, &it);
-    if constexpr (WQP == 1) few_item<DT, F8, D, 32, false, 4>(A, it, lds, s_anc, s_ml, false);
+    if constexpr (WQP == 1) few_item<DT, F8, D, 32, false>(A, it, lds, s_anc, s_ml, false);
     else paged_item<DT, F8, D, WQP>(A, it, lds, s_anc, s_ml);
     return;
   }
@@ -944,7 +980,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs 
   if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 32 * WQO, &it, &direct)) return;
   if (it.k1 > it.draft) ancestor_sets(A.R, s_anc, s_parent, tree...);
   __syncthreads();
-  if constexpr (WQO == 1) few_item<DT, F8, D, 32, false, 4>(A, it, lds, s_anc, s_ml, direct);
+  if constexpr (WQO == 1) few_item<DT, F8, D, 32, false>(A, it, lds, s_anc, s_ml, direct);
   else paged_item<DT, F8, D, WQO>(A, it, lds, s_anc, s_ml);
 }
 
@@ -1014,8 +1050,8 @@ namespace {
 
 // kernel(A) or kernel(A, parents).
 template <class Plain, class Tree>
-void launch(Plain plain, Tree tree, const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st, int waves = 4) {
-  const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks)), threads(64 * waves);
+void launch(Plain plain, Tree tree, const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(P.prefix_items + P.own_blocks)), threads(kAtThreads);
   if (parents) hipLaunchKernelGGL(tree, grid, threads, 0, st, A, *parents);
   else hipLaunchKernelGGL(plain, grid, threads, 0, st, A);
 }
@@ -1024,10 +1060,8 @@ template <int DT, bool F8, int D>
 void launch_dim(const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
   using T = TreeParents;
   if (P.few == 16) {
-    constexpr int kWide = F8 ? 16 : 8;  // (16-bit keys and values fill the LDS with 8 waves)
-    if (P.wide) launch(k_paged_few<DT, F8, D, 0, kWide>, k_paged_few<DT, F8, D, 0, kWide, T>, A, parents, P, st, kWide);
-    else if (P.prefix_items == 0 || P.prefix_waves == 1) launch(k_paged_few<DT, F8, D, 1, 4>, k_paged_few<DT, F8, D, 1, 4, T>, A, parents, P, st);
-    else launch(k_paged_few<DT, F8, D, 2, 4>, k_paged_few<DT, F8, D, 2, 4, T>, A, parents, P, st);
+    if (P.prefix_items == 0 || P.prefix_waves == 1) launch(k_paged_few<DT, F8, D, 1>, k_paged_few<DT, F8, D, 1, T>, A, parents, P, st);
+    else launch(k_paged_few<DT, F8, D, 2>, k_paged_few<DT, F8, D, 2, T>, A, parents, P, st);
   } else if (P.prefix_waves == 4) {
     // (a sequence's rows are no more than the batch's: 4 waves on them mean 4 on the prefix)
     if (P.own_waves == 4) launch(k_paged_attend<DT, F8, D, 4, 4>, k_paged_attend<DT, F8, D, 4, 4, T>, A, parents, P, st);

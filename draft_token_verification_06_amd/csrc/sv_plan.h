@@ -248,7 +248,7 @@ inline int64_t attend_range(int64_t keys, int64_t parts) { return ((keys + parts
 // there is work for many rounds already (crowded), ranges of about 1024 keys
 // keep the items even; longer sequences then have longer ranges, 16 of them or
 // what fills the chip once, so that partial outputs do not follow the length.
-inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded, int64_t slots = kAttendSlots) {
+inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded, int64_t slots = kAttendSlots, int64_t join = 64) {
   if (crowded) {
     const int64_t fill = (slots + items - 1) / items, cap = fill > 16 ? fill : 16;
     const int64_t p = (keys + 1023) / 1024;
@@ -261,7 +261,7 @@ inline int attend_parts(int64_t keys, int64_t items, int64_t rows, bool crowded,
     if (p == 8 * step) step *= 2;  // eight candidates, then four per doubling
     const int64_t last = items * p % slots;
     const int64_t rounds = items * p / slots * 20 + (last == 0 ? 0 : last <= slots / 2 ? 13 : 20);
-    const int64_t cost = rounds * (attend_range(keys, p) + kAttendMinKeys + 2 * rows) + 20 * 64 * p;
+    const int64_t cost = rounds * (attend_range(keys, p) + kAttendMinKeys + 2 * rows) + 20 * join * p;
     if (best < 0 || cost < best) {
       best = cost;
       parts = static_cast<int>(p);
@@ -307,16 +307,14 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
 
 // Attention over pages.  The rows of a sequence (times the heads of a group)
 // choose the kernel: up to 16 or 32 of them stay one tile (few), more go by
-// tiles of 64 or 128 as above.  Tiles of 16 rows hold half of the registers,
-// four workgroups on a CU; where there are no more items than CUs and no prefix,
-// a workgroup is 8 or 16 waves instead (wide), so that some thousands of keys need
-// no join.
+// tiles of 64 or 128 as above.  Tiles of 16 rows hold half of the registers: four
+// workgroups on a CU.  The join of pages reads 8 ranges at a time, so that a range
+// of a sequence costs it less (16 keys; a prefix's as above, where every row of
+// the batch writes and reads one: 132 us with 2 of them, 138 with 8).
 constexpr int64_t kPagedFewSlots = 1024;
-constexpr int64_t kPagedWideItems = 256;
-constexpr int64_t kPagedWideKeys = 2048;  // keys that such a workgroup takes alone
+constexpr int64_t kPagedJoin = 16;
 struct PagedPlan : AttendPlan {
   int few;
-  bool wide;
   bool direct;  // a sequence of one range needs no partial outputs
 };
 
@@ -324,25 +322,20 @@ inline PagedPlan plan_paged(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D
   PagedPlan L{};
   const int64_t n = Hq / Hkv, all = B * R * n, own = R * n;
   L.few = own <= 16 ? 16 : own <= 32 ? 32 : 0;
-  L.wide = L.few == 16 && P == 0 && B * Hkv <= kPagedWideItems;
   L.direct = L.few > 0 && P == 0;
   L.own_waves = own > kAttendWideRows ? 4 : own > 32 ? 2 : 1;
   L.prefix_waves = all > kAttendWideRows ? 4 : 1;
   const int64_t own_rows = L.few > 0 ? L.few : 32 * L.own_waves;
   const int64_t prefix_rows = L.few == 16 ? (L.prefix_waves == 4 ? 64 : 16) : 32 * L.prefix_waves;
   const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
-  const int64_t slots = L.wide ? kPagedWideItems : L.few == 16 ? kPagedFewSlots : kAttendSlots;
+  const int64_t slots = L.few == 16 ? kPagedFewSlots : kAttendSlots;
   L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
   const int64_t own_items = B * Hkv * L.own_tiles;
   const int longest = attend_bucket(static_cast<int>(max_ctx + R));
   for (int j = 0; j <= longest; ++j) {
     const int64_t keys = int64_t{128} << j;
     const bool crowded = own_items * ((keys + 1023) / 1024) >= 4 * slots;
-    int64_t parts = attend_parts(keys, own_items, own < own_rows ? own : own_rows, crowded, slots);
-    if (L.wide) {
-      const int64_t most = (keys + kPagedWideKeys / 2 - 1) / (kPagedWideKeys / 2);
-      parts = keys <= kPagedWideKeys ? 1 : parts < most ? parts : most;
-    }
+    int64_t parts = attend_parts(keys, own_items, own < own_rows ? own : own_rows, crowded, slots, kPagedJoin);
     const int64_t range = attend_range(keys, parts);
     L.split.tiles[j / 4] |= static_cast<uint64_t>(range / 128) << (16 * (j % 4));
     parts = (keys + range - 1) / range;

@@ -1,7 +1,6 @@
 """The paged cache's ABI (include/sv_cache.h): every declared function is
 exported and bound, and links from C11, whose host-only results equal those
 the Python side gets through ctypes; no GPU is needed."""
-import ctypes
 import os
 import re
 import shutil
@@ -41,6 +40,6 @@ def test_c_client(tmp_path):
     got = [line.split(" ", 1) for line in run.stdout.splitlines()]
     assert {v.split()[0] for k, v in got if k == "linked" and v.split()[1] == "1"} == _declared()
     got = {k: int(v) for k, v in got if k != "linked"}
-    assert got == {"turns": 0, "quarter": 1, "back": 1, "struct_bytes": ctypes.sizeof(_lib.PagedCacheArgs),
+    assert got == {"turns": 0, "quarter": 1, "back": 1, "struct_bytes": _lib.PAGED_CACHE.size,
                    "attention_ws": _lib.lib().sv_paged_attention_workspace(64, 9, 32, 8, 128, 8192, 1024), "attention_ws_bad": 0,
                    "rotary_null": -1, "append_null": -1, "attention_null": -1, "commit_null": -1}

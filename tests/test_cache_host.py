@@ -18,7 +18,7 @@ def _cache(**kw):
     a = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, dtype=F8, num_pages=100, page=64, block=32, Hkv=2, D=128,
              page_stride=0, token_stride=0, head_stride=0)
     a.update(kw)
-    return ctypes.byref(_lib.PagedCacheArgs(*a.values()))
+    return _lib.PAGED_CACHE.pack(*(x or 0 for x in a.values()))
 
 
 def _ints(xs):
