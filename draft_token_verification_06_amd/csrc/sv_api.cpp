@@ -850,10 +850,10 @@ bool table_ok(const int32_t *table, int64_t *stride, int32_t table_pages, int32_
 }
 
 // False for sizes outside the rules; else their plan.
-bool paged_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, PagedPlan *L) {
+bool paged_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, bool f8, PagedPlan *L) {
   AttendPlan same;  // the rules are sv_attention's
   if (!attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &same)) return false;
-  *L = plan_paged(B, R, Hq, Hkv, D, P, max_ctx);
+  *L = plan_paged(B, R, Hq, Hkv, D, P, max_ctx, f8);
   return L->prefix_items <= INT32_MAX && grid_fits(L->prefix_items + L->own_blocks, kAttendThreads);
 }
 
@@ -1030,8 +1030,10 @@ int sv_cache_commit(const sv_paged_cache *cache, int32_t layers, int64_t layer_s
 }
 
 size_t sv_paged_attention_workspace(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
-  PagedPlan L;
-  return paged_plan(B, R, Hq, Hkv, D, P, max_ctx, &L) ? L.total : 0;
+  // (for pages of either width)
+  PagedPlan L, M;
+  if (!paged_plan(B, R, Hq, Hkv, D, P, max_ctx, true, &L) || !paged_plan(B, R, Hq, Hkv, D, P, max_ctx, false, &M)) return 0;
+  return std::max(L.total, M.total);
 }
 
 int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_paged_cache *cache,
@@ -1046,7 +1048,7 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
   const int cst = cache_pool(cache, dtype, &c, &A.pool);
   if (cst != SV_OK) return cst;
   PagedPlan L;
-  if (!paged_plan(B, R, Hq, c.Hkv, c.D, P, max_ctx, &L)) return SV_EINVAL;
+  if (!paged_plan(B, R, Hq, c.Hkv, c.D, P, max_ctx, c.dtype == SV_DT_F8E4M3, &L)) return SV_EINVAL;
   TreeParents parents;
   if (parent_host) {
     const int tst = tree_parents(parent_host, R, &parents);

@@ -41,9 +41,9 @@ struct PagedItem {
 
 template <int D> constexpr int pg_key_row() { return D + 8; }
 template <int D> constexpr int pg_value_row() { return D + 16; }
-template <int WQ> constexpr int pg_tile_keys() { return WQ == 1 ? 128 : 64; }
+constexpr int kPgTileKeys = 64;
 template <int D, int WQ> constexpr size_t pg_tile_bytes() {
-  const size_t kv = static_cast<size_t>(pg_tile_keys<WQ>()) * (pg_key_row<D>() + pg_value_row<D>()) * 2;
+  const size_t kv = static_cast<size_t>(kPgTileKeys) * (pg_key_row<D>() + pg_value_row<D>()) * 2;
   const size_t merge = WQ < 4 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
   return kv > merge ? kv : merge;
 }
@@ -139,24 +139,18 @@ template <int DT> __device__ __forceinline__ pg_f32x4_t mma16(uint4 a, uint4 b, 
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(at_f16x8_t, a), __builtin_bit_cast(at_f16x8_t, b), c, 0, 0, 0);
 }
 
-// The sum / maximum over the lanes that hold one row: l ^ 32 (32 rows), and l ^ 16 (16 rows).
-template <int ROWS> __device__ __forceinline__ float row_max(float x) {
+// The maximum and the sum over the lanes that hold one row: l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float row_max(float x) {
   const float2 h = both_halves(x);
   x = fmaxf(h.x, h.y);
-  if (ROWS == 16) {
-    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-  }
-  return x;
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
-template <int ROWS> __device__ __forceinline__ float row_sum(float x) {
+__device__ __forceinline__ float row_sum(float x) {
   const float2 h = both_halves(x);
   x = h.x + h.y;
-  if (ROWS == 16) {
-    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-  }
-  return x;
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
 // Bytes between rows of LDS.  Key rows of 16 bytes more put the rows that 8 lanes
@@ -164,75 +158,77 @@ template <int ROWS> __device__ __forceinline__ float row_sum(float x) {
 // bits: 16 bytes more) or 4 of 32 (16 bits: 32 bytes more).
 template <bool F8, int D> constexpr int few_key_pitch() { return F8 ? D + 16 : 2 * D + 16; }
 template <bool F8, int D> constexpr int few_value_pitch() { return F8 ? D + 16 : 2 * D + 32; }
-template <bool F8, int D, int ROWS, bool SHARED> constexpr size_t few_bytes() {
-  const size_t tile = static_cast<size_t>(SHARED ? 64 : 32 * kFewWaves) * (few_key_pitch<F8, D>() + few_value_pitch<F8, D>());
-  const size_t merge = SHARED ? 0 : static_cast<size_t>(kFewWaves) * ROWS * (64 + 4) * 4;
+template <bool F8, int D, int NC> constexpr size_t few_bytes() {
+  const size_t tile = static_cast<size_t>(32 * kFewWaves) * (few_key_pitch<F8, D>() + few_value_pitch<F8, D>());
+  const size_t merge = static_cast<size_t>(kFewWaves) * 16 * NC * (64 + 4) * 4;
   return tile > merge ? tile : merge;
 }
 
 }  // namespace
 
-// Few rows: tiles of 16 or 32 stacked rows.  Keys and values lie in LDS as the
-// pages hold them and become operands in registers.  Apart (SHARED = false): every
-// wave has blocks of 32 keys of its own for the same rows, so the waves run
-// without barriers until the end; SHARED: the workgroup's waves have rows of
-// their own and read the same 64 keys.
+// Few rows: NC tiles of 16 stacked rows.  Keys and values lie in LDS as the pages
+// hold them and become operands in registers, once for all tiles.  Every wave has
+// blocks of 32 keys of its own for the same rows, so the waves run without
+// barriers until the end.
 //
 // The k order of a product may be any that both operands share, and so may the
 // keys' order in the score tile.  Keys are placed in LDS such that a lane's
-// exponentials belong to 8 (twice 8) consecutive keys: the operand of the second
-// product as they are, under one scale each, against values whose transposing
-// read takes 8 consecutive rows (no bank conflicts).
-template <int DT, bool F8, int D, int ROWS, bool SHARED>
+// exponentials belong to 8 consecutive keys: the operand of the second product as
+// they are, under one scale, against values whose transposing read takes 8
+// consecutive rows (no bank conflicts).
+template <int DT, bool F8, int D, int NC>
 __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedItem &it, char *lds, const uint32_t (*s_anc)[8],
                                          float2 *s_ml, bool direct) {
   using T = AtElt<DT>;
-  constexpr bool k16 = ROWS == 16;
-  constexpr int KB = SHARED ? 2 : 1;                 // blocks of 32 keys of a wave and tile
-  constexpr int WAVES = kFewWaves;
-  constexpr int KT = SHARED ? 64 : 32 * WAVES;
-  constexpr int kWaveKeys = SHARED ? KT / WAVES : 32;  // keys that a wave fetches
+  constexpr int ROWS = 16 * NC;
+  constexpr int KT = 32 * kFewWaves;                   // keys of a tile, 32 of them a wave's
   constexpr int kBytes = F8 ? 1 : 2;
-  constexpr int kChunks = D * kBytes / 16;           // 16-byte pieces of a row
-  constexpr int kWaveRows = 64 / kChunks;            // rows of one load of a wave: within a strip
-  constexpr int kLoads = kWaveKeys / kWaveRows;
-  constexpr int NK = k16 ? 8 : 16;                   // keys of a lane and block
+  constexpr int kChunks = D * kBytes / 16;             // 16-byte pieces of a row
+  constexpr int kWaveRows = 64 / kChunks;              // rows of one load of a wave: within a strip
+  constexpr int kLoads = 32 / kWaveRows;
   constexpr int kKP = few_key_pitch<F8, D>(), kVP = few_value_pitch<F8, D>();
   constexpr bool kRelative = F8 && T::kLift > 0;
-  static_assert(kWaveKeys % kWaveRows == 0 && kLoads >= 1, "whole loads");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & (ROWS - 1), grp = lane / ROWS;
-  char *s_k = lds + (SHARED ? 0 : wave * 32 * (kKP + kVP));
-  char *s_v = s_k + (SHARED ? KT : 32) * kKP;
+  const int col = lane & 15, grp = lane >> 4;
+  char *s_k = lds + wave * 32 * (kKP + kVP), *s_v = s_k + 32 * kKP;
 
-  // this lane's row, its query fragments
-  const int i = it.row0 + (SHARED ? wave * ROWS : 0) + col;
-  const int ic = min(i, it.rows - 1);
-  const int64_t qrow = it.base_row + ic / A.n;
-  const int head = it.kvh * A.n + ic % A.n;
-  constexpr int kSteps = D / (k16 ? 32 : 16);        // matrix steps of a score
-  uint4 qf[kSteps];
-  {
-    const uint16_t *p = A.q + qrow * A.q_row_stride + head * D;
+  // this lane's rows (col of each tile), their query fragments
+  constexpr int kSteps = D / 32;                       // matrix steps of a score
+  uint4 qf[NC][kSteps];
+  int rows[NC];                                        // rows of the step, for their ancestors
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int ic = min(it.row0 + 16 * c + col, it.rows - 1);
+    const int64_t qrow = it.base_row + ic / A.n;
+    const uint16_t *p = A.q + qrow * A.q_row_stride + (it.kvh * A.n + ic % A.n) * D;
+    rows[c] = static_cast<int>(qrow % A.R);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       // 8 bits: a 16-byte read of keys is two steps' operands
-      const int d = F8 ? (s >> 1) * (k16 ? 64 : 32) + 16 * grp + 8 * (s & 1) : s * (k16 ? 32 : 16) + 8 * grp;
-      qf[s] = load_vec(p + d);
+      qf[c][s] = load_vec(p + (F8 ? (s >> 1) * 64 + 16 * grp + 8 * (s & 1) : s * 32 + 8 * grp));
       // a negative scale acts on the queries' signs, so that larger products are larger scores
-      if (A.negate) qf[s] = make_uint4(qf[s].x ^ 0x80008000u, qf[s].y ^ 0x80008000u, qf[s].z ^ 0x80008000u, qf[s].w ^ 0x80008000u);
+      if (A.negate) qf[c][s] = make_uint4(qf[c][s].x ^ 0x80008000u, qf[c][s].y ^ 0x80008000u, qf[c][s].z ^ 0x80008000u, qf[c][s].w ^ 0x80008000u);
     }
   }
-  const int r = static_cast<int>(qrow % A.R);
 
-  constexpr int kTiles = D / ROWS, kOut = k16 ? 4 : 16;  // output tiles, values of a lane in each
-  typename std::conditional<k16, pg_f32x4_t, at_f32x16_t>::type o[kTiles];
+  constexpr int kTiles = D / 16;  // output tiles: values 16 t + 4 grp .. + 3 of a row
+  pg_f32x4_t o[NC][kTiles];
+  float m[NC], l[NC];             // l: this lane's keys only
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t)
+  for (int c = 0; c < NC; ++c) {
+    m[c] = kNegInf, l[c] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kOut; ++e) o[t][e] = 0.0f;
-  float m = kNegInf, l = 0.0f;  // l: this lane's keys only
+    for (int t = 0; t < kTiles; ++t) o[c][t] = pg_f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   float ref = kRelative ? 0.0f : 1.0f;
+  auto rescale_all = [&](const float (&f)[NC]) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][t][e] *= f[c];
+  };
 
   // the strips of the look-up that begins at token c0, one per lane
   int c0 = it.k0, pages = 0;
@@ -254,18 +250,18 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
   look_up(it.k0);
 
   uint4 rk[kLoads], rv[kLoads];
-  float ks[2 * KB], vs[2 * KB], ks_next[2 * KB], vs_next[2 * KB];  // scales of this wave's strips, of the tile and of the one loaded
+  float ks[2], vs[2], ks_next[2], vs_next[2];  // scales of this wave's strips, of the tile and of the one loaded
   const int piece = lane % kChunks, row_lane = lane / kChunks;
   const uint32_t lane_off = static_cast<uint32_t>(row_lane) * static_cast<uint32_t>(A.pool.token_bytes) + piece * 16;
   const int page_mask = (1 << A.pool.page_shift) - 1;
   const int64_t head_off = it.kvh * A.pool.head_bytes;
   // one sequence's pages are read once: streamed
-  auto fetch = [&](const uint8_t *p) { return SHARED ? load_vec(p) : load_stream(reinterpret_cast<const uint4 *>(p)); };
+  auto fetch = [&](const uint8_t *p) { return load_stream(reinterpret_cast<const uint4 *>(p)); };
   auto load = [&](int t0) {
     if (t0 - c0 >= kLookup) look_up(t0);
 #pragma unroll
-    for (int g = 0; g < kLoads * kWaveRows / kStrip; ++g) {
-      const int key = min(t0 + wave * kWaveKeys + g * kStrip, last);
+    for (int g = 0; g < 2; ++g) {
+      const int key = min(t0 + wave * 32 + g * kStrip, last);
       const int page = __builtin_amdgcn_readlane(pages, (key - c0) / kStrip);
       const int64_t off = page * A.pool.page_bytes + (key & page_mask) * A.pool.token_bytes + head_off;
 #pragma unroll
@@ -277,264 +273,210 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
     }
     if (F8)
 #pragma unroll
-      for (int g = 0; g < 2 * KB; ++g) {
-        const int at = (min(t0 + (SHARED ? 0 : wave * 32) + g * kStrip, last) - c0) / kStrip;
+      for (int g = 0; g < 2; ++g) {
+        const int at = (min(t0 + wave * 32 + g * kStrip, last) - c0) / kStrip;
         ks_next[g] = read_lane_f32(kscale, at);
         vs_next[g] = read_lane_f32(vscale, at);
       }
   };
-  auto tile_barrier = [&]() {
-    if (SHARED) __syncthreads();
-    else __builtin_amdgcn_wave_barrier();
-  };
-  // LDS row of the tile's key: see above
-  auto key_row = [](int key) {
-    const int a = key & 31;
-    const int at = k16 ? 16 * ((a >> 2) & 1) + 4 * (a >> 3) + (a & 3) : 8 * (2 * (a >> 4) + ((a >> 2) & 1)) + 4 * ((a >> 3) & 1) + (a & 3);
-    return (key & ~31) + at;
-  };
+  // LDS row of a key of the wave's: see above
+  auto key_row = [](int key) { return 16 * ((key >> 2) & 1) + 4 * (key >> 3) + (key & 3); };
   bool odd = false;
   load(it.k0);
   for (int t0 = it.k0; t0 < it.k1; t0 += KT) {
-    const int w0 = t0 + (SHARED ? 0 : wave * 32);  // the wave's first key
+    const int w0 = t0 + wave * 32;  // the wave's first key
     // Keys past the range get zero values: their exponentials are zero, but
     // zero times what a page holds behind the last token need not be.
     // Infinities and NaN among the step's own values, which must reach only the
     // rows that see them, are left out here and added at the end.
-    const bool masked = t0 + KT > it.draft, plain = !masked && t0 + KT <= it.k1;
-    tile_barrier();
+    const bool plain = t0 + KT <= it.draft && t0 + KT <= it.k1;
+    __builtin_amdgcn_wave_barrier();
     if (!plain) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int key = w0 + (SHARED ? wave * kWaveKeys : 0) + j * kWaveRows + row_lane;
+        const int key = w0 + j * kWaveRows + row_lane;
         if (key >= it.k1) rv[j] = make_uint4(0, 0, 0, 0);
         else if (key >= it.draft) rv[j] = drop_odd<DT, F8>(rv[j], &odd);
       }
     }
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int at = (SHARED ? wave * kWaveKeys : 0) + j * kWaveRows + row_lane;  // key within the LDS rows
+      const int at = j * kWaveRows + row_lane;
       *reinterpret_cast<uint4 *>(s_k + key_row(at) * kKP + piece * 16) = rk[j];
       *reinterpret_cast<uint4 *>(s_v + at * kVP + piece * 16) = rv[j];
     }
 #pragma unroll
-    for (int g = 0; g < 2 * KB; ++g) ks[g] = ks_next[g], vs[g] = vs_next[g];
-    tile_barrier();
+    for (int g = 0; g < 2; ++g) ks[g] = ks_next[g], vs[g] = vs_next[g];
+    __builtin_amdgcn_wave_barrier();
     if (t0 + KT < it.k1) load(t0 + KT);
     if (w0 >= it.k1) continue;  // nothing of this tile for this wave
-    // products of the wave's blocks: element e of a lane is key 8 grp + e (16 rows),
-    // 16 (e / 8) + 8 grp + e % 8 (32 rows) of the block
-    float s[KB][NK];
+    // products: element e of a lane is key 8 grp + e
+    float s[NC][8];
+    {
+      pg_f32x4_t acc[2][NC];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      if constexpr (k16) {
+      for (int tau = 0; tau < 2; ++tau)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[tau][c] = pg_f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < (F8 ? D / 64 : D / 32); ++x)
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau) {
-          pg_f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-          const char *row = s_k + (b * 32 + tau * 16 + col) * kKP + grp * 16;
+          const uint4 w = *reinterpret_cast<const uint4 *>(s_k + (tau * 16 + col) * kKP + grp * 16 + x * 64);
           if constexpr (F8) {
+            const uint4 k0 = widen8<DT>(make_uint2(w.x, w.y)), k1 = widen8<DT>(make_uint2(w.z, w.w));
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(row + x * 64);
-              acc = mma16<DT>(widen8<DT>(make_uint2(w.x, w.y)), qf[2 * x], acc);
-              acc = mma16<DT>(widen8<DT>(make_uint2(w.z, w.w)), qf[2 * x + 1], acc);
-            }
+            for (int c = 0; c < NC; ++c) acc[tau][c] = mma16<DT>(k0, qf[c][2 * x], acc[tau][c]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[tau][c] = mma16<DT>(k1, qf[c][2 * x + 1], acc[tau][c]);
           } else {
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) acc = mma16<DT>(*reinterpret_cast<const uint4 *>(row + x * 64), qf[x], acc);
+            for (int c = 0; c < NC; ++c) acc[tau][c] = mma16<DT>(w, qf[c][x], acc[tau][c]);
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[b][4 * tau + e] = acc[e];
-        }
-      } else {
-        at_f32x16_t acc;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-        const char *row = s_k + (b * 32 + col) * kKP + grp * 16;
-        if constexpr (F8) {
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(row + x * 32);
-            acc = T::mma(widen8<DT>(make_uint2(w.x, w.y)), qf[2 * x], acc);
-            acc = T::mma(widen8<DT>(make_uint2(w.z, w.w)), qf[2 * x + 1], acc);
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) acc = T::mma(*reinterpret_cast<const uint4 *>(row + x * 32), qf[x], acc);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[b][e] = acc[e];
-      }
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[c][e] = acc[e >> 2][c][e & 3];
     }
     if (!plain) {
 #pragma unroll
-      for (int b = 0; b < KB; ++b)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int e = 0; e < NK; ++e) {
-          const int key = w0 + b * 32 + 16 * (e >> 3) + 8 * grp + (e & 7);
+        for (int e = 0; e < 8; ++e) {
+          const int key = w0 + 8 * grp + e;
           const int own = key - it.draft;
-          const bool ok = key < it.k1 && (own < 0 || ((s_anc[r][(own & 255) >> 5] >> (own & 31)) & 1));
-          s[b][e] = ok ? s[b][e] : kNegInf;
+          const bool ok = key < it.k1 && (own < 0 || ((s_anc[rows[c]][(own & 255) >> 5] >> (own & 31)) & 1));
+          s[c][e] = ok ? s[c][e] : kNegInf;
         }
     }
-    // the scales of a lane's 8 (twice 8) keys
-    float kf[KB][NK / 8], vf[KB][NK / 8];
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int x = 0; x < NK / 8; ++x) {
-        kf[b][x] = !F8 ? 1.0f : k16 ? (grp < 2 ? ks[2 * b] : ks[2 * b + 1]) : ks[2 * b + x];
-        vf[b][x] = !F8 ? 1.0f : k16 ? (grp < 2 ? vs[2 * b] : vs[2 * b + 1]) : vs[2 * b + x];
-      }
-    float top = kNegInf;
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int x = 0; x < NK / 8; ++x) {
-        float most = s[b][8 * x];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) most = fmaxf(most, s[b][8 * x + e]);
-        top = fmaxf(top, F8 ? most * kf[b][x] : most);
-      }
-    const float mn = fmaxf(m, row_max<ROWS>(top));
+    // the scales of a lane's 8 keys
+    const float kf = !F8 ? 1.0f : grp < 2 ? ks[0] : ks[1];
+    float vf = !F8 ? 1.0f : grp < 2 ? vs[0] : vs[1];
     // Outputs are rescaled only when some row's maximum rose: 1 is exact.
-    if (__any(mn > m)) {
-      const float alpha = m == kNegInf ? 0.0f : exp2_fast((m - mn) * A.scale_log2);
-      l *= alpha;
+    float mn[NC];
+    bool rose = false;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
+    for (int c = 0; c < NC; ++c) {
+      float top = s[c][0];
 #pragma unroll
-        for (int e = 0; e < kOut; ++e) o[t][e] *= alpha;
-      m = mn;
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, s[c][e]);
+      mn[c] = fmaxf(m[c], row_max(F8 ? top * kf : top));
+      rose |= mn[c] > m[c];
+    }
+    if (__any(rose)) {
+      float alpha[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        alpha[c] = m[c] == kNegInf ? 0.0f : exp2_fast((m[c] - mn[c]) * A.scale_log2);
+        l[c] *= alpha[c];
+        m[c] = mn[c];
+      }
+      rescale_all(alpha);
     }
     if (kRelative) {
-      float most = vs[0];
-#pragma unroll
-      for (int g = 1; g < 2 * KB; ++g) most = fmaxf(most, vs[g]);
+      const float most = fmaxf(vs[0], vs[1]);
       if (most > ref) {
-        const float down = ref / most;
+        float down[NC];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int e = 0; e < kOut; ++e) o[t][e] *= down;
+        for (int c = 0; c < NC; ++c) down[c] = ref / most;
+        rescale_all(down);
         ref = most;
       }
-#pragma unroll
-      for (int b = 0; b < KB; ++b)
-#pragma unroll
-        for (int x = 0; x < NK / 8; ++x) vf[b][x] /= ref;
+      vf /= ref;
     }
     // One multiply-add per exponent, the key scale in its factor (never zero:
     // masked products are -inf).  In float16 the largest is 2^15, held there
     // however far the scores are and whatever their rounding (65504 ends the type).
-    const float mu = m == kNegInf ? 0.0f : m * A.scale_log2;
-    float sum = 0.0f;
+    const float factor = F8 ? fmaxf(A.scale_log2 * kf, __FLT_MIN__) : A.scale_log2;
+    uint4 p[NC];
 #pragma unroll
-    for (int b = 0; b < KB; ++b)
+    for (int c = 0; c < NC; ++c) {
+      const float mu = T::kLift - (m[c] == kNegInf ? 0.0f : m[c] * A.scale_log2);
+      float *e = s[c], sum = 0.0f;
 #pragma unroll
-      for (int x = 0; x < NK / 8; ++x) {
-        const float c = F8 ? fmaxf(A.scale_log2 * kf[b][x], __FLT_MIN__) : A.scale_log2;
-#pragma unroll
-        for (int e = 8 * x; e < 8 * x + 8; ++e) {
-          const float arg = __builtin_fmaf(s[b][e], c, T::kLift - mu);
-          s[b][e] = exp2_fast(T::kLift > 0 && arg > T::kLift ? T::kLift : arg);  // (NaN stays)
-          sum += s[b][e];
-          if (F8) s[b][e] *= vf[b][x];
-        }
+      for (int x = 0; x < 8; ++x) {
+        const float arg = __builtin_fmaf(e[x], factor, mu);
+        e[x] = exp2_fast(T::kLift > 0 && arg > T::kLift ? T::kLift : arg);  // (NaN stays)
+        sum += e[x];
+        if (F8) e[x] *= vf;
       }
-    l += sum;
+      l[c] += sum;
+      p[c] = make_uint4(T::pack(e[0], e[1]), T::pack(e[2], e[3]), T::pack(e[4], e[5]), T::pack(e[6], e[7]));
+    }
+    // values of keys 8 grp .. + 7
+    const char *row = s_v + (8 * grp + ((lane & 15) >> (F8 ? 1 : 2))) * kVP + (F8 ? (lane & 1) * 8 : (lane & 3) * 8);
+    uint2 w[kTiles][F8 ? 1 : 2];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-#pragma unroll
-      for (int x = 0; x < NK / 8; ++x) {
-        const float *e = &s[b][8 * x];
-        const uint4 p = make_uint4(T::pack(e[0], e[1]), T::pack(e[2], e[3]), T::pack(e[4], e[5]), T::pack(e[6], e[7]));
-        // values of keys 8 grp .. + 7 of these 32 (16) keys
-        const char *row = s_v + (b * 32 + 16 * x + 8 * grp + ((lane & 15) >> (F8 ? 1 : 2))) * kVP +
-                          (F8 ? (lane & 1) * 8 : (lane & 3) * 8) + (k16 ? 0 : ((lane >> 4) & 1) * 16 * kBytes);
-        if constexpr (F8) {
-          pg_i32x2_t w[kTiles];
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) w[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(row + t * ROWS));
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            const uint4 v = widen8<DT>(__builtin_bit_cast(uint2, w[t]));
-            if constexpr (k16) o[t] = mma16<DT>(v, p, o[t]);
-            else o[t] = T::mma(v, p, o[t]);
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * ROWS * 2)));
-            const uint2 c = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * ROWS * 2 + 4 * kVP)));
-            const uint4 v = make_uint4(a.x, a.y, c.x, c.y);
-            if constexpr (k16) o[t] = mma16<DT>(v, p, o[t]);
-            else o[t] = T::mma(v, p, o[t]);
-          }
-        }
+    for (int t = 0; t < kTiles; ++t) {
+      if constexpr (F8) {
+        w[t][0] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t)(row + t * 16)));
+      } else {
+        w[t][0] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * 32)));
+        w[t][F8 ? 0 : 1] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(row + t * 32 + 4 * kVP)));
       }
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const uint4 v = F8 ? widen8<DT>(w[t][0]) : make_uint4(w[t][0].x, w[t][0].y, w[t][F8 ? 0 : 1].x, w[t][F8 ? 0 : 1].y);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[c][t] = mma16<DT>(v, p[c], o[c][t]);
     }
   }
   // (also: every wave is done with the tiles)
   const bool any_odd = it.k1 > it.draft ? __syncthreads_or(odd) : (__syncthreads(), false);
-  l = row_sum<ROWS>(l);
-  if (__any(bad)) l = __builtin_nanf("");  // a page that is none: the rows are no numbers
+  const bool any_bad = __any(bad);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    l[c] = row_sum(l[c]);
+    if (any_bad) l[c] = __builtin_nanf("");  // a page that is none: the rows are no numbers
+  }
 
   const int64_t rows_all = static_cast<int64_t>(A.B) * A.R * A.Hq;
-  // value f of a lane's float4 number q: d = (k16 ? 16 t : 32 t + 8 q) + 4 grp + f
-  auto quad = [&](int t, int q, float f) { return make_float4(o[t][4 * q] * f, o[t][4 * q + 1] * f, o[t][4 * q + 2] * f, o[t][4 * q + 3] * f); };
-  if constexpr (SHARED) {
-    if (i < it.rows) {
-      const int64_t at = it.part * rows_all + qrow * A.Hq + head;
-      float *po = A.part_o + at * D;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int q = 0; q < kOut / 4; ++q) {
-          const int d = t * ROWS + 8 * q + 4 * grp;
-          float4 a = quad(t, q, ref);
-          if (any_odd) a = add_odd_paged<DT, F8>(A, it, s_anc[r], d, a);
-          *reinterpret_cast<float4 *>(po + d) = a;
-        }
-      if (grp == 0) A.part_ml[at] = make_float2(m, l);
-    }
-    return;
-  }
   // The waves hold the same rows over different keys: joined in wave order, 64
   // values of a row at a time.
   float *s_o = reinterpret_cast<float *>(lds);
   const int live = min(ROWS, it.rows - it.row0);
-  if (grp == 0) s_ml[wave * ROWS + col] = make_float2(m, l);
-  __syncthreads();
-  float M = kNegInf;
+  if (grp == 0)
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) M = fmaxf(M, s_ml[w * ROWS + col].x);
-  const float f = m == kNegInf ? 0.0f : exp2_fast((m - M) * A.scale_log2) * ref;
+    for (int c = 0; c < NC; ++c) s_ml[wave * ROWS + 16 * c + col] = make_float2(m[c], l[c]);
+  __syncthreads();
+  float f[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float M = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) M = fmaxf(M, s_ml[w * ROWS + 16 * c + col].x);
+    f[c] = m[c] == kNegInf ? 0.0f : exp2_fast((m[c] - M) * A.scale_log2) * ref;
+  }
 #pragma unroll
   for (int part = 0; part < D / 64; ++part) {
     if (part > 0) __syncthreads();
-    if (col < live)
 #pragma unroll
-      for (int t = part * (64 / ROWS); t < (part + 1) * (64 / ROWS); ++t)
+    for (int c = 0; c < NC; ++c)
+      if (16 * c + col < live)
 #pragma unroll
-        for (int q = 0; q < kOut / 4; ++q)
-          *reinterpret_cast<float4 *>(s_o + (wave * ROWS + col) * (64 + 4) + t * ROWS - part * 64 + 8 * q + 4 * grp) = quad(t, q, f);
+        for (int t = 0; t < 4; ++t) {
+          const pg_f32x4_t a = o[c][part * 4 + t];
+          *reinterpret_cast<float4 *>(s_o + (wave * ROWS + 16 * c + col) * (64 + 4) + t * 16 + 4 * grp) =
+            make_float4(a[0] * f[c], a[1] * f[c], a[2] * f[c], a[3] * f[c]);
+        }
     __syncthreads();
-    for (int z = tid; z < live * 16; z += 64 * WAVES) {
+    for (int z = tid; z < live * 16; z += kAtThreads) {
       const int q = z / 16, c = z % 16, d = part * 64 + c * 4;
       const int qi = it.row0 + q;
       float4 a = *reinterpret_cast<const float4 *>(s_o + q * (64 + 4) + c * 4);
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) {
+      for (int w = 1; w < kFewWaves; ++w) {
         const float4 b = *reinterpret_cast<const float4 *>(s_o + (w * ROWS + q) * (64 + 4) + c * 4);
         a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
       }
       if (any_odd) a = add_odd_paged<DT, F8>(A, it, s_anc[qi / A.n], d, a);
       float Mq = kNegInf, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) Mq = fmaxf(Mq, s_ml[w * ROWS + q].x);
+      for (int w = 0; w < kFewWaves; ++w) Mq = fmaxf(Mq, s_ml[w * ROWS + q].x);
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
+      for (int w = 0; w < kFewWaves; ++w) {
         const float2 v = s_ml[w * ROWS + q];
         L += v.x == kNegInf ? v.y : v.y * exp2_fast((v.x - Mq) * A.scale_log2);  // (no maximum: zero, or NaN)
       }
@@ -558,7 +500,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
                                            float2 *s_ml) {
   using T = AtElt<DT>;
   constexpr int WK = 4 / WQ;
-  constexpr int KT = pg_tile_keys<WQ>();
+  constexpr int KT = kPgTileKeys;
   constexpr int SB = KT / (32 * WK);  // 32-key blocks per wave and tile
   constexpr int kRow = pg_key_row<D>(), kVRow = pg_value_row<D>();
   constexpr int kBytes = F8 ? 1 : 2;
@@ -934,36 +876,37 @@ __device__ __forceinline__ void prefix_item(const PagedAttendArgs &A, int id, in
   it->draft = it->k1 + (1 << 30);
 }
 
-// Up to 16 stacked rows of a sequence.  PREFIX: 1 tiles of 16 rows (none where
-// there is no prefix), 2 tiles of 64 (rows of the whole batch).  tree: nothing
-// for a window, or the TreeParents.
-template <int DT, bool F8, int D, int PREFIX, class... Tree>
-__global__ void __launch_bounds__(kAtThreads, F8 ? 4 : 2) k_paged_few(PagedAttendArgs A, Tree... tree) {
-  constexpr size_t kOwn = few_bytes<F8, D, 16, false>(), kPrefix = PREFIX == 2 ? few_bytes<F8, D, 16, true>() : 0;
+// Up to 16 NC stacked rows of a sequence.  MANY: the prefix has the rows of a
+// batch, in tiles of 128 on four waves; else tiles of 16 NC, if there is a prefix.
+// tree: nothing for a window, or the TreeParents.
+template <int DT, bool F8, int D, int NC, bool MANY, class... Tree>
+__global__ void __launch_bounds__(kAtThreads, F8 && NC == 1 && !MANY ? 4 : 2) k_paged_few(PagedAttendArgs A, Tree... tree) {
+  constexpr size_t kOwn = few_bytes<F8, D, NC>(), kPrefix = MANY ? pg_tile_bytes<D, 4>() : 0;
   __shared__ uint4 s_tile[(kOwn > kPrefix ? kOwn : kPrefix) / sizeof(uint4)];
-  __shared__ uint32_t s_anc[16][8];  // (16 stacked rows are 16 rows at most)
-  __shared__ uint8_t s_parent[16];
-  __shared__ float2 s_ml[16 * kFewWaves];
+  __shared__ uint32_t s_anc[16 * NC][8];  // (16 stacked rows are 16 rows at most)
+  __shared__ uint8_t s_parent[16 * NC];
+  __shared__ float2 s_ml[16 * NC * kFewWaves];
   char *lds = reinterpret_cast<char *>(s_tile);
   PagedItem it{};
   if (static_cast<int>(blockIdx.x) < A.prefix_items) {
-    prefix_item(A, blockIdx.x, PREFIX == 2 ? 16 * kFewWaves : 16, &it);
-    few_item<DT, F8, D, 16, PREFIX == 2>(A, it, lds, s_anc, s_ml, false);
+    prefix_item(A, blockIdx.x, MANY ? 128 : 16 * NC, &it);
+    if constexpr (MANY) paged_item<DT, F8, D, 4>(A, it, lds, s_anc, s_ml);
+    else few_item<DT, F8, D, NC>(A, it, lds, s_anc, s_ml, false);
     return;
   }
   bool direct = false;
-  if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 16, &it, &direct)) return;
+  if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 16 * NC, &it, &direct)) return;
   if (it.k1 > it.draft) ancestor_sets(A.R, s_anc, s_parent, tree...);
   __syncthreads();
-  few_item<DT, F8, D, 16, false>(A, it, lds, s_anc, s_ml, direct);
+  few_item<DT, F8, D, NC>(A, it, lds, s_anc, s_ml, direct);
 }
 
-// More rows: tiles of 32, 64 or 128 stacked rows on 1, 2 or 4 waves, WQP of the
-// prefix and WQO of the sequences.
+// More rows: tiles of 64 or 128 stacked rows of a sequence on 2 or 4 waves (WQO),
+// of the prefix 32 or 128 (WQP waves).
 template <int DT, bool F8, int D, int WQP, int WQO, class... Tree>
 __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs A, Tree... tree) {
-  constexpr size_t kP = WQP == 1 ? few_bytes<F8, D, 32, false>() : pg_tile_bytes<D, WQP>();
-  constexpr size_t kO = WQO == 1 ? few_bytes<F8, D, 32, false>() : pg_tile_bytes<D, WQO>();
+  constexpr size_t kP = WQP == 1 ? few_bytes<F8, D, 2>() : pg_tile_bytes<D, WQP>();
+  constexpr size_t kO = pg_tile_bytes<D, WQO>();
   __shared__ uint4 s_tile[(kP > kO ? kP : kO) / sizeof(uint4)];
   __shared__ uint32_t s_anc[kTreeMaxNodes][8];
   __shared__ uint8_t s_parent[kTreeMaxNodes];
@@ -972,7 +915,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs 
   PagedItem it{};
   if (static_cast<int>(blockIdx.x) < A.prefix_items) {
     prefix_item(A, blockIdx.x, 32 * WQP, &it);
-    if constexpr (WQP == 1) few_item<DT, F8, D, 32, false>(A, it, lds, s_anc, s_ml, false);
+    if constexpr (WQP == 1) few_item<DT, F8, D, 2>(A, it, lds, s_anc, s_ml, false);
     else paged_item<DT, F8, D, WQP>(A, it, lds, s_anc, s_ml);
     return;
   }
@@ -980,8 +923,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs 
   if (!own_item<DT, D>(A, blockIdx.x - A.prefix_items, 32 * WQO, &it, &direct)) return;
   if (it.k1 > it.draft) ancestor_sets(A.R, s_anc, s_parent, tree...);
   __syncthreads();
-  if constexpr (WQO == 1) few_item<DT, F8, D, 32, false>(A, it, lds, s_anc, s_ml, direct);
-  else paged_item<DT, F8, D, WQO>(A, it, lds, s_anc, s_ml);
+  paged_item<DT, F8, D, WQO>(A, it, lds, s_anc, s_ml);
 }
 
 // One wave per (row, head): the row's items joined.  Their maxima and sums are
@@ -1056,20 +998,28 @@ void launch(Plain plain, Tree tree, const PagedAttendArgs &A, const TreeParents 
   else hipLaunchKernelGGL(plain, grid, threads, 0, st, A);
 }
 
+template <int DT, bool F8, int D, int NC>
+void launch_few(const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
+  using T = TreeParents;
+  if (P.prefix_items > 0 && P.prefix_waves == 4) launch(k_paged_few<DT, F8, D, NC, true>, k_paged_few<DT, F8, D, NC, true, T>, A, parents, P, st);
+  else launch(k_paged_few<DT, F8, D, NC, false>, k_paged_few<DT, F8, D, NC, false, T>, A, parents, P, st);
+}
+
 template <int DT, bool F8, int D>
 void launch_dim(const PagedAttendArgs &A, const TreeParents *parents, const PagedPlan &P, hipStream_t st) {
   using T = TreeParents;
   if (P.few == 16) {
-    if (P.prefix_items == 0 || P.prefix_waves == 1) launch(k_paged_few<DT, F8, D, 1>, k_paged_few<DT, F8, D, 1, T>, A, parents, P, st);
-    else launch(k_paged_few<DT, F8, D, 2>, k_paged_few<DT, F8, D, 2, T>, A, parents, P, st);
+    launch_few<DT, F8, D, 1>(A, parents, P, st);
+  } else if (P.few == 32) {
+    launch_few<DT, F8, D, 2>(A, parents, P, st);
+  } else if (P.few == 48) {
+    if constexpr (paged_few_rows(F8, D) == 48) launch_few<DT, F8, D, 3>(A, parents, P, st);
   } else if (P.prefix_waves == 4) {
     // (a sequence's rows are no more than the batch's: 4 waves on them mean 4 on the prefix)
     if (P.own_waves == 4) launch(k_paged_attend<DT, F8, D, 4, 4>, k_paged_attend<DT, F8, D, 4, 4, T>, A, parents, P, st);
-    else if (P.own_waves == 2) launch(k_paged_attend<DT, F8, D, 4, 2>, k_paged_attend<DT, F8, D, 4, 2, T>, A, parents, P, st);
-    else launch(k_paged_attend<DT, F8, D, 4, 1>, k_paged_attend<DT, F8, D, 4, 1, T>, A, parents, P, st);
+    else launch(k_paged_attend<DT, F8, D, 4, 2>, k_paged_attend<DT, F8, D, 4, 2, T>, A, parents, P, st);
   } else {
-    if (P.own_waves == 2) launch(k_paged_attend<DT, F8, D, 1, 2>, k_paged_attend<DT, F8, D, 1, 2, T>, A, parents, P, st);
-    else launch(k_paged_attend<DT, F8, D, 1, 1>, k_paged_attend<DT, F8, D, 1, 1, T>, A, parents, P, st);
+    launch(k_paged_attend<DT, F8, D, 1, 2>, k_paged_attend<DT, F8, D, 1, 2, T>, A, parents, P, st);
   }
   if (P.direct && P.own_parts == 1) return;
   const int64_t rows = static_cast<int64_t>(A.B) * A.R * A.Hq;

@@ -306,27 +306,29 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
 }
 
 // Attention over pages.  The rows of a sequence (times the heads of a group)
-// choose the kernel: up to 16 or 32 of them stay one tile (few), more go by
+// choose the kernel: up to 16, 32 or 48 of them stay one tile (few), more go by
 // tiles of 64 or 128 as above.  Tiles of 16 rows hold half of the registers: four
 // workgroups on a CU.  The join of pages reads 8 ranges at a time, so that a range
 // of a sequence costs it less (16 keys; a prefix's as above, where every row of
 // the batch writes and reads one: 132 us with 2 of them, 138 with 8).
 constexpr int64_t kPagedFewSlots = 1024;
 constexpr int64_t kPagedJoin = 16;
+// Most rows of a few (16-bit values of 128 leave no registers for 48).
+constexpr int paged_few_rows(bool f8, int D) { return f8 || D == 64 ? 48 : 32; }
 struct PagedPlan : AttendPlan {
   int few;
   bool direct;  // a sequence of one range needs no partial outputs
 };
 
-inline PagedPlan plan_paged(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx) {
+inline PagedPlan plan_paged(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx, bool f8) {
   PagedPlan L{};
   const int64_t n = Hq / Hkv, all = B * R * n, own = R * n;
-  L.few = own <= 16 ? 16 : own <= 32 ? 32 : 0;
+  L.few = own <= 16 ? 16 : own <= 32 ? 32 : own <= paged_few_rows(f8, D) ? 48 : 0;
   L.direct = L.few > 0 && P == 0;
   L.own_waves = own > kAttendWideRows ? 4 : own > 32 ? 2 : 1;
   L.prefix_waves = all > kAttendWideRows ? 4 : 1;
   const int64_t own_rows = L.few > 0 ? L.few : 32 * L.own_waves;
-  const int64_t prefix_rows = L.few == 16 ? (L.prefix_waves == 4 ? 64 : 16) : 32 * L.prefix_waves;
+  const int64_t prefix_rows = L.prefix_waves == 4 ? 128 : L.few > 0 ? L.few : 32;
   const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
   const int64_t slots = L.few == 16 ? kPagedFewSlots : kAttendSlots;
   L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
