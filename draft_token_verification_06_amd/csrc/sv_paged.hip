@@ -1013,7 +1013,7 @@ void launch_dim(const PagedAttendArgs &A, const TreeParents *parents, const Page
   } else if (P.few == 32) {
     launch_few<DT, F8, D, 2>(A, parents, P, st);
   } else if (P.few == 48) {
-    if constexpr (paged_few_rows(F8, D) == 48) launch_few<DT, F8, D, 3>(A, parents, P, st);
+    if constexpr (paged_few_rows(F8) == 48) launch_few<DT, F8, D, 3>(A, parents, P, st);
   } else if (P.prefix_waves == 4) {
     // (a sequence's rows are no more than the batch's: 4 waves on them mean 4 on the prefix)
     if (P.own_waves == 4) launch(k_paged_attend<DT, F8, D, 4, 4>, k_paged_attend<DT, F8, D, 4, 4, T>, A, parents, P, st);

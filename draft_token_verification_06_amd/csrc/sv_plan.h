@@ -313,8 +313,9 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
 // the batch writes and reads one: 132 us with 2 of them, 138 with 8).
 constexpr int64_t kPagedFewSlots = 1024;
 constexpr int64_t kPagedJoin = 16;
-// Most rows of a few (16-bit values of 128 leave no registers for 48).
-constexpr int paged_few_rows(bool f8, int D) { return f8 || D == 64 ? 48 : 32; }
+// Most rows of a few.  (16-bit pages: 41 rows of 4 trees over 983 keys 19.3 us
+// as 48, 17.1 as 64; and values of 128 leave no registers for 48.)
+constexpr int paged_few_rows(bool f8) { return f8 ? 48 : 32; }
 struct PagedPlan : AttendPlan {
   int few;
   bool direct;  // a sequence of one range needs no partial outputs
@@ -323,7 +324,7 @@ struct PagedPlan : AttendPlan {
 inline PagedPlan plan_paged(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D, int64_t P, int64_t max_ctx, bool f8) {
   PagedPlan L{};
   const int64_t n = Hq / Hkv, all = B * R * n, own = R * n;
-  L.few = own <= 16 ? 16 : own <= 32 ? 32 : own <= paged_few_rows(f8, D) ? 48 : 0;
+  L.few = own <= 16 ? 16 : own <= 32 ? 32 : own <= paged_few_rows(f8) ? 48 : 0;
   L.direct = L.few > 0 && P == 0;
   L.own_waves = own > kAttendWideRows ? 4 : own > 32 ? 2 : 1;
   L.prefix_waves = all > kAttendWideRows ? 4 : 1;
