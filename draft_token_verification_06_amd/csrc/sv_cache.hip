@@ -280,10 +280,11 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // The wave's values y (pass p, token p T + lane / units, 16 of it) whose bit in
 // `live` is set, to the block at `block` (token 0, this head): token u goes to
-// place u + shift.  Places below `first` hold earlier tokens, scaled by *scale.
+// place u + shift.  Places below `first` hold earlier tokens, scaled by held (the
+// value at `scale`, which the caller has asked for with the rows).
 template <int D, int kP>
 __device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live, int shift, int first, uint8_t *block,
-                                         int64_t token_bytes, float *scale, int2 piece) {
+                                         int64_t token_bytes, float *scale, float held, int2 piece) {
   const int lane = threadIdx.x & 63, t_lane = lane / kUnits<D>;
   float a = 0.0f;
 #pragma unroll
@@ -295,7 +296,7 @@ __device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live
   float base = kF8LeastScale;
   bool earlier = false;
   if (first > 0) {
-    const float s0 = read_lane_f32(*scale, 0);  // (the same in every lane: decisions on it are scalar)
+    const float s0 = read_lane_f32(held, 0);  // (the same in every lane: decisions on it are scalar)
     earlier = s0 > 0.0f && finite(s0);
     if (earlier) base = s0;
   }
@@ -420,6 +421,9 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
       }
     };
     if (F8 && !query) {
+      const int64_t at = ((static_cast<int64_t>(page) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * heads + h;
+      float *scale = (value ? A.pool.v_scale : A.pool.k_scale) + at;
+      const float held = t0 > 0 ? *scale : 0.0f;
       float y[kP][16];
       uint32_t live = 0;
 #pragma unroll
@@ -439,8 +443,7 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
         }
       }
       uint8_t *dst = (value ? A.pool.v : A.pool.k) + page * A.pool.page_bytes + in_page * A.pool.token_bytes + h * A.pool.head_bytes;
-      const int64_t at = ((static_cast<int64_t>(page) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * heads + h;
-      store_f8<D, kP>(y, live, t0, t0, dst, A.pool.token_bytes, (value ? A.pool.v_scale : A.pool.k_scale) + at, piece);
+      store_f8<D, kP>(y, live, t0, t0, dst, A.pool.token_bytes, scale, held, piece);
       continue;
     }
 #pragma unroll
@@ -478,15 +481,12 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
 // ---------------------------------------------------------------------------
 namespace {
 
-// Length of sequence b's accepted path; -1: the sequence is left alone.
-__device__ __forceinline__ int path_length(const CommitArgs &A, int b, int ctx) {
+// Nodes that sequence b's accepted path may have; -1: the sequence is left alone.
+__device__ __forceinline__ int path_most(const CommitArgs &A, int b, int ctx) {
   if (ctx < 0 || static_cast<int64_t>(ctx) + A.R > static_cast<int64_t>(A.table_pages) << A.pool.page_shift) return -1;
-  if (!A.nodes) return min(max(A.n_accepted[b], 0), A.R - 1);
-  const int most = min(max(A.n_accepted[b], 0), A.max_nodes);
-  int n = 0;
-  while (n < most && static_cast<uint32_t>(A.nodes[b * A.nodes_stride + n] - 1) < static_cast<uint32_t>(A.R - 1)) ++n;
-  return n;
+  return min(max(A.n_accepted[b], 0), A.nodes ? A.max_nodes : A.R - 1);
 }
+__device__ __forceinline__ bool on_path(const CommitArgs &A, int node) { return static_cast<uint32_t>(node - 1) < static_cast<uint32_t>(A.R - 1); }
 
 }  // namespace
 
@@ -500,8 +500,16 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
   const int task = blockIdx.x % groups * (kCommitThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x / groups % A.B, layer = blockIdx.x / groups / A.B;
   if (task >= 2 * heads) return;
+  // (what the path does not reach is read with the rest: one trip to memory, not one per node)
   const int ctx = A.ctx_len[b];
-  const int n = path_length(A, b, ctx);
+  const int32_t *nodes = A.nodes + b * A.nodes_stride;
+  const int mine = lane < A.max_nodes ? nodes[lane] : 0;
+  int node[kP];
+#pragma unroll
+  for (int p = 0; p < kP; ++p) node[p] = p * kT + t_lane < A.max_nodes ? nodes[p * kT + t_lane] : 0;
+  const int most = path_most(A, b, ctx);
+  const uint64_t off = ~__ballot(lane < most && on_path(A, mine));
+  const int n = most < 0 ? -1 : off ? __builtin_ctzll(off) : 64;
   if (A.new_len && layer == 0 && task == 0 && lane == 0) A.new_len[b] = n < 0 ? ctx : ctx + 1 + n;
   if (n <= 0) return;
   const bool value = task >= heads;
@@ -523,7 +531,7 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
   for (int p = 0; p < kP; ++p) {
     const int u = p * kT + t_lane;
     if (u >= n) continue;
-    const int slot = ctx + A.nodes[b * A.nodes_stride + u];
+    const int slot = ctx + node[p];
     const int from = home(slot);
     if (static_cast<uint32_t>(from) >= static_cast<uint32_t>(A.pool.num_pages)) continue;
     live |= 1u << p;
@@ -535,6 +543,9 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
       raw2[F8 ? 0 : p] = load_vec(token(from, slot) + j * 32 + 16);
     }
   }
+  const int block = F8 ? 1 << A.pool.block_shift : 1;
+  int slot0 = first & -block, to = __builtin_amdgcn_readfirstlane(home(slot0));  // the first block that takes rows
+  float held = F8 && static_cast<uint32_t>(to) < static_cast<uint32_t>(A.pool.num_pages) ? *scale_at(to, slot0) : 0.0f;
   // every row is in registers before the first store: a path's rows may lie
   // where others of it go
   __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
@@ -562,19 +573,20 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
         for (int k = 0; k < 4; ++k) y[p][4 * i + k] *= factor[p];
       }
     }
-    const int block = 1 << A.pool.block_shift;
-    for (int slot0 = first & -block; slot0 < first + n; slot0 += block) {
-      const int to = __builtin_amdgcn_readfirstlane(home(slot0));
-      if (static_cast<uint32_t>(to) >= static_cast<uint32_t>(A.pool.num_pages)) continue;
+    for (;;) {
       uint32_t here = 0;
 #pragma unroll
       for (int p = 0; p < kP; ++p) {
         const int t = first + p * kT + t_lane - slot0;
         if (t >= 0 && t < block) here |= live & 1u << p;
       }
-      if (!__any(here != 0)) continue;
-      store_f8<D, kP>(y, here, first - slot0, max(first - slot0, 0), token(to, slot0), A.pool.token_bytes, scale_at(to, slot0),
-                  make_int2(2 * j, 2 * j + 1));
+      if (static_cast<uint32_t>(to) < static_cast<uint32_t>(A.pool.num_pages) && __any(here != 0))
+        store_f8<D, kP>(y, here, first - slot0, max(first - slot0, 0), token(to, slot0), A.pool.token_bytes, scale_at(to, slot0), held,
+                        make_int2(2 * j, 2 * j + 1));
+      slot0 += block;
+      if (slot0 >= first + n) break;
+      to = __builtin_amdgcn_readfirstlane(home(slot0));
+      if (static_cast<uint32_t>(to) < static_cast<uint32_t>(A.pool.num_pages)) held = *scale_at(to, slot0);
     }
   }
 }
@@ -583,7 +595,11 @@ __global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
 __global__ void __launch_bounds__(64) k_advance(CommitArgs A) {
   const int b = blockIdx.x * 64 + threadIdx.x;
   if (b >= A.B) return;
-  const int ctx = A.ctx_len[b], n = path_length(A, b, ctx);
+  const int ctx = A.ctx_len[b], most = path_most(A, b, ctx);
+  int n = A.nodes ? 0 : most;
+  if (A.nodes)
+    while (n < most && on_path(A, A.nodes[b * A.nodes_stride + n])) ++n;
+  if (most < 0) n = -1;
   A.new_len[b] = n < 0 ? ctx : ctx + 1 + n;
 }
 
