@@ -87,11 +87,11 @@ __device__ __forceinline__ void turn_sincos(uint64_t phase, double *sine, double
   *cosine = (quarter + 1) & 2 ? -b : b;
 }
 
-// (cosine, sine) of row `pos` and frequency i, times the magnitude; lo: what
-// float32 leaves of them.
-__device__ __forceinline__ void angle(const Rotation &A, int64_t pos, int i, float2 *hi, float2 *lo) {
+// (cosine, sine) of row `pos` at a frequency (A.turns), times the magnitude; lo:
+// what float32 leaves of them.
+__device__ __forceinline__ void angle(const Rotation &A, uint64_t frequency, int64_t pos, float2 *hi, float2 *lo) {
   double s, c;
-  const uint64_t phase = static_cast<uint64_t>(pos) * A.turns[i];
+  const uint64_t phase = static_cast<uint64_t>(pos) * frequency;
   turn_sincos(A.inverse ? 0 - phase : phase, &s, &c);
   s *= A.magnitude, c *= A.magnitude;
   *hi = make_float2(static_cast<float>(c), static_cast<float>(s));
@@ -163,7 +163,7 @@ __device__ __forceinline__ int rotary_angles(const RotaryArgs &A, int64_t row0, 
     const int64_t b = row / A.R;
     const int64_t pos = (T.base_pos ? T.base_pos[b] : 0) + row_depth(static_cast<int>(row - b * A.R), tree...);
     float2 lo;
-    angle(T, pos, e % half, &s_cs[e], &lo);
+    angle(T, T.turns[e % half], pos, &s_cs[e], &lo);
   }
   __syncthreads();
   return rows;
@@ -383,16 +383,6 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
   const int half = T.rot / 2;
   const int row_angles = append_row_angles(T.rot);
   float2 *s_lo = s_cs + min(A.R, block) * row_angles;
-  const int64_t pos0 = T.base_pos ? T.base_pos[b] : ctx;
-  for (int e = threadIdx.x; e < (t1 - t0) * half; e += kAppendThreads) {
-    const int t = t0 + e / half, i = e % half;
-    float2 lo;
-    const int at = (t - t0) * row_angles + i;
-    angle(T, pos0 + row_depth(row0 + t, tree...), i, &s_cs[at], &lo);
-    if (F8) s_lo[at] = lo;
-  }
-  __syncthreads();
-
   constexpr int kU = kUnits<D>, kT = kPassTokens<D>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int j = lane % kU, t_lane = t0 + lane / kU;  // (passes begin at the first row)
@@ -402,24 +392,45 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
   const bool stored = static_cast<uint32_t>(page) < static_cast<uint32_t>(A.pool.num_pages);
   const int64_t seq_row = static_cast<int64_t>(b) * A.R + row0;
   const int in_page = static_cast<int>(slot0) & ((1 << A.pool.page_shift) - 1);
-  for (int task = blockIdx.y * (kAppendThreads / 64) + wave; task < 2 * heads + A.Hq; task += gridDim.y * (kAppendThreads / 64)) {
+  // Rows of a task (kG passes of them are asked for together; behind the last
+  // row the last one again, so that the loads stand in a known order).  The first
+  // task's are on their way while the angles are formed: those only wait for
+  // their own frequency, which a lane keeps.
+  constexpr int kG = kP < 4 ? kP : 4;
+  uint4 ra[kG], rb[kG];
+  auto fetch = [&](int task, int p0) {
     const bool query = task >= 2 * heads, value = !query && task >= heads;
-    if (!query && !stored) continue;
     const int h = query ? task - 2 * heads : value ? task - heads : task;
     const uint16_t *x = query ? A.q : value ? A.v : A.k;
     const int64_t stride = query ? A.q_stride : value ? A.v_stride : A.k_stride;
-    constexpr int kG = kP < 4 ? kP : 4;  // passes loaded together
-    uint4 ra[kG], rb[kG];
-    auto fetch = [&](int p0) {
 #pragma unroll
-      for (int p = 0; p < kG; ++p) {
-        const int t = (p0 + p) * kT + t_lane;
-        if (t >= t1) continue;
-        const uint16_t *row = x + (seq_row + t) * stride + h * D;
-        ra[p] = load_vec(row + piece.x * 8);
-        rb[p] = load_vec(row + piece.y * 8);
-      }
-    };
+    for (int p = 0; p < kG; ++p) {
+      const uint16_t *row = x + (seq_row + min((p0 + p) * kT + t_lane, t1 - 1)) * stride + h * D;
+      ra[p] = load_vec(row + piece.x * 8);
+      rb[p] = load_vec(row + piece.y * 8);
+    }
+  };
+  const int task0 = blockIdx.y * (kAppendThreads / 64) + wave, tasks = 2 * heads + A.Hq;
+  const int64_t pos0 = T.base_pos ? T.base_pos[b] : ctx;
+  const int shift = half > 1 ? 32 - __builtin_clz(half - 1) : 0, i = lane & ((1 << shift) - 1);  // lanes of a token (half <= 64), without divisions
+  const uint64_t frequency = i < half ? T.turns[i] : 0;
+  __builtin_amdgcn_sched_barrier(0);
+  constexpr bool kEarly = kP >= 4;
+  if (kEarly) fetch(min(task0, tasks - 1), 0);
+  __builtin_amdgcn_sched_barrier(0);
+  if (i < half)
+    for (int t = threadIdx.x >> shift; t < t1 - t0; t += kAppendThreads >> shift) {
+      float2 lo;
+      const int at = t * row_angles + i;
+      angle(T, frequency, pos0 + row_depth(row0 + t0 + t, tree...), &s_cs[at], &lo);
+      if (F8) s_lo[at] = lo;
+    }
+  __syncthreads();
+
+  for (int task = task0; task < tasks; task += gridDim.y * (kAppendThreads / 64)) {
+    const bool query = task >= 2 * heads, value = !query && task >= heads;
+    if (!query && !stored) continue;
+    const int h = query ? task - 2 * heads : value ? task - heads : task;
     if (F8 && !query) {
       const int64_t at = ((static_cast<int64_t>(page) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * heads + h;
       float *scale = (value ? A.pool.v_scale : A.pool.k_scale) + at;
@@ -428,7 +439,7 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
       uint32_t live = 0;
 #pragma unroll
       for (int p0 = 0; p0 < kP; p0 += kG) {
-        fetch(p0);
+        if (!kEarly || task != task0 || p0 > 0) fetch(task, p0);
 #pragma unroll
         for (int p = p0; p < p0 + kG; ++p) {
           const int t = p * kT + t_lane;
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
     }
 #pragma unroll
     for (int p0 = 0; p0 < kP; p0 += kG) {
-      fetch(p0);
+      if (!kEarly || task != task0 || p0 > 0) fetch(task, p0);
 #pragma unroll
       for (int p = 0; p < kG; ++p) {
         const int t = (p0 + p) * kT + t_lane;
