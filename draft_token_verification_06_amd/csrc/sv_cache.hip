@@ -644,8 +644,11 @@ template <int DT, bool F8, int D, int kP>
 void launch_append_passes(const AppendArgs &A, const TreeDepths *depths, hipStream_t st) {
   const int64_t x = static_cast<int64_t>(A.B) * A.blocks;
   const int64_t tasks = (2 * A.pool.Hkv + A.Hq + kAppendThreads / 64 - 1) / (kAppendThreads / 64);
-  // few blocks: their heads are spread over workgroups (each forms the block's angles again)
-  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(tasks, 2048 / x));
+  // Blocks that do not fill the chip: their heads are spread over workgroups, each
+  // of which forms the block's angles again.  Up to 4096 of them: a prompt of 4
+  // times 4096 rows in blocks of 16 took 71 us, with up to 2048 77, with 1024 88; in
+  // blocks of 64 113, 110 and 119.
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(tasks, 4096 / x));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y)), threads(kAppendThreads);
   const unsigned lds = std::min(A.R, 1 << A.pool.block_shift) * append_row_angles(A.rotation.rot) * sizeof(float2) * (F8 ? 2 : 1);
   if (depths) hipLaunchKernelGGL((k_append<DT, F8, D, kP, TreeDepths>), grid, threads, lds, st, A, *depths);
