@@ -875,7 +875,7 @@ bool rotation_ok(const uint64_t *turns, int32_t rot, int32_t step, int32_t D, fl
 bool rows_ok(const void *p, int64_t *stride, int64_t elems, int64_t rows, int bytes) {
   if (!p || !aligned(p, 16)) return false;
   if (*stride == 0) *stride = elems;
-  return rows == 1 || (*stride >= elems && *stride * bytes % 16 == 0 && *stride <= int64_t{1} << 40);
+  return rows == 1 || (*stride >= elems && *stride <= int64_t{1} << 40 && *stride * bytes % 16 == 0);
 }
 
 // out is in with the same stride, or the two spans are disjoint.
@@ -1001,8 +1001,11 @@ int sv_cache_commit(const sv_paged_cache *cache, int32_t layers, int64_t layer_s
   if (nodes && nodes_stride == 0) nodes_stride = max_nodes;
   if (nodes && B > 1 && nodes_stride < max_nodes) return SV_EINVAL;
   if (!nodes && !new_len) return SV_EINVAL;
-  const uintptr_t n0 = reinterpret_cast<uintptr_t>(new_len), c0 = reinterpret_cast<uintptr_t>(ctx_len);
-  if (new_len && n0 != c0 && n0 < c0 + 4 * static_cast<uintptr_t>(B) && c0 < n0 + 4 * static_cast<uintptr_t>(B)) return SV_EINVAL;
+  // new_len is written while other workgroups read: ctx_len itself (written last) or apart from both
+  const uintptr_t span = 4 * static_cast<uintptr_t>(B), n0 = reinterpret_cast<uintptr_t>(new_len);
+  const uintptr_t c0 = reinterpret_cast<uintptr_t>(ctx_len), a0 = reinterpret_cast<uintptr_t>(n_accepted);
+  if (new_len && n0 != c0 && n0 < c0 + span && c0 < n0 + span) return SV_EINVAL;
+  if (new_len && n0 < a0 + span && a0 < n0 + span) return SV_EINVAL;
   const int bytes = c.dtype == SV_DT_F8E4M3 ? 1 : 2;
   const int64_t dense = static_cast<int64_t>(c.num_pages) * c.Hkv * c.page * c.D;
   if (layer_stride == 0) layer_stride = dense;

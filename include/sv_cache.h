@@ -125,10 +125,10 @@ int sv_cache_append(const sv_paged_cache *cache, const int32_t *page_table, int6
  *   page_table  as for sv_cache_append; max_ctx + R <= table_pages * page.
  *   prefix_table  DEVICE [ceil(P / page)] page numbers of the P tokens that all
  *            sequences share (in front of them), NULL with P = 0.
- *   8-bit pages: keys and values are byte * scale, taken exactly: queries enter
- *            the products as sums of 8-bit numbers, without loss down to 2^-21 of
- *            a row's largest, and the exponentials times the values' scale are
- *            rounded to dtype.
+ *   8-bit pages: keys and values are byte * scale.  The bytes enter the products
+ *            exactly; scales are applied in float32 (or, powers of two, with the
+ *            bytes in bf16, exactly): to a key's scores, and of the values to the
+ *            exponentials before those are rounded to dtype.
  * A page number outside [0, num_pages) among a sequence's tokens makes its rows
  * NaN, one in the prefix all rows; no memory outside the pages is read.  Table
  * entries past a sequence's tokens do not matter. */
@@ -151,7 +151,8 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
  *            lengths advance.  max_nodes <= 64.
  *   n_accepted [B] int32, the first that many nodes (clamped to [0, max_nodes];
  *            of a window to [0, R - 1]).  A node outside [1, R) ends the path.
- *   new_len  [B] or NULL: ctx_len[b] + 1 + the path's length; may be ctx_len.
+ *   new_len  [B] or NULL: ctx_len[b] + 1 + the path's length; may be ctx_len,
+ *            apart from it and from n_accepted otherwise.
  * All rows of a path are read before one is stored.  8-bit rows (byte * scale)
  * are stored as sv_cache_append stores them, at token ctx_len[b] + 1 and on.
  * A sequence with ctx_len[b] < 0 or ctx_len[b] + R > table_pages * page is left

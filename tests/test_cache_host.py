@@ -285,3 +285,10 @@ def test_binding_refuses():
         sv.paged_attention(k[:1], None, table, n)
     with pytest.raises(ValueError):
         sv.paged_attention_workspace(0, 1, 1, 1, 64, 0, 0, "cpu")
+
+
+@pytest.mark.parametrize("at,status", [(0, -1), (4, -1), (-4, -1)])
+def test_commit_refuses_lengths_over_the_counts(at, status):
+    """new_len is written while n_accepted is still read."""
+    other = FAKE + (1 << 20)
+    assert _commit(n_accepted=other, new_len=other + at) == status

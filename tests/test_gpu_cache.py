@@ -376,3 +376,59 @@ def test_layers_and_refusals_on_the_device():
     for call in bad:
         with pytest.raises((ValueError, IndexError, sv.SvError)):
             call()
+
+
+# -- calls that the cases above do not make ---------------------------------------------
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("R,lens", [(64, [0, 63, 64]), (150, [5, 100, 1])])
+def test_append_largest_blocks(R, lens, inter):
+    """Blocks of 64 rows, every value of 128 turned: the most angles and registers that a workgroup has."""
+    page, D, H = 64, 128, 2
+    table, num = tables(3, (max(lens) + R + page - 1) // page, 1, R)
+    cache = make_cache(num, page, H, D, "f8", 64, 3)
+    q, k, v = rows_of(3, R, 3, H, D, "f16", R)
+    f, _ = sv.rotary_frequencies(D)
+    before = snapshot(cache)
+    out = torch.full((3, R, 3, D), 5.0, dtype=torch.float16, device=DEV)
+    q_before = host(out)
+    sv.cache_append(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), k, v, q=q, turns=sv.rotary_turns(f, DEV),
+                    interleaved=inter, q_out=out)
+    torch.cuda.synchronize()
+    check_append(cache, before, table, lens, [R] * 3, k, v, q, out, q_before, f=f, base=lens, parent=None, inter=inter, mag=1.0, dtype="f16")
+
+
+def test_many_sequences_of_one_token():
+    """More blocks than are spread over workgroups, each with one row; tables that are part of a wider one."""
+    B, page, D, H = 1100, 16, 64, 1
+    wide, num = tables(B, 4, 0, 6)
+    table = wide[:, 1:3]
+    cache = make_cache(num, page, H, D, "f8", 16, 3)
+    q, k, v = rows_of(B, 1, 2, H, D, "bf16", 2)
+    lens = [(7 * b) % 32 for b in range(B)]
+    f, _ = sv.rotary_frequencies(D)
+    before = snapshot(cache)
+    out = torch.empty(B, 1, 2, D, dtype=torch.bfloat16, device=DEV)
+    q_before = host(out)
+    sv.cache_append(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), k, v, q=q, turns=sv.rotary_turns(f, DEV), q_out=out)
+    torch.cuda.synchronize()
+    check_append(cache, before, table, lens, [1] * B, k, v, q, out, q_before, f=f, base=lens, parent=None, inter=False, mag=1.0, dtype="bf16")
+
+
+def test_commit_paths_with_repeats_and_backwards():
+    """A path may name a node twice, or nodes out of order: every row is the one that stood there before the call."""
+    page, D, H, R = 16, 64, 2, 12
+    table, num = tables(3, 3, 1, 8)
+    cache = make_cache(num, page, H, D, "f8", 16, 5)
+    before = snapshot(cache)
+    lens = [10, 0, 30]
+    nodes = np.array([[5, 5, 2, 1], [3, 2, 1, 11], [11, 4, 4, 4]], dtype=np.int32)
+    counts = [4, 3, 4]
+    got = sv.cache_commit(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), torch.from_numpy(nodes).to(DEV),
+                          torch.tensor(counts, dtype=torch.int32, device=DEV), rows=R)
+    torch.cuda.synchronize()
+    after = snapshot(cache)
+    for n in ("k", "v"):
+        pages, scales = before[n].copy(), before[n + "_scale"].copy()
+        for b in range(3):
+            assert oc.commit(pages, scales, table[b].tolist(), lens[b], nodes[b], counts[b], R, page=page, block=16) == int(got[b])
+        assert np.array_equal(after[n], pages) and np.array_equal(after[n + "_scale"], scales)

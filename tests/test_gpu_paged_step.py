@@ -267,3 +267,74 @@ def test_layers_are_committed_together():
         t.copy_(x)
     assert sv.cache_commit(many, table, n, nodes, acc, rows=R).tolist() == [4, 34, 71]
     assert all(torch.equal(a, b) for a, b in zip(raw + [many.k_scale, many.v_scale], one_by_one))
+
+
+@pytest.mark.parametrize("held", [F8, torch.bfloat16])
+def test_two_graphs_share_a_workspace(held):
+    """Two captured calls of different sizes with one workspace, replayed in turn on one stream, with eager calls on it
+    between: each replay equals the eager result."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    cache = sv.paged_cache(40, 32, 2, 64, held, DEV)
+    table = torch.randperm(40, generator=g, device=DEV).view(2, 20).to(torch.int32)
+    x = torch.randn(2, 600, 2, 64, generator=g, device=DEV).to(torch.bfloat16)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    sv.cache_append(cache, table, zero, x, x)
+    calls = []
+    for R, Hq, lens, P in ((1, 8, [599, 40], 0), (9, 16, [300, 580], 100)):
+        q = torch.randn(2, R, Hq, 64, generator=g, device=DEV).to(torch.bfloat16)
+        n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        out = sv.AttentionResult(torch.empty_like(q), torch.empty(2, R, Hq, device=DEV))
+        calls.append((q, n, dict(max_ctx=590 if R == 9 else 630, out=out, prefix_table=table[0, :4].contiguous() if P else None, prefix_len=P)))
+    ws = max((sv.paged_attention_workspace(2, q.shape[1], q.shape[2], 2, 64, kw["prefix_len"], kw["max_ctx"], DEV) for q, _, kw in calls),
+             key=lambda t: t.numel())
+    run = lambda c: sv.paged_attention(c[0], cache, table, c[1], ws=ws, **c[2])  # noqa: E731
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        want = []
+        for c in calls:
+            r = run(c)
+            want.append((r.out.clone(), r.lse.clone()))
+    torch.cuda.synchronize()
+    graphs = []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            run(c)
+    for rep in range(4):
+        with torch.cuda.stream(st):
+            for c in calls:
+                c[2]["out"].out.fill_(7)
+                c[2]["out"].lse.fill_(7)
+            if rep % 2:
+                ws.fill_(0xFF)
+            order = (0, 1) if rep < 2 else (1, 0)
+            for i in order:
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for c, w in zip(calls, want):
+            assert torch.equal(c[2]["out"].out, w[0]) and torch.equal(c[2]["out"].lse, w[1]), rep
+
+
+def test_every_other_row_count_and_wide_tables():
+    """Sequences without rows among others, tables that are columns of a wider one, on a stream of its own."""
+    B, R = 70, 3
+    g = torch.Generator(device=DEV).manual_seed(2)
+    cache = sv.paged_cache(B * 3, 16, 1, 128, F8, DEV)
+    wide = torch.randperm(B * 3, generator=g, device=DEV).view(B, 3).to(torch.int32)
+    table = wide[:, :2]
+    n = torch.arange(B, device=DEV, dtype=torch.int32) % 20
+    rc = torch.arange(B, device=DEV, dtype=torch.int32) % 2 * R
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        x = torch.randn(B, 20, 1, 128, generator=g, device=DEV).to(torch.bfloat16)
+        sv.cache_append(cache, table, torch.zeros_like(n), x, x, row_count=n)
+        q, k, v = (torch.randn(B, R, h, 128, generator=g, device=DEV).to(torch.bfloat16) for h in (4, 1, 1))
+        sv.cache_append(cache, table, n, k, v, row_count=rc)
+        out = sv.AttentionResult(torch.full((B, R, 4, 128), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((B, R, 4), 7.0, device=DEV))
+        sv.paged_attention(q, cache, table, n, row_count=rc, out=out, max_ctx=20)
+        alone = sv.paged_attention(q[1::2].contiguous(), cache, table[1::2].contiguous(), n[1::2].contiguous(), max_ctx=20, return_lse=True)
+    torch.cuda.synchronize()
+    assert (out.out[::2] == 7).all() and (out.lse[::2] == 7).all()
+    assert torch.equal(out.out[1::2], alone.out) and torch.equal(out.lse[1::2], alone.lse)
