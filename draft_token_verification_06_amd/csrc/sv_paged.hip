@@ -4,10 +4,10 @@
 //
 // Pages.  Ranges begin at multiples of 128 tokens and pages hold 16 at least, so
 // 16 aligned tokens (a strip) lie in one page and under one scale.  Each lane of
-// a wave looks up one strip of the next 1024 tokens (page, key scale, value
+// a wave looks up one strip of the next 1024 tokens (address, key scale, value
 // scale): one trip for the table and one for the scales, after which a strip's
-// page is a lane read, and its rows are read whole: rows past the range are
-// inside the page.
+// address is two lane reads, and its rows are read whole: rows past the range
+// are inside the page.
 //
 // Scales.  A score is its product times the key scale, one multiplication; the
 // value scale multiplies the exponential, and the product is rounded to the
@@ -57,6 +57,17 @@ template <int D, int WQ> constexpr size_t pg_tile_bytes() {
   const size_t kv = static_cast<size_t>(kPgTileKeys) * (pg_key_row<D>() + pg_value_row<D>()) * 2;
   const size_t merge = WQ < 4 ? 4 * 32 * static_cast<size_t>(D + 4) * 4 : 0;
   return kv > merge ? kv : merge;
+}
+
+// Bytes from the pools' start to a strip's first row (page, token in it, head), and
+// the offset that lane `at` holds.
+__device__ __forceinline__ int2 strip_offset(const PagedAttendArgs &A, int page, int in_page, int kvh) {
+  const int64_t off = page * A.pool.page_bytes + in_page * A.pool.token_bytes + kvh * A.pool.head_bytes;
+  return make_int2(static_cast<int>(off), static_cast<int>(off >> 32));
+}
+__device__ __forceinline__ int64_t strip_at(int2 strips, int at) {
+  return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(strips.y, at))) << 32 |
+                              static_cast<uint32_t>(__builtin_amdgcn_readlane(strips.x, at)));
 }
 
 // 16 bytes as 16 values of the storage type, times a power of two (exact).
@@ -250,18 +261,19 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
   };
 
   // the strips of the look-up that begins at token c0, one per lane
-  int c0 = it.k0, pages = 0;
+  int c0 = it.k0;
+  int2 strips{};
   float kscale = 1.0f, vscale = 1.0f;
   bool bad = false;
   const int last = (it.k1 - 1) & -kStrip;
   auto look_up = [&](int at) {
     c0 = at;
-    const int key = min(at + lane * kStrip, last);
-    pages = it.table[key >> A.pool.page_shift];
-    if (static_cast<uint32_t>(pages) >= static_cast<uint32_t>(A.pool.num_pages)) pages = 0, bad = true;
+    const int key = min(at + lane * kStrip, last), in_page = key & ((1 << A.pool.page_shift) - 1);
+    int page = it.table[key >> A.pool.page_shift];
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(A.pool.num_pages)) page = 0, bad = true;
+    strips = strip_offset(A, page, in_page, it.kvh);
     if (F8) {
-      const int in_page = key & ((1 << A.pool.page_shift) - 1);
-      const int64_t s = ((static_cast<int64_t>(pages) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * A.pool.Hkv + it.kvh;
+      const int64_t s = ((static_cast<int64_t>(page) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * A.pool.Hkv + it.kvh;
       kscale = A.pool.k_scale[s];
       vscale = A.pool.v_scale[s];
     }
@@ -272,17 +284,13 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
   float ks[2], vs[2], ks_next[2], vs_next[2];  // scales of this wave's strips, of the tile and of the one loaded
   const int piece = lane % kChunks, row_lane = lane / kChunks;
   const uint32_t lane_off = static_cast<uint32_t>(row_lane) * static_cast<uint32_t>(A.pool.token_bytes) + piece * 16;
-  const int page_mask = (1 << A.pool.page_shift) - 1;
-  const int64_t head_off = it.kvh * A.pool.head_bytes;
   // one sequence's pages are read once: streamed
   auto fetch = [&](const uint8_t *p) { return load_stream(reinterpret_cast<const uint4 *>(p)); };
   auto load = [&](int t0) {
     if (t0 - c0 >= kLookup) look_up(t0);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int key = min(t0 + wave * 32 + g * kStrip, last);
-      const int page = __builtin_amdgcn_readlane(pages, (key - c0) / kStrip);
-      const int64_t off = page * A.pool.page_bytes + (key & page_mask) * A.pool.token_bytes + head_off;
+      const int64_t off = strip_at(strips, (min(t0 + wave * 32 + g * kStrip, last) - c0) / kStrip);
 #pragma unroll
       for (int x = 0; x < kStrip / kWaveRows; ++x) {
         const int j = g * (kStrip / kWaveRows) + x;
@@ -564,18 +572,19 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   float ref = kRelative ? 0.0f : 1.0f;
 
   // the strips of the look-up that begins at token c0, one per lane
-  int c0 = it.k0, pages = 0;
+  int c0 = it.k0;
+  int2 strips{};
   float kscale = 1.0f, vscale = 1.0f;
   bool bad = false, whole = true;
   const int last = (it.k1 - 1) & -kStrip;
   auto look_up = [&](int at) {
     c0 = at;
-    const int key = min(at + lane * kStrip, last);
-    pages = it.table[key >> A.pool.page_shift];
-    if (static_cast<uint32_t>(pages) >= static_cast<uint32_t>(A.pool.num_pages)) pages = 0, bad = true;
+    const int key = min(at + lane * kStrip, last), in_page = key & ((1 << A.pool.page_shift) - 1);
+    int page = it.table[key >> A.pool.page_shift];
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(A.pool.num_pages)) page = 0, bad = true;
+    strips = strip_offset(A, page, in_page, it.kvh);
     if (F8) {
-      const int in_page = key & ((1 << A.pool.page_shift) - 1);
-      const int64_t s = ((static_cast<int64_t>(pages) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * A.pool.Hkv + it.kvh;
+      const int64_t s = ((static_cast<int64_t>(page) << (A.pool.page_shift - A.pool.block_shift)) + (in_page >> A.pool.block_shift)) * A.pool.Hkv + it.kvh;
       kscale = A.pool.k_scale[s];
       vscale = A.pool.v_scale[s];
       // powers of two alone, as cache_append leaves them, need no products
@@ -595,16 +604,14 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
   constexpr int kStep = 4 * kWaveRows;
   const int row0 = wave * kWaveRows;  // of this wave's first load
   const int row_lane = lane / kChunks;
-  const uint32_t lane_off = static_cast<uint32_t>(row_lane) * static_cast<uint32_t>(A.pool.token_bytes) + piece * 16;
-  const int page_mask = (1 << A.pool.page_shift) - 1;
+  static_assert(kStep % kStrip == 0, "a wave's rows have one place in their strips");
+  const uint32_t lane_off = static_cast<uint32_t>(row0 % kStrip + row_lane) * static_cast<uint32_t>(A.pool.token_bytes) + piece * 16;
   auto load = [&](int t0) {
     if (t0 - c0 >= kLookup) look_up(t0);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int key = t0 + row0 + j * kStep;  // (the wave's first row: rows follow within a strip)
-      const int strip = min(key, last + (key & (kStrip - 1)));
-      const int page = __builtin_amdgcn_readlane(pages, (strip - c0) / kStrip);
-      const int64_t off = page * A.pool.page_bytes + (strip & page_mask) * A.pool.token_bytes + it.kvh * A.pool.head_bytes;
+      // (the wave's first row's strip: its rows follow within it)
+      const int64_t off = strip_at(strips, (min(t0 + (row0 & -kStrip) + j * kStep, last) - c0) / kStrip);
       rk[j] = load_vec(A.pool.k + off + lane_off);
       rv[j] = load_vec(A.pool.v + off + lane_off);
     }
