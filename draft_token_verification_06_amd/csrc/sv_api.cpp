@@ -695,15 +695,19 @@ int sv_lmhead_quant(const void *hidden, int64_t hidden_row_stride, int dtype,
 
 namespace {
 
-// False for sizes outside the rules; else their plan.
-bool attention_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, AttendPlan *L) {
+// Whether an attention's sizes are within the rules.
+bool attention_sizes(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx) {
   if (B < 1 || R < 1 || R > SV_TREE_MAX_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > SV_ATTENTION_MAX_HEADS) return false;
   if (D != 64 && D != 128) return false;
   if (P < 0 || P > SV_ATTENTION_MAX_KEYS || max_ctx < 0 || max_ctx > SV_ATTENTION_MAX_KEYS) return false;
-  if (static_cast<int64_t>(B) * R > (int64_t{1} << 30) / Hq) return false;
+  return static_cast<int64_t>(B) * R <= (int64_t{1} << 30) / Hq && grid_fits((static_cast<int64_t>(B) * R * Hq + 3) / 4, 256);
+}
+
+// False for sizes outside the rules; else their plan.
+bool attention_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, AttendPlan *L) {
+  if (!attention_sizes(B, R, Hq, Hkv, D, P, max_ctx)) return false;
   *L = plan_attention(B, R, Hq, Hkv, D, P, max_ctx);
-  return grid_fits(L->prefix_items + L->own_blocks, kAttendThreads) &&
-         grid_fits((static_cast<int64_t>(B) * R * Hq + 3) / 4, 256);
+  return grid_fits(L->prefix_items + L->own_blocks, kAttendThreads);
 }
 
 }  // namespace
@@ -851,8 +855,7 @@ bool table_ok(const int32_t *table, int64_t *stride, int32_t table_pages, int32_
 
 // False for sizes outside the rules; else their plan.
 bool paged_plan(int32_t B, int32_t R, int32_t Hq, int32_t Hkv, int32_t D, int32_t P, int32_t max_ctx, bool f8, PagedPlan *L) {
-  AttendPlan same;  // the rules are sv_attention's
-  if (!attention_plan(B, R, Hq, Hkv, D, P, max_ctx, &same)) return false;
+  if (!attention_sizes(B, R, Hq, Hkv, D, P, max_ctx)) return false;  // (sv_attention's rules)
   *L = plan_paged(B, R, Hq, Hkv, D, P, max_ctx, f8);
   return L->prefix_items <= INT32_MAX && grid_fits(L->prefix_items + L->own_blocks, kAttendThreads);
 }
