@@ -148,7 +148,9 @@ template <class... Tree> __device__ __forceinline__ int row_depth(int r, const T
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Rotary positions alone.  Bound: memory (each value read and written once).
+// Rotary positions alone.  Bound: memory (each value read and written once): 4
+// times 8191 rows of 32 heads of 128 take 114 us, 4.7 TB/s of the 4.9 that a copy
+// reaches; 72 rows 3.1 us, a launch and two trips to memory.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -356,7 +358,18 @@ __device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live
 
 // ---------------------------------------------------------------------------
 // Appending.  A workgroup takes the rows that fall into one block of one
-// sequence; its waves take heads in turn: keys, values, queries.
+// sequence; its waves take heads in turn: keys, values, queries.  Every row is read
+// once, into registers, where 8-bit pages find their scale.
+//
+// Bound: memory for prompts.  4 times 4096 rows of 32 + 2 * 8 heads of 128, half
+// of each turned: 265 MB in 69 to 71 us (3.8 TB/s) in 8-bit blocks of 32, where float64
+// products and conversions take turns with the memory; 403 MB in 89 us (4.5 TB/s)
+// in 16 bits; 113 us in blocks of 64, whose 8 passes leave two waves a SIMD.
+// Steps are trips to memory after each other (length, page, rows, store): one
+// token 6.5 us, 64 windows of 9 rows 11 us, 128 single tokens 6.6.
+// Keys in float32, with a bound on the error and only passes with an open byte
+// once more in float64, were slower (107 us for 77, windows 13.1 for 11.5): the
+// test costs more than the products.
 // ---------------------------------------------------------------------------
 namespace {
 // Angles of a row in LDS: two more than there are, so that rows begin 16 bytes
@@ -489,6 +502,9 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
 // ---------------------------------------------------------------------------
 // Keeping an accepted path.  One wave per (layer, sequence, head, keys or
 // values): it holds the path's rows in registers before it stores the first.
+// Bound: trips to memory after each other (path, pages, rows and scales, store):
+// 2.9 us for 4 trees of one layer.  64 trees of 32 layers take 18 us, of which the
+// 12.6 MB alone would be 2.6: rows of 128 bytes over gigabytes of pages.
 // ---------------------------------------------------------------------------
 namespace {
 

@@ -16,14 +16,14 @@
 // scales relative to the largest so far, as either alone could leave the type.
 //
 // 8-bit products (keys against queries rounded to sums of 8-bit numbers) were
-// not taken: the scaled 8-bit matrix instruction's sums are off by 1.4e-4 of the
-// sum of the products' magnitudes, a float32 sum of 16-bit products by 1e-6.
+// not taken: the scaled 8-bit matrix instruction's sums are off by up to 1.4e-4 of the
+// sum of the products' magnitudes.
 //
 // Bounds.  Few rows are the pages' traffic: a copy reaches 4.9 TB/s here, reads
 // alone 7.0.  Single tokens of 128 sequences with 4000 keys of 8 heads of 128: 1.05
 // GB of 8-bit pages in 178 us (5.9 TB/s), 2.1 GB of bf16 pages in 337 us (6.2 TB/s).
 // Behind a shared prefix it is matrix and vector work on the same tiles: 18432
-// stacked rows over 8192 keys, 8-bit, are 77 GFLOP in 124 us.
+// stacked rows over 8192 keys, 8-bit, are 77 GFLOP in 112 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -206,6 +206,14 @@ __device__ __forceinline__ void wave_sync() {
 // exponentials belong to 8 consecutive keys: the operand of the second product as
 // they are, under one scale, against values whose transposing read takes 8
 // consecutive rows (no bank conflicts).
+//
+// Bound: memory.  128 single tokens of 32 / 8 heads of 128 over 4000 keys, 8-bit:
+// 178 us, 5.9 TB/s; over 1000 to 4000 behind 2048 shared ones 131 to 137.  32 rows of a
+// sequence in tiles of 16 rows of 16x16x32 products hold half the registers of tiles
+// of 32, so four workgroups are on a CU.  One sequence: trips to memory, 6.3 us
+// over 100 keys, 10 over 1033, 12 over 4000, 21 over 30000 (with the join).
+// Tried: 16 waves a workgroup (slower but for 32 sequences of 1000), two tiles in flight
+// (144 to 141 us at two waves a SIMD; the registers hold two more waves instead).
 template <int DT, bool F8, int D, int NC>
 __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedItem &it, char *lds, const uint32_t (*s_anc)[8],
                                          float2 *s_ml, bool direct) {
@@ -522,6 +530,18 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
   }
 }
 
+// Many rows: 32 of them on each of WQ waves, whose 4 / WQ groups take the keys of a
+// tile in turn.  Keys and values are widened once, on their way to LDS, for all
+// waves: tiles of 64 keys, requested one tile ahead.  Scores are formed transposed,
+// as k_attend does it: a lane's exponentials are the operand of the second product.
+//
+// Bound: 2304 rows of each of 8 kv heads over 8192 8-bit keys are 77 GFLOP, 53 us at
+// the rate of a large product; they take 112 (the matrix pipes are busy for 28 percent
+// of the cycles, the vector units for 42, both at once for 9).  Without its parts
+// one by one: loads -18, values' products -13, exponentials -8, widening -8 us.
+// Tried: two LDS buffers and one barrier (122 us for 124 alone, 149 for 136 beside
+// the sequences' own keys), the next tile's scores beside the softmax (129.5 for 130.5),
+// steps of 32 keys (136 for 124), three waves a SIMD (160), tiles of 16 and 48 rows (139 for 132).
 template <int DT, bool F8, int D, int WQ>
 __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const PagedItem &it, char *lds, const uint32_t (*s_anc)[8],
                                            float2 *s_ml) {
@@ -954,7 +974,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) k_paged_attend(PagedAttendArgs 
 
 // One wave per (row, head): the row's items joined.  Their maxima and sums are
 // read by the lanes, one each, and the outputs 8 at a time, all of them in
-// flight; the sums' order is the items'.
+// flight; the sums' order is the items'.  18432 rows of 128 with 4 ranges: 12 us
+// (38 MB of partial outputs); one token's 32 rows 3.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) k_paged_join(AttendJoin A, int direct) {
   constexpr int E = D / 64;
