@@ -418,7 +418,7 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
         rescale_all(down);
         ref = most;
       }
-      vf /= ref;
+      vf = ref > 0.0f ? vf / ref : 0.0f;  // (scales of zero alone so far)
     }
     // One multiply-add per exponent, the key scale in its factor (never zero:
     // masked products are -inf).  In float16 the largest is 2^15, held there
@@ -743,7 +743,7 @@ __device__ __forceinline__ void paged_item(const PagedAttendArgs &A, const Paged
         }
       }
 #pragma unroll
-      for (int g = 0; g < 2 * SB; ++g) wt[g] = kRelative ? vs[g] / ref : vs[g];
+      for (int g = 0; g < 2 * SB; ++g) wt[g] = !kRelative ? vs[g] : ref > 0.0f ? vs[g] / ref : 0.0f;  // (scales of zero alone so far)
     }
     // The lifted exponent is taken from the difference to the maximum, so that
     // the largest is 2^15 exactly however far the scores are (65504 ends the

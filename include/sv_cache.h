@@ -35,7 +35,8 @@ extern "C" {
  *   page    tokens of a page: 16, 32, 64, 128 or 256.
  *   block   8-bit pages: tokens that share a scale: 16, 32 or 64, at most page.
  *           A stored value is byte * scale[(p * (page / block) + t / block) *
- *           Hkv + h].  Scales are positive and finite.  Others: ignored.
+ *           Hkv + h].  Scales are finite and positive, or zero where a block is zeros.
+ *           Others (16-bit pages): ignored.
  *   k_scale, v_scale  [num_pages][page / block][Hkv] float; NULL for 16-bit pages.
  *   D       64 or 128.
  * Addresses are 16-byte aligned and so are strides in bytes (scales 4); no two

@@ -326,3 +326,21 @@ def test_refusals_on_the_device():
         a.update(kw)
         with pytest.raises((ValueError, sv.SvError)):
             sv.paged_attention(a.pop("q"), a.pop("cache"), a.pop("page_table"), a.pop("ctx_len"), **a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("R,Hq,P", [(3, 8, 0), (17, 16, 0), (4, 8, 70), (20, 16, 200)])
+def test_scales_of_zero(dtype, R, Hq, P):
+    """Blocks that another program scaled by zero, the first ones of a sequence and whole sequences among them, are
+    blocks of zeros (bytes that are none may count for up to 2^-117 of a unit each)."""
+    q, cache, table, prefix = make(3, R, Hq, 2, 64, P, 300, dtype, "f8", 16, 16, 4)
+    lens = [250, 40, 130]
+    none = table[0, ::2].long().tolist() + table[1].long().tolist() + table[2, 1:3].long().tolist() + prefix[:2].long().tolist()
+    cache.v_scale[none] = 0.0
+    cache.k_scale[none[1::2]] = 0.0
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    res = sv.paged_attention(q, cache, table, n, prefix_table=prefix if P else None, prefix_len=P, return_lse=True)
+    torch.cuda.synchronize()
+    check(res, q, cache, table, lens, prefix=prefix, P=P)
+    if P == 0:
+        assert np.abs(host(res.out[1])).max() < 2.0 ** -100
