@@ -509,9 +509,11 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
 namespace {
 
 // Nodes that sequence b's accepted path may have; -1: the sequence is left alone.
+// (R - 1 at most, also where nodes repeat: the rows' own places are what the
+// table has room for.)
 __device__ __forceinline__ int path_most(const CommitArgs &A, int b, int ctx) {
   if (ctx < 0 || static_cast<int64_t>(ctx) + A.R > static_cast<int64_t>(A.table_pages) << A.pool.page_shift) return -1;
-  return min(max(A.n_accepted[b], 0), A.nodes ? A.max_nodes : A.R - 1);
+  return min(max(A.n_accepted[b], 0), A.nodes ? min(A.max_nodes, A.R - 1) : A.R - 1);
 }
 __device__ __forceinline__ bool on_path(const CommitArgs &A, int node) { return static_cast<uint32_t>(node - 1) < static_cast<uint32_t>(A.R - 1); }
 

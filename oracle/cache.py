@@ -102,9 +102,10 @@ def store(pages, scales, table, rows, first, *, page, block):
 
 def commit(pages, scales, table, length, nodes, n_accepted, R, *, page, block):
     """Moves a path's rows (nodes, tokens length + node) to tokens length + 1 ..,
-    in place, and returns the new length.  Rows from pages outside are left out."""
+    in place, and returns the new length.  A path has at most R - 1 nodes.  Rows
+    from pages outside are left out."""
     path = []
-    for w in list(nodes)[:max(0, n_accepted)]:
+    for w in list(nodes)[:min(max(0, n_accepted), R - 1)]:
         if not 1 <= w < R:
             break
         path.append(int(w))

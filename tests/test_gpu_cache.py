@@ -432,3 +432,32 @@ def test_commit_paths_with_repeats_and_backwards():
         for b in range(3):
             assert oc.commit(pages, scales, table[b].tolist(), lens[b], nodes[b], counts[b], R, page=page, block=16) == int(got[b])
         assert np.array_equal(after[n], pages) and np.array_equal(after[n + "_scale"], scales)
+
+
+@pytest.mark.parametrize("held,D", [("f8", 64), ("f8", 128), ("bf16", 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_commit_at_the_tables_end(held, D, in_place):
+    """Paths that repeat nodes are no longer than the rows: nothing behind a sequence's table is looked up, no other page written."""
+    page, H = 16, 2
+    for R, most in ((2, 8), (4, 64), (1, 3), (5, 4)):
+        B = 3
+        wide, num = tables(B, 4, 2, R)
+        table = wide[:, 1:3]                       # the entries behind a row of it are pages that belong to nobody
+        cache = make_cache(num, page, H, D, held, 16, 7)
+        before = snapshot(cache)
+        lens = [2 * page - R, 2 * page - R, page - 2]
+        nodes = np.full((B, most), R - 1, dtype=np.int32)
+        nodes[1, ::2] = 1
+        counts = [most, most, 1 << 30]
+        length = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        got = sv.cache_commit(cache, table, length, torch.from_numpy(nodes).to(DEV), torch.tensor(counts, dtype=torch.int32, device=DEV),
+                              rows=R, new_len=length if in_place else None)
+        torch.cuda.synchronize()
+        after = snapshot(cache)
+        for n in ("k", "v"):
+            pages, scales = before[n].copy(), None if held != "f8" else before[n + "_scale"].copy()
+            for b in range(B):
+                new = oc.commit(pages, scales, table[b].tolist(), lens[b], nodes[b], counts[b], R, page=page, block=16)
+                assert new == int(got[b]) == lens[b] + (1 if R == 1 else 1 + min(most, R - 1))
+            assert np.array_equal(after[n], pages)
+            assert scales is None or np.array_equal(after[n + "_scale"], scales)

@@ -88,3 +88,18 @@ def test_commit_moves_the_path(np_rng, eight):
     # a node outside the rows ends the path
     assert oc.commit(pages, scales, table, length, [1, 14, 2], 3, R, page=page, block=block) == length + 2
     assert oc.commit(pages, scales, table, length, [1], -5, R, page=page, block=block) == length + 1
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_commit_stays_within_the_rows(np_rng, eight):
+    """A path that names more nodes than a tree of R can have ends at the rows' own places, the last that the table has room for."""
+    page, table = 16, [1, 3]
+    for R, nodes, moved in ((2, [1, 1, 1, 1], 1), (4, [3, 2, 2, 1, 1, 3], 3), (1, [1, 1], 0)):
+        pages = oc.f8_round(np_rng.uniform(-400, 400, (4, page, 2, 8)))
+        scales = np.full((4, 1, 2), 0.5) if eight else None
+        length = len(table) * page - R
+        want = pages.copy()
+        for i, w in enumerate(nodes[:moved]):
+            want[3, length + 1 + i - page] = pages[3, length + w - page]
+        assert oc.commit(pages, scales, table, length, nodes, len(nodes), R, page=page, block=page) == length + 1 + moved
+        assert np.array_equal(pages, want)
