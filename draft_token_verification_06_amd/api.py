@@ -642,6 +642,9 @@ class PagedCache:
             raise ValueError("k and v: the values of a head must be contiguous")
         if 0 in shape:
             raise ValueError("k and v: expected pages")
+        # (the library takes a stride of zero for a dense one)
+        if token_stride <= 0 or (num_pages > 1 and page_stride <= 0) or (Hkv > 1 and head_stride <= 0):
+            raise ValueError("k and v: pages, tokens or heads overlap")
         block, ks, vs = 0, 0, 0
         if code == SV_DT_F8E4M3:
             blocks = k_scale.shape[-2] if k_scale is not None and k_scale.dim() > 2 else 0

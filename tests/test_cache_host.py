@@ -292,3 +292,35 @@ def test_commit_refuses_lengths_over_the_counts(at, status):
     """new_len is written while n_accepted is still read."""
     other = FAKE + (1 << 20)
     assert _commit(n_accepted=other, new_len=other + at) == status
+
+
+class _Pages:
+    """What PagedCache looks at of a device tensor."""
+    def __init__(self, shape, stride, dtype=torch.bfloat16):
+        self.shape, self._stride, self.dtype, self.device = torch.Size(shape), stride, dtype, torch.device("cuda", 0)
+
+    def stride(self):
+        return self._stride
+
+    def data_ptr(self):
+        return FAKE
+
+
+@pytest.mark.parametrize("shape,stride", [
+    ((1000, 16, 2, 64), (0, 128, 64, 1)),       # one page for all
+    ((10, 16, 2, 64), (2048, 0, 64, 1)),        # one token for all
+    ((1, 16, 1, 64), (1024, 0, 64, 1)),
+    ((10, 16, 8, 64), (1024, 64, 0, 1)),        # one head for all
+    ((3, 1000, 16, 2, 64), (2048, 0, 128, 64, 1)),
+    ((3, 10, 16, 8, 64), (10240, 1024, 64, 0, 1)),
+    ((3, 10, 16, 2, 64), (0, 2048, 128, 64, 1)),   # one layer for all
+])
+def test_expanded_pages_are_refused(shape, stride):
+    """A stride of zero is no order of pages: the library would take it for a dense one and go past the storage."""
+    with pytest.raises(ValueError):
+        sv.PagedCache(_Pages(shape, stride), _Pages(shape, stride))
+
+
+def test_strides_of_single_entries_do_not_matter():
+    c = sv.PagedCache(_Pages((1, 16, 1, 64), (0, 64, 0, 1)), _Pages((1, 16, 1, 64), (0, 64, 0, 1)))
+    assert _lib.PAGED_CACHE.unpack(c.args) == (FAKE, FAKE, 0, 0, BF16, 1, 16, 0, 1, 64, 0, 64, 0)

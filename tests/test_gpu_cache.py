@@ -461,3 +461,15 @@ def test_commit_at_the_tables_end(held, D, in_place):
                 assert new == int(got[b]) == lens[b] + (1 if R == 1 else 1 + min(most, R - 1))
             assert np.array_equal(after[n], pages)
             assert scales is None or np.array_equal(after[n + "_scale"], scales)
+
+
+def test_expanded_tensors_are_refused():
+    """Pages, tokens or heads that are one in memory."""
+    x = torch.zeros(4, 16, 2, 64, dtype=torch.float16, device=DEV)
+    for t in (x[:1].expand(4, 16, 2, 64), x[:, :1].expand(4, 16, 2, 64), x[:, :, :1].expand(4, 16, 2, 64), x[:1, :1, :1].expand(1, 16, 1, 64)):
+        with pytest.raises(ValueError):
+            sv.PagedCache(t, t)
+    x8 = torch.zeros(4, 16, 2, 64, dtype=torch.uint8, device=DEV).view(F8)
+    s = torch.ones(4, 1, 1, device=DEV)
+    with pytest.raises(ValueError):
+        sv.PagedCache(x8, x8, s.expand(4, 1, 2), s.expand(4, 1, 2))
