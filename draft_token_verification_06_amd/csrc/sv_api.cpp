@@ -881,11 +881,21 @@ bool rows_ok(const void *p, int64_t *stride, int64_t elems, int64_t rows, int by
   return rows == 1 || (*stride >= elems && *stride <= int64_t{1} << 40 && *stride * bytes % 16 == 0);
 }
 
-// out is in with the same stride, or the two spans are disjoint.
+// Whether rows of `ae` elements at a and of `be` at b share no memory: spans that
+// are apart, or parts of the same wider rows.
+bool rows_apart(const void *a, int64_t a_stride, int64_t ae, const void *b, int64_t b_stride, int64_t be, int64_t rows, int bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  if (a0 + ((rows - 1) * a_stride + ae) * bytes <= b0 || b0 + ((rows - 1) * b_stride + be) * bytes <= a0) return true;
+  if (rows == 1 || a_stride != b_stride) return false;
+  // (the rows are no longer than the stride; b's begin `at` bytes into a's)
+  const uint64_t wide = static_cast<uint64_t>(a_stride) * bytes, at = b0 >= a0 ? (b0 - a0) % wide : (wide - (a0 - b0) % wide) % wide;
+  return at >= static_cast<uint64_t>(ae) * bytes && at + static_cast<uint64_t>(be) * bytes <= wide;
+}
+
+// out is in with the same stride, or the two are apart.
 bool in_place_or_apart(const void *in, int64_t in_stride, const void *out, int64_t out_stride, int64_t elems, int64_t rows, int bytes) {
   if (in == out) return rows == 1 || in_stride == out_stride;
-  const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
-  return i0 + ((rows - 1) * in_stride + elems) * bytes <= o0 || o0 + ((rows - 1) * out_stride + elems) * bytes <= i0;
+  return rows_apart(in, in_stride, elems, out, out_stride, elems, rows, bytes);
 }
 
 }  // namespace

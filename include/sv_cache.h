@@ -61,7 +61,8 @@ int sv_rotary_turns(const double *inv_freq, int32_t n, uint64_t *turns);
  *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin)
  *   x, out   [B][R] rows of x_row_stride / out_row_stride elements (0 = H * D),
  *            each H heads of D; `dtype` float32, bf16 or fp16.  out may be x
- *            (same stride); else the two do not overlap.  Values from rot on are
+ *            (same stride); else no value of the two shares memory (other heads
+ *            of the same wider rows: the same stride).  Values from rot on are
  *            copied.
  *   turns    DEVICE [rot / 2], see sv_rotary_turns.
  *   rot      even number of turned values, at most D.  (Multiples of 16 are
@@ -97,7 +98,8 @@ int sv_rotary(const void *x, int64_t x_row_stride, void *out, int64_t out_row_st
  *              hold the same type.
  *   q, q_out   NULL (Hq = 0), or [B][R] rows of q_row_stride / q_out_row_stride
  *              elements (0 = Hq * D), Hq heads of D: the queries, turned as the
- *              keys are.  q_out may be q (same stride); else they do not overlap.
+ *              keys are.  q_out may be q (same stride); else no value of the
+ *              two shares memory, as for sv_rotary.
  *   turns, rot, interleaved, magnitude  as for sv_rotary, rot a multiple of 16;
  *              turns NULL (rot 0): not turned (queries are copied).
  * Values are stored unturned, keys turned and rounded once: to dtype, or in 8-bit

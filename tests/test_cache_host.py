@@ -324,3 +324,9 @@ def test_expanded_pages_are_refused(shape, stride):
 def test_strides_of_single_entries_do_not_matter():
     c = sv.PagedCache(_Pages((1, 16, 1, 64), (0, 64, 0, 1)), _Pages((1, 16, 1, 64), (0, 64, 0, 1)))
     assert _lib.PAGED_CACHE.unpack(c.args) == (FAKE, FAKE, 0, 0, BF16, 1, 16, 0, 1, 64, 0, 64, 0)
+
+
+@pytest.mark.parametrize("at,wide", [(8, 320), (312, 640), (328 + 640, 640), (-8, 960), (640 * 3 + 312, 640), (960 - 312, 960), (320, 639 // 8 * 8)])
+def test_rotary_refuses_parts_that_meet(at, wide):
+    """Two parts of rows `wide` apart, each 320 long: out begins `at` elements behind x."""
+    assert _rotary(x=FAKE + 4096, x_stride=wide, out=FAKE + 4096 + 2 * at, out_stride=wide) == -1

@@ -473,3 +473,18 @@ def test_expanded_tensors_are_refused():
     s = torch.ones(4, 1, 1, device=DEV)
     with pytest.raises(ValueError):
         sv.PagedCache(x8, x8, s.expand(4, 1, 2), s.expand(4, 1, 2))
+
+
+def test_queries_turned_into_another_part_of_their_rows():
+    """q_out is a part of the projection's rows that nothing else reads."""
+    page, D, H, R, B = 16, 64, 2, 9, 3
+    table, num = tables(B, 3, 0, 2)
+    wide = torch.randn(B, R, 4 + 2 * H + 4, D, device=DEV).to(torch.float16)
+    q, k, v, q_out = wide[:, :, :4], wide[:, :, 4:4 + H], wide[:, :, 4 + H:4 + 2 * H], wide[:, :, 4 + 2 * H:]
+    cache = make_cache(num, page, H, D, "f8", 16, 9)
+    f, _ = sv.rotary_frequencies(D)
+    lens, before, kept = [0, 15, 30], snapshot(cache), wide.clone()
+    got = sv.cache_append(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), k, v, q=q, q_out=q_out, turns=sv.rotary_turns(f, DEV))
+    torch.cuda.synchronize()
+    assert got is q_out and torch.equal(wide[:, :, :4 + 2 * H], kept[:, :, :4 + 2 * H])
+    check_append(cache, before, table, lens, [R] * B, k, v, q, q_out, host(q_out), f=f, base=lens, parent=None, inter=False, mag=1.0, dtype="f16")

@@ -162,3 +162,23 @@ def test_refusals_on_the_device():
         a.update(kw)
         with pytest.raises((ValueError, sv.SvError)):
             sv.rotary(a.pop("x"), a.pop("turns"), a.pop("base_pos"), **a)
+
+
+@pytest.mark.parametrize("to", [0, 4, 6])
+def test_parts_of_the_same_rows(to):
+    """x and out may be different heads of one wide row: no two values meet."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    wide = torch.randn(3, 5, 8, 32, generator=g, device=DEV).to(torch.bfloat16)
+    f, _ = sv.rotary_frequencies(32)
+    turns, pos = sv.rotary_turns(f, DEV), torch.tensor([5, 900, 77], device=DEV)
+    x = wide[:, :, 2:4]
+    want, before = sv.rotary(x.contiguous(), turns, pos), wide.clone()
+    out = wide[:, :, to:to + 2]
+    assert sv.rotary(x, turns, pos, out=out) is out
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    before[:, :, to:to + 2] = want
+    assert torch.equal(wide, before)
+    for meets in (wide[:, :, 1:3], wide[:, :, 3:5]):
+        with pytest.raises(sv.SvError):
+            sv.rotary(x, turns, pos, out=meets)
