@@ -970,6 +970,9 @@ int sv_cache_append(const sv_paged_cache *cache, const int32_t *page_table, int6
   if (Hq > 0) {
     if (!rows_ok(q, &q_row_stride, elems, rows, 2) || !rows_ok(q_out, &q_out_row_stride, elems, rows, 2)) return SV_EINVAL;
     if (!in_place_or_apart(q, q_row_stride, q_out, q_out_row_stride, elems, rows, 2)) return SV_EINVAL;
+    // (other workgroups read keys and values while queries are written)
+    if (!rows_apart(k, k_row_stride, kv, q_out, q_out_row_stride, elems, rows, 2)) return SV_EINVAL;
+    if (!rows_apart(v, v_row_stride, kv, q_out, q_out_row_stride, elems, rows, 2)) return SV_EINVAL;
   } else if (q || q_out) {
     return SV_EINVAL;
   }

@@ -99,7 +99,7 @@ int sv_rotary(const void *x, int64_t x_row_stride, void *out, int64_t out_row_st
  *   q, q_out   NULL (Hq = 0), or [B][R] rows of q_row_stride / q_out_row_stride
  *              elements (0 = Hq * D), Hq heads of D: the queries, turned as the
  *              keys are.  q_out may be q (same stride); else no value of the
- *              two shares memory, as for sv_rotary.
+ *              two shares memory, as for sv_rotary; none of q_out is k's or v's.
  *   turns, rot, interleaved, magnitude  as for sv_rotary, rot a multiple of 16;
  *              turns NULL (rot 0): not turned (queries are copied).
  * Values are stored unturned, keys turned and rounded once: to dtype, or in 8-bit

@@ -330,3 +330,14 @@ def test_strides_of_single_entries_do_not_matter():
 def test_rotary_refuses_parts_that_meet(at, wide):
     """Two parts of rows `wide` apart, each 320 long: out begins `at` elements behind x."""
     assert _rotary(x=FAKE + 4096, x_stride=wide, out=FAKE + 4096 + 2 * at, out_stride=wide) == -1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=FAKE + (1 << 30)), dict(v=FAKE + (1 << 30) + 1024), dict(k=FAKE + (1 << 30) - 16), dict(v=FAKE + (1 << 30) + 10 * 1024 - 16),
+    # one projection's rows of 4 + 2 + 2 heads of 128: the queries to the place of keys and values
+    dict(q_out=FAKE + 1024, k=FAKE + 1024, v=FAKE + 1536, q_stride=1024, q_out_stride=1024, k_stride=1024, v_stride=1024),
+    dict(q_out=FAKE, k=FAKE + 1024, v=FAKE + 512, q_stride=1024, q_out_stride=1024, k_stride=1024, v_stride=1024),
+])
+def test_append_refuses_queries_over_keys_and_values(kw):
+    """q_out is written while k and v are still read."""
+    assert _append(**kw) == -1
