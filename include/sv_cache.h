@@ -104,6 +104,9 @@ int sv_rotary(const void *x, int64_t x_row_stride, void *out, int64_t out_row_st
  *              turns NULL (rot 0): not turned (queries are copied).
  * Values are stored unturned, keys turned and rounded once: to dtype, or in 8-bit
  * pages to the nearest 8-bit number (ties to even) of the quotient by the scale.
+ * (By a scale that is no power of two, as only other programs leave them: turned
+ * keys enter the quotient as float32 numbers, inexact ones with their last bit
+ * set.)
  * The scale of a block of tokens and kv head, for keys and values each, with a
  * the largest finite magnitude among the call's rows in the block:
  *   a block that begins with the call's rows: the least power of two s >= 2^-100
@@ -157,7 +160,8 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
  *   new_len  [B] or NULL: ctx_len[b] + 1 + the path's length; may be ctx_len,
  *            apart from it and from n_accepted otherwise.
  * All rows of a path are read before one is stored.  8-bit rows (byte * scale)
- * are stored as sv_cache_append stores them, at token ctx_len[b] + 1 and on.
+ * are stored as sv_cache_append stores them, at token ctx_len[b] + 1 and on
+ * (products by a scale that is no power of two: rounded to float32 first).
  * A sequence with ctx_len[b] < 0 or ctx_len[b] + R > table_pages * page is left
  * alone, its length too; rows from or to pages outside [0, num_pages) are left
  * out. */

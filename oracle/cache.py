@@ -102,8 +102,8 @@ def store(pages, scales, table, rows, first, *, page, block):
 
 def commit(pages, scales, table, length, nodes, n_accepted, R, *, page, block):
     """Moves a path's rows (nodes, tokens length + node) to tokens length + 1 ..,
-    in place, and returns the new length.  A path has at most R - 1 nodes.  Rows
-    from pages outside are left out."""
+    in place, and returns the new length.  A path has at most R - 1 nodes.  8-bit
+    rows times their scales are float32 numbers.  Rows from pages outside are left out."""
     path = []
     for w in list(nodes)[:min(max(0, n_accepted), R - 1)]:
         if not 1 <= w < R:
@@ -114,7 +114,7 @@ def commit(pages, scales, table, length, nodes, n_accepted, R, *, page, block):
         home, t = int(table[(length + w) // page]), (length + w) % page
         assert 0 <= home < len(pages)
         row = pages[home, t].copy()
-        rows.append(row if scales is None else row * scales[home, t // block][:, None])
+        rows.append(row if scales is None else (row * scales[home, t // block][:, None]).astype(np.float32).astype(np.float64))
     if rows:
         store(pages, scales, table, np.stack(rows), length + 1, page=page, block=block)
     return length + 1 + len(path)

@@ -488,3 +488,102 @@ def test_queries_turned_into_another_part_of_their_rows():
     torch.cuda.synchronize()
     assert got is q_out and torch.equal(wide[:, :, :4 + 2 * H], kept[:, :, :4 + 2 * H])
     check_append(cache, before, table, lens, [R] * B, k, v, q, q_out, host(q_out), f=f, base=lens, parent=None, inter=False, mag=1.0, dtype="f16")
+
+
+# -- scales that are no powers of two ----------------------------------------------------
+def near_middles(shape, dtype, seed):
+    """Numbers y of the type and float32 scales s whose quotients lie within 2^-24 of the middle t between two 8-bit numbers
+    (s is y / t rounded), at random."""
+    rng = np.random.default_rng(seed)
+    table = oc.f8_numbers()
+    t = ((table[1:] + table[:-1]) / 2)[rng.integers(8, 126, shape)]
+    y = torch.from_numpy(rng.uniform(1, 2, shape) * np.where(rng.random(shape) < 0.5, -1, 1)).to(DT[dtype])
+    return y, torch.from_numpy((np.abs(host(y)) / t).astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quotients_beside_a_middle(dtype):
+    """Unturned keys and values are rounded once, whatever the scale: to the nearer of two 8-bit numbers, however near the middle."""
+    page, D, H, B, R = 16, 64, 8, 64, 2
+    table, num = tables(B, 1, 0, 3)
+    cache = make_cache(num, page, H, D, "f8", 16, 4)
+    made = []
+    for i, s in enumerate((cache.k_scale, cache.v_scale)):
+        y, scale = near_middles((B, H), dtype, 5 + i)
+        s[table[:, 0].long(), 0] = scale.to(DEV)
+        x = torch.zeros(B, R, H, D, dtype=DT[dtype], device=DEV)
+        x[:, 0, :, 3], x[:, 1, :, 40], x[:, 1, :, 41] = y.to(DEV), -y.to(DEV), y.to(DEV) / 2
+        made.append(x)
+    k, v = made
+    lens = [5] * B
+    before = snapshot(cache)
+    sv.cache_append(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), k, v)
+    torch.cuda.synchronize()
+    check_append(cache, before, table, lens, [R] * B, k, v, None, None, None, f=None, base=lens, parent=None, inter=False, mag=1.0, dtype=dtype)
+
+
+@pytest.mark.parametrize("D,inter", [(64, False), (128, True)])
+def test_turned_keys_by_scales_of_other_programs(D, inter):
+    """Turned keys: the nearest 8-bit number of the quotient, but for quotients within 2^-22 of a middle (a key's float32
+    number, rounded to odd, is off by up to 2^-23 of it)."""
+    page, H, B, R = 32, 4, 8, 20
+    table, num = tables(B, 2, 1, 3)
+    draw = lambda shape, g: torch.exp2(torch.rand(shape, generator=g, device=DEV, dtype=torch.float64) * 3 - 8).float()  # noqa: E731
+    cache = make_cache(num, page, H, D, "f8", 32, 4, scales=draw)
+    f, _ = sv.rotary_frequencies(D)
+    _, k, v = rows_of(B, R, 0, H, D, "bf16", 6)
+    lens, before = [3, 31, 7, 1, 20, 12, 29, 5], snapshot(cache)
+    sv.cache_append(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), k, v, turns=sv.rotary_turns(f, DEV), interleaved=inter)
+    torch.cuda.synchronize()
+    after = snapshot(cache)
+    want = {n: x.copy() for n, x in before.items()}
+    for b in range(B):
+        turned = oc.rotate(host(k[b]), lens[b] + np.arange(R), f, interleaved=inter)
+        oc.store(want["k"], want["k_scale"], table[b].tolist(), turned, lens[b], page=page, block=32)
+        oc.store(want["v"], want["v_scale"], table[b].tolist(), host(v[b]), lens[b], page=page, block=32)
+        for r in range(R):  # keys beside a middle may be either number
+            t = lens[b] + r
+            at = (int(table[b, t // page]), t % page)
+            with np.errstate(invalid="ignore"):
+                x = turned[r] / want["k_scale"][at[0], 0][:, None]
+                mid = (after["k"][at] + want["k"][at]) / 2
+                beside = (after["k"][at] != want["k"][at]) & (np.abs(x - mid) <= 2.0 ** -22 * np.abs(mid))
+            want["k"][at] = np.where(beside, after["k"][at], want["k"][at])
+    for n in ("k", "v"):
+        assert np.array_equal(after[n + "_scale"], want[n + "_scale"])
+        same_8bit(after[n], want[n])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_commit_between_scales_of_other_programs(D):
+    """Moved bytes, times a scale and divided by another, neither a power of two: the definition's numbers."""
+    page, H, L, R = 16, 3, 6, 14
+    table, num = tables(4, 3, 1, 3)
+    draw = lambda shape, g: torch.exp2(torch.rand(shape, generator=g, device=DEV, dtype=torch.float64) * 4 - 8).float()  # noqa: E731
+    cache = make_cache(num, page, H, D, "f8", 16, 8, layers=L, scales=draw)
+    lens, nodes = [3, 14, 13, 29], np.array([[4, 13], [6, 7], [5, 9], [10, 11]], dtype=np.int32)
+    # quotients beside a middle: the target's scale is what byte * scale is of the middle
+    rng = np.random.default_rng(1)
+    mids = ((oc.f8_numbers()[1:] + oc.f8_numbers()[:-1]) / 2)[60:120]
+    tables_host = table.tolist()
+    for n in ("k", "v"):
+        x, s = host(getattr(cache, n).float()), host(getattr(cache, n + "_scale"))
+        for layer in range(L):
+            for b in (1, 2, 3):                    # the rows move to another block than they stand in
+                src, dst = lens[b] + int(nodes[b, 0]), lens[b] + 1
+                assert src // page == dst // page + 1
+                for h in range(H):
+                    y = np.abs(x[layer, tables_host[b][src // page], src % page, h, 5]) * s[layer, tables_host[b][src // page], 0, h]
+                    if y > 0:
+                        getattr(cache, n + "_scale")[layer, tables_host[b][dst // page], 0, h] = float(y / rng.choice(mids))
+    before = snapshot(cache)
+    got = sv.cache_commit(cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), torch.from_numpy(nodes).to(DEV),
+                          torch.tensor([2, 2, 2, 2], dtype=torch.int32, device=DEV), rows=R)
+    torch.cuda.synchronize()
+    after = snapshot(cache)
+    for n in ("k", "v"):
+        for layer in range(L):
+            pages, scales = before[n][layer].copy(), before[n + "_scale"][layer].copy()
+            for b in range(4):
+                assert oc.commit(pages, scales, tables_host[b], lens[b], nodes[b], 2, R, page=page, block=16) == int(got[b])
+            assert np.array_equal(after[n + "_scale"][layer], scales) and np.array_equal(after[n][layer], pages)

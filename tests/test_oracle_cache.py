@@ -103,3 +103,13 @@ def test_commit_stays_within_the_rows(np_rng, eight):
             want[3, length + 1 + i - page] = pages[3, length + w - page]
         assert oc.commit(pages, scales, table, length, nodes, len(nodes), R, page=page, block=page) == length + 1 + moved
         assert np.array_equal(pages, want)
+
+
+def test_commit_by_other_scales_goes_through_float32():
+    """3 bits' numbers times a scale of 24 bits, rounded to float32, over another scale."""
+    pages, scales = np.zeros((2, 16, 1, 4)), np.array([[[np.float32(0.0123)]], [[np.float32(0.37)]]], dtype=np.float64)
+    pages[0, 14, 0], pages[1, 1, 0] = 400.0, [448.0, 13.0, -0.0625, 0.001953125]
+    assert oc.commit(pages, scales, [0, 1], 14, [3], 1, 4, page=16, block=16) == 16
+    x = (np.array([448.0, 13.0, -0.0625, 0.001953125]).astype(np.float32) * np.float32(0.37)).astype(np.float64)
+    s = float(np.float32(0.0123)) * 32             # the least with 165.76 <= 448 s
+    assert scales[0, 0, 0] == s and np.array_equal(pages[0, 15, 0], oc.f8_round(x / s)) and (pages[0, 14, 0] == 12).all()
