@@ -420,19 +420,22 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
       }
       vf = ref > 0.0f ? vf / ref : 0.0f;  // (scales of zero alone so far)
     }
-    // One multiply-add per exponent, the key scale in its factor (never zero:
-    // masked products are -inf).  In float16 the largest is 2^15, held there
-    // however far the scores are and whatever their rounding (65504 ends the type).
+    // bf16: one multiply-add per exponent, the key scale in its factor (never
+    // zero: masked products are -inf).  In float16 the exponent is taken from the
+    // difference to the maximum, so that the largest is 2^15 exactly however far
+    // the scores are (65504 ends the type).
+    const float kq = F8 ? fmaxf(kf, __FLT_MIN__) : 1.0f;
     const float factor = F8 ? fmaxf(A.scale_log2 * kf, __FLT_MIN__) : A.scale_log2;
     uint4 p[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const float mu = T::kLift - (m[c] == kNegInf ? 0.0f : m[c] * A.scale_log2);
+      const float top_s = m[c] == kNegInf ? 0.0f : m[c], mu = top_s * A.scale_log2;
       float *e = s[c], sum = 0.0f;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const float arg = __builtin_fmaf(e[x], factor, mu);
-        e[x] = exp2_fast(T::kLift > 0 && arg > T::kLift ? T::kLift : arg);  // (NaN stays)
+#pragma clang fp contract(off)  // (the product is rounded as the maximum's was: no difference is above zero)
+        e[x] = exp2_fast(T::kLift > 0 ? __builtin_fmaf((F8 ? e[x] * kq : e[x]) - top_s, A.scale_log2, T::kLift)
+                                      : __builtin_fmaf(e[x], factor, -mu));
         sum += e[x];
         if (F8) e[x] *= vf;
       }

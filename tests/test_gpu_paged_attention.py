@@ -344,3 +344,45 @@ def test_scales_of_zero(dtype, R, Hq, P):
     check(res, q, cache, table, lens, prefix=prefix, P=P)
     if P == 0:
         assert np.abs(host(res.out[1])).max() < 2.0 ** -100
+
+
+@pytest.mark.parametrize("held", ["f8", "16"])
+@pytest.mark.parametrize("R,P", [(1, 0), (4, 0), (4, 700), (17, 700)])
+def test_large_scores_keep_their_differences(held, R, P):
+    """float16: scores of 131072 + d, exact in float32, weigh by d alone.  Tolerance: the one above, its term of the
+    scores' size A by that of their differences, as products and differences are exact here; a statistic of size S is
+    rounded five times (the scale, the maximum's product, the sum, the factor ln 2 and the product by it)."""
+    B, Hq, Hkv, D, page = 2, 8, 2, 64, 32
+    q, cache, table, prefix = make(B, R, Hq, Hkv, D, P, 900, "f16", held, page, 32, 12)
+    lens, size = [880, 300], 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(R)
+    q.zero_()
+    q[..., 0], q[..., 1] = 1024, torch.randint(1, 3, q.shape[:-1], generator=g, device=DEV).half()
+    k = torch.zeros(cache.k.shape, device=DEV)
+    k[..., 0] = size / 1024 if held == "16" else 256
+    k[..., 1] = torch.randint(-30, 31, k.shape[:-1], generator=g, device=DEV).float() * (1 if held == "16" else 0.5)
+    if held == "f8":   # powers of two apart, and numbers of 3 bits: -15 .. 15 times 1/4
+        k[..., 1] = torch.randint(-15, 16, k.shape[:-1], generator=g, device=DEV).float() / 4
+        cache.k_scale.fill_(4.0)
+        cache.k.copy_(k.to(F8))
+        assert torch.equal(cache.k.float(), k)
+    else:
+        cache.k.copy_(k)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    res = sv.paged_attention(q, cache, table, n, scale=0.125, prefix_table=prefix if P else None, prefix_len=P, return_lse=True)
+    torch.cuda.synchronize()
+    pk, pv = dense(cache, prefix, P) if P else (None, None)
+    h = HALF_STEP[q.dtype]
+    for b in range(B):
+        kb, vb = dense(cache, table[b], lens[b] + R)
+        qb = host(q[b])
+        out, lse = oracle.attention(qb, kb, vb, lens[b], prefix_k=pk, prefix_v=pv, scale=0.125)
+        weight, _ = oracle.attention(qb, kb, np.abs(vb), lens[b], prefix_k=pk, prefix_v=None if pv is None else np.abs(pv), scale=0.125)
+        values = vb if pv is None else np.concatenate([pv, vb])
+        N = len(values)
+        rel = 2 * (D + N + 16) * 2.0 ** -24 * (1 + 0.125 * 120)
+        tol = (h + rel) * weight * (1 + 2.0 ** -6) + h * np.abs(out) + 2.0 ** -24 + N * 2.0 ** -40 * np.abs(values).max()
+        err = np.abs(host(res.out[b]) - out)
+        assert (err <= tol).all(), (b, float((err / tol).max()))
+        err = np.abs(host(res.lse[b]) - lse)
+        assert (err <= 5 * 2.0 ** -24 * np.abs(lse) + rel).all(), (b, float(err.max()))
