@@ -308,13 +308,23 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
 // Attention over pages.  The rows of a sequence (times the heads of a group)
 // choose the kernel: up to 16, 32 or 48 of them stay one tile (few), more go by
 // tiles of 64 or 128 as above.  Tiles of 16 rows hold half of the registers: four
-// workgroups on a CU.  The join of pages reads 8 ranges at a time, so that a range
-// of a sequence costs it less (16 keys; a prefix's as above, where every row of
-// the batch writes and reads one: 132 us with 2 of them, 138 with 8).
+// workgroups on a CU, but for 16-bit heads of 128 (71 KB of LDS) and behind a
+// batch's prefix (the registers of its tiles of 128 rows), two.  With two counted
+// as such 64 windows of 4 rows over 300 keys, 16-bit, take 19 us for 31, 64 of them
+// behind 4096 keys, 8-bit, 46 for 58; over 215 batches, lengths and prefixes the mean is
+// 1.8% less (the worst 15% more: 64 single tokens over 1500 keys behind 8192).
+// Ranges of 1024 keys (crowded) begin at 4096 items for these tiles, however many
+// run at once, as sequences of one range write their outputs themselves: 128
+// single tokens over 2000 keys, 16-bit, 161 us, from 2048 items on 170.  The join
+// of pages reads 8 ranges at a time, so that a range of a sequence costs it less
+// (16 keys; a prefix's as above, where every row of the batch writes and reads
+// one: 132 us with 2 of them, 138 with 8).
 constexpr int64_t kPagedFewSlots = 1024;
 constexpr int64_t kPagedJoin = 16;
-// Most rows of a few.  (16-bit pages: 41 rows of 4 trees over 983 keys 19.3 us
-// as 48, 17.1 as 64; and values of 128 leave no registers for 48.)
+// Most rows of a few.  (16-bit pages, 36 to 48 rows as 48 and as tiles of 64: heads
+// of 128, which spill at 48, 64 windows of 9 rows over 300 keys 38 us for 32, one
+// over 1000 17.7 for 13.3; heads of 64 one 12.6 for 11.1, 64 behind 2048 keys 44 for
+// 40, but 64 without a prefix 16 for 24.)
 constexpr int paged_few_rows(bool f8) { return f8 ? 48 : 32; }
 struct PagedPlan : AttendPlan {
   int few;
@@ -331,13 +341,14 @@ inline PagedPlan plan_paged(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, int D
   const int64_t own_rows = L.few > 0 ? L.few : 32 * L.own_waves;
   const int64_t prefix_rows = L.prefix_waves == 4 ? 128 : L.few > 0 ? L.few : 32;
   const int64_t tiles = (all + prefix_rows - 1) / prefix_rows;
-  const int64_t slots = L.few == 16 ? kPagedFewSlots : kAttendSlots;
+  const bool batch_prefix = P > 0 && L.prefix_waves == 4;
+  const int64_t slots = L.few == 16 && !batch_prefix && (f8 || D == 64) ? kPagedFewSlots : kAttendSlots;
   L.own_tiles = static_cast<int>((own + own_rows - 1) / own_rows);
   const int64_t own_items = B * Hkv * L.own_tiles;
   const int longest = attend_bucket(static_cast<int>(max_ctx + R));
   for (int j = 0; j <= longest; ++j) {
     const int64_t keys = int64_t{128} << j;
-    const bool crowded = own_items * ((keys + 1023) / 1024) >= 4 * slots;
+    const bool crowded = own_items * ((keys + 1023) / 1024) >= 4 * (L.few == 16 ? kPagedFewSlots : kAttendSlots);
     int64_t parts = attend_parts(keys, own_items, own < own_rows ? own : own_rows, crowded, slots, kPagedJoin);
     const int64_t range = attend_range(keys, parts);
     L.split.tiles[j / 4] |= static_cast<uint64_t>(range / 128) << (16 * (j % 4));

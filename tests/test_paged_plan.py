@@ -52,3 +52,13 @@ def test_one_workspace_serves_both_page_widths(plans):
         for P, ctx in ((0, 100), (0, 40000), (2048, 4000), (100000, 131072)):
             assert size(*shape, P, ctx) == max(plans([(*shape, P, ctx, f8)])[0][4] for f8 in (0, 1))
     assert size(1, 1, 8, 3, 64, 0, 10) == 0
+
+
+def test_ranges_follow_the_workgroups_that_run_at_once(plans):
+    """512 items of 16 rows fill the chip where two workgroups fit on a CU (16-bit heads of 128, a batch's prefix in
+    front), and half of it where four do."""
+    own = lambda shape, P, f8: plans([(*shape, P, 300, f8)])[0][5]  # noqa: E731
+    wide, narrow = (64, 4, 32, 8, 128), (64, 4, 32, 8, 64)
+    assert own(wide, 0, 1) == 2 and own(narrow, 0, 1) == 2 and own(narrow, 0, 0) == 2
+    assert own(wide, 0, 0) == 1
+    assert own(wide, 4096, 1) == own(wide, 4096, 0) == own(narrow, 4096, 1) == 1
