@@ -57,18 +57,26 @@ __device__ __forceinline__ void unpack_f8(uint32_t w, float *x) {
   x[0] = lo[0], x[1] = lo[1], x[2] = hi[0], x[3] = hi[1];
 }
 
-// A number in float32, given as f, one of the two beside it, and the sign of what is
-// left: inexact, it has its last bit set (f where f is not finite).
-__device__ __forceinline__ float to_odd(float f, double rest) {
+// d in float32, an inexact result with its last bit set.
+__device__ __forceinline__ float round_to_odd(double d) {
+  const float f = static_cast<float>(d);
+  const double rest = d - static_cast<double>(f);  // (NaN and infinities: not a number, left alone)
   const uint32_t bits = __float_as_uint(f);
   const bool even = !(bits & 1) && finite(f);
   if (even && rest > 0) return __uint_as_float(bits + (f < 0 || bits == 0x80000000u ? -1 : 1));
   if (even && rest < 0) return __uint_as_float(bits + (f < 0 || bits == 0x80000000u ? 1 : -1));
   return f;
 }
-__device__ __forceinline__ float round_to_odd(double d) {
-  const float f = static_cast<float>(d);
-  return to_odd(f, d - static_cast<double>(f));  // (NaN and infinities: not a number, left alone)
+
+// y / n in float32, an inexact result with its last bit set (but for those below
+// 2^-60); n in [1/2, 1), about = 1 / n to a unit or so.  One step of refinement
+// leaves one of the two numbers beside the quotient, whose remainder float32 holds.
+__device__ __forceinline__ float odd_quotient(float y, float n, float about) {
+  const float g = y * about, f = __builtin_fmaf(__builtin_fmaf(-g, n, y), about, g);
+  const float rest = __builtin_fmaf(-f, n, y);
+  const uint32_t bits = __float_as_uint(f);
+  const int away = (__float_as_uint(rest) ^ bits) >> 31 ? -1 : 1;
+  return !(bits & 1) && fabsf(f) > 0x1p-60f && rest != 0.0f ? __uint_as_float(bits + away) : f;
 }
 
 // Sine and cosine of `phase` 2^-64 turns.
@@ -332,8 +340,7 @@ __device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live
   }
   if (lane == 0 && (!earlier || j > 0)) *scale = now;
   // A power of two (anything but a scale of the caller's own) divides exactly as
-  // its inverse.  Other quotients are formed one by one and rounded to odd: what
-  // the nearest leaves, times the scale, is exact in float64 (48 bits).
+  // its inverse.  Other quotients are formed one by one and rounded to odd.
   const bool exact = __builtin_amdgcn_readfirstlane((__float_as_uint(now) & 0x7FFFFF) == 0 && now >= 0x1p-126f);
   const float inverse = 1.0f / now;
 #pragma unroll
@@ -344,10 +351,11 @@ __device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = y[p][i] * inverse;
     } else {
+      const float part = __builtin_amdgcn_frexp_mantf(now), about = __builtin_amdgcn_rcpf(part);
+      const int e = __builtin_amdgcn_frexp_expf(now);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float f = y[p][i] / now;
-        x[i] = to_odd(f, fma(-static_cast<double>(f), static_cast<double>(now), static_cast<double>(y[p][i])));
+        x[i] = odd_quotient(__builtin_amdgcn_ldexpf(y[p][i], -e), part, about);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -525,10 +533,8 @@ __device__ __forceinline__ bool on_path(const CommitArgs &A, int node) { return 
 
 }  // namespace
 
-// (The waves are asked for so that float64 quotients, which few calls have, take no
-// registers from the others: 63 of them for 80, 18.3 us for 19.4.)
 template <bool F8, int D, int kP>
-__global__ void __launch_bounds__(kCommitThreads, !F8 || kP == 8 ? 1 : kP == 4 ? 3 : kP == 2 ? 5 : 8) k_commit(CommitArgs A) {
+__global__ void __launch_bounds__(kCommitThreads) k_commit(CommitArgs A) {
   constexpr int kU = kUnits<D>, kT = kPassTokens<D>;
   const int lane = threadIdx.x & 63;
   const int j = lane % kU, t_lane = lane / kU;
