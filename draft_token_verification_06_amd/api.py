@@ -3,7 +3,8 @@ argument marshalling only.
 
 Tensors must live on a ROCm device; every computation runs in the HIP
 library on the current torch stream of that device.  Results come back as
-device tensors; nothing synchronises.
+device tensors; nothing synchronises.  No call keeps an autograd history:
+outputs require no gradient, whatever the inputs do.
 """
 import ctypes
 import math
@@ -616,8 +617,8 @@ class PagedCache:
     k, v (num_pages, page, Hkv, D) in any non-overlapping order with unit
     stride along D: bf16 or fp16, or float8_e4m3fn with k_scale, v_scale
     (num_pages, page / block, Hkv) float32, contiguous.  One more leading
-    dimension on all of them holds the layers of a model (layer(i) is one of
-    them).  A handle on those tensors: they keep their storage while it is used.
+    dimension on all of them holds the layers of a model, behind each other
+    (layer(i) is one of them).  A handle on those tensors: they keep their storage while it is used.
     paged_cache() allocates one."""
     __slots__ = ("k", "v", "k_scale", "v_scale", "layers", "layer_stride", "code", "page", "heads", "dim", "device", "args")
 
@@ -746,8 +747,9 @@ def rotary(x, turns, base_pos=None, *, parent=None, interleaved=False, magnitude
     x (B, R, H, D) float32, bf16 or fp16; turns: rotary_turns of the pairs'
     frequencies, (rot / 2,) int64.  Row r stands at base_pos[b] + r, or with
     parent (a host sequence) at base_pos[b] + its depth; base_pos (B,) int64 or
-    None (0).  inverse turns back: with the same magnitude, the gradient.  out:
-    a tensor like x (x itself: in place), a new one when None."""
+    None (0).  inverse turns back: with the same magnitude, the gradient, which the
+    caller's backward pass asks for.  out: a tensor like x (x itself: in place), a
+    new one when None."""
     dtype, dev = x.dtype, x.device
     if x.dim() != 4 or dtype not in _DTYPE_CODE or dev.type != "cuda":
         raise ValueError("x: expected a float32, bf16 or fp16 device tensor of shape (B, R, H, D)")
@@ -785,7 +787,8 @@ def cache_append(cache, page_table, ctx_len, k, v, *, q=None, turns=None, base_p
     token ctx_len[b] + r.  k, v (B, R, Hkv, D) bf16 or fp16, q (B, R, Hq, D) or
     None (each may be a part of one projection's rows).  turns, base_pos, parent,
     interleaved, magnitude as in rotary (turns None: not turned; base_pos None:
-    ctx_len).  Returns q_out (a new tensor when None; q itself: in place), or
+    ctx_len; behind a prefix of P tokens that the batch shares it is P + ctx_len).
+    Returns q_out (a new tensor when None; q itself: in place), or
     None without q."""
     dtype, dev = k.dtype, k.device
     if k.dim() != 4 or (dtype != torch.bfloat16 and dtype != torch.float16) or dev.type != "cuda":

@@ -35,12 +35,15 @@ extern "C" {
  *   page    tokens of a page: 16, 32, 64, 128 or 256.
  *   block   8-bit pages: tokens that share a scale: 16, 32 or 64, at most page.
  *           A stored value is byte * scale[(p * (page / block) + t / block) *
- *           Hkv + h].  Scales are finite and positive, or zero where a block is zeros.
+ *           Hkv + h].  Scales are finite and positive, or zero where a block is
+ *           zeros.  (sv_cache_append leaves powers of two from 2^-100 on.  Of scales
+ *           below 2^-126 a value may count for anything up to 2^-117.)
  *           Others (16-bit pages): ignored.
  *   k_scale, v_scale  [num_pages][page / block][Hkv] float; NULL for 16-bit pages.
  *   D       64 or 128.
  * Addresses are 16-byte aligned and so are strides in bytes (scales 4); no two
- * values share memory (SV_EINVAL otherwise, also for strides that interleave). */
+ * values of k share memory, and none of v (SV_EINVAL otherwise, also for strides
+ * that interleave), nor may any of k and of v (not checked). */
 typedef struct {
   void *k, *v;
   float *k_scale, *v_scale;
@@ -92,7 +95,10 @@ int sv_rotary(const void *x, int64_t x_row_stride, void *out, int64_t out_row_st
  *   row_count  [B] or NULL (= R): rows to append (clamped to [0, R]).
  *   parent_host  NULL: row r stands at position base_pos[b] + r; else HOST [R],
  *              a tree as in sv_verify_tree: at base_pos[b] + the node's depth.
- *   base_pos   [B] int64, or NULL (= ctx_len).
+ *   base_pos   [B] int64, or NULL (= ctx_len: the pages hold a sequence from its
+ *              first token on).  Behind P tokens that the batch shares (the
+ *              prefix_table of sv_paged_attention, whose own keys were appended
+ *              at 0 .. P - 1) rows stand at P + ctx_len: the caller gives that.
  *   k, v       [B][R] rows of k_row_stride / v_row_stride elements (0 = Hkv * D),
  *              each Hkv heads of D, `dtype` SV_DT_BF16 or SV_DT_F16; 16-bit pages
  *              hold the same type.
@@ -134,7 +140,12 @@ int sv_cache_append(const sv_paged_cache *cache, const int32_t *page_table, int6
  *   8-bit pages: keys and values are byte * scale.  The bytes enter the products
  *            exactly; scales are applied in float32 (or, powers of two, with the
  *            bytes in bf16, exactly): to a key's scores, and of the values to the
- *            exponentials before those are rounded to dtype.
+ *            exponentials before those are rounded to dtype.  (fp16: exponentials
+ *            are held 2^15 times larger, relative to the largest value scale of
+ *            the range; products below 2^-29 of it lose up to 2^-40 of it.)
+ * Rows are a step's, as for sv_attention: windows of SV_MAX_GAMMA + 1 at most,
+ * trees of SV_TREE_MAX_NODES.  (sv_cache_append takes prompts of any length; their
+ * own attention is not among these operators.)
  * A page number outside [0, num_pages) among a sequence's tokens makes its rows
  * NaN, one in the prefix all rows; no memory outside the pages is read.  Table
  * entries past a sequence's tokens do not matter. */
@@ -149,8 +160,8 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
 /* Keeps a tree's accepted path: the keys and values of its nodes, stored by
  * sv_cache_append at tokens ctx_len[b] + node, move to tokens ctx_len[b] + 1 ..
  * behind the root's, in every layer.  (Their positions were the depths already.)
- *   layers   caches of one shape, layer_stride elements apart in k and v (0 =
- *            dense), their scales num_pages * (page / block) * Hkv apart; all
+ *   layers   caches of one shape behind each other, layer_stride elements apart
+ *            in k and v (0 = dense), their scales num_pages * (page / block) * Hkv apart; all
  *            follow the one page_table.
  *   nodes    [B] rows of nodes_stride int32 (0 = max_nodes): out_nodes of
  *            sv_verify_tree.  NULL (a window, max_nodes = 0): nothing moves, the
