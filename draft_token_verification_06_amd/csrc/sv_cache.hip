@@ -161,8 +161,9 @@ template <class... Tree> __device__ __forceinline__ int row_depth(int r, const T
 
 // ---------------------------------------------------------------------------
 // Rotary positions alone.  Bound: memory (each value read and written once): 4
-// times 8191 rows of 32 heads of 128 take 114 us, 4.7 TB/s of the 4.9 that a copy
-// reaches; 72 rows 3.1 us, a launch and two trips to memory.
+// times 8191 rows of 32 heads of 128 in 16 bits take 114 us, 4.7 TB/s of the 4.9
+// that a copy reaches, half of the rows in float32, as many bytes, 133 us, 4.0 TB/s;
+// 72 rows 3.1 to 3.6 us, a launch and two trips to memory.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -244,7 +245,9 @@ __global__ void __launch_bounds__(kRotaryThreads) k_rotary(RotaryArgs A, Tree...
 }
 
 // Any even number of turned values: a thread per pair (and per two values
-// behind them), 2 or 4 bytes at a time.  Only for what units of 16 do not cover.
+// behind them), 2 or 4 bytes at a time.  Only for what units of 16 do not cover:
+// the same bytes take 240 us in 16 bits (2.2 TB/s) and 180 in float32 (3.0), bound by
+// the number of loads and stores; 72 rows 6.5 us.
 template <int DT, class... Tree>
 __global__ void __launch_bounds__(kRotaryThreads) k_rotary_pairs(RotaryArgs A, Tree... tree) {
   extern __shared__ float2 s_cs[];
@@ -376,14 +379,17 @@ __device__ __forceinline__ void store_f8(const float (&y)[kP][16], uint32_t live
 // once, into registers, where 8-bit pages find their scale.
 //
 // Bound: memory for prompts.  4 times 4096 rows of 32 + 2 * 8 heads of 128, half
-// of each turned: 265 MB in 69 to 71 us (3.8 TB/s) in 8-bit blocks of 32, where float64
-// products and conversions take turns with the memory; 403 MB in 89 us (4.5 TB/s)
-// in 16 bits; 113 us in blocks of 64, whose 8 passes leave two waves a SIMD.
+// of each turned: 369 MB in 84 us in 8-bit blocks of 16 (4.4 TB/s), 95 in blocks of 32
+// and 112 in blocks of 64, where float64 products and conversions take turns with
+// the memory and 4 and 8 passes leave three and two waves a SIMD; 403 MB in 95 us
+// (4.2 TB/s) in 16 bits.  Whole heads turned cost up to 3 us more.  One prompt of 512
+// rows has few workgroups: 9.6, 15 and 26 us in blocks of 16, 32 and 64, 9.4 in 16 bits.
 // Steps are trips to memory after each other (length, page, rows, store): one
-// token 6.5 us, 64 windows of 9 rows 11 us, 128 single tokens 6.6.
+// token 6.5 to 7.3 us, 64 windows of 9 rows 11, 128 single tokens 6.6 to 7.1; in 16
+// bits 4.1, 8.9 and 5.7.
 // Keys in float32, with a bound on the error and only passes with an open byte
-// once more in float64, were slower (107 us for 77, windows 13.1 for 11.5): the
-// test costs more than the products.
+// once more in float64, were slower (11776 rows of four prompts in blocks of 32 107
+// us for 77, windows 13.1 for 11.5): the test costs more than the products.
 // ---------------------------------------------------------------------------
 namespace {
 // Angles of a row in LDS: two more than there are, so that rows begin 16 bytes
@@ -517,8 +523,9 @@ __global__ void __launch_bounds__(kAppendThreads, kP == 8 ? 2 : kP == 4 ? 3 : 4)
 // Keeping an accepted path.  One wave per (layer, sequence, head, keys or
 // values): it holds the path's rows in registers before it stores the first.
 // Bound: trips to memory after each other (path, pages, rows and scales, store):
-// 2.9 us for 4 trees of one layer.  64 trees of 32 layers take 18 us, of which the
-// 12.6 MB alone would be 2.6: rows of 128 bytes over gigabytes of pages.
+// 2.9 to 3.3 us for 4 trees of one layer.  64 trees of 32 layers take 18 us, of which
+// the 12.6 MB alone would be 2.6: rows of 128 bytes over gigabytes of pages.  Paths of
+// three nodes each are 25 MB, 21 us, in 16-bit pages 50 MB, 14 us (3.5 TB/s).
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -677,9 +684,10 @@ void launch_append_passes(const AppendArgs &A, const TreeDepths *depths, hipStre
   const int64_t x = static_cast<int64_t>(A.B) * A.blocks;
   const int64_t tasks = (2 * A.pool.Hkv + A.Hq + kAppendThreads / 64 - 1) / (kAppendThreads / 64);
   // Blocks that do not fill the chip: their heads are spread over workgroups, each
-  // of which forms the block's angles again.  Up to 4096 of them: a prompt of 4
-  // times 4096 rows in blocks of 16 took 71 us, with up to 2048 77, with 1024 88; in
-  // blocks of 64 113, 110 and 119.
+  // of which forms the block's angles again.  Up to 4096 of them: prompts of 4 times
+  // 4096 rows, half of each head turned, take 84, 95 and 112 us in blocks of 16, 32
+  // and 64; with up to 1024 88, 113 and 124, 2048 88, 94 and 112, 8192 83, 104 and 112
+  // (16 bits 95, 93, 96 and 95).
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(tasks, 4096 / x));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y)), threads(kAppendThreads);
   const unsigned lds = std::min(A.R, 1 << A.pool.block_shift) * append_row_angles(A.rotation.rot) * sizeof(float2) * (F8 ? 2 : 1);

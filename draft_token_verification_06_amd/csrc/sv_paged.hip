@@ -208,10 +208,12 @@ __device__ __forceinline__ void wave_sync() {
 // consecutive rows (no bank conflicts).
 //
 // Bound: memory.  128 single tokens of 32 / 8 heads of 128 over 4000 keys, 8-bit:
-// 178 us, 5.9 TB/s; over 1000 to 4000 behind 2048 shared ones 131 to 137.  32 rows of a
-// sequence in tiles of 16 rows of 16x16x32 products hold half the registers of tiles
-// of 32, so four workgroups are on a CU.  One sequence: trips to memory, 6.3 us
-// over 100 keys, 10 over 1033, 12 over 4000, 21 over 30000 (with the join).
+// 178 to 182 us, 5.9 TB/s; over 1000 to 4000 behind 2048 shared ones 127 to 130.  Rows
+// of a sequence in tiles of 16 rows of 16x16x32 products hold half the registers of
+// tiles of 32: of 16 rows four workgroups are on a CU (two with 16-bit heads of 128,
+// whose tiles are 71 KB of LDS, or where a batch's prefix is in the same kernel).
+// One sequence: trips to memory, 6.3 to 6.9 us over 100 keys, 10 over 1033, 12 over 4000,
+// 21 over 30000 (with the join).
 // Tried: 16 waves a workgroup (slower but for 32 sequences of 1000), two tiles in flight
 // (144 to 141 us at two waves a SIMD; the registers hold two more waves instead).
 template <int DT, bool F8, int D, int NC>
@@ -540,7 +542,8 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
 //
 // Bound: 2304 rows of each of 8 kv heads over 8192 8-bit keys are 77 GFLOP, 53 us at
 // the rate of a large product; they take 112 (the matrix pipes are busy for 28 percent
-// of the cycles, the vector units for 42, both at once for 9).  Without its parts
+// of the cycles, the vector units for 42, both at once for 9).  With the join 123, in
+// float16, whose scales are products of their own, 139; 16-bit pages 118 and 124.  Without its parts
 // one by one: loads -18, values' products -13, exponentials -8, widening -8 us.
 // Tried: two LDS buffers and one barrier (122 us for 124 alone, 149 for 136 beside
 // the sequences' own keys), the next tile's scores beside the softmax (129.5 for 130.5),
