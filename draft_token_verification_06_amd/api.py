@@ -618,8 +618,8 @@ class PagedCache:
     stride along D: bf16 or fp16, or float8_e4m3fn with k_scale, v_scale
     (num_pages, page / block, Hkv) float32, contiguous.  One more leading
     dimension on all of them holds the layers of a model, behind each other
-    (layer(i) is one of them).  A handle on those tensors: they keep their storage while it is used.
-    paged_cache() allocates one."""
+    (layer(i) is one of them).  A handle on those tensors: they keep their
+    storage while it is used.  paged_cache() allocates one."""
     __slots__ = ("k", "v", "k_scale", "v_scale", "layers", "layer_stride", "code", "page", "heads", "dim", "device", "args")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):

@@ -543,8 +543,9 @@ __device__ __forceinline__ void few_item(const PagedAttendArgs &A, const PagedIt
 // Bound: 2304 rows of each of 8 kv heads over 8192 8-bit keys are 77 GFLOP, 53 us at
 // the rate of a large product; they take 112 (the matrix pipes are busy for 28 percent
 // of the cycles, the vector units for 42, both at once for 9).  With the join 123, in
-// float16, whose scales are products of their own, 139; 16-bit pages 118 and 124.  Without its parts
-// one by one: loads -18, values' products -13, exponentials -8, widening -8 us.
+// float16, whose scales are products of their own, 139; 16-bit pages 118 and 124.
+// Without its parts one by one: loads -18, values' products -13, exponentials -8,
+// widening -8 us.
 // Tried: two LDS buffers and one barrier (122 us for 124 alone, 149 for 136 beside
 // the sequences' own keys), the next tile's scores beside the softmax (129.5 for 130.5),
 // steps of 32 keys (136 for 124), three waves a SIMD (160), tiles of 16 and 48 rows (139 for 132).

@@ -309,16 +309,17 @@ inline AttendPlan plan_attention(int64_t B, int64_t R, int64_t Hq, int64_t Hkv, 
 // choose the kernel: up to 16, 32 or 48 of them stay one tile (few), more go by
 // tiles of 64 or 128 as above.  Tiles of 16 rows hold half of the registers: four
 // workgroups on a CU, but for 16-bit heads of 128 (71 KB of LDS) and behind a
-// batch's prefix (the registers of its tiles of 128 rows), two.  With two counted
-// as such 64 windows of 4 rows over 300 keys, 16-bit, take 19 us for 31, 64 of them
-// behind 4096 keys, 8-bit, 46 for 58; over 215 batches, lengths and prefixes the mean is
-// 1.8% less (the worst 15% more: 64 single tokens over 1500 keys behind 8192).
-// Ranges of 1024 keys (crowded) begin at 4096 items for these tiles, however many
-// run at once, as sequences of one range write their outputs themselves: 128
-// single tokens over 2000 keys, 16-bit, 161 us, from 2048 items on 170.  The join
-// of pages reads 8 ranges at a time, so that a range of a sequence costs it less
-// (16 keys; a prefix's as above, where every row of the batch writes and reads
-// one: 132 us with 2 of them, 138 with 8).
+// batch's prefix (the registers of its tiles of 128 rows; with heads of 64 three
+// are counted as two), two.  With two counted as such 64 windows of 4 rows over
+// 300 keys, 16-bit, take 19 us for 31, 64 of them behind 4096 keys, 8-bit, 46 for
+// 58; over 215 batches, lengths and prefixes the mean is 1.8% less (the worst 15%
+// more: 64 single tokens over 1500 keys behind 8192).  Ranges of 1024 keys
+// (crowded) begin at 4096 items for these tiles, however many run at once, as
+// sequences of one range write their outputs themselves: 128 single tokens over
+// 2000 keys, 16-bit, 161 us, from 2048 items on 170.  The join of pages reads 8
+// ranges at a time, so that a range of a sequence costs it less (16 keys; a
+// prefix's as above, where every row of the batch writes and reads one: 132 us
+// with 2 of them, 138 with 8).
 constexpr int64_t kPagedFewSlots = 1024;
 constexpr int64_t kPagedJoin = 16;
 // Most rows of a few.  (16-bit pages, 36 to 48 rows as 48 and as tiles of 64: heads

@@ -161,13 +161,13 @@ int sv_paged_attention(const void *q, int64_t q_row_stride, int dtype, const sv_
  * sv_cache_append at tokens ctx_len[b] + node, move to tokens ctx_len[b] + 1 ..
  * behind the root's, in every layer.  (Their positions were the depths already.)
  *   layers   caches of one shape behind each other, layer_stride elements apart
- *            in k and v (0 = dense), their scales num_pages * (page / block) * Hkv apart; all
- *            follow the one page_table.
+ *            in k and v (0 = dense), their scales num_pages * (page / block) *
+ *            Hkv apart; all follow the one page_table.
  *   nodes    [B] rows of nodes_stride int32 (0 = max_nodes): out_nodes of
  *            sv_verify_tree.  NULL (a window, max_nodes = 0): nothing moves, the
  *            lengths advance.  max_nodes <= 64.
- *   n_accepted [B] int32, the first that many nodes (clamped to [0, R - 1] and
- *            to max_nodes).  A node outside [1, R) ends the path.
+ *   n_accepted [B] int32, the first that many nodes (clamped to [0, R - 1], with
+ *            nodes to max_nodes too).  A node outside [1, R) ends the path.
  *   new_len  [B] or NULL: ctx_len[b] + 1 + the path's length; may be ctx_len,
  *            apart from it and from n_accepted otherwise.
  * All rows of a path are read before one is stored.  8-bit rows (byte * scale)
